@@ -354,6 +354,167 @@ int gdn_recurrence(const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t l
  */
 int nvfp4_weight_stream_read(const void* w_packed, int64_t n, int64_t k, uint32_t* sink, nvfp4_stream_t stream);
 
+/*
+ * The paged serving step of the hybrid model's softmax-attention layers (the
+ * pages' model interleaves them with the Gated DeltaNet layers and keeps their
+ * K/V cache in FP8 with calibrated scales; bayesiansapien page, Figure and "Two
+ * practical repairs"): paged_plan, paged_kv_write, paged_attention and
+ * verify_drafts.  A step serves `num_requests` requests; request r has
+ * ctx_lens[r] tokens in the cache and brings new_lens[r] >= 0 new ones (a prompt
+ * chunk, one token, or the last token and its drafts).  New tokens of all
+ * requests are laid end to end: token i of request r is row q_start[r] + i of
+ * every per-token tensor.  Lengths stay on the device; the host only knows
+ * bounds (max_tokens, max_new, max_seq), so a step can be captured in a graph.
+ *
+ * The cache is two buffers (K and V) of num_pages pages of page_size tokens, a
+ * power of two from 16 to 1024, for num_kv_heads heads of head_dim.  Element
+ * (page, head, token in page, d) of either lies at page * page_stride +
+ * head * head_stride + token * token_stride + d (elements; every stride a
+ * multiple of 16 bytes, 16 tokens of a page less than 2^31 bytes apart; pages
+ * may lie past 2^32 bytes).  Slot s is token
+ * s % page_size of page s / page_size.  Element types: NVFP4_CACHE_BF16, or
+ * NVFP4_CACHE_E4M3 with the value x held as E4M3(x / scale[head]).
+ */
+#define NVFP4_CACHE_BF16 0
+#define NVFP4_CACHE_E4M3 1
+
+#define NVFP4_LOGITS_F32 0
+#define NVFP4_LOGITS_BF16 1
+
+/*
+ * paged_plan -- block tables and slot maps of a step, built on the device from
+ * the requests' lengths (one launch).  With P = page_size, c = max(ctx_lens, 0),
+ * n = max(new_lens, 0):
+ *     q_start[r]  = n[0] + ... + n[r - 1],   seq_lens[r] = c[r] + n[r];
+ *     request r needs the table's columns min(ceil(c / P), max_pages) ..
+ *     min(ceil((c + n) / P), max_pages) - 1, and gets, in the order of the
+ *     requests and columns, the free pages free_pages[*free_cursor],
+ *     free_pages[*free_cursor + 1], ...; -1 once num_free is passed;
+ *     positions[t] = c[r] + i,  slots[t] = the slot of that position
+ *     (-1 without a page) for token i of request r at t = q_start[r] + i;
+ *     both -1 for t >= the total (padding).
+ *
+ *   ctx_lens, new_lens  int32 [num_requests], num_requests >= 0.
+ *   free_pages   int32 [num_free], num_free >= 0.
+ *   free_cursor  int32 [1]: how many of free_pages earlier steps took; may be
+ *                null (0).  Must not lie in counts.
+ *   block_table  int32 [num_requests, max_pages], row stride ld_table: read for
+ *                the contexts' columns, written for the new ones, else untouched.
+ *   q_start [num_requests + 1], seq_lens [num_requests], positions
+ *   [max_tokens], counts [4]: int32, out; slots [max_tokens]: int64, out.
+ *   counts       total new tokens; pages taken; pages missing; the cursor after
+ *                this step.  A total above max_tokens means that the step does
+ *                not fit (q_start stops at max_tokens).
+ */
+int paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t num_requests, int page_size,
+               const int32_t* free_pages, int64_t num_free, const int32_t* free_cursor, int32_t* block_table,
+               int64_t max_pages, int64_t ld_table, int32_t* q_start, int32_t* seq_lens, int32_t* positions,
+               int64_t* slots, int64_t max_tokens, int32_t* counts, nvfp4_stream_t stream);
+
+/*
+ * paged_kv_write -- the new tokens' K and V rows into the paged cache.
+ *
+ *   k, v         bf16 [tokens, num_kv_heads * head_dim], row strides ld_k, ld_v
+ *                (multiples of 8), 16-byte aligned; may be column slices of a
+ *                fused projection.
+ *   slots        int64 [tokens]; rows whose slot is outside the cache are
+ *                skipped.  Slots of one call must differ.
+ *   tokens >= 0 (0 enqueues nothing); head_dim 64, 128 or 256.
+ *   k_cache, v_cache  as above, cache_dtype NVFP4_CACHE_*.
+ *   k_scale, v_scale  device float [num_kv_heads], E4M3 only (null = 1): the
+ *                cache gets round-to-nearest-even of x / scale, clamped to
+ *                +-448.
+ */
+int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, const int64_t* slots,
+                   int64_t tokens, void* k_cache, void* v_cache, int cache_dtype, int64_t num_pages, int page_size,
+                   int num_kv_heads, int head_dim, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                   const float* k_scale, const float* v_scale, nvfp4_stream_t stream);
+
+/*
+ * paged_attention -- softmax attention of each request's new tokens over its
+ * cached keys, the new ones among them (written before by paged_kv_write).
+ * Token i of request r stands at position p = seq_lens[r] - n + i (n =
+ * q_start[r+1] - q_start[r]) and sees key j if j <= p, j > p - window (window
+ * > 0) and the table holds a page of the cache for j.  Query head h uses KV
+ * head h / (num_heads / num_kv_heads).  Over the keys it sees,
+ *     s_j = scale * k_scale * (q . k_j),  lse = log sum_j exp(s_j),
+ *     out = v_scale * sum_j exp(s_j - lse) v_j;
+ * a row that sees none gets 0 and lse = -inf.  Nothing is read of what the
+ * cache holds outside the keys of a request (it may be NaN).  Statistics and
+ * sums are fp32; the weights are rounded to bf16 for the product with V.
+ *
+ *   q            bf16 [tokens, num_heads * head_dim], row stride ld_q (multiple
+ *                of 8), 16-byte aligned.
+ *   q_start, seq_lens   as from paged_plan; rows of q from q_start[num_requests]
+ *                on (padding) are left untouched in out and lse.
+ *   max_new      >= every request's new tokens; max_seq >= every seq_lens[r]
+ *                (it only sizes the split of the work).
+ *   head_dim     64, 128 or 256 (others NVFP4_EUNSUPPORTED).
+ *   block_table  int32 [num_requests, max_pages], row stride ld_table.
+ *   k_scale, v_scale  device float [num_kv_heads], E4M3 only (null = 1).
+ *   out          [tokens, num_heads * head_dim] of out_dtype, row stride ld_out
+ *                (multiple of 4), 16-byte aligned.
+ *   lse          optional fp32 [tokens, num_heads] contiguous (natural log).
+ *   workspace    16-byte aligned, at least paged_attention_workspace_bytes of
+ *                the same sizes; any contents; not shared by calls in flight on
+ *                different streams.
+ * tokens == 0 or num_requests == 0 enqueues nothing.  Results are
+ * deterministic.
+ */
+size_t paged_attention_workspace_bytes(int64_t tokens, int64_t num_requests, int num_heads, int num_kv_heads,
+                                       int head_dim, int64_t max_new, int64_t max_seq);
+int paged_attention(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32_t* q_start, const int32_t* seq_lens,
+                    int64_t num_requests, int64_t max_new, int64_t max_seq, int num_heads, const void* k_cache,
+                    const void* v_cache, int cache_dtype, int64_t num_pages, int page_size, int num_kv_heads,
+                    int head_dim, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                    const int32_t* block_table, int64_t max_pages, int64_t ld_table, float scale, int64_t window,
+                    const float* k_scale, const float* v_scale, void* out, int out_dtype, int64_t ld_out, float* lse,
+                    void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * verify_drafts -- verification of drafted tokens (the multi-token-prediction
+ * drafting of the aipulsen page) against the target's probabilities, from given
+ * random numbers, so that the emitted tokens are distributed as the target's
+ * own.  Request r has n = num_drafts[r] drafts; row row_start[r] + i of the
+ * logits (0 <= i <= n) is the target's after i kept drafts: the rows of its
+ * chunk, so row_start may be a plan's q_start.  With x = logits / temperature,
+ * p_i = softmax(x_i), q_i = draft_probs[r, i] (one at the draft if null):
+ *     draft i is kept while uniform[r, i] * q_i(d_i) < p_i(d_i);
+ *     the token after the a kept ones is argmax_v of w_v / noise[r, v], -1 where
+ *     w_v is not positive (the lowest v of equals), with w = p_a - q_a, or p_a if
+ *     a == n or no w is positive.
+ * With standard exponential noise that argmax is v with probability
+ * w_v / sum(w).  temperature 0 is greedy: a draft is kept while it is the
+ * lowest argument of the row's maximum, which is also the next token.
+ *
+ *   logits       [rows, vocab] of logits_dtype NVFP4_LOGITS_*, row stride
+ *                ld_logits >= vocab; finite or -inf (NaN counts as -inf).
+ *   row_start, num_drafts  int32 [num_requests]; num_drafts < 0 (or rows
+ *                outside the logits): nothing is sampled for r.
+ *   draft_tokens int32 [num_requests, max_drafts]; one outside the vocabulary
+ *                is refused.
+ *   draft_probs  optional fp32 [num_requests * max_drafts, vocab], row stride
+ *                ld_probs.
+ *   temperature  optional fp32 [num_requests] (null = 1), >= 0.
+ *   uniform      fp32 [num_requests, max_drafts] in [0, 1).
+ *   noise        fp32 [num_requests, vocab], row stride ld_noise; positive.
+ *   out_tokens   int32 [num_requests, max_drafts + 1]: the kept drafts and the
+ *                token drawn, then -1 (-1 too where no token has a
+ *                probability).
+ *   num_accepted int32 [num_requests].
+ *   logprobs     fp32 [num_requests, max_drafts + 1]: log p of each emitted
+ *                token (temperature 0: of 1), 0 in the places of -1.
+ *   num_requests 0..65535 (0 enqueues nothing), max_drafts 0..255, vocab >= 1.
+ *   workspace    16-byte aligned, at least verify_drafts_workspace_bytes.
+ */
+size_t verify_drafts_workspace_bytes(int64_t num_requests, int64_t max_drafts, int64_t vocab);
+int verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64_t rows, int64_t vocab,
+                  const int32_t* row_start, const int32_t* num_drafts, int64_t num_requests, int64_t max_drafts,
+                  const int32_t* draft_tokens, const float* draft_probs, int64_t ld_probs, const float* temperature,
+                  const float* uniform, const float* noise, int64_t ld_noise, int32_t* out_tokens,
+                  int32_t* num_accepted, float* logprobs, void* workspace, size_t workspace_bytes,
+                  nvfp4_stream_t stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* nvfp4_status_string(int status);
 

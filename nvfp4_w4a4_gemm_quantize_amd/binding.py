@@ -6,6 +6,7 @@ device memory (output tensors are allocated here with torch.empty) and the
 current HIP stream.  The functions carry the C names.  If the library is not
 built, or there is no GPU, they raise -- there is no CPU fallback.
 """
+import collections
 import ctypes
 import os
 
@@ -46,6 +47,17 @@ _SIGNATURES = {
     "gdn_recurrence": (_int, [_c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _i64, _i64, _int, _int, _int,
                               _c_p, _c_p, _c_p, _int, _i64, _c_p]),
     "nvfp4_weight_stream_read": (_int, [_c_p, _i64, _i64, _c_p, _c_p]),
+    "paged_plan": (_int, [_c_p, _c_p, _i64, _int, _c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i64,
+                          _c_p, _c_p]),
+    "paged_kv_write": (_int, [_c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _c_p, _int, _i64, _int, _int, _int, _i64, _i64,
+                              _i64, _c_p, _c_p, _c_p]),
+    "paged_attention_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _int, _int, _int, _i64, _i64]),
+    "paged_attention": (_int, [_c_p, _i64, _i64, _c_p, _c_p, _i64, _i64, _i64, _int, _c_p, _c_p, _int, _i64, _int, _int,
+                               _int, _i64, _i64, _i64, _c_p, _i64, _i64, ctypes.c_float, _i64, _c_p, _c_p, _c_p, _int,
+                               _i64, _c_p, _c_p, ctypes.c_size_t, _c_p]),
+    "verify_drafts_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "verify_drafts": (_int, [_c_p, _int, _i64, _i64, _i64, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i64, _c_p, _c_p, _c_p,
+                             _i64, _c_p, _c_p, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "nvfp4_status_string": (ctypes.c_char_p, [_int]),
     "nvfp4_last_hip_error": (_int, []),
 }
@@ -434,3 +446,195 @@ def gdn_recurrence(q, k, v, beta, g, hk, hv, s_init=None, return_state=False, ou
                             T, hk, hv, 128, _ptr(s_init), _ptr(s_final), _ptr(out), od, _ld(out), _stream())
     _check(rc, "gdn_recurrence")
     return (out, s_final) if return_state else out
+
+
+# ------------------------------------------------- the paged serving step ----
+
+CACHE_BF16, CACHE_E4M3 = 0, 1
+LOGITS_F32, LOGITS_BF16 = 0, 1
+
+PagedPlan = collections.namedtuple("PagedPlan", "q_start seq_lens positions slots counts")
+
+
+def _vec(t, dtype, n, name):
+    """A contiguous GPU vector (or matrix) of n elements."""
+    _dev(t, dtype, name)
+    if t.numel() != n or not t.is_contiguous():
+        raise NVFP4Error("%s must be contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
+    return t
+
+
+def _rows(t, dtype, name, rows=None, cols=None):
+    """Row stride of a 2-D view with unit column stride."""
+    _dev(t, dtype, name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise NVFP4Error("%s must be a 2-D view with unit column stride" % name)
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise NVFP4Error("%s must be [%s, %s], got %s" % (name, rows, cols, tuple(t.shape)))
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """(cache_dtype, pages, page size, heads, head dim, strides) of a pair of [pages, heads, page size, head dim] views."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise NVFP4Error("k_cache must be a bfloat16 or float8_e4m3fn tensor")
+    _dev(k_cache, k_cache.dtype, "k_cache")
+    _dev(v_cache, k_cache.dtype, "v_cache")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+        raise NVFP4Error("k_cache and v_cache must be [pages, heads, page size, head dim] views of one shape and strides, "
+                         "with unit last stride")
+    pages, heads, page_size, dim = k_cache.shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            _vec(t, torch.float32, heads, name)
+    ps, hs, ts, _ = k_cache.stride()                # a size-1 dimension's stride is arbitrary
+    return (CACHE_BF16 if k_cache.dtype == torch.bfloat16 else CACHE_E4M3, pages, page_size, heads, dim,
+            ps if pages > 1 else 0, hs if heads > 1 else 0, ts)
+
+
+def paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens, free_cursor=None, plan=None):
+    """Block tables and slot maps of a step from the requests' lengths, on the device.
+
+    ctx_lens, new_lens int32 [R]; free_pages int32 [F]; block_table int32 [R, max_pages] (written in place for the
+    new pages); free_cursor int32 [1] or None.  Returns PagedPlan(q_start int32 [R + 1], seq_lens int32 [R],
+    positions int32 [max_tokens], slots int64 [max_tokens], counts int32 [4]: new tokens, pages taken, pages missing,
+    cursor after the step); ``plan`` reuses the tensors of an earlier one.
+    """
+    lib = load()
+    _dev(ctx_lens, torch.int32, "ctx_lens")
+    R = ctx_lens.numel()
+    _vec(ctx_lens, torch.int32, R, "ctx_lens")
+    _vec(new_lens, torch.int32, R, "new_lens")
+    _vec(free_pages, torch.int32, free_pages.numel(), "free_pages")
+    ld = _rows(block_table, torch.int32, "block_table", rows=R)
+    if free_cursor is not None:
+        _vec(free_cursor, torch.int32, 1, "free_cursor")
+    if plan is None:
+        i32 = torch.empty(2 * R + 5 + max_tokens, dtype=torch.int32, device=ctx_lens.device)
+        plan = PagedPlan(i32[:R + 1], i32[R + 1:2 * R + 1], i32[2 * R + 1:2 * R + 1 + max_tokens],
+                         torch.empty(max_tokens, dtype=torch.int64, device=ctx_lens.device), i32[2 * R + 1 + max_tokens:])
+    for name, n, dtype in (("q_start", R + 1, torch.int32), ("seq_lens", R, torch.int32),
+                           ("positions", max_tokens, torch.int32), ("slots", max_tokens, torch.int64),
+                           ("counts", 4, torch.int32)):
+        _vec(getattr(plan, name), dtype, n, name)
+    rc = lib.paged_plan(_ptr(ctx_lens), _ptr(new_lens), R, page_size, _ptr(free_pages), free_pages.numel(),
+                        _ptr(free_cursor), _ptr(block_table), block_table.shape[1], ld, _ptr(plan.q_start),
+                        _ptr(plan.seq_lens), _ptr(plan.positions), _ptr(plan.slots), max_tokens, _ptr(plan.counts),
+                        _stream())
+    _check(rc, "paged_plan")
+    return plan
+
+
+def paged_kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
+    """Write the rows of k, v (bf16 2-D views [T, heads * head_dim]) into the caches at slots (int64 [T]; -1: skip).
+
+    k_cache, v_cache: [pages, heads, page size, head dim] views, bfloat16 or float8_e4m3fn (then x / scale[head],
+    rounded to nearest even and clamped to +-448, is stored)."""
+    lib = load()
+    kind, pages, page_size, heads, dim, ps, hs, ts = _cache(k_cache, v_cache, k_scale, v_scale)
+    ld_k, ld_v = (_rows(x, torch.bfloat16, n, cols=heads * dim) for x, n in ((k, "k"), (v, "v")))
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise NVFP4Error("k and v must have the same number of rows")
+    _vec(slots, torch.int64, T, "slots")
+    rc = lib.paged_kv_write(_ptr(k), ld_k, _ptr(v), ld_v, _ptr(slots), T, _ptr(k_cache), _ptr(v_cache), kind, pages,
+                            page_size, heads, dim, ps, hs, ts, _ptr(k_scale), _ptr(v_scale), _stream())
+    _check(rc, "paged_kv_write")
+
+
+def paged_attention_workspace(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new, max_seq, device="cuda"):
+    """A workspace for paged_attention calls of up to these sizes."""
+    n = load().paged_attention_workspace_bytes(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new, max_seq)
+    if n == 0:
+        raise NVFP4Error("paged_attention does not take these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new, max_seq, scale=None, window=0,
+                    k_scale=None, v_scale=None, out_dtype=torch.bfloat16, out=None, lse=None, return_lse=False,
+                    workspace=None):
+    """Attention of every request's new tokens over its cached keys (causal, optionally a sliding window).
+
+    q: bf16 [T, num_heads * head_dim] view, rows of request r from q_start[r] to q_start[r + 1]; caches as in
+    paged_kv_write; block_table int32 [R, max_pages]; max_new and max_seq bound the requests' new tokens and lengths.
+    Returns out [T, num_heads * head_dim] (and lse fp32 [T, num_heads] with return_lse)."""
+    lib = load()
+    kind, pages, page_size, heads, dim, ps, hs, ts = _cache(k_cache, v_cache, k_scale, v_scale)
+    ld_q = _rows(q, torch.bfloat16, "q")
+    T, cols = q.shape
+    if cols == 0 or cols % dim or (cols // dim) % heads:
+        raise NVFP4Error("q must be [T, num_heads * %d] with num_heads a multiple of %d" % (dim, heads))
+    num_heads = cols // dim
+    _dev(seq_lens, torch.int32, "seq_lens")
+    R = seq_lens.numel()
+    _vec(seq_lens, torch.int32, R, "seq_lens")
+    _vec(q_start, torch.int32, R + 1, "q_start")
+    ld_t = _rows(block_table, torch.int32, "block_table", rows=R)
+    out, od = _out(out, T, cols, out_dtype, q.device)
+    if lse is not None:
+        _vec(lse, torch.float32, T * num_heads, "lse")
+    elif return_lse:
+        lse = torch.empty((T, num_heads), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = paged_attention_workspace(T, R, num_heads, heads, dim, max_new, max_seq, q.device)
+    _dev(workspace, torch.uint8, "workspace")
+    rc = lib.paged_attention(_ptr(q), ld_q, T, _ptr(q_start), _ptr(seq_lens), R, max_new, max_seq, num_heads,
+                             _ptr(k_cache), _ptr(v_cache), kind, pages, page_size, heads, dim, ps, hs, ts,
+                             _ptr(block_table), block_table.shape[1], ld_t, dim ** -0.5 if scale is None else scale,
+                             window, _ptr(k_scale), _ptr(v_scale), _ptr(out), od, _ld(out), _ptr(lse), _ptr(workspace),
+                             workspace.numel(), _stream())
+    _check(rc, "paged_attention")
+    return (out, lse) if return_lse else out
+
+
+def verify_drafts_workspace(num_requests, max_drafts, vocab, device="cuda"):
+    """A workspace for verify_drafts calls of these sizes."""
+    n = load().verify_drafts_workspace_bytes(num_requests, max_drafts, vocab)
+    if n == 0:
+        raise NVFP4Error("verify_drafts does not take these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def verify_drafts(logits, row_start, num_drafts, draft_tokens, uniform, noise, draft_probs=None, temperature=None,
+                  workspace=None):
+    """Keep or refuse drafted tokens and draw the next one, from given random numbers.
+
+    logits bf16 or fp32 [N, V] view: row row_start[r] + i is the target's after i kept drafts of request r;
+    row_start, num_drafts int32 [R]; draft_tokens int32 [R, K]; uniform fp32 [R, K]; noise fp32 [R, V] (standard
+    exponential); draft_probs fp32 [R, K, V] or None; temperature fp32 [R] or None (0: greedy).
+    Returns (tokens int32 [R, K + 1], accepted int32 [R], logprobs fp32 [R, K + 1])."""
+    lib = load()
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise NVFP4Error("logits must be a bfloat16 or float32 tensor")
+    ld = _rows(logits, logits.dtype, "logits")
+    N, V = logits.shape
+    _dev(draft_tokens, torch.int32, "draft_tokens")
+    if draft_tokens.dim() != 2:
+        raise NVFP4Error("draft_tokens must be [requests, max drafts]")
+    R, K = draft_tokens.shape
+    _vec(draft_tokens, torch.int32, R * K, "draft_tokens")
+    _vec(row_start, torch.int32, R, "row_start")
+    _vec(num_drafts, torch.int32, R, "num_drafts")
+    _vec(uniform, torch.float32, R * K, "uniform")
+    ld_noise = _rows(noise, torch.float32, "noise", rows=R, cols=V)
+    ld_probs = V
+    if draft_probs is not None:
+        _dev(draft_probs, torch.float32, "draft_probs")
+        if draft_probs.shape != (R, K, V) or (V > 1 and draft_probs.stride(2) != 1) or \
+                (R > 1 and K > 0 and draft_probs.stride(0) != K * draft_probs.stride(1)):
+            raise NVFP4Error("draft_probs must be [requests, max drafts, vocab] with evenly spaced rows")
+        ld_probs = draft_probs.stride(1) if K > 1 else (draft_probs.stride(0) if R > 1 and K == 1 else V)
+    if temperature is not None:
+        _vec(temperature, torch.float32, R, "temperature")
+    if workspace is None:
+        workspace = verify_drafts_workspace(R, K, V, logits.device)
+    _dev(workspace, torch.uint8, "workspace")
+    both = torch.empty((2, R, K + 1), dtype=torch.int32, device=logits.device)
+    tokens, logprobs = both[0], both[1].view(torch.float32)
+    accepted = torch.empty(R, dtype=torch.int32, device=logits.device)
+    rc = lib.verify_drafts(_ptr(logits), LOGITS_F32 if logits.dtype == torch.float32 else LOGITS_BF16, ld, N, V,
+                           _ptr(row_start), _ptr(num_drafts), R, K, _ptr(draft_tokens), _ptr(draft_probs), ld_probs,
+                           _ptr(temperature), _ptr(uniform), _ptr(noise), ld_noise, _ptr(tokens), _ptr(accepted),
+                           _ptr(logprobs), _ptr(workspace), workspace.numel(), _stream())
+    _check(rc, "verify_drafts")
+    return tokens, accepted, logprobs

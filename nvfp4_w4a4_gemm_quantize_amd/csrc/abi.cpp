@@ -10,7 +10,7 @@ using namespace nvfp4;
 
 static thread_local int g_last_hip_error = 0;
 
-static int hip_status(hipError_t e) {
+int nvfp4::hip_status(hipError_t e) {
   if (e == hipSuccess) return NVFP4_OK;
   g_last_hip_error = (int)e;
   return NVFP4_EHIP;

@@ -1,0 +1,516 @@
+// Attention of a few new tokens a request (a decoded token, a handful of
+// drafts) over the paged cache on gfx950: the streaming kernel.
+//
+// Mathematics, per row (new token, query head) with c = scale * k_scale * log2 e
+// and m the running maximum of q.k over the keys seen so far:
+//     l <- l 2^(c (m_old - m)) + sum_j 2^(c (s_j - m)),
+//     O <- O 2^(c (m_old - m)) + sum_j 2^(c (s_j - m)) v_j,
+// so K and V are read once; O / l * v_scale is the output.  A negative c is
+// folded into the sign of q, so that the largest s is always the largest score.
+//
+// Bound by the cache's bytes.  The rows of one KV head's group (tokens x heads
+// of the group, up to 32) share each key tile, as the columns of 16x16x32
+// bf16 MFMAs: S^T = K Q^T and O^T = V^T P^T.  Everything stays in registers:
+//   - K: a lane loads 16 bytes of one key; lanes l & 15 are the tile's keys.
+//   - S^T: column = row of q = l & 15, rows = keys 4 g + r (g = l >> 4), so a
+//     softmax row lies in four lanes and P^T is already the B operand of the
+//     second product if its k index (g, j) stands for key 4 g + j (j < 4) and
+//     16 + 4 g + j - 4 (j >= 4): a sum does not mind the order of its terms.
+//   - V: a lane loads, for those eight keys, D / 16 neighbouring columns; an
+//     8 x (D / 16) transpose inside the lane (v_perm) makes the A operands,
+//     whose row l & 15 of operand i stands for column (l & 15) D / 16 + i.
+// So there is no LDS traffic and no barrier in the loop, every load is a
+// whole cache line over a wave, and the next tile's loads are in flight while a
+// tile is computed.  An E4M3 cache halves the bytes; its elements become bf16
+// exactly after the load (scales go into c and the output).
+//
+// Split: the key tiles of all requests and KV heads form one line that a fixed
+// grid shares evenly, so a long request among short ones, or one request alone,
+// fills the chip.  A workgroup that holds all of a (request, head) writes its
+// output; a part leaves (max, sum, O) in the workspace (at most two a
+// workgroup) and a second kernel joins the parts in the order of their keys.
+// The line's prefix is recomputed by every workgroup (8 bytes a request).
+#include "attention.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 64 * kDecodeWaves;
+
+struct DecodeWorkspace {
+  int64_t* prefix;   // [requests + 1] tiles before a request (of one head); then the tiles per workgroup
+  float2* ml;        // [2 * grid][kDecodeRows] (max in log2 units, sum)
+  float* o;          // [2 * grid][kDecodeRows][dim]
+};
+__host__ __device__ inline DecodeWorkspace decode_workspace(void* ws, int64_t requests) {
+  DecodeWorkspace w;
+  w.prefix = (int64_t*)ws;
+  uint8_t* p = (uint8_t*)ws + ((requests + 2) * 8 + 255) / 256 * 256;
+  w.ml = (float2*)p;
+  w.o = (float*)(p + (size_t)2 * kDecodeGrid * kDecodeRows * sizeof(float2));
+  return w;
+}
+
+// A request's part of the line: first key (a tile's start) and tiles of one
+// head; 0 tiles if it has no rows here.  A request whose rows see nothing has one.
+struct DecodeItem {
+  RequestLens l;
+  int64_t begin, tiles;
+};
+__device__ __forceinline__ DecodeItem decode_item(const AttentionArgs& a, int64_t r) {
+  DecodeItem it;
+  it.l = request_lens(a, r);
+  it.begin = 0;
+  if (a.window) it.begin = max(token_pos(a, r, it.l, 0) - a.window + 1, (int64_t)0) / kDecodeTile * kDecodeTile;
+  it.tiles = max((it.l.keys - it.begin + kDecodeTile - 1) / kDecodeTile, (int64_t)1);
+  if (it.l.tokens == 0 || it.l.tokens * a.group > kDecodeRows) it.tiles = 0;
+  return it;
+}
+
+// One key tile's K and V in registers.
+template <int D, bool FP8>
+struct DecodeTile {
+  static constexpr int KW = FP8 ? D / 64 : D / 32;             // 16-byte words a lane holds of a key
+  static constexpr int VW = D / 16 * (FP8 ? 1 : 2) / 4;        // 4-byte words a lane holds of a value row
+  u32x4 k[2][KW];
+  uint32_t v[8][VW];
+};
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t* out, const uint8_t* p) {
+  if constexpr (W == 1) {
+    out[0] = *(const uint32_t*)p;
+  } else if constexpr (W == 2) {
+    const u32x2 x = *(const u32x2*)p;
+    out[0] = x[0], out[1] = x[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const u32x4 x = *(const u32x4*)(p + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[4 * i + j] = x[j];
+    }
+  }
+}
+
+}  // namespace
+
+template <int D, bool FP8, int NF>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_kernel(AttentionArgs a) {
+  using Tile = DecodeTile<D, FP8>;
+  constexpr int KS = D / 32;      // k steps of the first product
+  constexpr int DV = D / 16;      // value columns a lane holds = fragments of O
+  constexpr int EB = FP8 ? 1 : 2;
+  constexpr int LD = D + 4;
+  __shared__ int64_t before[kThreads + 1];
+  __shared__ int64_t wave_sum[kDecodeWaves];
+  __shared__ __attribute__((aligned(16))) float o_part[kDecodeWaves][16][LD];
+  __shared__ float2 ml_part[kDecodeWaves][16];
+
+  const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hkv = a.cache.heads, group = a.group;
+  const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
+
+  // prefix of the tiles over runs of requests
+  const int64_t run = (a.requests + kThreads - 1) / kThreads;
+  const int64_t r0 = min(tid * run, a.requests), r1 = min(r0 + run, a.requests);
+  int64_t sum = 0;
+  for (int64_t r = r0; r < r1; ++r) sum += decode_item(a, r).tiles;
+  int64_t inc = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t u = __shfl_up(inc, d);
+    if (lane >= d) inc += u;
+  }
+  if (lane == 63) wave_sum[wave] = inc;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) inc += wave_sum[w];
+  if (tid == 0) before[0] = 0;
+  before[tid + 1] = inc;
+  __syncthreads();
+  const int64_t total = before[kThreads] * hkv;
+  // at least one tile a wave: a smaller share would only add parts to join
+  const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kDecodeWaves);
+  if (blockIdx.x == 0) {
+    int64_t t = inc - sum;
+    for (int64_t r = r0; r < r1; ++r) {
+      ws.prefix[r] = t;
+      t += decode_item(a, r).tiles;
+    }
+    if (tid == 0) {
+      ws.prefix[a.requests] = before[kThreads];
+      ws.prefix[a.requests + 1] = per;
+    }
+  }
+
+  const int64_t x_begin = blockIdx.x * per, x_end = min(x_begin + per, total);
+  const int64_t page_mask = ((int64_t)1 << a.cache.page_shift) - 1;
+  int row_token[NF], row_head[NF];
+#pragma unroll
+  for (int n = 0; n < NF; ++n) {
+    row_token[n] = (n * 16 + c16) / group;
+    row_head[n] = (n * 16 + c16) % group;
+  }
+
+  for (int64_t x = x_begin; x < x_end;) {
+    // the request and head at x
+    int lo = 0;
+#pragma unroll
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+      if (before[lo + step] * hkv <= x) lo += step;
+    int64_t r = lo * run, base = before[lo];
+    DecodeItem it = decode_item(a, r);
+    while (x >= (base + it.tiles) * hkv) {   // ends: x < before[lo + 1] * hkv
+      base += it.tiles;
+      it = decode_item(a, ++r);
+    }
+    const int64_t in_request = x - base * hkv;
+    const int head = (int)(in_request / it.tiles);
+    const int64_t first = in_request - head * it.tiles;
+    const int64_t last = min(first + (x_end - x), it.tiles);   // tiles [first, last) of this head
+    const bool whole = first == 0 && last == it.tiles;
+    const int part = x == x_begin ? 0 : 1;
+    x += last - first;
+
+    const int nrows = (int)it.l.tokens * group;
+    const int64_t pos0 = token_pos(a, r, it.l, 0), pos_last = pos0 + it.l.tokens - 1;
+    const int64_t keys = min(it.l.keys, pos_last + 1);
+    const int64_t low = a.window ? max(pos0 - a.window + 1, (int64_t)0) : 0;   // first key that a row may see
+    float c = a.scale * kLog2e;
+    if (a.cache.k_scale) c *= a.cache.k_scale[head];
+    const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
+    c = fabsf(c);
+
+    // Q, the B operand: column c16 = row of q, k = 8 columns of q
+    bf16x8 q[NF][KS];
+    int64_t row_pos[NF];
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+      const bool live = n * 16 + c16 < nrows;
+      row_pos[n] = live ? pos0 + row_token[n] : -1;
+      const uint16_t* qr = a.q + (it.l.start + (live ? row_token[n] : 0)) * a.ld_q + (head * group + (live ? row_head[n] : 0)) * D;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        // E4M3 keys are loaded 16 columns at a time: steps 2 i, 2 i + 1 take a lane's halves
+        const int chunk = FP8 ? (s >> 1) * 8 + g * 2 + (s & 1) : s * 4 + g;
+        u32x4 w = *(const u32x4*)(qr + chunk * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = live ? w[i] ^ flip : 0u;
+        q[n][s] = __builtin_bit_cast(bf16x8, w);
+      }
+    }
+
+    float m[NF], l[NF];
+    f32x4 o[NF][DV];
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DV; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t* table = a.block_table + r * a.ld_table;
+    const int64_t head_off = head * a.cache.head_stride;
+    const uint32_t ts = (uint32_t)a.cache.token_stride;
+    const uint32_t k_lane = ((uint32_t)c16 * ts + g * (FP8 ? 16 : 8)) * EB, v_lane = (4 * g * ts + c16 * DV) * EB;
+
+    // The page of 16 keys from key0 (they never cross one); -1: none.
+    auto page_of = [&](int64_t key0) {
+      int32_t p = -1;
+      if (key0 < keys) p = table[key0 >> a.cache.page_shift];
+      return p >= 0 && p < a.cache.num_pages ? p : -1;
+    };
+    struct Pages {
+      int32_t p[2];
+    };
+    auto pages_of = [&](int64_t t) {
+      Pages pg;
+      const int64_t key0 = it.begin + t * kDecodeTile;
+      pg.p[0] = __builtin_amdgcn_readfirstlane(page_of(key0));
+      pg.p[1] = __builtin_amdgcn_readfirstlane(page_of(key0 + 16));
+      return pg;
+    };
+    // element offset of 16 keys; without a page any page serves: its scores are hidden and its values cleared
+    auto place = [&](int64_t t, int f, const Pages& pg) {
+      const int64_t key0 = it.begin + t * kDecodeTile + 16 * f;
+      return max(pg.p[f], 0) * a.cache.page_stride + head_off + (key0 & page_mask) * a.cache.token_stride;
+    };
+    auto load_keys = [&](Tile& tile, int64_t t, const Pages& pg) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint8_t* kp = (const uint8_t*)a.cache.k + place(t, f, pg) * EB;
+#pragma unroll
+        for (int s = 0; s < Tile::KW; ++s) tile.k[f][s] = *(const u32x4*)(kp + k_lane + s * 64);
+      }
+    };
+    auto load_values = [&](Tile& tile, int64_t t, const Pages& pg) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint8_t* vp = (const uint8_t*)a.cache.v + place(t, f, pg) * EB;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words<Tile::VW>(tile.v[4 * f + j], vp + v_lane + j * ts * EB);
+      }
+    };
+    auto scores = [&](Tile& tile, f32x4 (&s)[NF][2]) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+#pragma unroll
+        for (int n = 0; n < NF; ++n) s[n][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+          bf16x8 kf;
+          if constexpr (FP8) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              w[2 * i] = e4m3_bf16<false>(tile.k[f][st >> 1][(st & 1) * 2 + i]);
+              w[2 * i + 1] = e4m3_bf16<true>(tile.k[f][st >> 1][(st & 1) * 2 + i]);
+            }
+            kf = __builtin_bit_cast(bf16x8, w);
+          } else {
+            kf = __builtin_bit_cast(bf16x8, tile.k[f][st]);
+          }
+#pragma unroll
+          for (int n = 0; n < NF; ++n) s[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][st], s[n][f], 0, 0, 0);
+        }
+      }
+    };
+    // softmax step and second product
+    auto values = [&](Tile& tile, f32x4 (&s)[NF][2], int64_t t, const Pages& pg) {
+      const int64_t key0 = it.begin + t * kDecodeTile;
+      // a tile that every row sees in full needs no masks
+      const bool full = pg.p[0] >= 0 && pg.p[1] >= 0 && key0 + kDecodeTile - 1 <= pos0 && key0 + kDecodeTile <= keys &&
+                        (a.window == 0 || key0 > pos_last - a.window);
+      if (!full) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t key = key0 + 16 * f + 4 * g + j;
+            const bool held = pg.p[f] >= 0 && key < keys && key >= low;
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+              if (!held || key > row_pos[n] || (a.window && key <= row_pos[n] - a.window)) s[n][f][j] = -INFINITY;
+            // what lies in unwritten or foreign places may be NaN, and 0 * NaN is not 0
+            if (!held)
+#pragma unroll
+              for (int w = 0; w < Tile::VW; ++w) tile.v[4 * f + j][w] = 0u;
+          }
+      }
+      bf16x8 p[NF];
+#pragma unroll
+      for (int n = 0; n < NF; ++n) {
+        float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
+                          fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
+        if (__any(top > m[n])) {   // rare after the first tiles: a new maximum somewhere
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float to = fmaxf(m[n], top);
+          const float by = m[n] == to ? 1.f : m[n] == -INFINITY ? 0.f : exp2_fast(c * (m[n] - to));
+          m[n] = to;
+          l[n] *= by;
+#pragma unroll
+          for (int i = 0; i < DV; ++i) o[n][i] *= by;
+        }
+        const float ref = m[n] == -INFINITY ? 0.f : c * m[n];
+        u32x4 w;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[j] = exp2_fast(fmaf(s[n][f][j], c, -ref));
+            if (!full && s[n][f][j] == -INFINITY) e[j] = 0.f;
+          }
+          l[n] += (e[0] + e[1]) + (e[2] + e[3]);
+          // P in bf16, the matrix instruction's type with V: 2^-8 relative a term at most, averaged over the keys
+          w[2 * f] = pack_bf16(e[0], e[1]);
+          w[2 * f + 1] = pack_bf16(e[2], e[3]);
+        }
+        p[n] = __builtin_bit_cast(bf16x8, w);
+      }
+#pragma unroll
+      for (int i4 = 0; i4 < DV / 4; ++i4) {
+        u32x4 vt[4];   // A operands of columns 4 i4 .. 4 i4 + 3
+        if constexpr (FP8) {
+          uint32_t b[2][4];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t x0 = tile.v[4 * f][i4], x1 = tile.v[4 * f + 1][i4], x2 = tile.v[4 * f + 2][i4], x3 = tile.v[4 * f + 3][i4];
+            const uint32_t a01 = __builtin_amdgcn_perm(x1, x0, 0x05010400u), b01 = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
+            const uint32_t a23 = __builtin_amdgcn_perm(x3, x2, 0x05010400u), b23 = __builtin_amdgcn_perm(x3, x2, 0x07030602u);
+            b[f][0] = __builtin_amdgcn_perm(a23, a01, 0x05040100u);
+            b[f][1] = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
+            b[f][2] = __builtin_amdgcn_perm(b23, b01, 0x05040100u);
+            b[f][3] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            vt[i] = u32x4{e4m3_bf16<false>(b[0][i]), e4m3_bf16<true>(b[0][i]), e4m3_bf16<false>(b[1][i]), e4m3_bf16<true>(b[1][i])};
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              vt[i][j] = __builtin_amdgcn_perm(tile.v[2 * j + 1][2 * i4 + (i >> 1)], tile.v[2 * j][2 * i4 + (i >> 1)],
+                                               (i & 1) ? 0x07060302u : 0x05040100u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < NF; ++n)
+            o[n][4 * i4 + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vt[i]), p[n], o[n][4 * i4 + i], 0, 0, 0);
+      }
+    };
+
+    // wave w takes tiles first + w, + 4, ...; a tile's keys are loaded once the
+    // tile before has given its scores, its values once the products with the
+    // values before are done, its page numbers two tiles ahead
+    Tile tile;
+    int64_t t = first + wave;
+    if (t < last) {
+      Pages now = pages_of(t), next = pages_of(t + kDecodeWaves);
+      load_keys(tile, t, now);
+      load_values(tile, t, now);
+      while (true) {
+        const bool more = t + kDecodeWaves < last;
+        const Pages after = pages_of(t + 2 * kDecodeWaves);
+        f32x4 s[NF][2];
+        scores(tile, s);
+        if (more) load_keys(tile, t + kDecodeWaves, next);
+        values(tile, s, t, now);
+        if (!more) break;
+        load_values(tile, t + kDecodeWaves, next);
+        t += kDecodeWaves;
+        now = next;
+        next = after;
+      }
+    }
+
+    // join the waves in their order, 16 rows at a time
+    const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+      float ls = l[n];
+      ls += __shfl_xor(ls, 16);
+      ls += __shfl_xor(ls, 32);
+      __syncthreads();   // the buffers of the fragment or item before have been read
+      if (g == 0) ml_part[wave][c16] = make_float2(m[n] == -INFINITY ? -INFINITY : c * m[n], ls);
+#pragma unroll
+      for (int rr = 0; rr < 4; ++rr)
+#pragma unroll
+        for (int i = 0; i < DV; i += 4)
+          *(f32x4*)&o_part[wave][c16][(4 * g + rr) * DV + i] = f32x4{o[n][i][rr], o[n][i + 1][rr], o[n][i + 2][rr], o[n][i + 3][rr]};
+      __syncthreads();
+      for (int e = tid; e < 16 * D / 4; e += kThreads) {
+        const int row = e / (D / 4), d = (e % (D / 4)) * 4, at = n * 16 + row;
+        if (at >= nrows) continue;
+        float top = -INFINITY, den = 0.f;
+        f32x4 num = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kDecodeWaves; ++w) top = fmaxf(top, ml_part[w][row].x);
+#pragma unroll
+        for (int w = 0; w < kDecodeWaves; ++w) {
+          const float2 ml = ml_part[w][row];
+          const float by = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+          den = fmaf(by, ml.y, den);
+          const f32x4 ow = *(const f32x4*)&o_part[w][row][d];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
+        }
+        if (whole) {
+          const int64_t trow = it.l.start + at / group;
+          const int hq = head * group + at % group;
+          const float inv = den == 0.f ? 0.f : vs / den;
+          if (a.out_bf16)
+            *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
+          else
+            *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
+          if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
+        } else {
+          const int64_t slot = ((int64_t)blockIdx.x * 2 + part) * kDecodeRows + at;
+          *(f32x4*)(ws.o + slot * D + d) = num;
+          if (d == 0) ws.ml[slot] = make_float2(top, den);
+        }
+      }
+    }
+  }
+}
+
+// Joins the parts of a (request, head) that several workgroups of the
+// streaming kernel hold, in the order of their keys.
+template <int D>
+__global__ __launch_bounds__(256) void attention_decode_join_kernel(AttentionArgs a) {
+  const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
+  const int hkv = a.cache.heads, group = a.group;
+  const int64_t r = blockIdx.x / hkv;
+  const int head = blockIdx.x % hkv;
+  const int64_t p0 = ws.prefix[r], tiles = ws.prefix[r + 1] - p0, per = ws.prefix[a.requests + 1];
+  if (tiles == 0) return;
+  const int64_t x0 = p0 * hkv + head * tiles, g0 = x0 / per, g1 = (x0 + tiles - 1) / per;
+  if (g0 == g1) return;
+  const RequestLens l = request_lens(a, r);
+  const int nrows = (int)l.tokens * group;
+  const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
+  for (int e = threadIdx.x; e < nrows * (D / 4); e += 256) {
+    const int at = e / (D / 4), d = (e % (D / 4)) * 4;
+    // workgroup g's part is its first unless the item starts inside g's share
+    auto slot_of = [&](int64_t wg) { return (wg * 2 + (x0 > wg * per ? 1 : 0)) * kDecodeRows + at; };
+    float top = -INFINITY, den = 0.f;
+    for (int64_t wg = g0; wg <= g1; ++wg) top = fmaxf(top, ws.ml[slot_of(wg)].x);
+    f32x4 num = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t wg = g0; wg <= g1; ++wg) {
+      const int64_t slot = slot_of(wg);
+      const float2 ml = ws.ml[slot];
+      const float by = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+      den = fmaf(by, ml.y, den);
+      const f32x4 ow = *(const f32x4*)(ws.o + slot * D + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
+    }
+    const int64_t trow = l.start + at / group;
+    const int hq = head * group + at % group;
+    const float inv = den == 0.f ? 0.f : vs / den;
+    if (a.out_bf16)
+      *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
+    else
+      *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
+    if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
+  }
+}
+
+size_t attention_decode_workspace(int64_t requests, int dim) {
+  const DecodeWorkspace w = decode_workspace(nullptr, requests);
+  return (size_t)(uintptr_t)w.o + (size_t)2 * kDecodeGrid * kDecodeRows * dim * sizeof(float);
+}
+
+namespace {
+
+template <int D, bool FP8>
+hipError_t launch(const AttentionArgs& a, hipStream_t st) {
+  // rows a request may have here: one fragment of 16 or two
+  const int64_t rows = min(a.max_new, (int64_t)(kDecodeRows / a.group)) * a.group;
+  if (rows <= 16)
+    attention_decode_kernel<D, FP8, 1><<<kDecodeGrid, kThreads, 0, st>>>(a);
+  else
+    attention_decode_kernel<D, FP8, 2><<<kDecodeGrid, kThreads, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  attention_decode_join_kernel<D><<<(unsigned)(a.requests * a.cache.heads), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_decode(const AttentionArgs& a, hipStream_t st) {
+  switch (a.cache.dim) {
+    case 64: return a.cache.fp8 ? launch<64, true>(a, st) : launch<64, false>(a, st);
+    case 128: return a.cache.fp8 ? launch<128, true>(a, st) : launch<128, false>(a, st);
+    default: return a.cache.fp8 ? launch<256, true>(a, st) : launch<256, false>(a, st);
+  }
+}
+
+}  // namespace nvfp4

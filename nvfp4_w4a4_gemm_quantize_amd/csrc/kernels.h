@@ -41,6 +41,10 @@ struct EpilogueArgs {
   int64_t h_amax_base;
 };
 
+// Status of a launch: NVFP4_OK, or NVFP4_EHIP with the error kept for
+// nvfp4_last_hip_error (abi.cpp).
+int hip_status(hipError_t e);
+
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 hipError_t launch_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, float* g,

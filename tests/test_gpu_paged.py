@@ -1,0 +1,221 @@
+"""GPU parity of paged_plan and paged_kv_write against the oracle: whole numbers
+equal, cache values equal bit by bit (a copy, or one rounding to E4M3)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as OP
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def run_plan(lib, ctx, new, free, cursor, table, page, max_tokens):
+    t = i32(table).reshape(len(ctx), -1) if len(ctx) else torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    p = lib.paged_plan(i32(ctx), i32(new), i32(free), t, page, max_tokens,
+                       free_cursor=None if cursor is None else i32([cursor]))
+    return [x.cpu().numpy() for x in (t, p.q_start, p.seq_lens, p.positions, p.slots, p.counts)]
+
+
+def check_plan(lib, ctx, new, free, cursor, table, page, max_tokens):
+    got = run_plan(lib, ctx, new, free, cursor, table, page, max_tokens)
+    want = OP.plan(np.asarray(ctx, np.int64), np.asarray(new, np.int64), free, cursor or 0, table, page, max_tokens)
+    for g, w, name in zip(got, want, ("block_table", "q_start", "seq_lens", "positions", "slots", "counts")):
+        np.testing.assert_array_equal(g, w, err_msg=name)
+
+
+def context_table(ctx, pages, page, rng):
+    """Pages 1000.. for the contexts, -7 in the unset columns (they must stay)."""
+    t = np.full((len(ctx), pages), -7, np.int32)
+    at = 1000
+    for r, c in enumerate(ctx):
+        for col in range(min(-(-max(c, 0) // page), pages)):
+            t[r, col] = at = at + 1
+    return t
+
+
+@pytest.mark.parametrize("ctx,new,page,pages,cursor,spare", [
+    ([0], [1], 16, 4, 0, 10),
+    ([16], [1], 16, 4, 0, 10),                     # a page ends with the context
+    ([15], [1], 16, 4, 3, 10),                     # the last place of a page: no page needed
+    ([5, 0, 33, 7], [1, 0, 17, 40], 16, 8, 2, 20),  # a request without new tokens among others
+    ([0, 0, 0], [0, 0, 0], 32, 4, 0, 4),           # nothing at all
+    ([100, 3], [200, 1], 64, 3, 0, 9),             # runs past the table: no page, no slot
+    ([10, 20, 30], [30, 30, 30], 16, 8, 1, 3),     # the free list runs out
+    ([1024, 4096], [1024, 1], 1024, 8, 0, 4),      # the largest pages
+    ([-3, 5], [2, -1], 16, 4, 0, 4),               # negative lengths count as none
+])
+def test_plan_small(gpu_lib, ctx, new, page, pages, cursor, spare):
+    rng = np.random.default_rng(1)
+    table = context_table(ctx, pages, page, rng)
+    free = rng.permutation(500)[:spare].astype(np.int32)
+    check_plan(gpu_lib, ctx, new, free, cursor, table, page, max(sum(max(n, 0) for n in new), 1) + 5)
+
+
+@pytest.mark.parametrize("requests", [1, 255, 256, 257, 1000, 5000])
+def test_plan_many_requests(gpu_lib, requests):
+    rng = np.random.default_rng(requests)
+    ctx, new = rng.integers(0, 300, requests), rng.integers(0, 40, requests)
+    new[rng.random(requests) < 0.3] = 0
+    table = context_table(ctx, 24, 16, rng)
+    free = rng.permutation(int(new.sum()) + requests).astype(np.int32)[:int(new.sum()) // 16 + requests]
+    check_plan(gpu_lib, ctx, new, free, 3, table, 16, int(new.sum()) + 1)
+
+
+def test_plan_step_larger_than_its_buffers(gpu_lib):
+    table = context_table([0, 9], 8, 16, None)
+    check_plan(gpu_lib, [0, 9], [20, 30], np.arange(40, dtype=np.int32), 0, table, 16, 37)
+
+
+def test_plan_without_requests_and_without_free_pages(gpu_lib):
+    got = run_plan(gpu_lib, [], [], [], None, [], 16, 3)
+    assert got[1].tolist() == [0] and got[3].tolist() == [-1] * 3 and got[4].tolist() == [-1] * 3
+    assert got[5].tolist() == [0, 0, 0, 0]
+    check_plan(gpu_lib, [4], [30], np.zeros(0, np.int32), None, context_table([4], 4, 16, None), 16, 30)
+
+
+def test_plan_slots_past_32_bits(gpu_lib):
+    """Page numbers near 2^31 in pages of 1024 tokens: slots near 2^41."""
+    big = np.array([2 ** 31 - 1, 2 ** 31 - 2], np.int64).astype(np.int32)
+    check_plan(gpu_lib, [0], [1500], big, 0, np.full((1, 2), -7, np.int32), 1024, 1500)
+
+
+def test_plan_reuses_its_tensors_and_strided_tables(gpu_lib):
+    wide = torch.full((3, 16), -7, dtype=torch.int32, device="cuda")
+    table, ctx, new = wide[:, :6], i32([0, 0, 0]), i32([20, 1, 33])
+    free = i32(np.arange(10, 30))
+    p = gpu_lib.paged_plan(ctx, new, free, table, 16, 60)
+    again = gpu_lib.paged_plan(ctx, new, free, table, 16, 60, plan=p)
+    assert again is p and p.counts.tolist() == [54, 6, 0, 6]
+    assert wide[:, 6:].eq(-7).all()
+    assert table.tolist() == [[10, 11, -7, -7, -7, -7], [12, -7, -7, -7, -7, -7], [13, 14, 15, -7, -7, -7]]
+
+
+# --------------------------------------------------------------- K/V write --
+
+FP8 = torch.float8_e4m3fn
+
+
+def e4m3_values():
+    return torch.arange(256, dtype=torch.uint8).view(FP8).float().numpy().astype(np.float64)
+
+
+def to_e4m3(x):
+    """Round to nearest even of clamped float64 values of float32 operands, by distance over the table of all values."""
+    v = e4m3_values()
+    order = np.argsort(v[:127])                    # 0 .. 448
+    grid, codes = v[:127][order], np.arange(127)[order]
+    a = np.abs(x)
+    hi = np.clip(np.searchsorted(grid, a), 1, len(grid) - 1)
+    lo = hi - 1
+    up = (grid[hi] - a < a - grid[lo]) | ((grid[hi] - a == a - grid[lo]) & (codes[hi] % 2 == 0))
+    c = np.where(up, codes[hi], codes[lo]).astype(np.uint8)
+    return np.where(np.signbit(x), c | 0x80, c).astype(np.uint8)
+
+
+@pytest.mark.parametrize("tokens,heads,dim,page,fp8,layout", [
+    (1, 8, 128, 16, False, "phtd"), (1, 8, 128, 16, True, "phtd"), (37, 1, 64, 16, True, "pthd"),
+    (130, 4, 256, 64, False, "pthd"), (65, 3, 64, 32, False, "phtd"), (300, 2, 256, 1024, True, "phtd"),
+    (7, 40, 128, 128, True, "pthd"),
+])
+def test_kv_write(gpu_lib, tokens, heads, dim, page, fp8, layout):
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    pages = -(-tokens // page) + 2
+    qkv = torch.randn(tokens, heads * dim * 3 + 8, generator=g, device="cuda").mul(3).to(torch.bfloat16)
+    k, v = qkv[:, 8:8 + heads * dim], qkv[:, 8 + heads * dim:8 + 2 * heads * dim]
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:tokens]
+    if tokens > 3:
+        slots[1], slots[2], slots[3] = -1, pages * page, -2 ** 40      # padding, past the end, nonsense: skipped
+    dtype = FP8 if fp8 else torch.bfloat16
+    ks, vs = (0.5 + torch.rand(heads, generator=g, device="cuda") for _ in range(2)) if fp8 else (None, None)
+    if fp8:
+        ks[0] = 1e-3                               # exceeds the scale: saturates at 448
+    raw = torch.uint8 if fp8 else torch.int16
+    before = torch.randint(0, 100, (2, pages, heads, page, dim), generator=g, device="cuda").to(raw)
+    if layout == "pthd":
+        store = before.permute(0, 1, 3, 2, 4).contiguous()
+        caches = store.permute(0, 1, 3, 2, 4)
+    else:
+        caches = before.clone()
+    gpu_lib.paged_kv_write(k, v, slots, caches[0].view(dtype), caches[1].view(dtype), k_scale=ks, v_scale=vs)
+    for x, cache, scale, old in ((k, caches[0], ks, before[0]), (v, caches[1], vs, before[1])):
+        want = old.cpu().numpy().copy()
+        xs = x.float().cpu().numpy()
+        for t, slot in enumerate(slots.tolist()):
+            if not 0 <= slot < pages * page:
+                continue
+            row = xs[t].reshape(heads, dim)
+            if fp8:                                # one fp32 division, then one rounding
+                row = to_e4m3(np.clip(row / scale.cpu().numpy()[:, None], np.float32(-448), np.float32(448)).astype(np.float64))
+            else:
+                row = x[t].view(torch.int16).cpu().numpy().reshape(heads, dim)
+            want[slot // page, :, slot % page] = row
+        np.testing.assert_array_equal(cache.cpu().numpy(), want)
+
+
+def test_kv_write_rounds_every_step_to_nearest_even(gpu_lib):
+    """Every midpoint between neighbouring E4M3 values, and both sides of it in bf16 steps."""
+    v = np.sort(e4m3_values()[:127])
+    mid = np.concatenate([v, (v[1:] + v[:-1]) / 2, [464.0, 1e4, 3e38]]).astype(np.float32)
+    t = torch.tensor(np.concatenate([mid, -mid])).to(torch.bfloat16)
+    bits = t.view(torch.int16).int()
+    x = torch.cat([bits, (bits + 1).clamp(-32768, 32767), bits - 1]).to(torch.int16).view(torch.bfloat16)
+    x = x[torch.isfinite(x.float())]
+    n = -(-x.numel() // 64)
+    rows = torch.zeros(n * 64, dtype=torch.bfloat16)
+    rows[:x.numel()] = x
+    rows = rows.view(n, 64).cuda()
+    cache = torch.zeros(2, -(-n // 16), 1, 16, 64, dtype=torch.uint8, device="cuda")
+    gpu_lib.paged_kv_write(rows, rows, torch.arange(n, device="cuda"), cache[0].view(FP8), cache[1].view(FP8))
+    want = to_e4m3(np.clip(rows.float().cpu().numpy().astype(np.float64), -448, 448))
+    got = cache[0].reshape(-1, 64)[:n].cpu().numpy()
+    np.testing.assert_array_equal(got, want)
+    assert torch.equal(cache[0], cache[1])
+
+
+def test_kv_write_far_pages(gpu_lib):
+    """A cache of more than 2^32 bytes: the last page's offset passes 32 bits."""
+    pages, heads, page, dim = 70000, 2, 128, 128
+    store = torch.zeros(pages * heads * page * dim, dtype=torch.bfloat16, device="cuda")
+    cache = store.view(pages, heads, page, dim)
+    assert store.numel() * 2 > 2 ** 32
+    x = torch.randn(3, heads * dim, device="cuda").to(torch.bfloat16)
+    slots = torch.tensor([pages * page - 1, 0, (pages - 2) * page + 5], device="cuda")
+    gpu_lib.paged_kv_write(x, x, slots, cache, cache)
+    for t, s in enumerate(slots.tolist()):
+        assert torch.equal(cache[s // page, :, s % page], x[t].view(heads, dim))
+    assert int(store.ne(0).sum()) == int(x.ne(0).sum())
+
+
+def test_refusals(gpu_lib):
+    E = gpu_lib.NVFP4Error
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    k, slots = z(4, 256), z(4, dtype=torch.int64)
+    good = z(2, 2, 16, 128)
+    gpu_lib.paged_kv_write(k, k, slots[:4] + torch.arange(4, device="cuda"), good, good.clone())
+    for bad in (z(2, 2, 24, 128), z(2, 2, 16, 96), z(2, 4, 16, 64).transpose(2, 3), z(2, 2, 16, 128, dtype=torch.float16)):
+        with pytest.raises(E):
+            gpu_lib.paged_kv_write(z(4, bad.shape[1] * bad.shape[3]), z(4, bad.shape[1] * bad.shape[3]), slots, bad, bad)
+    with pytest.raises(E):
+        gpu_lib.paged_kv_write(k.float(), k, slots, good, good)
+    with pytest.raises(E):
+        gpu_lib.paged_kv_write(k, k[:3], slots, good, good)
+    with pytest.raises(E):
+        gpu_lib.paged_kv_write(k, k, slots.int(), good, good)
+    with pytest.raises(E):
+        gpu_lib.paged_kv_write(k, k, slots, good, good, k_scale=z(2, dtype=torch.float32))   # a scale without an FP8 cache
+    with pytest.raises(E):
+        gpu_lib.paged_kv_write(k.cpu(), k, slots, good, good)
+    with pytest.raises(E):
+        gpu_lib.paged_kv_write(z(4, 260)[:, 4:], k, slots, good, good)                       # not 16-byte aligned
+    lens, table = z(2, dtype=torch.int32), z(2, 4, dtype=torch.int32)
+    for bad in (dict(page_size=24), dict(page_size=8), dict(page_size=2048), dict(max_tokens=-1)):
+        with pytest.raises((E, RuntimeError)):
+            gpu_lib.paged_plan(lens, lens, lens, table, **{**dict(page_size=16, max_tokens=4), **bad})
+    with pytest.raises(E):
+        gpu_lib.paged_plan(lens.long(), lens, lens, table, 16, 4)
+    with pytest.raises(E):
+        gpu_lib.paged_plan(lens, z(3, dtype=torch.int32), lens, table, 16, 4)

@@ -370,8 +370,8 @@ int nvfp4_weight_stream_read(const void* w_packed, int64_t n, int64_t k, uint32_
  * power of two from 16 to 1024, for num_kv_heads heads of head_dim.  Element
  * (page, head, token in page, d) of either lies at page * page_stride +
  * head * head_stride + token * token_stride + d (elements; every stride a
- * multiple of 16 bytes, 16 tokens of a page less than 2^31 bytes apart; pages
- * may lie past 2^32 bytes).  Slot s is token
+ * multiple of 16 bytes, the tokens of a page less than 2^31 bytes apart; the
+ * pages may lie past 2^32 bytes).  Slot s is token
  * s % page_size of page s / page_size.  Element types: NVFP4_CACHE_BF16, or
  * NVFP4_CACHE_E4M3 with the value x held as E4M3(x / scale[head]).
  */

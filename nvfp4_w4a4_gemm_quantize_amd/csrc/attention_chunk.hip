@@ -11,6 +11,8 @@
 // waves of 32 rows; K and V pass through LDS a tile of 64 keys at a time (32
 // for heads of 256).  An E4M3 cache becomes bf16 on its way into LDS, once for
 // all eight waves.
+#include <float.h>
+
 #include "attention.h"
 
 namespace nvfp4 {
@@ -18,23 +20,52 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 64 * kChunkWaves;
+constexpr int kSlots = 3;    // key tiles in LDS: one in use, one arriving, one asked for
 
 // LDS layout of a tile: [keys][D] bf16, the 16-byte pieces of a row permuted so
 // that the lanes of one read instruction meet different banks: keys are read as
-// 16 bytes of 32 rows, values as 32 bytes of 4 rows (the transposing read).
+// 16 bytes of 32 rows, values as 64 bytes of 4 rows (the transposing read).
 template <int D>
 __device__ __forceinline__ int key_swizzle(int row) {
   return D == 64 ? (row >> 1) & 7 : row & 15;
 }
 template <int D>
 __device__ __forceinline__ int value_swizzle(int row) {
-  return (D == 64 ? (row >> 1) & 3 : row & 3) << 1;
+  return (D == 64 ? (row >> 1) & 1 : row & 3) << 2;
 }
 
 // 4 keys x 16 columns a group of 16 lanes; a lane gets the keys of its column.
 __device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
   typedef __attribute__((address_space(3))) bf16x4* lds_ptr;
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(uintptr_t)p));
+}
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Global -> LDS copy of 16 bytes a lane: lane l's bytes land at dst + 16 l, read
+// from base + voff (a uniform base and 32-bit lane offsets).  In inline asm, so
+// that the compiler adds no waits of its own before later LDS reads; arrival is
+// waited for with wait_arrived and published with the barrier.  It has no register
+// results.  The s_nop covers five wait states between a VALU write of the base
+// (or of M0) and its use.
+__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t voff, uint8_t* dst) {
+  const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)dst;
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(at) : "memory");
+}
+// All but the last N vector memory instructions have arrived.
+template <int N>
+__device__ __forceinline__ void wait_arrived() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// LDS writes done, then a barrier that nothing is moved across.
+__device__ __forceinline__ void phase_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 struct ChunkWorkspace {
@@ -61,19 +92,19 @@ int chunk_splits(int64_t tokens, int64_t requests, int group, int hkv, int64_t m
 
 template <int D, bool FP8>
 __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionArgs a, ChunkWorkspace ws, int splits) {
-  constexpr int KT = D == 256 ? 32 : 64;
+  constexpr int KT = D == 256 ? 32 : 64;      // keys of a tile
   constexpr int NK = KT / 32;                 // key fragments of a tile
+  constexpr int NG = KT / 16;                 // 16-key groups: a page holds whole ones
   constexpr int KS = D / 16;                  // k steps of the first product
   constexpr int DF = D / 32;                  // fragments of O
   constexpr int EB = FP8 ? 1 : 2;
   constexpr int ROW = D * 2;                  // bytes of an LDS row
-  constexpr int EP = 16 / EB;                 // elements of a 16-byte piece in the cache
-  constexpr int PIECES = KT * D / EP / kThreads;   // 16-byte pieces a thread brings of K (and of V)
-  constexpr int PPR = D / EP;                 // pieces a row
-  static_assert(KT * D / EP % kThreads == 0 || KT * D / EP < kThreads, "");
-  constexpr int NP = PIECES > 0 ? PIECES : 1;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[2][KT * ROW], lds_v[2][KT * ROW];
-  __shared__ int32_t lds_held[2][KT / 16];
+  constexpr int PPR = D * EB / 16;            // 16-byte pieces of a row in the cache
+  constexpr int RPI = 64 / PPR;               // rows that one load instruction of a wave brings
+  constexpr int LOADS = KT / RPI / kChunkWaves;   // such instructions a wave issues for K (and for V)
+  constexpr bool SPARE = LOADS == 0;          // heads of 64 in FP8: half of the waves bring a tile
+  constexpr int NL = SPARE ? 1 : LOADS;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[kSlots][KT * ROW], lds_v[kSlots][KT * ROW];
 
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -91,8 +122,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     const int64_t mid = (lo + hi + 1) >> 1;
     if ((int64_t)a.q_start[mid] * group / kChunkRows + mid <= vt) lo = mid; else hi = mid - 1;
   }
-  const int64_t r = lo;
-  const RequestLens l = request_lens(a, r);
+  const int64_t r = uniform(lo);
+  RequestLens l = request_lens(a, r);
+  l.start = uniform(l.start), l.tokens = uniform(l.tokens), l.keys = uniform(l.keys);
   const int64_t nrows = l.tokens * group, b = vt - ((int64_t)a.q_start[r] * group / kChunkRows + r);
   if (nrows <= kDecodeRows || b < 0 || b * kChunkRows >= nrows) return;
 
@@ -104,22 +136,18 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const int64_t all = max((keys - begin + KT - 1) / KT, (int64_t)0);
   const int64_t share = (all + splits - 1) / splits;
   const int64_t t_begin = min(split * share, all), t_end = min(t_begin + share, all);
+  const int n = __builtin_amdgcn_readfirstlane((int)(t_end - t_begin));
 
   float c = a.scale * kLog2e;
   if (a.cache.k_scale) c *= a.cache.k_scale[head];
   const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
-  c = fabsf(c);
+  c = fmaxf(fabsf(c), FLT_MIN);   // never 0: a hidden score's -inf stays one
 
   // this lane's row of q, the B operand: column c32, k = 8 columns of q
   const int64_t my_row = row0 + wave * 32 + c32;
   const bool live = my_row < nrows;
   const int64_t my_token = live ? my_row / group : 0;
   const int my_head = head * group + (live ? (int)(my_row % group) : 0);
-  const int64_t my_pos = live ? token_pos(a, r, l, my_token) : -1;
-  const int64_t wave_row = row0 + wave * 32;
-  const bool wave_live = wave_row < nrows;
-  const int64_t wave_pos0 = token_pos(a, r, l, wave_row / group);
-  const int64_t wave_pos1 = token_pos(a, r, l, min(wave_row + 31, nrows - 1) / group);
   bf16x8 q[KS];
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
@@ -128,54 +156,121 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     for (int i = 0; i < 4; ++i) w[i] = live ? w[i] ^ flip : 0u;
     q[s] = __builtin_bit_cast(bf16x8, w);
   }
+  // positions relative to the first key of the part
+  const int origin = __builtin_amdgcn_readfirstlane((int)(begin + t_begin * KT));
+  auto rel = [&](int64_t x) { return (int)min(max(x - origin, (int64_t)INT32_MIN / 2), (int64_t)INT32_MAX / 2); };
+  const int my_pos = live ? rel(token_pos(a, r, l, my_token)) : INT32_MIN / 2;
+  const int my_low = a.window && live ? rel(token_pos(a, r, l, my_token) - a.window + 1) : INT32_MIN / 2;
+  const int64_t wave_row = min(row0 + wave * 32, nrows - 1);
+  const int wave_pos = __builtin_amdgcn_readfirstlane(rel(token_pos(a, r, l, wave_row / group)));   // keys up to it are seen by all rows
+  const int wave_low = __builtin_amdgcn_readfirstlane(
+      a.window ? rel(token_pos(a, r, l, min(wave_row + 31, nrows - 1) / group) - a.window + 1) : INT32_MIN / 2);
+  const int keys_rel = __builtin_amdgcn_readfirstlane(rel(keys)), low_rel = __builtin_amdgcn_readfirstlane(rel(low));
 
-  const int32_t* table = a.block_table + r * a.ld_table;
-  const int64_t page_mask = ((int64_t)1 << a.cache.page_shift) - 1;
-  const int64_t head_off = head * a.cache.head_stride;
-  u32x4 kr[NP], vr[NP];
-  int32_t held_r[NP];
-  const bool loads = PIECES > 0 || tid < KT * D / EP;
-  auto load = [&](int64_t t) {
+  // Where a tile's keys lie, read through the scalar cache; beyond the last key, its page.
+  typedef const __attribute__((address_space(4))) int32_t* table_ptr;
+  const table_ptr table = (table_ptr)(uintptr_t)(a.block_table + r * a.ld_table);
+  const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
+  const uint32_t num_pages = (uint32_t)a.cache.num_pages;
+  auto page_at = [&](int key) { return (uint32_t)table[(uint32_t)(origin + min(key, keys_rel - 1)) >> page_shift]; };
+  // A missing page is looked for once in the part's whole table: only if there is one do the tiles look again.
+  bool missing = false;
+  if (n > 0) {
+    const int last = (origin + min(n * KT, keys_rel) - 1) >> page_shift;
+    const int32_t* entries = a.block_table + r * a.ld_table;
+    for (int i = (origin >> page_shift) + lane; i <= last; i += 64) missing |= (uint32_t)entries[i] >= num_pages;
+    missing = __any(missing);
+  }
+  // A bit for every key of tile j that the request holds.
+  constexpr uint64_t kAll = ~(uint64_t)0 >> (64 - KT);
+  auto held_keys = [&](int j) {
+    uint64_t held = kAll;
+    const int top = keys_rel - j * KT, bottom = low_rel - j * KT;   // keys of the tile in [bottom, top)
+    if (top < KT) held &= top > 0 ? ((uint64_t)1 << top) - 1 : 0;
+    if (bottom > 0) held &= bottom < 64 ? ~(((uint64_t)1 << bottom) - 1) : 0;
+    if (missing)
+      for (int g = 0; g < NG; ++g)
+        if (page_at(min(j, n - 1) * KT + 16 * g) >= num_pages) held &= ~((uint64_t)0xffff << (16 * g));
+    return held;
+  };
+
+  // A load instruction i of this wave brings rows (i * 8 + wave) * RPI on; a
+  // lane's 16 bytes go to consecutive LDS addresses, so the bank permutation is
+  // made on the source side.  Without a page any page serves: its scores are
+  // hidden and its values cleared.
+  const uint32_t page_units = (uint32_t)(a.cache.page_stride * EB / 16), row_bytes = (uint32_t)a.cache.token_stride * EB;
+  const int lane_row = lane / PPR, lane_col = lane % PPR;
+  const int wave_rows = wave * RPI % 16;      // the permutations depend on the row modulo 16
+  const uint32_t k_voff = (uint32_t)lane_row * row_bytes + (FP8 ? lane_col : lane_col ^ key_swizzle<D>(wave_rows + lane_row)) * 16;
+  const uint32_t v_voff = (uint32_t)lane_row * row_bytes + (FP8 ? lane_col : lane_col ^ value_swizzle<D>(wave_rows + lane_row)) * 16;
+  const bool brings = !SPARE || wave < KT / RPI;
+  const uint8_t* k_base = (const uint8_t*)a.cache.k + head * a.cache.head_stride * EB;
+  const uint8_t* v_base = (const uint8_t*)a.cache.v + head * a.cache.head_stride * EB;
+  auto row_of = [&](int i) { return (i * kChunkWaves + wave) * RPI; };
+  typedef uint32_t Pages __attribute__((ext_vector_type(2)));   // of this wave's load instructions
+  typedef int64_t Offsets __attribute__((ext_vector_type(2)));
+  auto pages_of = [&](int j) {
+    Pages p = {0, 0};
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int piece = i * kThreads + tid, row = piece / PPR, col = piece % PPR;
-      const int64_t key = begin + t * KT + row;
-      int32_t page = -1;
-      if (loads && key < keys) page = table[key >> a.cache.page_shift];
-      held_r[i] = page >= 0 && page < a.cache.num_pages;
-      kr[i] = vr[i] = u32x4{0u, 0u, 0u, 0u};   // what lies in unwritten or foreign places may be NaN
-      if (held_r[i] && key >= low) {
-        const int64_t at = (page * a.cache.page_stride + head_off + (key & page_mask) * a.cache.token_stride + col * EP) * EB;
-        kr[i] = *(const u32x4*)((const uint8_t*)a.cache.k + at);
-        vr[i] = *(const u32x4*)((const uint8_t*)a.cache.v + at);
+    for (int i = 0; i < NL; ++i) p[i] = page_at(min(j, n - 1) * KT + row_of(i));
+    return p;
+  };
+  auto offsets_of = [&](int j, const Pages& p) {
+    Offsets at = {0, 0};
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      at[i] = uniform((int64_t)((uint64_t)(p[i] < num_pages ? p[i] : 0) * page_units << 4) +
+                      (uint32_t)((origin + min(j, n - 1) * KT + row_of(i)) & page_mask) * row_bytes);
+    return at;
+  };
+  // bf16: straight into LDS.  E4M3: into registers, a step later converted into LDS.
+  u32x4 kr[FP8 ? NL : 1], vr[FP8 ? NL : 1];
+  auto bring = [&](const uint8_t* base, const Offsets& at, int i, uint8_t* lds, uint32_t voff, u32x4* regs) {
+    if constexpr (FP8) {
+      if (brings) regs[i] = *(const u32x4*)(base + at[i] + voff);
+    } else {
+      dma16(base + at[i], voff, lds + (i * kChunkWaves + wave) * 1024);
+    }
+  };
+  auto bring_all = [&](const uint8_t* base, const Offsets& at, uint8_t* lds, uint32_t voff, u32x4* regs) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) bring(base, at, i, lds, voff, regs);
+  };
+  // Values of keys that the request does not hold are cleared in LDS, by the
+  // lanes that brought them: they may be NaN, and 0 * NaN is not 0.
+  auto settle = [&](uint8_t* lds, const u32x4* regs, bool values, uint64_t held) {
+    if constexpr (FP8) {
+      if (brings) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int row = (i * kChunkWaves + wave) * RPI + lane_row;
+          const int x = values ? value_swizzle<D>(row) : key_swizzle<D>(row);
+          const uint32_t keep = !values || (held >> row & 1) ? 0xffffffffu : 0u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w0 = regs[i][2 * k] & keep, w1 = regs[i][2 * k + 1] & keep;
+            *(u32x4*)(lds + row * ROW + ((2 * lane_col + k) ^ x) * 16) =
+                u32x4{e4m3_bf16<false>(w0), e4m3_bf16<true>(w0), e4m3_bf16<false>(w1), e4m3_bf16<true>(w1)};
+          }
+        }
       }
     }
   };
-  auto store = [&](int stage) {
-    if (!loads) return;
+  auto clear_values = [&](uint8_t* lds, uint64_t held) {
+    if constexpr (!FP8) {
+      if (held != kAll) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int piece = i * kThreads + tid, row = piece / PPR, col = piece % PPR;
-      uint8_t* kp = lds_k[stage] + row * ROW;
-      uint8_t* vp = lds_v[stage] + row * ROW;
-      const int ks = key_swizzle<D>(row), vs = value_swizzle<D>(row);
-      if constexpr (FP8) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          *(u32x4*)(kp + ((2 * col + j) ^ ks) * 16) = u32x4{e4m3_bf16<false>(kr[i][2 * j]), e4m3_bf16<true>(kr[i][2 * j]), e4m3_bf16<false>(kr[i][2 * j + 1]), e4m3_bf16<true>(kr[i][2 * j + 1])};
-          *(u32x4*)(vp + ((2 * col + j) ^ vs) * 16) = u32x4{e4m3_bf16<false>(vr[i][2 * j]), e4m3_bf16<true>(vr[i][2 * j]), e4m3_bf16<false>(vr[i][2 * j + 1]), e4m3_bf16<true>(vr[i][2 * j + 1])};
+        for (int i = 0; i < NL; ++i) {
+          const int at = i * kChunkWaves + wave;
+          if (!(held >> (at * RPI + lane_row) & 1)) *(u32x4*)(lds + at * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
         }
-      } else {
-        *(u32x4*)(kp + (col ^ ks) * 16) = kr[i];
-        *(u32x4*)(vp + (col ^ vs) * 16) = vr[i];
       }
-      // a page holds 16 keys or a multiple: one key of 16 tells whether there is one
-      if (col == 0 && row % 16 == 0) lds_held[stage][row / 16] = held_r[i];
     }
   };
 
   float m = -INFINITY, sum = 0.f;
-  f32x16 o[DF];
+  f32x16 o[DF], s[NK];
+  bf16x8 p[2 * NK];
 #pragma unroll
   for (int i = 0; i < DF; ++i)
 #pragma unroll
@@ -186,83 +281,169 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const int v_r = 4 * h + ((lane & 15) >> 2);
   const int v_row = v_r * ROW + (lane & 1) * 8, v_x = ((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<D>(v_r)) * 16;
 
-  if (t_begin < t_end) {
-    load(t_begin);
-    store(0);
-  }
-  __syncthreads();
-  for (int64_t t = t_begin; t < t_end; ++t) {
-    const int stage = (int)(t - t_begin) & 1;
-    const bool more = t + 1 < t_end;
-    if (more) load(t + 1);
-    const int64_t key0 = begin + t * KT;
-    if (wave_live && key0 <= wave_pos1 && !(a.window && key0 + KT <= wave_pos0 - a.window + 1)) {
-      f32x16 s[NK];
+  auto key_fragment = [&](const uint8_t* kt, int e) {     // e-th of the first product: key fragment fastest
+    return *(const bf16x8*)(kt + (e % NK) * 32 * ROW + k_row + (((e / NK) * 32) ^ k_x));
+  };
+  auto value_fragment = [&](const uint8_t* vt, int e) {   // e-th of the second product: O's fragment fastest
+    const uint8_t* vp = vt + (e / DF) * 16 * ROW + v_row + (((e % DF) * 64) ^ v_x);
+    const u32x2 v0 = read_transposed(vp), v1 = read_transposed(vp + 8 * ROW);
+    return __builtin_bit_cast(bf16x8, u32x4{v0[0], v0[1], v1[0], v1[1]});
+  };
+  auto clear_scores = [&] {
 #pragma unroll
-      for (int f = 0; f < NK; ++f) {
+    for (int f = 0; f < NK; ++f)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[f][j] = 0.f;
+      for (int j = 0; j < 16; ++j) s[f][j] = 0.f;
+  };
+  auto multiply_keys = [&](const bf16x8& kf, int e) {
+    s[e % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[e / NK], s[e % NK], 0, 0, 0);
+  };
+  auto multiply_values = [&](const bf16x8& vf, int e) {
+    o[e % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[e / DF], o[e % DF], 0, 0, 0);
+  };
+  // Both products, two fragments of each a step, their operands read kAhead
+  // steps before: an LDS read takes longer than the four instructions of a step.
+  constexpr int kAhead = D == 256 ? 1 : 2;
+  constexpr int STEPS = NK * DF;
+  auto products = [&](const uint8_t* kt, const uint8_t* vt, auto between) {
+    bf16x8 vf[kAhead + 1][2], kf[kAhead + 1][2];
+    clear_scores();
 #pragma unroll
-        for (int st = 0; st < KS; ++st) {
-          const bf16x8 kf = *(const bf16x8*)(lds_k[stage] + f * 32 * ROW + k_row + ((st * 32) ^ k_x));
-          s[f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[st], s[f], 0, 0, 0);
+    for (int t = 0; t < STEPS + kAhead; ++t) {
+      if (t < STEPS) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vf[t % (kAhead + 1)][i] = value_fragment(vt, 2 * t + i);
+          kf[t % (kAhead + 1)][i] = key_fragment(kt, 2 * t + i);
         }
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);   // six LDS reads, then four products
       }
-      int32_t held = 1;
+      if (t >= kAhead) {
+        const int d = t - kAhead;
 #pragma unroll
-      for (int i = 0; i < KT / 16; ++i) held &= lds_held[stage][i];
-      const bool full = __builtin_amdgcn_readfirstlane(held) && key0 + KT - 1 <= wave_pos0 && key0 + KT <= keys &&
-                        (a.window == 0 || key0 > wave_pos1 - a.window);
-      if (!full) {
-#pragma unroll
-        for (int f = 0; f < NK; ++f)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int in = f * 32 + 8 * (j >> 2) + 4 * h + (j & 3);
-            const int64_t key = key0 + in;
-            if (key > my_pos || key >= keys || !lds_held[stage][in / 16] || (a.window && key <= my_pos - a.window)) s[f][j] = -INFINITY;
-          }
+        for (int i = 0; i < 2; ++i) {
+          multiply_values(vf[d % (kAhead + 1)][i], 2 * d + i);
+          multiply_keys(kf[d % (kAhead + 1)][i], 2 * d + i);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        between(d);
       }
-      float top = s[0][0];
+    }
+  };
+  auto softmax_step = [&](int j, uint64_t held) {
+    const int key0 = j * KT;
+    const bool full = held == kAll && key0 + KT - 1 <= wave_pos && key0 >= wave_low;
+    if (!full) {
 #pragma unroll
       for (int f = 0; f < NK; ++f)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, s[f][j]);
-      if (__any(top > m)) {
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float to = fmaxf(m, top);
-        const float by = m == to ? 1.f : m == -INFINITY ? 0.f : exp2_fast(c * (m - to));
-        m = to;
-        sum *= by;
-#pragma unroll
-        for (int i = 0; i < DF; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[i][j] *= by;
-      }
-      const float ref = m == -INFINITY ? 0.f : c * m;
-#pragma unroll
-      for (int f = 0; f < NK; ++f)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float e[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            e[j] = exp2_fast(fmaf(s[f][8 * u + j], c, -ref));
-            if (!full && s[f][8 * u + j] == -INFINITY) e[j] = 0.f;
-          }
-          sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-          // P in bf16, the matrix instruction's type with V: 2^-8 relative a term at most, averaged over the keys
-          const bf16x8 p = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
-#pragma unroll
-          for (int i = 0; i < DF; ++i) {
-            const uint8_t* vp = lds_v[stage] + (f * 32 + u * 16) * ROW + v_row + ((i * 64) ^ v_x);
-            const u32x2 v0 = read_transposed(vp), v1 = read_transposed(vp + 8 * ROW);
-            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, u32x4{v0[0], v0[1], v1[0], v1[1]}), p, o[i], 0, 0, 0);
-          }
+        for (int i = 0; i < 16; ++i) {
+          const int in = f * 32 + 8 * (i >> 2) + (i & 3);   // + 4 h
+          const int key = key0 + in + 4 * h;
+          const bool hidden = (key > my_pos) | (key < my_low) | !((uint32_t)(held >> in) >> (4 * h) & 1);
+          s[f][i] = hidden ? -INFINITY : s[f][i];
         }
     }
-    if (more) store(stage ^ 1);
-    __syncthreads();
+    float top = s[0][0];
+#pragma unroll
+    for (int f = 0; f < NK; ++f)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[f][i]);
+    // The maximum may lag behind by a factor of 2^8, which costs no precision: O
+    // is scaled anew only when it does not suffice any more.
+    if (__any(c * (top - m) > 8.f || (m == -INFINITY && top > m))) {
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float to = fmaxf(m, top);
+      const float by = m == to ? 1.f : m == -INFINITY ? 0.f : exp2_fast(c * (m - to));
+      m = to;
+      sum *= by;
+#pragma unroll
+      for (int i = 0; i < DF; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[i][k] *= by;
+    }
+    const float ref = m == -INFINITY ? 0.f : c * m;
+#pragma unroll
+    for (int u = 0; u < 2 * NK; ++u) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = exp2_fast(fmaf(s[u >> 1][8 * (u & 1) + i], c, -ref));
+      sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      // P in bf16, the matrix instruction's type with V: 2^-8 relative a term at most, averaged over the keys
+      p[u] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
+    }
+  };
+
+  if (n > 0) {
+    // Tile j's keys and values lie in slot j % 3.  Before the loop: keys 0 - 2, values 0 and 1.
+    uint64_t held_now = held_keys(0), held_next = held_keys(1), held_then = held_keys(2);
+    Pages page = pages_of(3);
+    Offsets value_at;                        // offsets of the tile whose values are brought next
+    {
+      const Offsets at0 = offsets_of(0, pages_of(0)), at1 = offsets_of(1, pages_of(1));
+      value_at = offsets_of(2, pages_of(2));
+      bring_all(k_base, at0, lds_k[0], k_voff, kr);
+      settle(lds_k[0], kr, false, 0);
+      bring_all(k_base, at1, lds_k[1], k_voff, kr);
+      settle(lds_k[1], kr, false, 0);
+      bring_all(v_base, at0, lds_v[0], v_voff, vr);
+      settle(lds_v[0], vr, true, held_now);
+      bring_all(k_base, value_at, lds_k[2], k_voff, kr);
+      settle(lds_k[2], kr, false, 0);
+      bring_all(v_base, at1, lds_v[1], v_voff, vr);
+      settle(lds_v[1], vr, true, held_next);
+    }
+    if constexpr (FP8) {                     // in registers: keys 3, values 2
+      bring_all(v_base, value_at, nullptr, v_voff, vr);
+      value_at = offsets_of(3, page);
+      bring_all(k_base, value_at, nullptr, k_voff, kr);
+      page = pages_of(4);
+    }
+    wait_arrived<0>();
+    clear_values(lds_v[0], held_now);
+    clear_values(lds_v[1], held_next);
+    phase_barrier();
+    // The two waves of a SIMD take turns: while waves 0-3 multiply, waves 4-7,
+    // one barrier behind, run their softmax, and the other way round.
+    if (wave >= kChunkWaves / 2) phase_barrier();
+    clear_scores();
+#pragma unroll
+    for (int e = 0; e < KS * NK; ++e) multiply_keys(key_fragment(lds_k[0], e), e);
+    phase_barrier();
+    softmax_step(0, held_now);
+    phase_barrier();
+    int slot = 0, next = 1, then = 2;        // slots of tiles j, j + 1, j + 2
+    for (int j = 0; j < n; ++j) {
+      // products: O += values j, S = keys j + 1; tile j + 3's keys take the place of
+      // tile j's, tile j + 2's values that of tile j - 1's, read by all two phases ago
+      settle(lds_k[slot], kr, false, 0);
+      settle(lds_v[then], vr, true, held_then);
+      const Offsets key_at = offsets_of(FP8 ? j + 4 : j + 3, page);
+      page = pages_of(FP8 ? j + 5 : j + 4);
+      __builtin_amdgcn_s_setprio(1);
+      products(lds_k[next], lds_v[slot], [&](int step) {
+        if (step < NL) bring(k_base, key_at, step, lds_k[slot], k_voff, kr);
+        else if (step < 2 * NL) bring(v_base, value_at, step - NL, lds_v[then], v_voff, vr);
+      });
+      __builtin_amdgcn_s_setprio(0);
+      value_at = key_at;
+      if constexpr (!FP8) {                  // all but what this phase asked for has arrived: tile j + 1's values
+        wait_arrived<2 * NL>();
+        clear_values(lds_v[next], held_next);
+      }
+      phase_barrier();
+      held_now = held_next;
+      held_next = held_then;
+      held_then = held_keys(j + 3);
+      if (j + 1 < n) softmax_step(j + 1, held_now);
+      phase_barrier();
+      const int t = slot;
+      slot = next;
+      next = then;
+      then = t;
+    }
+    if (wave < kChunkWaves / 2) phase_barrier();
+    wait_arrived<0>();                       // nothing may still be on its way into LDS when the workgroup ends
   }
 
   sum += __shfl_xor(sum, 32);
@@ -287,7 +468,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   } else {
     const int64_t slot = (split * a.tokens + trow) * a.hq + my_head;
     if (h == 0) ws.ml[slot] = make_float2(top, sum);
-    if (t_begin < t_end)
+    if (n > 0)
 #pragma unroll
       for (int i = 0; i < DF; ++i)
 #pragma unroll

@@ -51,7 +51,8 @@ int validate_cache(const void* k_cache, const void* v_cache, int cache_dtype, in
   if (page_stride < 0 || head_stride < 0 || token_stride < head_dim) return NVFP4_ESHAPE;
   if (!k_cache || !v_cache || (cache_dtype == NVFP4_CACHE_BF16 && (k_scale || v_scale))) return NVFP4_EINVAL;
   const int64_t bytes = cache_dtype == NVFP4_CACHE_BF16 ? 2 : 1;
-  if (token_stride > INT32_MAX / (16 * bytes)) return NVFP4_EUNSUPPORTED;   // 32-bit offsets inside 16 tokens
+  // 32-bit offsets inside a page, page strides in 32 bits of 16-byte units
+  if (token_stride > INT32_MAX / (page_size * bytes) || page_stride / (16 / bytes) > UINT32_MAX) return NVFP4_EUNSUPPORTED;
   const int64_t unit = 16 / bytes;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || page_stride % unit || head_stride % unit ||
       token_stride % unit || !aligned(k_scale, 4) || !aligned(v_scale, 4))

@@ -50,7 +50,7 @@ def write(lib, k=A16, ldk=256, v=A16, ldv=256, slots=A16, T=4, kc=A16, vc=A16, d
 def test_kv_write_validation(lib):
     for bad in (dict(T=-1), dict(heads=0), dict(pages=0), dict(dim=0), dict(ldk=255), dict(ldv=0), dict(ts=127), dict(ps=-8)):
         assert write(lib, **bad) == ESHAPE, bad
-    for bad in (dict(dim=96, ts=96, hs=96 * 16), dict(page=20), dict(T=2 ** 31), dict(ts=2 ** 27)):
+    for bad in (dict(dim=96, ts=96, hs=96 * 16), dict(page=20), dict(T=2 ** 31), dict(ts=2 ** 27), dict(ps=2 ** 36)):
         assert write(lib, **bad) == EUNSUPPORTED, bad
     for bad in (dict(k=None), dict(v=None), dict(slots=None), dict(kc=None), dict(vc=None), dict(dt=2), dict(ks=A16)):
         assert write(lib, **bad) == EINVAL, bad

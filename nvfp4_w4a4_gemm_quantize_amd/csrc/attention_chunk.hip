@@ -20,7 +20,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 64 * kChunkWaves;
-constexpr int kSlots = 3;    // key tiles in LDS: one in use, one arriving, one asked for
+constexpr int kSlots = 4;    // tiles in LDS: tile j lies in slot j % 4
 
 // LDS layout of a tile: [keys][D] bf16, the 16-byte pieces of a row permuted so
 // that the lanes of one read instruction meet different banks: keys are read as
@@ -61,10 +61,14 @@ template <int N>
 __device__ __forceinline__ void wait_arrived() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
-// LDS writes done, then a barrier that nothing is moved across.
+// A barrier that nothing is moved across; WRITES: after this wave's LDS writes.
+template <bool WRITES>
 __device__ __forceinline__ void phase_barrier() {
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if (WRITES)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else
+    asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -167,18 +171,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       a.window ? rel(token_pos(a, r, l, min(wave_row + 31, nrows - 1) / group) - a.window + 1) : INT32_MIN / 2);
   const int keys_rel = __builtin_amdgcn_readfirstlane(rel(keys)), low_rel = __builtin_amdgcn_readfirstlane(rel(low));
 
-  // Where a tile's keys lie, read through the scalar cache; beyond the last key, its page.
-  typedef const __attribute__((address_space(4))) int32_t* table_ptr;
-  const table_ptr table = (table_ptr)(uintptr_t)(a.block_table + r * a.ld_table);
+  // Where the keys lie.  A missing page is looked for once in the part's whole
+  // table: only if there is one do tiles look again.
   const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
   const uint32_t num_pages = (uint32_t)a.cache.num_pages;
+  const int32_t* table = a.block_table + r * a.ld_table;
   auto page_at = [&](int key) { return (uint32_t)table[(uint32_t)(origin + min(key, keys_rel - 1)) >> page_shift]; };
-  // A missing page is looked for once in the part's whole table: only if there is one do the tiles look again.
   bool missing = false;
   if (n > 0) {
     const int last = (origin + min(n * KT, keys_rel) - 1) >> page_shift;
-    const int32_t* entries = a.block_table + r * a.ld_table;
-    for (int i = (origin >> page_shift) + lane; i <= last; i += 64) missing |= (uint32_t)entries[i] >= num_pages;
+    for (int i = (origin >> page_shift) + lane; i <= last; i += 64) missing |= (uint32_t)table[i] >= num_pages;
     missing = __any(missing);
   }
   // A bit for every key of tile j that the request holds.
@@ -191,8 +193,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     if (missing)
       for (int g = 0; g < NG; ++g)
         if (page_at(min(j, n - 1) * KT + 16 * g) >= num_pages) held &= ~((uint64_t)0xffff << (16 * g));
-    return held;
+    return (uint64_t)uniform((int64_t)held);
   };
+  // Tiles [held_from, held_to) are held in full, tiles [seen_from, seen_to) also
+  // seen in full by every row of this wave.
+  const int held_from = missing ? 0 : max(low_rel + KT - 1, 0) / KT, held_to = missing ? 0 : max(keys_rel, 0) / KT;
+  const int seen_from = max(held_from, (max(wave_low, 0) + KT - 1) / KT);
+  const int seen_to = min(held_to, (max(wave_pos, -1) + 1) / KT);
 
   // A load instruction i of this wave brings rows (i * 8 + wave) * RPI on; a
   // lane's 16 bytes go to consecutive LDS addresses, so the bank permutation is
@@ -207,20 +214,25 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const uint8_t* k_base = (const uint8_t*)a.cache.k + head * a.cache.head_stride * EB;
   const uint8_t* v_base = (const uint8_t*)a.cache.v + head * a.cache.head_stride * EB;
   auto row_of = [&](int i) { return (i * kChunkWaves + wave) * RPI; };
-  typedef uint32_t Pages __attribute__((ext_vector_type(2)));   // of this wave's load instructions
-  typedef int64_t Offsets __attribute__((ext_vector_type(2)));
-  auto pages_of = [&](int j) {
-    Pages p = {0, 0};
+  // Byte offsets of this wave's load instructions for 64 tiles at a time, a tile a lane.
+  int64_t lane_at[NL];
+  auto locate = [&](int j0) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) p[i] = page_at(min(j, n - 1) * KT + row_of(i));
-    return p;
+    for (int i = 0; i < NL; ++i) {
+      const int key = min(j0 + lane, n - 1) * KT + row_of(i);
+      const uint32_t page = page_at(key);
+      lane_at[i] = (int64_t)((uint64_t)(page < num_pages ? page : 0) * page_units << 4) +
+                   (uint32_t)((origin + key) & page_mask) * row_bytes;
+    }
   };
-  auto offsets_of = [&](int j, const Pages& p) {
+  typedef int64_t Offsets __attribute__((ext_vector_type(2)));
+  auto offsets_of = [&](int j) {
     Offsets at = {0, 0};
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
-      at[i] = uniform((int64_t)((uint64_t)(p[i] < num_pages ? p[i] : 0) * page_units << 4) +
-                      (uint32_t)((origin + min(j, n - 1) * KT + row_of(i)) & page_mask) * row_bytes);
+    for (int i = 0; i < NL; ++i) {
+      const uint32_t lo = __builtin_amdgcn_readlane((int)lane_at[i], j & 63), hi = __builtin_amdgcn_readlane((int)(lane_at[i] >> 32), j & 63);
+      at[i] = (int64_t)((uint64_t)hi << 32 | lo);
+    }
     return at;
   };
   // bf16: straight into LDS.  E4M3: into registers, a step later converted into LDS.
@@ -258,12 +270,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   };
   auto clear_values = [&](uint8_t* lds, uint64_t held) {
     if constexpr (!FP8) {
-      if (held != kAll) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          const int at = i * kChunkWaves + wave;
-          if (!(held >> (at * RPI + lane_row) & 1)) *(u32x4*)(lds + at * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
-        }
+      for (int i = 0; i < NL; ++i) {
+        const int at = i * kChunkWaves + wave;
+        if (!(held >> (at * RPI + lane_row) & 1)) *(u32x4*)(lds + at * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
       }
     }
   };
@@ -302,38 +312,39 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     o[e % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[e / DF], o[e % DF], 0, 0, 0);
   };
   // Both products, two fragments of each a step, their operands read kAhead
-  // steps before: an LDS read takes longer than the four instructions of a step.
+  // steps before (an LDS read takes longer than the four instructions of a step);
+  // those of the first steps are read before the barrier that begins the phase.
   constexpr int kAhead = D == 256 ? 1 : 2;
   constexpr int STEPS = NK * DF;
-  auto products = [&](const uint8_t* kt, const uint8_t* vt, auto between) {
-    bf16x8 vf[kAhead + 1][2], kf[kAhead + 1][2];
-    clear_scores();
+  bf16x8 vf[kAhead + 1][2], kf[kAhead + 1][2];
+  auto read_operands = [&](const uint8_t* kt, const uint8_t* vt, int t) {
 #pragma unroll
-    for (int t = 0; t < STEPS + kAhead; ++t) {
-      if (t < STEPS) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          vf[t % (kAhead + 1)][i] = value_fragment(vt, 2 * t + i);
-          kf[t % (kAhead + 1)][i] = key_fragment(kt, 2 * t + i);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);   // six LDS reads, then four products
-      }
-      if (t >= kAhead) {
-        const int d = t - kAhead;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          multiply_values(vf[d % (kAhead + 1)][i], 2 * d + i);
-          multiply_keys(kf[d % (kAhead + 1)][i], 2 * d + i);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-        between(d);
-      }
+    for (int i = 0; i < 2; ++i) {
+      vf[t % (kAhead + 1)][i] = value_fragment(vt, 2 * t + i);
+      kf[t % (kAhead + 1)][i] = key_fragment(kt, 2 * t + i);
     }
   };
-  auto softmax_step = [&](int j, uint64_t held) {
-    const int key0 = j * KT;
-    const bool full = held == kAll && key0 + KT - 1 <= wave_pos && key0 >= wave_low;
-    if (!full) {
+  auto products = [&](const uint8_t* kt, const uint8_t* vt, auto between) {
+    clear_scores();
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      if (t + kAhead < STEPS) {
+        read_operands(kt, vt, t + kAhead);
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);   // six LDS reads, then four products
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        multiply_values(vf[t % (kAhead + 1)][i], 2 * t + i);
+        multiply_keys(kf[t % (kAhead + 1)][i], 2 * t + i);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+      between(t);
+    }
+  };
+  auto softmax_step = [&](int j) {
+    if (j < seen_from || j >= seen_to) {
+      const int key0 = j * KT;
+      const uint64_t held = held_keys(j);
 #pragma unroll
       for (int f = 0; f < NK; ++f)
 #pragma unroll
@@ -375,74 +386,69 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   };
 
   if (n > 0) {
-    // Tile j's keys and values lie in slot j % 3.  Before the loop: keys 0 - 2, values 0 and 1.
-    uint64_t held_now = held_keys(0), held_next = held_keys(1), held_then = held_keys(2);
-    Pages page = pages_of(3);
-    Offsets value_at;                        // offsets of the tile whose values are brought next
-    {
-      const Offsets at0 = offsets_of(0, pages_of(0)), at1 = offsets_of(1, pages_of(1));
-      value_at = offsets_of(2, pages_of(2));
-      bring_all(k_base, at0, lds_k[0], k_voff, kr);
-      settle(lds_k[0], kr, false, 0);
-      bring_all(k_base, at1, lds_k[1], k_voff, kr);
-      settle(lds_k[1], kr, false, 0);
-      bring_all(v_base, at0, lds_v[0], v_voff, vr);
-      settle(lds_v[0], vr, true, held_now);
-      bring_all(k_base, value_at, lds_k[2], k_voff, kr);
-      settle(lds_k[2], kr, false, 0);
-      bring_all(v_base, at1, lds_v[1], v_voff, vr);
-      settle(lds_v[1], vr, true, held_next);
+    // Before the loop: keys 0 - 3, values 0 - 2.
+    constexpr int kLead = FP8 ? 5 : 4;       // the tile whose keys are asked for while tile 0's values are multiplied
+    locate(0);
+    Offsets key_at, value_at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      key_at = offsets_of(j);
+      bring_all(k_base, key_at, lds_k[j], k_voff, kr);
+      settle(lds_k[j], kr, false, 0);
+      if (j == 3) break;
+      bring_all(v_base, key_at, lds_v[j], v_voff, vr);
+      settle(lds_v[j], vr, true, held_keys(j));
     }
-    if constexpr (FP8) {                     // in registers: keys 3, values 2
+    value_at = key_at;
+    if constexpr (FP8) {                     // in registers: keys 4, values 3
       bring_all(v_base, value_at, nullptr, v_voff, vr);
-      value_at = offsets_of(3, page);
+      value_at = offsets_of(4);
       bring_all(k_base, value_at, nullptr, k_voff, kr);
-      page = pages_of(4);
     }
+    key_at = offsets_of(kLead);
     wait_arrived<0>();
-    clear_values(lds_v[0], held_now);
-    clear_values(lds_v[1], held_next);
-    phase_barrier();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) clear_values(lds_v[j], held_keys(j));
+    phase_barrier<true>();
     // The two waves of a SIMD take turns: while waves 0-3 multiply, waves 4-7,
     // one barrier behind, run their softmax, and the other way round.
-    if (wave >= kChunkWaves / 2) phase_barrier();
+    if (wave >= kChunkWaves / 2) phase_barrier<false>();
     clear_scores();
 #pragma unroll
     for (int e = 0; e < KS * NK; ++e) multiply_keys(key_fragment(lds_k[0], e), e);
-    phase_barrier();
-    softmax_step(0, held_now);
-    phase_barrier();
-    int slot = 0, next = 1, then = 2;        // slots of tiles j, j + 1, j + 2
+    phase_barrier<false>();
+    softmax_step(0);
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) read_operands(lds_k[1], lds_v[0], t);
+    phase_barrier<false>();
     for (int j = 0; j < n; ++j) {
-      // products: O += values j, S = keys j + 1; tile j + 3's keys take the place of
-      // tile j's, tile j + 2's values that of tile j - 1's, read by all two phases ago
-      settle(lds_k[slot], kr, false, 0);
-      settle(lds_v[then], vr, true, held_then);
-      const Offsets key_at = offsets_of(FP8 ? j + 4 : j + 3, page);
-      page = pages_of(FP8 ? j + 5 : j + 4);
+      // Products: O += values j, S = keys j + 1.  Tile j + 4's keys take the place of
+      // tile j's, tile j + 3's values that of tile j - 1's, which all have read; they
+      // are waited for in the next products and read at the end of the softmax after.
+      uint8_t* const free_k = lds_k[j & 3];
+      uint8_t* const free_v = lds_v[(j + 3) & 3];
+      settle(free_k, kr, false, 0);
+      settle(free_v, vr, true, FP8 && (j + 3 < held_from || j + 3 >= held_to) ? held_keys(j + 3) : kAll);
       __builtin_amdgcn_s_setprio(1);
-      products(lds_k[next], lds_v[slot], [&](int step) {
-        if (step < NL) bring(k_base, key_at, step, lds_k[slot], k_voff, kr);
-        else if (step < 2 * NL) bring(v_base, value_at, step - NL, lds_v[then], v_voff, vr);
+      products(lds_k[(j + 1) & 3], lds_v[j & 3], [&](int step) {
+        if (step < NL) bring(k_base, key_at, step, free_k, k_voff, kr);
+        else if (step < 2 * NL) bring(v_base, value_at, step - NL, free_v, v_voff, vr);
       });
       __builtin_amdgcn_s_setprio(0);
-      value_at = key_at;
-      if constexpr (!FP8) {                  // all but what this phase asked for has arrived: tile j + 1's values
+      if constexpr (!FP8) {                  // all but what this phase asked for has arrived: tile j + 2's values
         wait_arrived<2 * NL>();
-        clear_values(lds_v[next], held_next);
+        if (j + 2 < held_from || j + 2 >= held_to) clear_values(lds_v[(j + 2) & 3], held_keys(j + 2));
       }
-      phase_barrier();
-      held_now = held_next;
-      held_next = held_then;
-      held_then = held_keys(j + 3);
-      if (j + 1 < n) softmax_step(j + 1, held_now);
-      phase_barrier();
-      const int t = slot;
-      slot = next;
-      next = then;
-      then = t;
+      phase_barrier<true>();
+      if (j + 1 < n) softmax_step(j + 1);
+      if (((j + 1 + kLead) & 63) == 0) locate(j + 1 + kLead);
+      value_at = key_at;
+      key_at = offsets_of(j + 1 + kLead);
+#pragma unroll
+      for (int t = 0; t < kAhead; ++t) read_operands(lds_k[(j + 2) & 3], lds_v[(j + 1) & 3], t);
+      phase_barrier<false>();
     }
-    if (wave < kChunkWaves / 2) phase_barrier();
+    if (wave < kChunkWaves / 2) phase_barrier<false>();
     wait_arrived<0>();                       // nothing may still be on its way into LDS when the workgroup ends
   }
 

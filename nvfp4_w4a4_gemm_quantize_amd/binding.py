@@ -455,41 +455,54 @@ LOGITS_F32, LOGITS_BF16 = 0, 1
 
 PagedPlan = collections.namedtuple("PagedPlan", "q_start seq_lens positions slots counts")
 
+# A step of the serving loop makes these calls for every layer, and its smallest ones take the GPU a few microseconds:
+# the checks below read each tensor once, and addresses go to ctypes as plain integers.
+_Tensor, _i32, _i64t, _f32, _bf16, _u8 = torch.Tensor, torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
+_e4m3 = torch.float8_e4m3fn
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _refuse(t, dtype, name, shape):
+    _dev(t, dtype, name)
+    raise NVFP4Error("%s must be %s, got %s with strides %s" % (name, shape, tuple(t.shape), t.stride()))
+
 
 def _vec(t, dtype, n, name):
-    """A contiguous GPU vector (or matrix) of n elements."""
-    _dev(t, dtype, name)
-    if t.numel() != n or not t.is_contiguous():
-        raise NVFP4Error("%s must be contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
-    return t
+    """The address of a contiguous GPU tensor of n elements."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _refuse(t, dtype, name, "contiguous with %d elements" % n)
+    return t.data_ptr()
 
 
-def _rows(t, dtype, name, rows=None, cols=None):
-    """Row stride of a 2-D view with unit column stride."""
-    _dev(t, dtype, name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise NVFP4Error("%s must be a 2-D view with unit column stride" % name)
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise NVFP4Error("%s must be [%s, %s], got %s" % (name, rows, cols, tuple(t.shape)))
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, dtype, rows, cols, name):
+    """(address, row stride, columns) of a 2-D GPU view with unit column stride; rows and cols None: any."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != 2:
+        _refuse(t, dtype, name, "a 2-D view")
+    r, c = t.shape
+    ld, unit = t.stride()
+    if (unit != 1 and c > 1) or (rows is not None and r != rows) or (cols is not None and c != cols):
+        _refuse(t, dtype, name, "[%s, %s] with unit column stride" % (rows, cols))
+    return t.data_ptr(), (ld if r > 1 else c), c    # a size-1 dimension's stride is arbitrary
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale):
-    """(cache_dtype, pages, page size, heads, head dim, strides) of a pair of [pages, heads, page size, head dim] views."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    """The C arguments that describe a pair of [pages, heads, page size, head dim] views, and (heads, head dim)."""
+    kind = k_cache.dtype if isinstance(k_cache, _Tensor) else None
+    if kind is not _bf16 and kind is not _e4m3:
         raise NVFP4Error("k_cache must be a bfloat16 or float8_e4m3fn tensor")
-    _dev(k_cache, k_cache.dtype, "k_cache")
-    _dev(v_cache, k_cache.dtype, "v_cache")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
-        raise NVFP4Error("k_cache and v_cache must be [pages, heads, page size, head dim] views of one shape and strides, "
-                         "with unit last stride")
+    if not isinstance(v_cache, _Tensor) or not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype is not kind:
+        raise NVFP4Error("k_cache and v_cache must be GPU tensors of one type")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise NVFP4Error("k_cache and v_cache must be [pages, heads, page size, head dim] views of one shape and strides")
     pages, heads, page_size, dim = k_cache.shape
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None:
-            _vec(t, torch.float32, heads, name)
-    ps, hs, ts, _ = k_cache.stride()                # a size-1 dimension's stride is arbitrary
-    return (CACHE_BF16 if k_cache.dtype == torch.bfloat16 else CACHE_E4M3, pages, page_size, heads, dim,
-            ps if pages > 1 else 0, hs if heads > 1 else 0, ts)
+    ps, hs, ts, unit = k_cache.stride()
+    if unit != 1:
+        raise NVFP4Error("the caches need a unit last stride")
+    ks = None if k_scale is None else _vec(k_scale, _f32, heads, "k_scale")
+    vs = None if v_scale is None else _vec(v_scale, _f32, heads, "v_scale")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), CACHE_BF16 if kind is _bf16 else CACHE_E4M3, pages, page_size, heads,
+            dim, ps if pages > 1 else 0, hs if heads > 1 else 0, ts), ks, vs, heads, dim
 
 
 def paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens, free_cursor=None, plan=None):
@@ -500,28 +513,24 @@ def paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size, max_token
     positions int32 [max_tokens], slots int64 [max_tokens], counts int32 [4]: new tokens, pages taken, pages missing,
     cursor after the step); ``plan`` reuses the tensors of an earlier one.
     """
-    lib = load()
-    _dev(ctx_lens, torch.int32, "ctx_lens")
-    R = ctx_lens.numel()
-    _vec(ctx_lens, torch.int32, R, "ctx_lens")
-    _vec(new_lens, torch.int32, R, "new_lens")
-    _vec(free_pages, torch.int32, free_pages.numel(), "free_pages")
-    ld = _rows(block_table, torch.int32, "block_table", rows=R)
-    if free_cursor is not None:
-        _vec(free_cursor, torch.int32, 1, "free_cursor")
+    lib = _lib or load()
+    if not isinstance(ctx_lens, _Tensor) or not isinstance(free_pages, _Tensor):
+        raise NVFP4Error("ctx_lens and free_pages must be GPU tensors")
+    R, F = ctx_lens.numel(), free_pages.numel()
+    ctx, new, free = _vec(ctx_lens, _i32, R, "ctx_lens"), _vec(new_lens, _i32, R, "new_lens"), _vec(free_pages, _i32, F, "free_pages")
+    table, ld, cols = _rows(block_table, _i32, R, None, "block_table")
+    cursor = None if free_cursor is None else _vec(free_cursor, _i32, 1, "free_cursor")
+    if max_tokens < 0:
+        raise NVFP4Error("max_tokens must not be negative")
     if plan is None:
-        i32 = torch.empty(2 * R + 5 + max_tokens, dtype=torch.int32, device=ctx_lens.device)
-        plan = PagedPlan(i32[:R + 1], i32[R + 1:2 * R + 1], i32[2 * R + 1:2 * R + 1 + max_tokens],
-                         torch.empty(max_tokens, dtype=torch.int64, device=ctx_lens.device), i32[2 * R + 1 + max_tokens:])
-    for name, n, dtype in (("q_start", R + 1, torch.int32), ("seq_lens", R, torch.int32),
-                           ("positions", max_tokens, torch.int32), ("slots", max_tokens, torch.int64),
-                           ("counts", 4, torch.int32)):
-        _vec(getattr(plan, name), dtype, n, name)
-    rc = lib.paged_plan(_ptr(ctx_lens), _ptr(new_lens), R, page_size, _ptr(free_pages), free_pages.numel(),
-                        _ptr(free_cursor), _ptr(block_table), block_table.shape[1], ld, _ptr(plan.q_start),
-                        _ptr(plan.seq_lens), _ptr(plan.positions), _ptr(plan.slots), max_tokens, _ptr(plan.counts),
-                        _stream())
-    _check(rc, "paged_plan")
+        q_start, seq_lens, positions, counts = ctx_lens.new_empty(2 * R + 5 + max_tokens).split((R + 1, R, max_tokens, 4))
+        plan = PagedPlan(q_start, seq_lens, positions, ctx_lens.new_empty(max_tokens, dtype=_i64t), counts)
+    rc = lib.paged_plan(ctx, new, R, page_size, free, F, cursor, table, cols, ld, _vec(plan.q_start, _i32, R + 1, "q_start"),
+                        _vec(plan.seq_lens, _i32, R, "seq_lens"), _vec(plan.positions, _i32, max_tokens, "positions"),
+                        _vec(plan.slots, _i64t, max_tokens, "slots"), max_tokens, _vec(plan.counts, _i32, 4, "counts"),
+                        _raw_stream(ctx_lens.get_device()))
+    if rc:
+        _check(rc, "paged_plan")
     return plan
 
 
@@ -530,24 +539,23 @@ def paged_kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
 
     k_cache, v_cache: [pages, heads, page size, head dim] views, bfloat16 or float8_e4m3fn (then x / scale[head],
     rounded to nearest even and clamped to +-448, is stored)."""
-    lib = load()
-    kind, pages, page_size, heads, dim, ps, hs, ts = _cache(k_cache, v_cache, k_scale, v_scale)
-    ld_k, ld_v = (_rows(x, torch.bfloat16, n, cols=heads * dim) for x, n in ((k, "k"), (v, "v")))
+    lib = _lib or load()
+    (kc, vc, kind, pages, page_size, heads, dim, ps, hs, ts), ks, vs, _, _ = _cache(k_cache, v_cache, k_scale, v_scale)
+    kp, ld_k, _ = _rows(k, _bf16, None, heads * dim, "k")
     T = k.shape[0]
-    if v.shape[0] != T:
-        raise NVFP4Error("k and v must have the same number of rows")
-    _vec(slots, torch.int64, T, "slots")
-    rc = lib.paged_kv_write(_ptr(k), ld_k, _ptr(v), ld_v, _ptr(slots), T, _ptr(k_cache), _ptr(v_cache), kind, pages,
-                            page_size, heads, dim, ps, hs, ts, _ptr(k_scale), _ptr(v_scale), _stream())
-    _check(rc, "paged_kv_write")
+    vp, ld_v, _ = _rows(v, _bf16, T, heads * dim, "v")
+    rc = lib.paged_kv_write(kp, ld_k, vp, ld_v, _vec(slots, _i64t, T, "slots"), T, kc, vc, kind, pages, page_size, heads, dim,
+                            ps, hs, ts, ks, vs, _raw_stream(k.get_device()))
+    if rc:
+        _check(rc, "paged_kv_write")
 
 
 def paged_attention_workspace(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new, max_seq, device="cuda"):
-    """A workspace for paged_attention calls of up to these sizes."""
+    """A workspace for paged_attention calls of these sizes."""
     n = load().paged_attention_workspace_bytes(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new, max_seq)
     if n == 0:
         raise NVFP4Error("paged_attention does not take these sizes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=_u8, device=device)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new, max_seq, scale=None, window=0,
@@ -558,32 +566,35 @@ def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new
     q: bf16 [T, num_heads * head_dim] view, rows of request r from q_start[r] to q_start[r + 1]; caches as in
     paged_kv_write; block_table int32 [R, max_pages]; max_new and max_seq bound the requests' new tokens and lengths.
     Returns out [T, num_heads * head_dim] (and lse fp32 [T, num_heads] with return_lse)."""
-    lib = load()
-    kind, pages, page_size, heads, dim, ps, hs, ts = _cache(k_cache, v_cache, k_scale, v_scale)
-    ld_q = _rows(q, torch.bfloat16, "q")
-    T, cols = q.shape
-    if cols == 0 or cols % dim or (cols // dim) % heads:
-        raise NVFP4Error("q must be [T, num_heads * %d] with num_heads a multiple of %d" % (dim, heads))
+    lib = _lib or load()
+    cache, ks, vs, heads, dim = _cache(k_cache, v_cache, k_scale, v_scale)
+    qp, ld_q, cols = _rows(q, _bf16, None, None, "q")
+    T = q.shape[0]
     num_heads = cols // dim
-    _dev(seq_lens, torch.int32, "seq_lens")
+    if cols == 0 or cols % dim or num_heads % heads:
+        raise NVFP4Error("q must be [T, num_heads * %d] with num_heads a multiple of %d" % (dim, heads))
+    if not isinstance(seq_lens, _Tensor):
+        raise NVFP4Error("seq_lens must be a GPU tensor")
     R = seq_lens.numel()
-    _vec(seq_lens, torch.int32, R, "seq_lens")
-    _vec(q_start, torch.int32, R + 1, "q_start")
-    ld_t = _rows(block_table, torch.int32, "block_table", rows=R)
-    out, od = _out(out, T, cols, out_dtype, q.device)
-    if lse is not None:
-        _vec(lse, torch.float32, T * num_heads, "lse")
-    elif return_lse:
-        lse = torch.empty((T, num_heads), dtype=torch.float32, device=q.device)
+    table, ld_t, max_pages = _rows(block_table, _i32, R, None, "block_table")
+    if out is None:
+        out = q.new_empty((T, cols), dtype=_bf16 if out_dtype in (OUT_BF16, _bf16) else _f32)
+        op, ld_o = out.data_ptr(), cols
+    else:
+        op, ld_o, _ = _rows(out, _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32, T, cols, "out")
+    if lse is None and return_lse:
+        lse = q.new_empty((T, num_heads), dtype=_f32)
     if workspace is None:
         workspace = paged_attention_workspace(T, R, num_heads, heads, dim, max_new, max_seq, q.device)
-    _dev(workspace, torch.uint8, "workspace")
-    rc = lib.paged_attention(_ptr(q), ld_q, T, _ptr(q_start), _ptr(seq_lens), R, max_new, max_seq, num_heads,
-                             _ptr(k_cache), _ptr(v_cache), kind, pages, page_size, heads, dim, ps, hs, ts,
-                             _ptr(block_table), block_table.shape[1], ld_t, dim ** -0.5 if scale is None else scale,
-                             window, _ptr(k_scale), _ptr(v_scale), _ptr(out), od, _ld(out), _ptr(lse), _ptr(workspace),
-                             workspace.numel(), _stream())
-    _check(rc, "paged_attention")
+    bytes_ = workspace.numel()
+    rc = lib.paged_attention(qp, ld_q, T, _vec(q_start, _i32, R + 1, "q_start"), _vec(seq_lens, _i32, R, "seq_lens"), R,
+                             max_new, max_seq, num_heads, *cache, table, max_pages, ld_t,
+                             dim ** -0.5 if scale is None else scale, window, ks, vs, op,
+                             OUT_BF16 if out.dtype is _bf16 else OUT_F32, ld_o,
+                             None if lse is None else _vec(lse, _f32, T * num_heads, "lse"),
+                             _vec(workspace, _u8, bytes_, "workspace"), bytes_, _raw_stream(q.get_device()))
+    if rc:
+        _check(rc, "paged_attention")
     return (out, lse) if return_lse else out
 
 
@@ -592,7 +603,7 @@ def verify_drafts_workspace(num_requests, max_drafts, vocab, device="cuda"):
     n = load().verify_drafts_workspace_bytes(num_requests, max_drafts, vocab)
     if n == 0:
         raise NVFP4Error("verify_drafts does not take these sizes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=_u8, device=device)
 
 
 def verify_drafts(logits, row_start, num_drafts, draft_tokens, uniform, noise, draft_probs=None, temperature=None,
@@ -603,38 +614,35 @@ def verify_drafts(logits, row_start, num_drafts, draft_tokens, uniform, noise, d
     row_start, num_drafts int32 [R]; draft_tokens int32 [R, K]; uniform fp32 [R, K]; noise fp32 [R, V] (standard
     exponential); draft_probs fp32 [R, K, V] or None; temperature fp32 [R] or None (0: greedy).
     Returns (tokens int32 [R, K + 1], accepted int32 [R], logprobs fp32 [R, K + 1])."""
-    lib = load()
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
+    lib = _lib or load()
+    kind = logits.dtype if isinstance(logits, _Tensor) else None
+    if kind is not _bf16 and kind is not _f32:
         raise NVFP4Error("logits must be a bfloat16 or float32 tensor")
-    ld = _rows(logits, logits.dtype, "logits")
-    N, V = logits.shape
-    _dev(draft_tokens, torch.int32, "draft_tokens")
-    if draft_tokens.dim() != 2:
+    lp, ld, V = _rows(logits, kind, None, None, "logits")
+    if not isinstance(draft_tokens, _Tensor) or draft_tokens.dim() != 2:
         raise NVFP4Error("draft_tokens must be [requests, max drafts]")
     R, K = draft_tokens.shape
-    _vec(draft_tokens, torch.int32, R * K, "draft_tokens")
-    _vec(row_start, torch.int32, R, "row_start")
-    _vec(num_drafts, torch.int32, R, "num_drafts")
-    _vec(uniform, torch.float32, R * K, "uniform")
-    ld_noise = _rows(noise, torch.float32, "noise", rows=R, cols=V)
-    ld_probs = V
+    np_, ld_noise, _ = _rows(noise, _f32, R, V, "noise")
+    probs, ld_probs = None, V
     if draft_probs is not None:
-        _dev(draft_probs, torch.float32, "draft_probs")
-        if draft_probs.shape != (R, K, V) or (V > 1 and draft_probs.stride(2) != 1) or \
-                (R > 1 and K > 0 and draft_probs.stride(0) != K * draft_probs.stride(1)):
+        _dev(draft_probs, _f32, "draft_probs")
+        sr, sk, sv = draft_probs.stride() if draft_probs.dim() == 3 else (0, 0, 0)
+        if draft_probs.shape != (R, K, V) or (V > 1 and sv != 1) or (R > 1 and K > 1 and sr != K * sk):
             raise NVFP4Error("draft_probs must be [requests, max drafts, vocab] with evenly spaced rows")
-        ld_probs = draft_probs.stride(1) if K > 1 else (draft_probs.stride(0) if R > 1 and K == 1 else V)
-    if temperature is not None:
-        _vec(temperature, torch.float32, R, "temperature")
+        probs, ld_probs = draft_probs.data_ptr(), sk if K > 1 else sr if R > 1 else V
     if workspace is None:
         workspace = verify_drafts_workspace(R, K, V, logits.device)
-    _dev(workspace, torch.uint8, "workspace")
-    both = torch.empty((2, R, K + 1), dtype=torch.int32, device=logits.device)
-    tokens, logprobs = both[0], both[1].view(torch.float32)
-    accepted = torch.empty(R, dtype=torch.int32, device=logits.device)
-    rc = lib.verify_drafts(_ptr(logits), LOGITS_F32 if logits.dtype == torch.float32 else LOGITS_BF16, ld, N, V,
-                           _ptr(row_start), _ptr(num_drafts), R, K, _ptr(draft_tokens), _ptr(draft_probs), ld_probs,
-                           _ptr(temperature), _ptr(uniform), _ptr(noise), ld_noise, _ptr(tokens), _ptr(accepted),
-                           _ptr(logprobs), _ptr(workspace), workspace.numel(), _stream())
-    _check(rc, "verify_drafts")
+    bytes_ = workspace.numel()
+    tokens = draft_tokens.new_empty((R, K + 1))
+    accepted = draft_tokens.new_empty(R)
+    logprobs = noise.new_empty((R, K + 1))
+    rc = lib.verify_drafts(lp, LOGITS_F32 if kind is _f32 else LOGITS_BF16, ld, logits.shape[0], V,
+                           _vec(row_start, _i32, R, "row_start"), _vec(num_drafts, _i32, R, "num_drafts"), R, K,
+                           _vec(draft_tokens, _i32, R * K, "draft_tokens"), probs, ld_probs,
+                           None if temperature is None else _vec(temperature, _f32, R, "temperature"),
+                           _vec(uniform, _f32, R * K, "uniform"), np_, ld_noise, tokens.data_ptr(), accepted.data_ptr(),
+                           logprobs.data_ptr(), _vec(workspace, _u8, bytes_, "workspace"), bytes_,
+                           _raw_stream(logits.get_device()))
+    if rc:
+        _check(rc, "verify_drafts")
     return tokens, accepted, logprobs

@@ -27,6 +27,13 @@ constexpr int kDecodeWaves = 4, kDecodeGrid = 512, kDecodeTile = 32;
 // Rows and waves of a workgroup of the tiled kernel.
 constexpr int kChunkRows = 256, kChunkWaves = 8;
 
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

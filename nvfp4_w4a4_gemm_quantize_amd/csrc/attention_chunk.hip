@@ -40,12 +40,6 @@ __device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(uintptr_t)p));
 }
 
-// A value that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // Global -> LDS copy of 16 bytes a lane: lane l's bytes land at dst + 16 l, read
 // from base + voff (a uniform base and 32-bit lane offsets).  In inline asm, so
 // that the compiler adds no waits of its own before later LDS reads; arrival is

@@ -30,6 +30,8 @@
 // output; a part leaves (max, sum, O) in the workspace (at most two a
 // workgroup) and a second kernel joins the parts in the order of their keys.
 // The line's prefix is recomputed by every workgroup (8 bytes a request).
+#include <float.h>
+
 #include "attention.h"
 
 namespace nvfp4 {
@@ -146,7 +148,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   }
 
   const int64_t x_begin = blockIdx.x * per, x_end = min(x_begin + per, total);
-  const int64_t page_mask = ((int64_t)1 << a.cache.page_shift) - 1;
+  const int page_mask = (1 << a.cache.page_shift) - 1;
+  const uint32_t page_units = (uint32_t)(a.cache.page_stride * EB / 16), row_bytes = (uint32_t)a.cache.token_stride * EB;
+  const uint32_t k_lane = (uint32_t)c16 * row_bytes + g * 16;
+  uint32_t v_lane[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v_lane[j] = (uint32_t)(4 * g + j) * row_bytes + c16 * DV * EB;
   int row_token[NF], row_head[NF];
 #pragma unroll
   for (int n = 0; n < NF; ++n) {
@@ -166,30 +173,39 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       base += it.tiles;
       it = decode_item(a, ++r);
     }
+    r = uniform(r);
     const int64_t in_request = x - base * hkv;
-    const int head = (int)(in_request / it.tiles);
-    const int64_t first = in_request - head * it.tiles;
+    const int head = uniform((int)(in_request / it.tiles));
+    const int64_t first = uniform(in_request - head * it.tiles);
     const int64_t last = min(first + (x_end - x), it.tiles);   // tiles [first, last) of this head
     const bool whole = first == 0 && last == it.tiles;
     const int part = x == x_begin ? 0 : 1;
     x += last - first;
 
     const int nrows = (int)it.l.tokens * group;
+    const int n = uniform((int)(last - first));
+    // positions relative to the first key of the part
+    const int origin = uniform((int)(it.begin + first * kDecodeTile));
+    auto rel = [&](int64_t at) { return (int)min(max(at - origin, (int64_t)INT32_MIN / 2), (int64_t)INT32_MAX / 2); };
     const int64_t pos0 = token_pos(a, r, it.l, 0), pos_last = pos0 + it.l.tokens - 1;
-    const int64_t keys = min(it.l.keys, pos_last + 1);
-    const int64_t low = a.window ? max(pos0 - a.window + 1, (int64_t)0) : 0;   // first key that a row may see
+    const int keys = uniform(rel(min(it.l.keys, pos_last + 1)));
+    const int low = uniform(a.window ? rel(max(pos0 - a.window + 1, (int64_t)0)) : INT32_MIN / 2);   // first key that a row may see
+    // tiles [seen_from, seen_to) are seen in full by every row
+    const int seen_from = uniform(a.window ? (max(rel(pos_last - a.window + 1), 0) + kDecodeTile - 1) / kDecodeTile : 0);
+    const int seen_to = uniform(min(keys, max(rel(pos0) + 1, 0)) / kDecodeTile);
     float c = a.scale * kLog2e;
     if (a.cache.k_scale) c *= a.cache.k_scale[head];
     const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
-    c = fabsf(c);
+    c = fmaxf(fabsf(c), FLT_MIN);   // never 0: a hidden score's -inf stays one
 
     // Q, the B operand: column c16 = row of q, k = 8 columns of q
     bf16x8 q[NF][KS];
-    int64_t row_pos[NF];
+    int row_pos[NF], row_low[NF];
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
       const bool live = n * 16 + c16 < nrows;
-      row_pos[n] = live ? pos0 + row_token[n] : -1;
+      row_pos[n] = live ? rel(pos0 + row_token[n]) : INT32_MIN / 2;
+      row_low[n] = live && a.window ? rel(pos0 + row_token[n] - a.window + 1) : INT32_MIN / 2;
       const uint16_t* qr = a.q + (it.l.start + (live ? row_token[n] : 0)) * a.ld_q + (head * group + (live ? row_head[n] : 0)) * D;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
@@ -212,46 +228,43 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       for (int i = 0; i < DV; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
+    // Byte offsets of the two 16-key groups of this wave's tiles, 64 tiles at a
+    // time, a tile a lane: tile k of the wave is tile wave + 4 k of the part.
+    // Without a page any page serves: its scores are hidden and its values cleared.
     const int32_t* table = a.block_table + r * a.ld_table;
-    const int64_t head_off = head * a.cache.head_stride;
-    const uint32_t ts = (uint32_t)a.cache.token_stride;
-    const uint32_t k_lane = ((uint32_t)c16 * ts + g * (FP8 ? 16 : 8)) * EB, v_lane = (4 * g * ts + c16 * DV) * EB;
-
-    // The page of 16 keys from key0 (they never cross one); -1: none.
-    auto page_of = [&](int64_t key0) {
-      int32_t p = -1;
-      if (key0 < keys) p = table[key0 >> a.cache.page_shift];
-      return p >= 0 && p < a.cache.num_pages ? p : -1;
-    };
-    struct Pages {
-      int32_t p[2];
-    };
-    auto pages_of = [&](int64_t t) {
-      Pages pg;
-      const int64_t key0 = it.begin + t * kDecodeTile;
-      pg.p[0] = __builtin_amdgcn_readfirstlane(page_of(key0));
-      pg.p[1] = __builtin_amdgcn_readfirstlane(page_of(key0 + 16));
-      return pg;
-    };
-    // element offset of 16 keys; without a page any page serves: its scores are hidden and its values cleared
-    auto place = [&](int64_t t, int f, const Pages& pg) {
-      const int64_t key0 = it.begin + t * kDecodeTile + 16 * f;
-      return max(pg.p[f], 0) * a.cache.page_stride + head_off + (key0 & page_mask) * a.cache.token_stride;
-    };
-    auto load_keys = [&](Tile& tile, int64_t t, const Pages& pg) {
+    const uint32_t num_pages = (uint32_t)a.cache.num_pages;
+    int64_t lane_at[2];
+    uint64_t without[2];            // a bit for each of these tiles whose group has no page
+    auto locate = [&](int k0) {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const uint8_t* kp = (const uint8_t*)a.cache.k + place(t, f, pg) * EB;
-#pragma unroll
-        for (int s = 0; s < Tile::KW; ++s) tile.k[f][s] = *(const u32x4*)(kp + k_lane + s * 64);
+        const int key = (wave + (k0 + lane) * kDecodeWaves) * kDecodeTile + 16 * f;
+        const uint32_t page = key < keys ? (uint32_t)table[(uint32_t)(origin + key) >> a.cache.page_shift] : num_pages;
+        without[f] = __ballot(page >= num_pages);
+        lane_at[f] = (int64_t)((uint64_t)(page < num_pages ? page : 0) * page_units << 4) +
+                     (uint32_t)((origin + key) & page_mask) * row_bytes;
       }
     };
-    auto load_values = [&](Tile& tile, int64_t t, const Pages& pg) {
+    auto group_at = [&](int k, int f) {
+      const uint32_t lo = __builtin_amdgcn_readlane((int)lane_at[f], k & 63), hi = __builtin_amdgcn_readlane((int)(lane_at[f] >> 32), k & 63);
+      return (int64_t)((uint64_t)hi << 32 | lo);
+    };
+    const uint8_t* k_base = (const uint8_t*)a.cache.k + head * a.cache.head_stride * EB;
+    const uint8_t* v_base = (const uint8_t*)a.cache.v + head * a.cache.head_stride * EB;
+    auto load_keys = [&](Tile& tile, int k) {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const uint8_t* vp = (const uint8_t*)a.cache.v + place(t, f, pg) * EB;
+        const uint8_t* kp = k_base + group_at(k, f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_words<Tile::VW>(tile.v[4 * f + j], vp + v_lane + j * ts * EB);
+        for (int st = 0; st < Tile::KW; ++st) tile.k[f][st] = *(const u32x4*)(kp + k_lane + st * 64);
+      }
+    };
+    auto load_values = [&](Tile& tile, int k) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint8_t* vp = v_base + group_at(k, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words<Tile::VW>(tile.v[4 * f + j], vp + v_lane[j]);
       }
     };
     auto scores = [&](Tile& tile, f32x4 (&s)[NF][2]) {
@@ -279,25 +292,23 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       }
     };
     // softmax step and second product
-    auto values = [&](Tile& tile, f32x4 (&s)[NF][2], int64_t t, const Pages& pg) {
-      const int64_t key0 = it.begin + t * kDecodeTile;
-      // a tile that every row sees in full needs no masks
-      const bool full = pg.p[0] >= 0 && pg.p[1] >= 0 && key0 + kDecodeTile - 1 <= pos0 && key0 + kDecodeTile <= keys &&
-                        (a.window == 0 || key0 > pos_last - a.window);
-      if (!full) {
+    auto values = [&](Tile& tile, f32x4 (&s)[NF][2], int k, bool gap0, bool gap1) {
+      const int at = wave + k * kDecodeWaves;
+      if (gap0 || gap1 || at < seen_from || at >= seen_to) {
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int64_t key = key0 + 16 * f + 4 * g + j;
-            const bool held = pg.p[f] >= 0 && key < keys && key >= low;
+            const int key = at * kDecodeTile + 16 * f + 4 * g + j;
+            const bool held = !(f ? gap1 : gap0) & (key < keys) & (key >= low);
 #pragma unroll
-            for (int n = 0; n < NF; ++n)
-              if (!held || key > row_pos[n] || (a.window && key <= row_pos[n] - a.window)) s[n][f][j] = -INFINITY;
+            for (int n = 0; n < NF; ++n) {
+              const bool seen = held & (key <= row_pos[n]) & (key >= row_low[n]);
+              s[n][f][j] = seen ? s[n][f][j] : -INFINITY;
+            }
             // what lies in unwritten or foreign places may be NaN, and 0 * NaN is not 0
-            if (!held)
 #pragma unroll
-              for (int w = 0; w < Tile::VW; ++w) tile.v[4 * f + j][w] = 0u;
+            for (int w = 0; w < Tile::VW; ++w) tile.v[4 * f + j][w] = held ? tile.v[4 * f + j][w] : 0u;
           }
       }
       bf16x8 p[NF];
@@ -305,7 +316,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       for (int n = 0; n < NF; ++n) {
         float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
                           fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-        if (__any(top > m[n])) {   // rare after the first tiles: a new maximum somewhere
+        // The maximum may lag behind by a factor of 2^8, which costs no precision: O
+        // is scaled anew only when it does not suffice any more.
+        if (__any(c * (top - m[n]) > 8.f || (m[n] == -INFINITY && top > m[n]))) {
           top = fmaxf(top, __shfl_xor(top, 16));
           top = fmaxf(top, __shfl_xor(top, 32));
           const float to = fmaxf(m[n], top);
@@ -321,10 +334,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
         for (int f = 0; f < 2; ++f) {
           float e[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            e[j] = exp2_fast(fmaf(s[n][f][j], c, -ref));
-            if (!full && s[n][f][j] == -INFINITY) e[j] = 0.f;
-          }
+          for (int j = 0; j < 4; ++j) e[j] = exp2_fast(fmaf(s[n][f][j], c, -ref));
           l[n] += (e[0] + e[1]) + (e[2] + e[3]);
           // P in bf16, the matrix instruction's type with V: 2^-8 relative a term at most, averaged over the keys
           w[2 * f] = pack_bf16(e[0], e[1]);
@@ -366,27 +376,25 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       }
     };
 
-    // wave w takes tiles first + w, + 4, ...; a tile's keys are loaded once the
-    // tile before has given its scores, its values once the products with the
-    // values before are done, its page numbers two tiles ahead
+    // a tile's keys are loaded once the tile before has given its scores, its
+    // values once the products with the values before are done
     Tile tile;
-    int64_t t = first + wave;
-    if (t < last) {
-      Pages now = pages_of(t), next = pages_of(t + kDecodeWaves);
-      load_keys(tile, t, now);
-      load_values(tile, t, now);
-      while (true) {
-        const bool more = t + kDecodeWaves < last;
-        const Pages after = pages_of(t + 2 * kDecodeWaves);
+    const int mine = (n - wave + kDecodeWaves - 1) / kDecodeWaves;   // tiles of this wave
+    if (mine > 0) {
+      locate(0);
+      load_keys(tile, 0);
+      load_values(tile, 0);
+      for (int k = 0; k < mine; ++k) {
+        const bool gap0 = without[0] >> (k & 63) & 1, gap1 = without[1] >> (k & 63) & 1;
         f32x4 s[NF][2];
         scores(tile, s);
-        if (more) load_keys(tile, t + kDecodeWaves, next);
-        values(tile, s, t, now);
-        if (!more) break;
-        load_values(tile, t + kDecodeWaves, next);
-        t += kDecodeWaves;
-        now = next;
-        next = after;
+        const bool more = k + 1 < mine;
+        if (more) {
+          if (((k + 1) & 63) == 0) locate(k + 1);
+          load_keys(tile, k + 1);
+        }
+        values(tile, s, k, gap0, gap1);
+        if (more) load_values(tile, k + 1);
       }
     }
 
@@ -441,7 +449,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
 }
 
 // Joins the parts of a (request, head) that several workgroups of the
-// streaming kernel hold, in the order of their keys.
+// streaming kernel hold, in the order of their keys; four columns a thread.
 template <int D>
 __global__ __launch_bounds__(256) void attention_decode_join_kernel(AttentionArgs a) {
   const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
@@ -455,7 +463,9 @@ __global__ __launch_bounds__(256) void attention_decode_join_kernel(AttentionArg
   const RequestLens l = request_lens(a, r);
   const int nrows = (int)l.tokens * group;
   const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
-  for (int e = threadIdx.x; e < nrows * (D / 4); e += 256) {
+  {
+    const int e = blockIdx.y * 256 + threadIdx.x;
+    if (e >= nrows * (D / 4)) return;
     const int at = e / (D / 4), d = (e % (D / 4)) * 4;
     // workgroup g's part is its first unless the item starts inside g's share
     auto slot_of = [&](int64_t wg) { return (wg * 2 + (x0 > wg * per ? 1 : 0)) * kDecodeRows + at; };
@@ -493,13 +503,14 @@ template <int D, bool FP8>
 hipError_t launch(const AttentionArgs& a, hipStream_t st) {
   // rows a request may have here: one fragment of 16 or two
   const int64_t rows = min(a.max_new, (int64_t)(kDecodeRows / a.group)) * a.group;
+  const unsigned grid = D <= 128 ? kDecodeGrid : kDecodeGrid / 2;   // as many workgroups as the registers let be resident
   if (rows <= 16)
-    attention_decode_kernel<D, FP8, 1><<<kDecodeGrid, kThreads, 0, st>>>(a);
+    attention_decode_kernel<D, FP8, 1><<<grid, kThreads, 0, st>>>(a);
   else
-    attention_decode_kernel<D, FP8, 2><<<kDecodeGrid, kThreads, 0, st>>>(a);
+    attention_decode_kernel<D, FP8, 2><<<grid, kThreads, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attention_decode_join_kernel<D><<<(unsigned)(a.requests * a.cache.heads), 256, 0, st>>>(a);
+  attention_decode_join_kernel<D><<<dim3((unsigned)(a.requests * a.cache.heads), (unsigned)((rows * (D / 4) + 255) / 256)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -14,8 +14,15 @@
 // its argument and its sum of exponentials (verify_rows_kernel), then one row a
 // request again, with the draft row and the noise (verify_draw_kernel), then
 // the parts are joined (verify_join_kernel).  A row is cut into slices so
-// that a single request still fills the chip; the parts' order is fixed.
+// that a single request still fills the chip; the parts' order is fixed.  A
+// thread takes 32 logits at a time: their loads are in flight together, and the
+// running maximum and sum are touched once for all of them.  Exponentials are
+// 2^((x - top) k), k = log2 e / T (not x k - top k: logits may be the type's
+// lowest value, whose product overflows); scores use the hardware reciprocal of the noise (1 ulp): a word
+// is only misjudged against one whose score is the same to 2^-22.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "serving.h"
 
@@ -24,10 +31,13 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kSlice = 8192;      // elements of a slice at least: 32 a thread
+constexpr int kBatch = 4;              // vectors of 8 logits that a thread has in flight
+constexpr int64_t kSlice = 8192;      // elements of a slice at least: one batch a thread
+constexpr int kMaxSlices = 64;        // one a lane of the joins
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct RowPart {
-  float top, sum;      // largest x (x = logit / T) and sum of exp(x - top)
+  float top, sum;      // largest logit and sum of exp((logit - top) / T)
   int32_t at, pad;     // its lowest index
 };
 struct DrawPart {
@@ -36,7 +46,7 @@ struct DrawPart {
 };
 struct VerifyWorkspace {
   RowPart* rows;       // [requests][max_drafts + 1][slices]
-  DrawPart* draws;     // [requests][slices][2]: from w, and from p in its place
+  DrawPart* draws;     // [requests][slices]
 };
 __host__ __device__ inline VerifyWorkspace verify_workspace(void* ws, int64_t requests, int64_t max_drafts, int slices) {
   VerifyWorkspace w;
@@ -45,10 +55,15 @@ __host__ __device__ inline VerifyWorkspace verify_workspace(void* ws, int64_t re
   return w;
 }
 
-int verify_slices(int64_t vocab) {
-  const int64_t n = (vocab + kSlice - 1) / kSlice;
-  return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+// Slices of a row: of one batch a thread while the rows alone do not give ten
+// workgroups a CU, then fewer and longer ones.
+int verify_slices(int64_t requests, int64_t max_drafts, int64_t vocab) {
+  const int64_t most = (vocab + kSlice - 1) / kSlice, rows = requests * (max_drafts + 1);
+  const int64_t n = min(most, max((2560 + rows - 1) / max(rows, (int64_t)1), (int64_t)1));
+  return (int)min(n, (int64_t)kMaxSlices);
 }
+// Elements of a slice: whole vectors, so that aligned rows stay aligned.
+__device__ __forceinline__ int64_t slice_length(int64_t vocab, int slices) { return ((vocab + slices - 1) / slices + 63) / 64 * 64; }
 
 // Four or eight neighbouring elements; rows may start at any element.
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
@@ -70,10 +85,12 @@ __device__ __forceinline__ float load1(const void* row, int64_t v) {
   return F32 ? ((const float*)row)[v] : __uint_as_float((uint32_t)((const uint16_t*)row)[v] << 16);
 }
 
-// A logit as x = logit / T; NaN counts as -inf.
-__device__ __forceinline__ float scaled(float logit, float t) { return fmaxf(logit, -INFINITY) / t; }
-
-__device__ __forceinline__ float softmax_term(float x, float top) { return top == -INFINITY ? 0.f : __expf(x - top); }
+// NaN counts as -inf.
+__device__ __forceinline__ float clean(float logit) { return fmaxf(logit, -INFINITY); }
+// exp((x - top) / T), k = log2 e / T; 0 if nothing has a probability
+__device__ __forceinline__ float term(float x, float top, float k) {
+  return top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x - top) * k);
+}
 
 struct Best {
   float score;
@@ -120,44 +137,54 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Ver
   const int n = drafts_of(a, r);
   if (i > n) return;
   bool greedy;
-  const float t = temperature_of(a, r, &greedy);
+  const float k = kLog2e / temperature_of(a, r, &greedy);
   const void* row = logits_row<F32>(a, r, i);
-  const int64_t each = (a.vocab + slices - 1) / slices, v0 = slice * each, v1 = min(v0 + each, a.vocab);
+  const int64_t each = slice_length(a.vocab, slices), v0 = min(slice * each, a.vocab), v1 = min(v0 + each, a.vocab);
   float top = -INFINITY, sum = 0.f;
   int32_t at = INT32_MAX;
-  auto take = [&](const float (&x)[8], int64_t v, int count) {
-    float m = x[0];
+  for (int64_t base = v0; base < v1; base += kBatch * kThreads * 8) {
+    float x[kBatch][8];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m = fmaxf(m, x[j]);
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t v = base + (b * kThreads + tid) * 8;
+      if (v + 8 <= v1) {
+        load8<F32>(x[b], row, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[b][j] = v + j < v1 ? load1<F32>(row, v + j) : -INFINITY;
+      }
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, x[b][j]);
     if (m > top) {
-#pragma unroll
-      for (int j = 7; j >= 0; --j)
-        if (x[j] == m) at = (int32_t)(v + j);
-      sum *= top == -INFINITY ? 0.f : __expf(top - m);
+      sum *= term(top, m, k);   // 0 before the first
       top = m;
+#pragma unroll
+      for (int b = kBatch - 1; b >= 0; --b)   // a thread's elements rise with b and j
+#pragma unroll
+        for (int j = 7; j >= 0; --j)
+          if (x[b][j] == m) at = (int32_t)(base + (b * kThreads + tid) * 8 + j);
     }
-    float e = 0.f;
+    if (top > -INFINITY) {
+      float e[kBatch];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e += softmax_term(x[j], top);
-    sum += e;
-  };
-  for (int64_t v = v0 + tid * 8; v < v1; v += kThreads * 8) {
-    float x[8];
-    if (v + 8 <= v1) {
-      load8<F32>(x, row, v);
+      for (int b = 0; b < kBatch; ++b) {
+        e[b] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = scaled(x[j], t);
-    } else {
+        for (int j = 0; j < 8; ++j) e[b] += __builtin_amdgcn_exp2f((clean(x[b][j]) - top) * k);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = v + j < v1 ? scaled(load1<F32>(row, v + j), t) : -INFINITY;
+      for (int b = 0; b < kBatch; ++b) sum += e[b];
     }
-    take(x, v, 8);
   }
   __shared__ RowPart part[kThreads / 64];
   float m = top;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-  sum *= softmax_term(top, m);
+  sum *= term(top, m, k);
   if (top != m) at = INT32_MAX;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
@@ -172,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Ver
     for (int w = 1; w < kThreads / 64; ++w) {
       const RowPart o = part[w];
       const float to = fmaxf(p.top, o.top);
-      p.sum = p.sum * softmax_term(p.top, to) + o.sum * softmax_term(o.top, to);
+      p.sum = p.sum * term(p.top, to, k) + o.sum * term(o.top, to, k);
       p.at = p.top == o.top ? min(p.at, o.at) : p.top == to ? p.at : o.at;
       p.top = to;
     }
@@ -182,47 +209,113 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Ver
 
 namespace {
 
-// A row's slices joined in their order.
-__device__ __forceinline__ RowPart join_row(const RowPart* parts, int slices) {
-  RowPart p = parts[0];
-  for (int s = 1; s < slices; ++s) {
-    const RowPart o = parts[s];
-    const float to = fmaxf(p.top, o.top);
-    p.sum = p.sum * softmax_term(p.top, to) + o.sum * softmax_term(o.top, to);
-    p.at = p.top == o.top ? min(p.at, o.at) : p.top == to ? p.at : o.at;
-    p.top = to;
-  }
-  return p;
-}
-
-// Every row's statistics and the number of drafts kept, by the whole workgroup
-// (thread i: row i).  rows: LDS [256].
+// Every row's statistics (into LDS, [256]) and the number of drafts kept, by the
+// whole workgroup: a wave joins a row's slices, a slice a lane, in a fixed order.
 template <bool F32>
-__device__ int accept(const VerifyArgs& a, const VerifyWorkspace& ws, int64_t r, int n, int slices, float t, bool greedy,
+__device__ int accept(const VerifyArgs& a, const VerifyWorkspace& ws, int64_t r, int n, int slices, float k, bool greedy,
                       RowPart* rows) {
   __shared__ int kept;
-  const int i = threadIdx.x;
-  if (i == 0) kept = n;
-  __syncthreads();
-  if (i <= n) {
-    const RowPart p = join_row(ws.rows + (r * (a.max_drafts + 1) + i) * slices, slices);
-    rows[i] = p;
-    if (i < n) {
-      const int32_t d = a.draft_tokens[r * a.max_drafts + i];
-      bool ok = d >= 0 && d < a.vocab;
-      if (ok && greedy) {
-        ok = d == p.at;
-      } else if (ok) {
-        const float x = scaled(load1<F32>(logits_row<F32>(a, r, i), d), t);
-        const float pd = p.sum > 0.f ? softmax_term(x, p.top) / p.sum : 0.f;
-        const float qd = a.draft_probs ? a.draft_probs[(r * a.max_drafts + i) * a.ld_probs + d] : 1.f;
-        ok = a.uniform[r * a.max_drafts + i] * qd < pd;
-      }
-      if (!ok) atomicMin(&kept, i);   // a minimum: the order does not matter
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (tid == 0) kept = n;
+  for (int i = tid >> 6; i <= n; i += kThreads / 64) {
+    RowPart p = {-INFINITY, 0.f, INT32_MAX, 0};
+    if (lane < slices) p = ws.rows[(r * (a.max_drafts + 1) + i) * slices + lane];
+    float m = p.top;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    p.sum *= term(p.top, m, k);
+    if (p.top != m) p.at = INT32_MAX;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      p.sum += __shfl_xor(p.sum, d);
+      p.at = min(p.at, __shfl_xor(p.at, d));
+    }
+    if (lane == 0) rows[i] = RowPart{m, p.sum, p.at, 0};
+  }
+  // thread i: draft i (its loads do not wait for the joins)
+  int32_t d = -1;
+  float x = 0.f, uq = 0.f;
+  if (tid < n) {
+    d = a.draft_tokens[r * a.max_drafts + tid];
+    if (d >= 0 && d < a.vocab && !greedy) {
+      x = clean(load1<F32>(logits_row<F32>(a, r, tid), d));
+      uq = a.uniform[r * a.max_drafts + tid] * (a.draft_probs ? a.draft_probs[(r * a.max_drafts + tid) * a.ld_probs + d] : 1.f);
     }
   }
   __syncthreads();
+  if (tid < n) {
+    const RowPart p = rows[tid];
+    const bool inside = d >= 0 && d < a.vocab;
+    const bool ok = inside && (greedy ? d == p.at : p.sum > 0.f && uq < term(x, p.top, k) / p.sum);
+    if (!ok) atomicMin(&kept, tid);   // a minimum: the order does not matter
+  }
+  __syncthreads();
   return kept;
+}
+
+// The race over words [v0, v1) of a row by the whole workgroup; q and refused: what
+// is taken off (null, -1: nothing).  All threads have the result.
+template <bool F32>
+__device__ DrawPart race(const void* row, const RowPart& p, float k, const float* q, int32_t refused, const float* noise,
+                         int64_t v0, int64_t v1) {
+  __shared__ Best part[kThreads / 64];
+  __shared__ int part_any[kThreads / 64];
+  const int tid = threadIdx.x;
+  const float inv = p.sum > 0.f ? 1.f / p.sum : 0.f, top = p.top == -INFINITY ? 0.f : p.top;
+  Best best = {-INFINITY, INT32_MAX};
+  bool any = false;
+  auto take = [&](float x, float qv, float e, int32_t v) {   // v rises: the first of equals stays
+    const float w = __builtin_amdgcn_exp2f((clean(x) - top) * k) * inv - qv;
+    const float score = w > 0.f ? w * __builtin_amdgcn_rcpf(e) : -1.f;
+    any |= w > 0.f;
+    best.at = score > best.score ? v : best.at;
+    best.score = fmaxf(best.score, score);
+  };
+  auto run = [&](auto taken) {   // 0: nothing, 1: q, 2: one word
+    constexpr int kTaken = decltype(taken)::value;
+    constexpr int B = kBatch / 2;
+    const int vectors = (int)((v1 - v0) >> 3);
+    for (int base = 0; base < vectors; base += B * kThreads) {
+      float x[B][8], e[B][8], qv[B][8];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int64_t v = v0 + 8 * (int64_t)min(base + b * kThreads + tid, vectors - 1);   // beyond: the last again, not taken
+        load8<F32>(x[b], row, v);
+        load8<true>(e[b], noise, v);
+        if (kTaken == 1) load8<true>(qv[b], q, v);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int i = base + b * kThreads + tid;
+        if (i < vectors) {
+          const int32_t v = (int32_t)(v0 + 8 * (int64_t)i);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) take(x[b][j], kTaken == 1 ? qv[b][j] : kTaken == 2 && v + j == refused ? 1.f : 0.f, e[b][j], v + j);
+        }
+      }
+    }
+    const int64_t v = v0 + 8 * (int64_t)vectors + tid;   // what is left of a vector
+    if (v < v1) take(load1<F32>(row, v), kTaken == 1 ? q[v] : kTaken == 2 && v == refused ? 1.f : 0.f, noise[v], (int32_t)v);
+  };
+  if (q) run(std::integral_constant<int, 1>{});
+  else if (refused >= 0) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 0>{});
+  best = wave_best(best);
+  const int some = __any(any);
+  if ((tid & 63) == 0) {
+    part[tid >> 6] = best;
+    part_any[tid >> 6] = some;
+  }
+  __syncthreads();
+  best = part[0];
+  int all = part_any[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) {
+    best = better(best, part[w]);
+    all |= part_any[w];
+  }
+  __syncthreads();
+  return DrawPart{best.score, best.at, all, 0};
 }
 
 }  // namespace
@@ -231,79 +324,21 @@ __device__ int accept(const VerifyArgs& a, const VerifyWorkspace& ws, int64_t r,
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, VerifyWorkspace ws) {
   __shared__ RowPart rows[kThreads];
-  __shared__ Best part[2][kThreads / 64];
-  __shared__ int part_any[2][kThreads / 64];
-  const int slices = gridDim.x, slice = blockIdx.x, tid = threadIdx.x;
+  const int slices = gridDim.x, slice = blockIdx.x;
   const int64_t r = blockIdx.y;
   const int n = drafts_of(a, r);
   if (n < 0) return;
   bool greedy;
-  const float t = temperature_of(a, r, &greedy);
+  const float k = kLog2e / temperature_of(a, r, &greedy);
   if (greedy) return;   // the argument of the maximum is known
-  const int kept = accept<F32>(a, ws, r, n, slices, t, greedy, rows);
-  const RowPart p = rows[kept];
-  const void* row = logits_row<F32>(a, r, kept);
+  const int kept = accept<F32>(a, ws, r, n, slices, k, greedy, rows);
   const bool rest = kept < n;   // a draft was refused: draw from what it leaves
-  const float* q = rest && a.draft_probs ? a.draft_probs + (r * a.max_drafts + kept) * a.ld_probs : nullptr;
-  const int32_t refused = rest && !a.draft_probs ? a.draft_tokens[r * a.max_drafts + kept] : -1;
-  const float* noise = a.noise + r * a.ld_noise;
-  const int64_t each = (a.vocab + slices - 1) / slices, v0 = slice * each, v1 = min(v0 + each, a.vocab);
-  // [0]: from w; [1]: from p in its place.  The first word of weight 0 stands for all of them.
-  Best best[2] = {{-INFINITY, INT32_MAX}, {-INFINITY, INT32_MAX}};
-  int32_t none[2] = {INT32_MAX, INT32_MAX};
-  int any[2] = {0, 0};
-  auto take = [&](float x, float qv, float e, int64_t v) {
-    const float pv = p.sum > 0.f ? softmax_term(x, p.top) / p.sum : 0.f;
-    const float w[2] = {pv - qv, pv};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (w[k] > 0.f) {
-        best[k] = better(best[k], Best{w[k] / e, (int32_t)v});
-        any[k] = 1;
-      } else {
-        none[k] = min(none[k], (int32_t)v);
-      }
-    }
-  };
-  for (int64_t v = v0 + tid * 8; v < v1; v += kThreads * 8) {
-    float x[8], e[8], qv[8];
-    if (v + 8 <= v1) {
-      load8<F32>(x, row, v);
-      load8<true>(e, noise, v);
-      if (q) load8<true>(qv, q, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = v + j < v1;
-        x[j] = in ? load1<F32>(row, v + j) : -INFINITY;
-        e[j] = in ? noise[v + j] : 1.f;
-        if (q) qv[j] = in ? q[v + j] : 0.f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (v + j < v1) take(scaled(x[j], t), q ? qv[j] : v + j == refused ? 1.f : 0.f, e[j], v + j);
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const Best b = wave_best(none[k] == INT32_MAX ? best[k] : better(best[k], Best{-1.f, none[k]}));
-    const int some = __any(any[k]);
-    if ((tid & 63) == 0) {
-      part[k][tid >> 6] = b;
-      part_any[k][tid >> 6] = some;
-    }
-  }
-  __syncthreads();
-  if (tid < 2) {
-    Best b = part[tid][0];
-    int some = part_any[tid][0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 64; ++w) {
-      b = better(b, part[tid][w]);
-      some |= part_any[tid][w];
-    }
-    ws.draws[(r * slices + slice) * 2 + tid] = DrawPart{b.score, b.at, some, 0};
-  }
+  const int64_t each = slice_length(a.vocab, slices), v0 = min(slice * each, a.vocab), v1 = min(v0 + each, a.vocab);
+  const DrawPart d = race<F32>(logits_row<F32>(a, r, kept), rows[kept], k,
+                               rest && a.draft_probs ? a.draft_probs + (r * a.max_drafts + kept) * a.ld_probs : nullptr,
+                               rest && !a.draft_probs ? a.draft_tokens[r * a.max_drafts + kept] : -1,
+                               a.noise + r * a.ld_noise, v0, v1);
+  if (threadIdx.x == 0) ws.draws[r * slices + slice] = d;
 }
 
 // Grid (requests): the tokens, their count and their log-probabilities.
@@ -322,49 +357,41 @@ __global__ __launch_bounds__(kThreads) void verify_join_kernel(VerifyArgs a, Ver
     return;
   }
   bool greedy;
-  const float t = temperature_of(a, r, &greedy);
-  const int kept = accept<F32>(a, ws, r, n, slices, t, greedy, rows);
+  const float t = temperature_of(a, r, &greedy), k = kLog2e / t;
+  DrawPart d = {-INFINITY, INT32_MAX, 0, 0};   // every wave joins the slices, a slice a lane
+  if (!greedy && (i & 63) < slices) d = ws.draws[r * slices + (i & 63)];
+  const int kept = accept<F32>(a, ws, r, n, slices, k, greedy, rows);
+  if (!greedy) {
+    const Best b = wave_best(Best{d.score, d.at});
+    d = DrawPart{b.score, b.at, __any(d.any), 0};
+    // a refused draft that leaves nothing (p = q up to rounding): p in its place
+    if (!d.any && kept < n)
+      d = race<F32>(logits_row<F32>(a, r, kept), rows[kept], k, nullptr, -1, a.noise + r * a.ld_noise, 0, a.vocab);
+  }
   if (i == 0) a.num_accepted[r] = kept;
   if (i > a.max_drafts) return;
   int32_t token = -1;
-  if (i < kept) {
-    token = a.draft_tokens[r * a.max_drafts + i];
-  } else if (i == kept) {
-    if (greedy) {
-      token = rows[i].at;
-    } else {
-      Best left = {-INFINITY, INT32_MAX}, whole = left;
-      int left_any = 0, whole_any = 0;
-      for (int s = 0; s < slices; ++s) {
-        const DrawPart* d = ws.draws + (r * slices + s) * 2;
-        left = better(left, Best{d[0].score, d[0].at});
-        whole = better(whole, Best{d[1].score, d[1].at});
-        left_any |= d[0].any;
-        whole_any |= d[1].any;
-      }
-      token = left_any ? left.at : whole_any ? whole.at : -1;
-    }
-    if (token == INT32_MAX) token = -1;   // nothing has a probability
-  }
+  if (i < kept) token = a.draft_tokens[r * a.max_drafts + i];
+  if (i == kept) token = greedy ? (rows[i].at == INT32_MAX ? -1 : rows[i].at) : d.any ? d.at : -1;
   float lp = 0.f;
   if (token >= 0) {
-    const float x = scaled(load1<F32>(logits_row<F32>(a, r, i), token), t);
-    lp = x - rows[i].top - __logf(rows[i].sum);
+    const float x = clean(load1<F32>(logits_row<F32>(a, r, i), token));
+    lp = (x - rows[i].top) / t - kLn2 * __builtin_amdgcn_logf(rows[i].sum);
   }
   a.out_tokens[out] = token;
   a.logprobs[out] = lp;
 }
 
 size_t verify_workspace_bytes(int64_t requests, int64_t max_drafts, int64_t vocab) {
-  const int slices = verify_slices(vocab);
-  return (size_t)(uintptr_t)(verify_workspace(nullptr, requests, max_drafts, slices).draws + requests * slices * 2) + 16;
+  const int slices = verify_slices(requests, max_drafts, vocab);
+  return (size_t)(uintptr_t)(verify_workspace(nullptr, requests, max_drafts, slices).draws + requests * slices) + 16;
 }
 
 namespace {
 
 template <bool F32>
 hipError_t launch(const VerifyArgs& a, hipStream_t st) {
-  const int slices = verify_slices(a.vocab);
+  const int slices = verify_slices(a.requests, a.max_drafts, a.vocab);
   const VerifyWorkspace ws = verify_workspace(a.workspace, a.requests, a.max_drafts, slices);
   verify_rows_kernel<F32><<<dim3(slices, (unsigned)a.max_drafts + 1, (unsigned)a.requests), kThreads, 0, st>>>(a, ws);
   hipError_t e = hipGetLastError();

@@ -121,7 +121,7 @@ int paged_attention(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32
   a.max_new = max_new;
   a.max_seq = max_seq;
   a.max_pages = max_pages;
-  a.window = window;
+  a.window = window > INT32_MAX ? 0 : (int)window;   // no sequence is that long
   a.scale = scale;
   a.hq = num_heads;
   a.group = num_heads / num_kv_heads;

@@ -24,8 +24,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 constexpr int kDecodeRows = 32;
 // The streaming kernel's workgroups: a fixed grid that shares all key tiles.
 constexpr int kDecodeWaves = 4, kDecodeGrid = 512, kDecodeTile = 32;
-// Rows and waves of a workgroup of the tiled kernel.
-constexpr int kChunkRows = 256, kChunkWaves = 8;
+// Rows and waves of a workgroup of the tiled kernel, and its grid: one workgroup a CU.
+constexpr int kChunkRows = 256, kChunkWaves = 8, kChunkGrid = 256;
 
 // A value that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -50,30 +50,75 @@ __device__ __forceinline__ uint32_t e4m3_bf16(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
 }
 
-// A request's new tokens and keys.
+// A request's new tokens and keys.  Lengths fit 32 bits; none is negative but
+// pos0 where the request is shorter than its chunk.
 struct RequestLens {
-  int64_t start;    // first row of q
-  int64_t tokens;   // new tokens
-  int64_t keys;     // keys, the new ones among them
+  int start;    // first row of q
+  int tokens;   // new tokens
+  int keys;     // keys that the table has room for, the new ones among them
+  int pos0;     // position of the first new token
 };
-__device__ __forceinline__ RequestLens request_lens(const AttentionArgs& a, int64_t r) {
+__device__ __forceinline__ RequestLens request_lens(const AttentionArgs& a, int r) {
   RequestLens l;
-  const int64_t s0 = min(max((int64_t)a.q_start[r], (int64_t)0), a.tokens);
-  const int64_t s1 = min((int64_t)a.q_start[r + 1], a.tokens);
-  l.start = s0;
-  l.tokens = max(s1 - s0, (int64_t)0);
-  l.keys = min(max((int64_t)a.seq_lens[r], (int64_t)0), a.max_pages << a.cache.page_shift);
+  const int rows = (int)a.tokens, seq = max(a.seq_lens[r], 0);
+  l.start = min(max(a.q_start[r], 0), rows);
+  l.tokens = max(min(a.q_start[r + 1], rows) - l.start, 0);
+  l.keys = (int)min((int64_t)seq, a.max_pages << a.cache.page_shift);
+  l.pos0 = seq - l.tokens;
   return l;
 }
-// The position of new token i; keys past the table are cut off, positions are not.
-__device__ __forceinline__ int64_t token_pos(const AttentionArgs& a, int64_t r, const RequestLens& l, int64_t i) {
-  return (int64_t)a.seq_lens[r] - l.tokens + i;
+// First key that a row at this position may see (it sees none at a negative one).
+__device__ __forceinline__ int low_of(const AttentionArgs& a, int pos) {
+  return a.window && pos >= a.window ? pos - a.window + 1 : 0;
+}
+// n / group for 0 <= n < 2^31.
+__device__ __forceinline__ int div_group(const AttentionArgs& a, int n) {
+  return a.group == 1 ? n : (int)(__umulhi((uint32_t)n, a.group_mul) >> a.group_shift);
+}
+// floor(n / d) through the fp64 reciprocal, 0 <= n < 2^43, 0 < d.
+__device__ __forceinline__ int64_t div_f64(int64_t n, int64_t d) { return (int64_t)((double)n / (double)d); }
+
+// Parts of workgroups g0 .. g1 joined in their order, four columns at d: their
+// common maximum (log2 units), the sum and the unnormalised output.  Four parts'
+// loads are in flight together.
+template <int D, class Slot>
+__device__ __forceinline__ float join_parts(const float2* ml, const float* o, Slot slot_of, int g0, int g1, int d, float* den,
+                                            f32x4* num) {
+  float top = -INFINITY;
+  *den = 0.f;
+  *num = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int g = g0; g <= g1; g += 4) {
+    float2 m[4];
+    f32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t slot = slot_of(min(g + i, g1));
+      m[i] = ml[slot];
+      x[i] = *(const f32x4*)(o + slot * D + d);
+    }
+    float to = top;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to = fmaxf(to, m[i].x);
+    const float by = top == to ? 1.f : exp2_fast(top - to);   // -inf before the first part: 0
+    *den *= by;
+    *num *= by;
+    top = to;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = g + i > g1 || m[i].x == -INFINITY ? 0.f : exp2_fast(m[i].x - top);
+      const float part = g + i > g1 ? 0.f : m[i].y;
+      *den = fmaf(w, part, *den);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) (*num)[k] = fmaf(w, g + i > g1 ? 0.f : x[i][k], (*num)[k]);
+    }
+  }
+  return top;
 }
 
 // Launches of the two kernels and of their joins (attention_*.hip).
 hipError_t launch_attention_decode(const AttentionArgs& a, hipStream_t st);
 hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipStream_t st);
 size_t attention_decode_workspace(int64_t requests, int dim);
-size_t attention_chunk_workspace(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_seq);
+size_t attention_chunk_workspace(int64_t requests, int dim);
 
 }  // namespace nvfp4

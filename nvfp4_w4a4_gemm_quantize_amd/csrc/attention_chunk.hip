@@ -66,30 +66,69 @@ __device__ __forceinline__ void phase_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-struct ChunkWorkspace {
-  float2* ml;   // [splits][tokens * hq]
-  float* o;     // [splits][tokens * hq][dim]
+// The work of all row tiles and KV heads forms one line that a fixed grid shares
+// evenly.  A row tile's length on it is the keys that its last row may see, in
+// units of 1 / group keys, and a constant for what a tile costs beside; it
+// grows by 256 from a request's tile to the next until the window ends it, so a
+// request's length has a closed form.
+struct ChunkLine {
+  int tiles, rising;
+  int64_t context, cap, extra;
 };
-__host__ __device__ inline ChunkWorkspace chunk_workspace(void* ws, int64_t rows, int splits) {
+__device__ __forceinline__ ChunkLine chunk_line(const AttentionArgs& a, const RequestLens& l) {
+  ChunkLine c;
+  const int rows = l.tokens * a.group;
+  c.tiles = rows > kDecodeRows ? (rows + kChunkRows - 1) / kChunkRows : 0;
+  c.context = (int64_t)max(l.pos0, 0) * a.group;
+  c.cap = a.window ? (int64_t)a.window * a.group + kChunkRows : INT64_MAX / 4;
+  c.extra = 128 * a.group;
+  c.rising = (int)min(max((c.cap - c.context) >> 8, (int64_t)0), (int64_t)c.tiles);
+  return c;
+}
+static_assert(kChunkRows == 256, "");
+__device__ __forceinline__ int64_t line_length(const ChunkLine& c, int b) {
+  return min(c.context + (int64_t)(b + 1) * kChunkRows, c.cap) + c.extra;
+}
+__device__ __forceinline__ int64_t line_before(const ChunkLine& c, int b) {   // the tiles before tile b
+  const int k = min(b, c.rising);
+  return k * (c.context + c.extra) + (int64_t)(kChunkRows / 2) * k * (k + 1) + (b > k ? (b - k) * (c.cap + c.extra) : 0);
+}
+
+struct ChunkWorkspace {
+  int64_t* prefix;   // [requests + 1]: length before a request (of one head); then a workgroup's share
+  float2* ml;        // [2 * grid][kChunkRows]
+  float* o;          // [2 * grid][kChunkRows][dim]
+};
+__host__ __device__ inline ChunkWorkspace chunk_workspace(void* ws, int64_t requests) {
   ChunkWorkspace w;
-  w.ml = (float2*)ws;
-  w.o = (float*)((uint8_t*)ws + (rows * splits * 8 + 255) / 256 * 256);
+  w.prefix = (int64_t*)ws;
+  uint8_t* p = (uint8_t*)ws + ((requests + 2) * 8 + 255) / 256 * 256;
+  w.ml = (float2*)p;
+  w.o = (float*)(p + (size_t)2 * kChunkGrid * kChunkRows * sizeof(float2));
   return w;
 }
 
+// Row tiles can also be numbered without a prefix sum: request r's start at
+// floor(q_start[r] G / 256) + r, which leaves room for all of them and
+// sometimes a number that stands for none.
 int64_t row_tiles(int64_t tokens, int64_t requests, int group) { return tokens * group / kChunkRows + requests; }
-
-// Parts of the keys: enough for two workgroups a CU, of at least 512 keys.
-int chunk_splits(int64_t tokens, int64_t requests, int group, int hkv, int64_t max_seq) {
-  const int64_t wgs = row_tiles(tokens, requests, group) * hkv;
-  if (wgs >= 256) return 1;
-  return (int)max(min(min(512 / wgs, (max_seq + 511) / 512), (int64_t)64), (int64_t)1);
+struct RowTile {
+  int r, b;   // request and its row tile
+};
+__device__ __forceinline__ RowTile row_tile(const AttentionArgs& a, int number) {
+  int lo = 0, hi = (int)a.requests - 1;
+  auto start = [&](int r) { return (int)((int64_t)a.q_start[r] * a.group >> 8) + r; };
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start(mid) <= number) lo = mid; else hi = mid - 1;
+  }
+  return RowTile{lo, number - start(lo)};
 }
 
 }  // namespace
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionArgs a, ChunkWorkspace ws, int splits) {
+__global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionArgs a, ChunkWorkspace ws, int numbers) {
   constexpr int KT = D == 256 ? 32 : 64;      // keys of a tile
   constexpr int NK = KT / 32;                 // key fragments of a tile
   constexpr int NG = KT / 16;                 // 16-key groups: a page holds whole ones
@@ -107,34 +146,112 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hkv = a.cache.heads, group = a.group;
-  const int head = blockIdx.x % hkv;
-  const int split = blockIdx.x / hkv % splits;
-  const int64_t tiles = gridDim.x / hkv / splits;
-  const int64_t vt = tiles - 1 - blockIdx.x / hkv / splits;   // long tiles of a prompt first
 
-  // Row tiles are numbered without a prefix sum: request r's start at
-  // floor(q_start[r] G / 256) + r, which leaves room for all of them and
-  // sometimes a number that stands for none.
-  int64_t lo = 0, hi = a.requests - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if ((int64_t)a.q_start[mid] * group / kChunkRows + mid <= vt) lo = mid; else hi = mid - 1;
+  // prefix of the line over runs of requests
+  __shared__ int64_t before[kThreads + 1];
+  __shared__ int64_t wave_sum[kChunkWaves];
+  const int requests = (int)a.requests, run = (requests + kThreads - 1) / kThreads;
+  const int place = blockIdx.x % 8 * (kChunkGrid / 8) + blockIdx.x / 8;
+  int64_t x_begin = 0, x_end = 1, per_head = 0;
+  if (numbers == 0) {
+    const int r0 = min(tid * run, requests), r1 = min(r0 + run, requests);
+    int64_t own = 0;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+      const ChunkLine cl = chunk_line(a, request_lens(a, r));
+      own += line_before(cl, cl.tiles);
+    }
+    int64_t inc = own;
+#pragma unroll 1
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t u = __shfl_up(inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 63) wave_sum[wave] = inc;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < wave; ++w) inc += wave_sum[w];
+    if (tid == 0) before[0] = 0;
+    before[tid + 1] = inc;
+    __syncthreads();
+    per_head = uniform(before[kThreads]);
+    // Shares of at least four tiles' keys.  Workgroups take their shares XCD by XCD,
+    // so that those of an XCD, which have one L2, read the same heads' keys.
+    const int64_t share = uniform(max((per_head * hkv + kChunkGrid - 1) / kChunkGrid, (int64_t)384 * group));
+    if (place == 0) {
+      int64_t t = inc - own;
+#pragma unroll 1
+      for (int r = r0; r < r1; ++r) {
+        ws.prefix[r] = t;
+        const ChunkLine cl = chunk_line(a, request_lens(a, r));
+        t += line_before(cl, cl.tiles);
+      }
+      if (tid == 0) {
+        ws.prefix[requests] = per_head;
+        ws.prefix[requests + 1] = share;
+      }
+    }
+    x_begin = place * share;
+    x_end = uniform(min(x_begin + share, per_head * hkv));
   }
-  const int64_t r = uniform(lo);
-  RequestLens l = request_lens(a, r);
-  l.start = uniform(l.start), l.tokens = uniform(l.tokens), l.keys = uniform(l.keys);
-  const int64_t nrows = l.tokens * group, b = vt - ((int64_t)a.q_start[r] * group / kChunkRows + r);
-  if (nrows <= kDecodeRows || b < 0 || b * kChunkRows >= nrows) return;
 
-  const int64_t row0 = b * kChunkRows, row_end = min(row0 + kChunkRows, nrows);
-  const int64_t pos_first = token_pos(a, r, l, row0 / group), pos_last = token_pos(a, r, l, (row_end - 1) / group);
-  const int64_t keys = min(l.keys, pos_last + 1);
-  const int64_t low = a.window ? max(pos_first - a.window + 1, (int64_t)0) : 0;
-  const int64_t begin = low / KT * KT;
-  const int64_t all = max((keys - begin + KT - 1) / KT, (int64_t)0);
-  const int64_t share = (all + splits - 1) / splits;
-  const int64_t t_begin = min(split * share, all), t_end = min(t_begin + share, all);
-  const int n = __builtin_amdgcn_readfirstlane((int)(t_end - t_begin));
+  for (int64_t x = x_begin; x < x_end;) {
+  // the head, request and row tile, and the part of its keys
+  int head, r, b, part = 0;
+  bool whole = true;
+  double share_from = 0., share_to = 1.;
+  RequestLens l;
+  if (numbers) {              // a row tile a workgroup, long tiles of a prompt first
+    head = blockIdx.x % hkv;
+    const RowTile t = row_tile(a, numbers - 1 - (int)blockIdx.x / hkv);
+    r = uniform(t.r), b = uniform(t.b);
+    l = request_lens(a, r);
+    if (l.tokens * group <= kDecodeRows || b < 0 || b * kChunkRows >= l.tokens * group) return;
+    x = x_end;
+  } else {                    // a share of the line
+    head = 0;
+#pragma unroll 1
+    for (int step = 1 << (31 - __builtin_clz(hkv)); step > 0; step >>= 1)
+      if (head + step < hkv && (head + step) * per_head <= x) head += step;
+    const int64_t y = uniform(x - head * per_head);
+    int at = 0;
+#pragma unroll 1
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+      if (before[at + step] <= y) at += step;
+    r = uniform(at * run);
+    int64_t base = before[at];
+    l = request_lens(a, r);
+    ChunkLine line = chunk_line(a, l);
+#pragma unroll 1
+    while (y >= base + line_before(line, line.tiles)) {   // ends: y < before[at + 1]
+      base += line_before(line, line.tiles);
+      l = request_lens(a, ++r);
+      line = chunk_line(a, l);
+    }
+    r = uniform(r);
+    b = 0;                                                // the last tile that begins at or before y
+    int b_end = line.tiles;
+#pragma unroll 1
+    while (b_end - b > 1) {
+      const int mid = (b + b_end) >> 1;
+      if (base + line_before(line, mid) <= y) b = mid; else b_end = mid;
+    }
+    b = uniform(b);
+    const int64_t length = line_length(line, b), from = y - base - line_before(line, b), to = min(from + (x_end - x), length);
+    whole = uniform((int)(to - from == length));
+    part = x == x_begin ? 0 : 1;
+    x = uniform(x + to - from);
+    share_from = (double)from / (double)length;           // the same on both sides of a cut
+    share_to = to == length ? 1. : (double)to / (double)length;
+  }
+  l.start = uniform(l.start), l.tokens = uniform(l.tokens), l.keys = uniform(l.keys), l.pos0 = uniform(l.pos0);
+
+  const int nrows = l.tokens * group;
+  const int row0 = b * kChunkRows, row_end = min(row0 + kChunkRows, nrows);
+  const int pos_first = l.pos0 + div_group(a, row0), pos_last = l.pos0 + div_group(a, row_end - 1);
+  const int keys = min(l.keys, max(pos_last, -1) + 1), low = low_of(a, pos_first);
+  const int begin = low & ~(KT - 1), all = max(keys - begin + KT - 1, 0) / KT;
+  const int t_begin = uniform((int)(all * share_from)), n = uniform((int)(all * share_to) - t_begin);
 
   float c = a.scale * kLog2e;
   if (a.cache.k_scale) c *= a.cache.k_scale[head];
@@ -142,38 +259,36 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   c = fmaxf(fabsf(c), FLT_MIN);   // never 0: a hidden score's -inf stays one
 
   // this lane's row of q, the B operand: column c32, k = 8 columns of q
-  const int64_t my_row = row0 + wave * 32 + c32;
+  const int my_row = row0 + wave * 32 + c32;
   const bool live = my_row < nrows;
-  const int64_t my_token = live ? my_row / group : 0;
-  const int my_head = head * group + (live ? (int)(my_row % group) : 0);
+  const int my_token = live ? div_group(a, my_row) : 0;
+  const int my_head = head * group + (live ? my_row - my_token * group : 0);
   bf16x8 q[KS];
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
-    u32x4 w = *(const u32x4*)(a.q + (l.start + my_token) * a.ld_q + (int64_t)my_head * D + s * 16 + h * 8);
+    u32x4 w = *(const u32x4*)(a.q + (int64_t)(l.start + my_token) * a.ld_q + my_head * D + s * 16 + h * 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = live ? w[i] ^ flip : 0u;
     q[s] = __builtin_bit_cast(bf16x8, w);
   }
   // positions relative to the first key of the part
-  const int origin = __builtin_amdgcn_readfirstlane((int)(begin + t_begin * KT));
-  auto rel = [&](int64_t x) { return (int)min(max(x - origin, (int64_t)INT32_MIN / 2), (int64_t)INT32_MAX / 2); };
-  const int my_pos = live ? rel(token_pos(a, r, l, my_token)) : INT32_MIN / 2;
-  const int my_low = a.window && live ? rel(token_pos(a, r, l, my_token) - a.window + 1) : INT32_MIN / 2;
-  const int64_t wave_row = min(row0 + wave * 32, nrows - 1);
-  const int wave_pos = __builtin_amdgcn_readfirstlane(rel(token_pos(a, r, l, wave_row / group)));   // keys up to it are seen by all rows
-  const int wave_low = __builtin_amdgcn_readfirstlane(
-      a.window ? rel(token_pos(a, r, l, min(wave_row + 31, nrows - 1) / group) - a.window + 1) : INT32_MIN / 2);
-  const int keys_rel = __builtin_amdgcn_readfirstlane(rel(keys)), low_rel = __builtin_amdgcn_readfirstlane(rel(low));
+  const int origin = uniform(begin + t_begin * KT);
+  const int my_pos = live ? max(l.pos0 + my_token, -1) - origin : INT32_MIN / 2, my_low = low_of(a, l.pos0 + my_token) - origin;
+  const int wave_row = min(row0 + wave * 32, nrows - 1);
+  const int wave_pos = uniform(max(l.pos0 + div_group(a, wave_row), -1) - origin);   // keys up to it are seen by all rows
+  const int wave_low = uniform(low_of(a, l.pos0 + div_group(a, min(wave_row + 31, nrows - 1))) - origin);
+  const int keys_rel = uniform(keys - origin), low_rel = uniform(low - origin);
 
   // Where the keys lie.  A missing page is looked for once in the part's whole
   // table: only if there is one do tiles look again.
   const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
   const uint32_t num_pages = (uint32_t)a.cache.num_pages;
-  const int32_t* table = a.block_table + r * a.ld_table;
+  const int32_t* table = a.block_table + (int64_t)r * a.ld_table;
   auto page_at = [&](int key) { return (uint32_t)table[(uint32_t)(origin + min(key, keys_rel - 1)) >> page_shift]; };
   bool missing = false;
   if (n > 0) {
     const int last = (origin + min(n * KT, keys_rel) - 1) >> page_shift;
+#pragma unroll 1
     for (int i = (origin >> page_shift) + lane; i <= last; i += 64) missing |= (uint32_t)table[i] >= num_pages;
     missing = __any(missing);
   }
@@ -185,6 +300,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     if (top < KT) held &= top > 0 ? ((uint64_t)1 << top) - 1 : 0;
     if (bottom > 0) held &= bottom < 64 ? ~(((uint64_t)1 << bottom) - 1) : 0;
     if (missing)
+#pragma unroll 1
       for (int g = 0; g < NG; ++g)
         if (page_at(min(j, n - 1) * KT + 16 * g) >= num_pages) held &= ~((uint64_t)0xffff << (16 * g));
     return (uint64_t)uniform((int64_t)held);
@@ -337,17 +453,18 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   };
   auto softmax_step = [&](int j) {
     if (j < seen_from || j >= seen_to) {
-      const int key0 = j * KT;
-      const uint64_t held = held_keys(j);
+      // a bit for every key of the tile that this lane's row sees
+      const int bottom = my_low - j * KT, end = my_pos + 1 - j * KT;
+      uint64_t see = held_keys(j);
+      see = end <= 0 ? 0 : end < 64 ? see & (((uint64_t)1 << end) - 1) : see;
+      see = bottom <= 0 ? see : bottom < 64 ? see & (~(uint64_t)0 << bottom) : 0;
 #pragma unroll
-      for (int f = 0; f < NK; ++f)
+      for (int f = 0; f < NK; ++f) {
+        const uint32_t bits = (uint32_t)(see >> (32 * f)) >> (4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int in = f * 32 + 8 * (i >> 2) + (i & 3);   // + 4 h
-          const int key = key0 + in + 4 * h;
-          const bool hidden = (key > my_pos) | (key < my_low) | !((uint32_t)(held >> in) >> (4 * h) & 1);
-          s[f][i] = hidden ? -INFINITY : s[f][i];
-        }
+        for (int i = 0; i < 16; ++i)
+          s[f][i] = bits >> (8 * (i >> 2) + (i & 3)) & 1 ? s[f][i] : -INFINITY;
+      }
     }
     float top = s[0][0];
 #pragma unroll
@@ -380,42 +497,43 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   };
 
   if (n > 0) {
-    // Before the loop: keys 0 - 3, values 0 - 2.
+    // Before the loop: keys 0 - 2, values 0 and 1.  The loop begins at tile -1, whose
+    // values and weights are 0, so that tile 0's scores need no code of their own.
     constexpr int kLead = FP8 ? 5 : 4;       // the tile whose keys are asked for while tile 0's values are multiplied
     locate(0);
     Offsets key_at, value_at;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < KT * ROW / 16 / kThreads; ++i) *(u32x4*)(lds_v[3] + (i * kThreads + tid) * 16) = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int j = 0; j < 3; ++j) {
       key_at = offsets_of(j);
       bring_all(k_base, key_at, lds_k[j], k_voff, kr);
       settle(lds_k[j], kr, false, 0);
-      if (j == 3) break;
+      if (j == 2) break;
       bring_all(v_base, key_at, lds_v[j], v_voff, vr);
       settle(lds_v[j], vr, true, held_keys(j));
     }
     value_at = key_at;
-    if constexpr (FP8) {                     // in registers: keys 4, values 3
+    if constexpr (FP8) {                     // in registers: keys 3, values 2
       bring_all(v_base, value_at, nullptr, v_voff, vr);
-      value_at = offsets_of(4);
+      value_at = offsets_of(3);
       bring_all(k_base, value_at, nullptr, k_voff, kr);
     }
-    key_at = offsets_of(kLead);
-    wait_arrived<0>();
+    key_at = offsets_of(kLead - 1);
 #pragma unroll
-    for (int j = 0; j < 3; ++j) clear_values(lds_v[j], held_keys(j));
+    for (int u = 0; u < 2 * NK; ++u) p[u] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+    wait_arrived<0>();
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j)
+      if (j < held_from || j >= held_to) clear_values(lds_v[j], held_keys(j));
     phase_barrier<true>();
     // The two waves of a SIMD take turns: while waves 0-3 multiply, waves 4-7,
     // one barrier behind, run their softmax, and the other way round.
     if (wave >= kChunkWaves / 2) phase_barrier<false>();
-    clear_scores();
 #pragma unroll
-    for (int e = 0; e < KS * NK; ++e) multiply_keys(key_fragment(lds_k[0], e), e);
-    phase_barrier<false>();
-    softmax_step(0);
-#pragma unroll
-    for (int t = 0; t < kAhead; ++t) read_operands(lds_k[1], lds_v[0], t);
-    phase_barrier<false>();
-    for (int j = 0; j < n; ++j) {
+    for (int t = 0; t < kAhead; ++t) read_operands(lds_k[0], lds_v[3], t);
+#pragma unroll 1
+    for (int j = -1; j < n; ++j) {
       // Products: O += values j, S = keys j + 1.  Tile j + 4's keys take the place of
       // tile j's, tile j + 3's values that of tile j - 1's, which all have read; they
       // are waited for in the next products and read at the end of the softmax after.
@@ -447,89 +565,91 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   }
 
   sum += __shfl_xor(sum, 32);
-  if (!live) return;
-  const int64_t trow = l.start + my_token;
   const float top = m == -INFINITY ? -INFINITY : c * m;
-  if (splits == 1) {
+  if (live) {
+    const int trow = l.start + my_token;
+    const int64_t slot = ((int64_t)place * 2 + part) * kChunkRows + wave * 32 + c32;
     const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
-    const float inv = sum == 0.f ? 0.f : vs / sum;
-#pragma unroll
-    for (int i = 0; i < DF; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t at = trow * a.ld_out + (int64_t)my_head * D + 32 * i + 8 * j + 4 * h;
-        const f32x4 x = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]} * inv;
-        if (a.out_bf16)
-          *(u32x2*)((uint16_t*)a.out + at) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-        else
-          *(f32x4*)((float*)a.out + at) = x;
-      }
-    if (a.lse && h == 0) a.lse[trow * a.hq + my_head] = sum == 0.f ? -INFINITY : kLn2 * (top + __log2f(sum));
-  } else {
-    const int64_t slot = (split * a.tokens + trow) * a.hq + my_head;
-    if (h == 0) ws.ml[slot] = make_float2(top, sum);
-    if (n > 0)
+    const float by = !whole ? 1.f : sum == 0.f ? 0.f : vs / sum;
+    const int64_t at = (int64_t)trow * a.ld_out + my_head * D + 4 * h;
+    if (whole && a.out_bf16) {
 #pragma unroll
       for (int i = 0; i < DF; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *(f32x4*)(ws.o + slot * D + 32 * i + 8 * j + 4 * h) = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+          *(u32x2*)((uint16_t*)a.out + at + 32 * i + 8 * j) =
+              u32x2{pack_bf16(o[i][4 * j] * by, o[i][4 * j + 1] * by), pack_bf16(o[i][4 * j + 2] * by, o[i][4 * j + 3] * by)};
+    } else {
+      float* to = whole ? (float*)a.out + at : ws.o + slot * D + 4 * h;
+#pragma unroll
+      for (int i = 0; i < DF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *(f32x4*)(to + 32 * i + 8 * j) = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]} * by;
+    }
+    if (h == 0) {
+      if (!whole) ws.ml[slot] = make_float2(top, sum);
+      else if (a.lse) a.lse[(int64_t)trow * a.hq + my_head] = sum == 0.f ? -INFINITY : kLn2 * (top + __log2f(sum));
+    }
+  }
   }
 }
 
-// Joins the parts of a token's rows in the order of their keys; a part without keys has sum 0.
+// Joins the parts of a row tile that several workgroups hold, in the order of
+// their keys.  Grid (row tile numbers x KV heads, 8): 32 rows a workgroup.
 template <int D>
-__global__ __launch_bounds__(256) void attention_chunk_join_kernel(AttentionArgs a, ChunkWorkspace ws, int splits) {
-  const int64_t trow = blockIdx.x;
-  int64_t lo = 0, hi = a.requests - 1;   // the request of the token: the last that starts at or before it
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (a.q_start[mid] <= trow) lo = mid; else hi = mid - 1;
-  }
-  const RequestLens l = request_lens(a, lo);
-  if (trow >= l.start + l.tokens || l.tokens * a.group <= kDecodeRows) return;
-  for (int e = threadIdx.x; e < a.hq * (D / 4); e += 256) {
-    const int hq = e / (D / 4), d = (e % (D / 4)) * 4;
-    float top = -INFINITY, den = 0.f;
-    f32x4 num = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, ws.ml[(s * a.tokens + trow) * a.hq + hq].x);
-    for (int s = 0; s < splits; ++s) {
-      const int64_t slot = (s * a.tokens + trow) * a.hq + hq;
-      const float2 ml = ws.ml[slot];
-      if (ml.y == 0.f) continue;
-      const float by = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
-      den = fmaf(by, ml.y, den);
-      const f32x4 ow = *(const f32x4*)(ws.o + slot * D + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
-    }
-    const float vs = a.cache.v_scale ? a.cache.v_scale[hq / a.group] : 1.f;
+__global__ __launch_bounds__(256) void attention_chunk_join_kernel(AttentionArgs a, ChunkWorkspace ws) {
+  const int hkv = a.cache.heads, group = a.group;
+  const int head = blockIdx.x % hkv;
+  const RowTile t = row_tile(a, blockIdx.x / hkv);
+  const RequestLens l = request_lens(a, t.r);
+  const ChunkLine line = chunk_line(a, l);
+  if (t.b < 0 || t.b >= line.tiles) return;
+  const int64_t share = ws.prefix[a.requests + 1];
+  const int64_t x0 = head * ws.prefix[a.requests] + ws.prefix[t.r] + line_before(line, t.b);
+  const int g0 = (int)div_f64(x0, share), g1 = (int)div_f64(x0 + line_length(line, t.b) - 1, share);
+  if (g0 == g1) return;
+  const int nrows = min(l.tokens * group - t.b * kChunkRows, kChunkRows);
+  const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
+  for (int e = threadIdx.x; e < 32 * (D / 4); e += 256) {
+    const int at = blockIdx.y * 32 + e / (D / 4), d = (e % (D / 4)) * 4;
+    if (at >= nrows) return;
+    // workgroup g's part is its first unless the tile begins inside g's share
+    auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (x0 > wg * share ? 1 : 0)) * kChunkRows + at; };
+    float den;
+    f32x4 num;
+    const float top = join_parts<D>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
+    const int row = t.b * kChunkRows + at, token = div_group(a, row), hq = head * group + row - token * group;
+    const int64_t trow = l.start + token;
     const float inv = den == 0.f ? 0.f : vs / den;
     if (a.out_bf16)
-      *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + (int64_t)hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
+      *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
     else
-      *(f32x4*)((float*)a.out + trow * a.ld_out + (int64_t)hq * D + d) = num * inv;
+      *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
     if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
   }
 }
 
-size_t attention_chunk_workspace(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_seq) {
-  const int splits = chunk_splits(tokens, requests, hq / hkv, hkv, max_seq);
-  if (splits == 1) return 0;
-  return (size_t)(uintptr_t)chunk_workspace(nullptr, tokens * hq, splits).o + (size_t)splits * tokens * hq * dim * sizeof(float);
+size_t attention_chunk_workspace(int64_t requests, int dim) {
+  return (size_t)(uintptr_t)chunk_workspace(nullptr, requests).o + (size_t)2 * kChunkGrid * kChunkRows * dim * sizeof(float);
 }
 
 namespace {
 
 template <int D, bool FP8>
 hipError_t launch(const AttentionArgs& a, void* workspace, hipStream_t st) {
-  const int splits = chunk_splits(a.tokens, a.requests, a.group, a.cache.heads, a.max_seq);
-  const ChunkWorkspace ws = chunk_workspace(workspace, a.tokens * a.hq, splits);
-  const unsigned grid = (unsigned)(row_tiles(a.tokens, a.requests, a.group) * a.cache.heads * splits);
-  attention_chunk_kernel<D, FP8><<<grid, kThreads, 0, st>>>(a, ws, splits);
+  const ChunkWorkspace ws = chunk_workspace(workspace, a.requests);
+  const int64_t numbers = row_tiles(a.tokens, a.requests, a.group);
+  // Row tiles alone keep the chip busy: one a workgroup, handed out as they finish, and
+  // nothing to join.  Fewer are cut into equal shares.
+  if (a.tokens * a.group / kChunkRows * a.cache.heads >= 3 * kChunkGrid) {
+    attention_chunk_kernel<D, FP8><<<(unsigned)(numbers * a.cache.heads), kThreads, 0, st>>>(a, ws, (int)numbers);
+    return hipGetLastError();
+  }
+  attention_chunk_kernel<D, FP8><<<kChunkGrid, kThreads, 0, st>>>(a, ws, 0);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  attention_chunk_join_kernel<D><<<(unsigned)a.tokens, 256, 0, st>>>(a, ws, splits);
+  if (e != hipSuccess) return e;
+  attention_chunk_join_kernel<D><<<dim3((unsigned)(numbers * a.cache.heads), 8), 256, 0, st>>>(a, ws);
   return hipGetLastError();
 }
 
@@ -555,11 +675,18 @@ size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int h
   const int group = hq / hkv;
   size_t n = 16;
   if (may_stream(max_new, group)) n += (attention_decode_workspace(requests, dim) + 255) / 256 * 256;
-  if (may_tile(max_new, group)) n += attention_chunk_workspace(tokens, requests, hq, hkv, dim, max_seq);
+  if (may_tile(max_new, group)) n += attention_chunk_workspace(requests, dim);
   return n;
 }
 
-hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t st) {
+hipError_t launch_paged_attention(const AttentionArgs& args, hipStream_t st) {
+  AttentionArgs a = args;
+  if (a.group > 1) {
+    int s = 31 - __builtin_clz(a.group);
+    const bool power = (a.group & (a.group - 1)) == 0;
+    a.group_mul = power ? 1u << 31 : (uint32_t)(((uint64_t)1 << (32 + s)) / a.group + 1);
+    a.group_shift = power ? s - 1 : s;
+  }
   uint8_t* ws = (uint8_t*)a.workspace;
   if (may_stream(a.max_new, a.group)) {
     hipError_t e = launch_attention_decode(a, st);

@@ -58,17 +58,17 @@ __host__ __device__ inline DecodeWorkspace decode_workspace(void* ws, int64_t re
 // head; 0 tiles if it has no rows here.  A request whose rows see nothing has one.
 struct DecodeItem {
   RequestLens l;
-  int64_t begin, tiles;
+  int begin, tiles;
 };
-__device__ __forceinline__ DecodeItem decode_item(const AttentionArgs& a, int64_t r) {
+__device__ __forceinline__ DecodeItem decode_item(const AttentionArgs& a, int r) {
   DecodeItem it;
   it.l = request_lens(a, r);
-  it.begin = 0;
-  if (a.window) it.begin = max(token_pos(a, r, it.l, 0) - a.window + 1, (int64_t)0) / kDecodeTile * kDecodeTile;
-  it.tiles = max((it.l.keys - it.begin + kDecodeTile - 1) / kDecodeTile, (int64_t)1);
-  if (it.l.tokens == 0 || it.l.tokens * a.group > kDecodeRows) it.tiles = 0;
+  it.begin = low_of(a, it.l.pos0) & ~(kDecodeTile - 1);
+  it.tiles = max((it.l.keys - it.begin + kDecodeTile - 1) >> 5, 1);
+  if (it.l.tokens == 0 || it.l.tokens > kDecodeRows || it.l.tokens * a.group > kDecodeRows) it.tiles = 0;
   return it;
 }
+static_assert(kDecodeTile == 32, "");
 
 // One key tile's K and V in registers.
 template <int D, bool FP8>
@@ -98,6 +98,9 @@ __device__ __forceinline__ void load_words(uint32_t* out, const uint8_t* p) {
 
 }  // namespace
 
+// As many workgroups as the registers let be resident.
+constexpr int decode_grid(int dim) { return dim <= 128 ? kDecodeGrid : kDecodeGrid / 2; }
+
 template <int D, bool FP8, int NF>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_kernel(AttentionArgs a) {
   using Tile = DecodeTile<D, FP8>;
@@ -105,6 +108,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   constexpr int DV = D / 16;      // value columns a lane holds = fragments of O
   constexpr int EB = FP8 ? 1 : 2;
   constexpr int LD = D + 4;
+  constexpr int GRID = decode_grid(D);
   __shared__ int64_t before[kThreads + 1];
   __shared__ int64_t wave_sum[kDecodeWaves];
   __shared__ __attribute__((aligned(16))) float o_part[kDecodeWaves][16][LD];
@@ -116,10 +120,10 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
 
   // prefix of the tiles over runs of requests
-  const int64_t run = (a.requests + kThreads - 1) / kThreads;
-  const int64_t r0 = min(tid * run, a.requests), r1 = min(r0 + run, a.requests);
+  const int requests = (int)a.requests, run = (requests + kThreads - 1) / kThreads;
+  const int r0 = min(tid * run, requests), r1 = min(r0 + run, requests);
   int64_t sum = 0;
-  for (int64_t r = r0; r < r1; ++r) sum += decode_item(a, r).tiles;
+  for (int r = r0; r < r1; ++r) sum += decode_item(a, r).tiles;
   int64_t inc = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -132,12 +136,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   if (tid == 0) before[0] = 0;
   before[tid + 1] = inc;
   __syncthreads();
-  const int64_t total = before[kThreads] * hkv;
+  const int64_t total = uniform(before[kThreads] * hkv);
   // at least one tile a wave: a smaller share would only add parts to join
-  const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kDecodeWaves);
+  const int64_t per = max((total + GRID - 1) / GRID, (int64_t)kDecodeWaves);
   if (blockIdx.x == 0) {
     int64_t t = inc - sum;
-    for (int64_t r = r0; r < r1; ++r) {
+    for (int r = r0; r < r1; ++r) {
       ws.prefix[r] = t;
       t += decode_item(a, r).tiles;
     }
@@ -157,8 +161,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   int row_token[NF], row_head[NF];
 #pragma unroll
   for (int n = 0; n < NF; ++n) {
-    row_token[n] = (n * 16 + c16) / group;
-    row_head[n] = (n * 16 + c16) % group;
+    row_token[n] = div_group(a, n * 16 + c16);
+    row_head[n] = n * 16 + c16 - row_token[n] * group;
   }
 
   for (int64_t x = x_begin; x < x_end;) {
@@ -167,32 +171,33 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
 #pragma unroll
     for (int step = kThreads / 2; step > 0; step >>= 1)
       if (before[lo + step] * hkv <= x) lo += step;
-    int64_t r = lo * run, base = before[lo];
+    int r = lo * run;
+    int64_t base = before[lo];
     DecodeItem it = decode_item(a, r);
     while (x >= (base + it.tiles) * hkv) {   // ends: x < before[lo + 1] * hkv
       base += it.tiles;
       it = decode_item(a, ++r);
     }
     r = uniform(r);
+    it.l.start = uniform(it.l.start), it.l.tokens = uniform(it.l.tokens), it.l.pos0 = uniform(it.l.pos0);
+    it.tiles = uniform(it.tiles);
     const int64_t in_request = x - base * hkv;
-    const int head = uniform((int)(in_request / it.tiles));
-    const int64_t first = uniform(in_request - head * it.tiles);
-    const int64_t last = min(first + (x_end - x), it.tiles);   // tiles [first, last) of this head
-    const bool whole = first == 0 && last == it.tiles;
+    const int head = uniform((int)div_f64(in_request, it.tiles));
+    const int first = uniform((int)(in_request - (int64_t)head * it.tiles));
+    const int n = uniform((int)min((int64_t)(it.tiles - first), x_end - x));   // tiles [first, first + n) of this head
+    const bool whole = n == it.tiles;
     const int part = x == x_begin ? 0 : 1;
-    x += last - first;
+    x += n;
 
-    const int nrows = (int)it.l.tokens * group;
-    const int n = uniform((int)(last - first));
+    const int nrows = it.l.tokens * group;
     // positions relative to the first key of the part
-    const int origin = uniform((int)(it.begin + first * kDecodeTile));
-    auto rel = [&](int64_t at) { return (int)min(max(at - origin, (int64_t)INT32_MIN / 2), (int64_t)INT32_MAX / 2); };
-    const int64_t pos0 = token_pos(a, r, it.l, 0), pos_last = pos0 + it.l.tokens - 1;
-    const int keys = uniform(rel(min(it.l.keys, pos_last + 1)));
-    const int low = uniform(a.window ? rel(max(pos0 - a.window + 1, (int64_t)0)) : INT32_MIN / 2);   // first key that a row may see
+    const int origin = uniform(it.begin + first * kDecodeTile);
+    const int pos0 = it.l.pos0, pos_last = pos0 + it.l.tokens - 1;
+    const int keys = uniform(min(it.l.keys, max(pos_last, -1) + 1) - origin);
+    const int low = uniform(low_of(a, pos0) - origin);   // first key that a row may see
     // tiles [seen_from, seen_to) are seen in full by every row
-    const int seen_from = uniform(a.window ? (max(rel(pos_last - a.window + 1), 0) + kDecodeTile - 1) / kDecodeTile : 0);
-    const int seen_to = uniform(min(keys, max(rel(pos0) + 1, 0)) / kDecodeTile);
+    const int seen_from = uniform((max(low_of(a, pos_last) - origin, 0) + kDecodeTile - 1) >> 5);
+    const int seen_to = uniform(max(min(keys, max(pos0, -1) + 1 - origin), 0) >> 5);
     float c = a.scale * kLog2e;
     if (a.cache.k_scale) c *= a.cache.k_scale[head];
     const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
@@ -204,9 +209,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
       const bool live = n * 16 + c16 < nrows;
-      row_pos[n] = live ? rel(pos0 + row_token[n]) : INT32_MIN / 2;
-      row_low[n] = live && a.window ? rel(pos0 + row_token[n] - a.window + 1) : INT32_MIN / 2;
-      const uint16_t* qr = a.q + (it.l.start + (live ? row_token[n] : 0)) * a.ld_q + (head * group + (live ? row_head[n] : 0)) * D;
+      row_pos[n] = live ? max(pos0 + row_token[n], -1) - origin : INT32_MIN / 2;
+      row_low[n] = low_of(a, pos0 + row_token[n]) - origin;
+      const uint16_t* qr = a.q + (int64_t)(it.l.start + (live ? row_token[n] : 0)) * a.ld_q + (head * group + (live ? row_head[n] : 0)) * D;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         // E4M3 keys are loaded 16 columns at a time: steps 2 i, 2 i + 1 take a lane's halves
@@ -231,7 +236,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
     // Byte offsets of the two 16-key groups of this wave's tiles, 64 tiles at a
     // time, a tile a lane: tile k of the wave is tile wave + 4 k of the part.
     // Without a page any page serves: its scores are hidden and its values cleared.
-    const int32_t* table = a.block_table + r * a.ld_table;
+    const int32_t* table = a.block_table + (int64_t)r * a.ld_table;
     const uint32_t num_pages = (uint32_t)a.cache.num_pages;
     int64_t lane_at[2];
     uint64_t without[2];            // a bit for each of these tiles whose group has no page
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
     // a tile's keys are loaded once the tile before has given its scores, its
     // values once the products with the values before are done
     Tile tile;
-    const int mine = (n - wave + kDecodeWaves - 1) / kDecodeWaves;   // tiles of this wave
+    const int mine = (n - wave + kDecodeWaves - 1) >> 2;   // tiles of this wave
     if (mine > 0) {
       locate(0);
       load_keys(tile, 0);
@@ -430,8 +435,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
           for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
         }
         if (whole) {
-          const int64_t trow = it.l.start + at / group;
-          const int hq = head * group + at % group;
+          const int token = div_group(a, at), hq = head * group + at - token * group;
+          const int64_t trow = it.l.start + token;
           const float inv = den == 0.f ? 0.f : vs / den;
           if (a.out_bf16)
             *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
@@ -454,11 +459,11 @@ template <int D>
 __global__ __launch_bounds__(256) void attention_decode_join_kernel(AttentionArgs a) {
   const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
   const int hkv = a.cache.heads, group = a.group;
-  const int64_t r = blockIdx.x / hkv;
-  const int head = blockIdx.x % hkv;
+  const int r = blockIdx.x / hkv, head = blockIdx.x % hkv;
   const int64_t p0 = ws.prefix[r], tiles = ws.prefix[r + 1] - p0, per = ws.prefix[a.requests + 1];
   if (tiles == 0) return;
-  const int64_t x0 = p0 * hkv + head * tiles, g0 = x0 / per, g1 = (x0 + tiles - 1) / per;
+  const int64_t x0 = p0 * hkv + head * tiles;
+  const int g0 = (int)div_f64(x0, per), g1 = (int)div_f64(x0 + tiles - 1, per);
   if (g0 == g1) return;
   const RequestLens l = request_lens(a, r);
   const int nrows = (int)l.tokens * group;
@@ -468,21 +473,12 @@ __global__ __launch_bounds__(256) void attention_decode_join_kernel(AttentionArg
     if (e >= nrows * (D / 4)) return;
     const int at = e / (D / 4), d = (e % (D / 4)) * 4;
     // workgroup g's part is its first unless the item starts inside g's share
-    auto slot_of = [&](int64_t wg) { return (wg * 2 + (x0 > wg * per ? 1 : 0)) * kDecodeRows + at; };
-    float top = -INFINITY, den = 0.f;
-    for (int64_t wg = g0; wg <= g1; ++wg) top = fmaxf(top, ws.ml[slot_of(wg)].x);
-    f32x4 num = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t wg = g0; wg <= g1; ++wg) {
-      const int64_t slot = slot_of(wg);
-      const float2 ml = ws.ml[slot];
-      const float by = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
-      den = fmaf(by, ml.y, den);
-      const f32x4 ow = *(const f32x4*)(ws.o + slot * D + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
-    }
-    const int64_t trow = l.start + at / group;
-    const int hq = head * group + at % group;
+    auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (x0 > wg * per ? 1 : 0)) * kDecodeRows + at; };
+    float den;
+    f32x4 num;
+    const float top = join_parts<D>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
+    const int token = div_group(a, at), hq = head * group + at - token * group;
+    const int64_t trow = l.start + token;
     const float inv = den == 0.f ? 0.f : vs / den;
     if (a.out_bf16)
       *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
@@ -503,7 +499,7 @@ template <int D, bool FP8>
 hipError_t launch(const AttentionArgs& a, hipStream_t st) {
   // rows a request may have here: one fragment of 16 or two
   const int64_t rows = min(a.max_new, (int64_t)(kDecodeRows / a.group)) * a.group;
-  const unsigned grid = D <= 128 ? kDecodeGrid : kDecodeGrid / 2;   // as many workgroups as the registers let be resident
+  const unsigned grid = decode_grid(D);
   if (rows <= 16)
     attention_decode_kernel<D, FP8, 1><<<grid, kThreads, 0, st>>>(a);
   else

@@ -58,9 +58,12 @@ struct AttentionArgs {
   float* lse;                  // [tokens, hq] or null
   void* workspace;
   int64_t ld_q, ld_table, ld_out, requests, tokens, max_new, max_seq, max_pages;
-  int64_t window;              // 0: none
+  int window;                  // 0: none
   float scale;
   int hq, group, out_bf16;
+  // n / group = mulhi(n, group_mul) >> group_shift for n < 2^31, group > 1; set by the launcher
+  uint32_t group_mul;
+  int group_shift;
 };
 size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_new,
                                  int64_t max_seq);

@@ -20,6 +20,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 64 * kChunkWaves;
+constexpr int kExtraKeys = 512;
 constexpr int kSlots = 4;    // tiles in LDS: tile j lies in slot j % 4
 
 // LDS layout of a tile: [keys][D] bf16, the 16-byte pieces of a row permuted so
@@ -68,9 +69,11 @@ __device__ __forceinline__ void phase_barrier() {
 
 // The work of all row tiles and KV heads forms one line that a fixed grid shares
 // evenly.  A row tile's length on it is the keys that its last row may see, in
-// units of 1 / group keys, and a constant for what a tile costs beside; it
-// grows by 256 from a request's tile to the next until the window ends it, so a
-// request's length has a closed form.
+// units of 1 / group keys, and `extra`, what a tile costs beside (about 11 us:
+// its queries, page numbers and first keys have to arrive); it grows by 256 from
+// a request's tile to the next until the window ends it, so a request's length
+// has a closed form.  A cut between two shares that falls less than `extra` from
+// a tile's end or start is moved there.
 struct ChunkLine {
   int tiles, rising;
   int64_t context, cap, extra;
@@ -78,10 +81,10 @@ struct ChunkLine {
 __device__ __forceinline__ ChunkLine chunk_line(const AttentionArgs& a, const RequestLens& l) {
   ChunkLine c;
   const int rows = l.tokens * a.group;
-  c.tiles = rows > kDecodeRows ? (rows + kChunkRows - 1) / kChunkRows : 0;
+  c.tiles = rows > a.stream_rows ? (rows + kChunkRows - 1) / kChunkRows : 0;
   c.context = (int64_t)max(l.pos0, 0) * a.group;
   c.cap = a.window ? (int64_t)a.window * a.group + kChunkRows : INT64_MAX / 4;
-  c.extra = 128 * a.group;
+  c.extra = (int64_t)kExtraKeys * a.group;
   c.rising = (int)min(max((c.cap - c.context) >> 8, (int64_t)0), (int64_t)c.tiles);
   return c;
 }
@@ -96,7 +99,7 @@ __device__ __forceinline__ int64_t line_before(const ChunkLine& c, int b) {   //
 
 struct ChunkWorkspace {
   int64_t* prefix;   // [requests + 1]: length before a request (of one head); then a workgroup's share
-  float2* ml;        // [2 * grid][kChunkRows]
+  float2* ml;        // [2 * grid][kChunkRows]: a workgroup's part that begins inside a tile, and that begins with one
   float* o;          // [2 * grid][kChunkRows][dim]
 };
 __host__ __device__ inline ChunkWorkspace chunk_workspace(void* ws, int64_t requests) {
@@ -175,9 +178,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     before[tid + 1] = inc;
     __syncthreads();
     per_head = uniform(before[kThreads]);
-    // Shares of at least four tiles' keys.  Workgroups take their shares XCD by XCD,
-    // so that those of an XCD, which have one L2, read the same heads' keys.
-    const int64_t share = uniform(max((per_head * hkv + kChunkGrid - 1) / kChunkGrid, (int64_t)384 * group));
+    // Workgroups take their shares XCD by XCD, so that those of an XCD, which have one
+    // L2, read the same heads' keys.
+    const int64_t share = uniform(max((per_head * hkv + kChunkGrid - 1) / kChunkGrid, (int64_t)kExtraKeys * group));
     if (place == 0) {
       int64_t t = inc - own;
 #pragma unroll 1
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     const RowTile t = row_tile(a, numbers - 1 - (int)blockIdx.x / hkv);
     r = uniform(t.r), b = uniform(t.b);
     l = request_lens(a, r);
-    if (l.tokens * group <= kDecodeRows || b < 0 || b * kChunkRows >= l.tokens * group) return;
+    if (l.tokens * group <= a.stream_rows || b < 0 || b * kChunkRows >= l.tokens * group) return;
     x = x_end;
   } else {                    // a share of the line
     head = 0;
@@ -237,10 +240,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       if (base + line_before(line, mid) <= y) b = mid; else b_end = mid;
     }
     b = uniform(b);
-    const int64_t length = line_length(line, b), from = y - base - line_before(line, b), to = min(from + (x_end - x), length);
+    const int64_t length = line_length(line, b), offset = y - base - line_before(line, b);
+    int64_t from = offset, to = min(from + (x_end - x), length);
+    if (x == x_begin) from = from < line.extra ? 0 : length - from < line.extra ? length : from;
+    to = to < line.extra ? 0 : length - to < line.extra ? length : to;
+    x = uniform(x + length - offset);                     // the next tile begins there
+    if (from >= to) continue;
     whole = uniform((int)(to - from == length));
-    part = x == x_begin ? 0 : 1;
-    x = uniform(x + to - from);
+    part = from == 0;                                     // at most one part begins with its tile, and one inside
     share_from = (double)from / (double)length;           // the same on both sides of a cut
     share_to = to == length ? 1. : (double)to / (double)length;
   }
@@ -607,15 +614,15 @@ __global__ __launch_bounds__(256) void attention_chunk_join_kernel(AttentionArgs
   if (t.b < 0 || t.b >= line.tiles) return;
   const int64_t share = ws.prefix[a.requests + 1];
   const int64_t x0 = head * ws.prefix[a.requests] + ws.prefix[t.r] + line_before(line, t.b);
-  const int g0 = (int)div_f64(x0, share), g1 = (int)div_f64(x0 + line_length(line, t.b) - 1, share);
-  if (g0 == g1) return;
+  // the first part is held by the workgroup of the last cut that was moved to the tile's start or before it
+  const int g0 = (int)div_f64(x0 + line.extra - 1, share), g1 = (int)div_f64(x0 + line_length(line, t.b) - line.extra, share);
+  if (g0 >= g1) return;
   const int nrows = min(l.tokens * group - t.b * kChunkRows, kChunkRows);
   const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
   for (int e = threadIdx.x; e < 32 * (D / 4); e += 256) {
     const int at = blockIdx.y * 32 + e / (D / 4), d = (e % (D / 4)) * 4;
     if (at >= nrows) return;
-    // workgroup g's part is its first unless the tile begins inside g's share
-    auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (x0 > wg * share ? 1 : 0)) * kChunkRows + at; };
+    auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (wg == g0 ? 1 : 0)) * kChunkRows + at; };
     float den;
     f32x4 num;
     const float top = join_parts<D>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
@@ -666,15 +673,20 @@ hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipSt
 // ------------------------------------------------------------- dispatch ----
 
 // A request with at most 32 rows a KV head goes to the streaming kernel, any
-// other to the tiled one; both are launched where the batch may hold both.
-static bool may_stream(int64_t max_new, int group) { return max_new > 0 && group <= kDecodeRows; }
+// other to the tiled one; both are launched where the batch may hold both.  Where
+// the batch has 64 rows a request and more on average, the tiled kernel takes all
+// of them: it streams a lone token's keys at 4 TB/s, and two launches are spared
+// (10 us of a 2048-token prompt's 95).
 static bool may_tile(int64_t max_new, int group) { return max_new * group > kDecodeRows; }
+static bool may_stream(int64_t tokens, int64_t requests, int64_t max_new, int group) {
+  return max_new > 0 && group <= kDecodeRows && !(may_tile(max_new, group) && tokens * group >= 64 * requests);
+}
 
 size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_new,
                                  int64_t max_seq) {
   const int group = hq / hkv;
   size_t n = 16;
-  if (may_stream(max_new, group)) n += (attention_decode_workspace(requests, dim) + 255) / 256 * 256;
+  if (may_stream(tokens, requests, max_new, group)) n += (attention_decode_workspace(requests, dim) + 255) / 256 * 256;
   if (may_tile(max_new, group)) n += attention_chunk_workspace(requests, dim);
   return n;
 }
@@ -688,7 +700,9 @@ hipError_t launch_paged_attention(const AttentionArgs& args, hipStream_t st) {
     a.group_shift = power ? s - 1 : s;
   }
   uint8_t* ws = (uint8_t*)a.workspace;
-  if (may_stream(a.max_new, a.group)) {
+  a.stream_rows = 0;
+  if (may_stream(a.tokens, a.requests, a.max_new, a.group)) {
+    a.stream_rows = kDecodeRows;
     hipError_t e = launch_attention_decode(a, st);
     if (e != hipSuccess) return e;
     ws += (attention_decode_workspace(a.requests, a.cache.dim) + 255) / 256 * 256;

@@ -64,6 +64,7 @@ struct AttentionArgs {
   // n / group = mulhi(n, group_mul) >> group_shift for n < 2^31, group > 1; set by the launcher
   uint32_t group_mul;
   int group_shift;
+  int stream_rows;             // requests with at most so many rows a KV head are the streaming kernel's; likewise
 };
 size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_new,
                                  int64_t max_seq);

@@ -456,7 +456,8 @@ int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t l
  *                (multiple of 4), 16-byte aligned.
  *   lse          optional fp32 [tokens, num_heads] contiguous (natural log).
  *   workspace    16-byte aligned, at least paged_attention_workspace_bytes of
- *                the same sizes; any contents; not shared by calls in flight on
+ *                the same sizes; its first 2048 bytes zero before its first use
+ *                (each call leaves them so); not shared by calls in flight on
  *                different streams.
  * tokens == 0 or num_requests == 0 enqueues nothing.  Results are
  * deterministic.

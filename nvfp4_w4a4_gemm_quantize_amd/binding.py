@@ -525,9 +525,13 @@ def paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size, max_token
     if plan is None:
         q_start, seq_lens, positions, counts = ctx_lens.new_empty(2 * R + 5 + max_tokens).split((R + 1, R, max_tokens, 4))
         plan = PagedPlan(q_start, seq_lens, positions, ctx_lens.new_empty(max_tokens, dtype=_i64t), counts)
-    rc = lib.paged_plan(ctx, new, R, page_size, free, F, cursor, table, cols, ld, _vec(plan.q_start, _i32, R + 1, "q_start"),
-                        _vec(plan.seq_lens, _i32, R, "seq_lens"), _vec(plan.positions, _i32, max_tokens, "positions"),
-                        _vec(plan.slots, _i64t, max_tokens, "slots"), max_tokens, _vec(plan.counts, _i32, 4, "counts"),
+        p0 = q_start.data_ptr()
+        p1, p2, p3, p4 = p0 + 4 * (R + 1), p0 + 4 * (2 * R + 1), plan.slots.data_ptr(), p0 + 4 * (2 * R + 1 + max_tokens)
+    else:
+        p0, p1 = _vec(plan.q_start, _i32, R + 1, "q_start"), _vec(plan.seq_lens, _i32, R, "seq_lens")
+        p2, p3 = _vec(plan.positions, _i32, max_tokens, "positions"), _vec(plan.slots, _i64t, max_tokens, "slots")
+        p4 = _vec(plan.counts, _i32, 4, "counts")
+    rc = lib.paged_plan(ctx, new, R, page_size, free, F, cursor, table, cols, ld, p0, p1, p2, p3, max_tokens, p4,
                         _raw_stream(ctx_lens.get_device()))
     if rc:
         _check(rc, "paged_plan")
@@ -551,11 +555,13 @@ def paged_kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
 
 
 def paged_attention_workspace(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new, max_seq, device="cuda"):
-    """A workspace for paged_attention calls of these sizes."""
+    """A workspace for paged_attention calls of these sizes (zero where the first call needs it)."""
     n = load().paged_attention_workspace_bytes(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new, max_seq)
     if n == 0:
         raise NVFP4Error("paged_attention does not take these sizes")
-    return torch.empty(n, dtype=_u8, device=device)
+    workspace = torch.empty(n, dtype=_u8, device=device)
+    workspace[:2048].zero_()
+    return workspace
 
 
 def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new, max_seq, scale=None, window=0,

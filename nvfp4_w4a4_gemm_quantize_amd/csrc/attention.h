@@ -78,47 +78,84 @@ __device__ __forceinline__ int div_group(const AttentionArgs& a, int n) {
 // floor(n / d) through the fp64 reciprocal, 0 <= n < 2^43, 0 < d.
 __device__ __forceinline__ int64_t div_f64(int64_t n, int64_t d) { return (int64_t)((double)n / (double)d); }
 
+// Two neighbouring floats as one device-scope atomic: past the XCD's own L2.
+__device__ __forceinline__ void store_shared(float* p, float x, float y) {
+  const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+  __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_shared(const float* p) {
+  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+// This wave's stores have been acknowledged, and none is moved behind this.
+__device__ __forceinline__ void wait_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // Parts of workgroups g0 .. g1 joined in their order, four columns at d: their
-// common maximum (log2 units), the sum and the unnormalised output.  Four parts'
+// common maximum (log2 units), the sum and the unnormalised output.  Eight parts'
 // loads are in flight together.
-template <int D, class Slot>
+// SHARED: parts that workgroups of the same launch have left (load_shared).
+template <int D, bool SHARED, class Slot>
 __device__ __forceinline__ float join_parts(const float2* ml, const float* o, Slot slot_of, int g0, int g1, int d, float* den,
                                             f32x4* num) {
+  constexpr int kAtOnce = 8;
   float top = -INFINITY;
   *den = 0.f;
   *num = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int g = g0; g <= g1; g += 4) {
-    float2 m[4];
-    f32x4 x[4];
+#pragma unroll 1
+  for (int g = g0; g <= g1; g += kAtOnce) {
+    float2 m[kAtOnce];
+    f32x4 x[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const int64_t slot = slot_of(min(g + i, g1));
-      m[i] = ml[slot];
-      x[i] = *(const f32x4*)(o + slot * D + d);
+      if constexpr (SHARED) {
+        m[i] = load_shared((const float*)(ml + slot));
+        const float2 lo = load_shared(o + slot * D + d), hi = load_shared(o + slot * D + d + 2);
+        x[i] = f32x4{lo.x, lo.y, hi.x, hi.y};
+      } else {
+        m[i] = ml[slot];
+        x[i] = *(const f32x4*)(o + slot * D + d);
+      }
     }
     float to = top;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) to = fmaxf(to, m[i].x);
+    for (int i = 0; i < kAtOnce; ++i) to = fmaxf(to, m[i].x);
     const float by = top == to ? 1.f : exp2_fast(top - to);   // -inf before the first part: 0
     *den *= by;
     *num *= by;
     top = to;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float w = g + i > g1 || m[i].x == -INFINITY ? 0.f : exp2_fast(m[i].x - top);
-      const float part = g + i > g1 ? 0.f : m[i].y;
-      *den = fmaf(w, part, *den);
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (g + i > g1) break;
+      const float w = m[i].x == -INFINITY ? 0.f : exp2_fast(m[i].x - top);
+      *den = fmaf(w, m[i].y, *den);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) (*num)[k] = fmaf(w, g + i > g1 ? 0.f : x[i][k], (*num)[k]);
+      for (int k = 0; k < 4; ++k) (*num)[k] = fmaf(w, x[i][k], (*num)[k]);
     }
   }
   return top;
 }
 
+// Four columns of row `at` of a head's rows that begin at token `start`, and its
+// log-sum-exp: num / den * vs and log(den) + top.
+template <int D>
+__device__ __forceinline__ void write_row(const AttentionArgs& a, int start, int head, int at, int d, float top, float den,
+                                          f32x4 num, float vs) {
+  const int token = div_group(a, at), hq = head * a.group + at - token * a.group;
+  const int64_t trow = start + token;
+  const float inv = den == 0.f ? 0.f : vs / den;
+  if (a.out_bf16)
+    *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
+  else
+    *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
+  if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
+}
+
 // Launches of the two kernels and of their joins (attention_*.hip).
 hipError_t launch_attention_decode(const AttentionArgs& a, hipStream_t st);
 hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipStream_t st);
-size_t attention_decode_workspace(int64_t requests, int dim);
+constexpr size_t kArrivedBytes = kDecodeGrid * sizeof(uint32_t);
+size_t attention_decode_workspace(int dim);   // beside the counters
 size_t attention_chunk_workspace(int64_t requests, int dim);
 
 }  // namespace nvfp4

@@ -625,15 +625,8 @@ __global__ __launch_bounds__(256) void attention_chunk_join_kernel(AttentionArgs
     auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (wg == g0 ? 1 : 0)) * kChunkRows + at; };
     float den;
     f32x4 num;
-    const float top = join_parts<D>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
-    const int row = t.b * kChunkRows + at, token = div_group(a, row), hq = head * group + row - token * group;
-    const int64_t trow = l.start + token;
-    const float inv = den == 0.f ? 0.f : vs / den;
-    if (a.out_bf16)
-      *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
-    else
-      *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
-    if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
+    const float top = join_parts<D, false>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
+    write_row<D>(a, l.start, head, t.b * kChunkRows + at, d, top, den, num, vs);
   }
 }
 
@@ -685,8 +678,8 @@ static bool may_stream(int64_t tokens, int64_t requests, int64_t max_new, int gr
 size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_new,
                                  int64_t max_seq) {
   const int group = hq / hkv;
-  size_t n = 16;
-  if (may_stream(tokens, requests, max_new, group)) n += (attention_decode_workspace(requests, dim) + 255) / 256 * 256;
+  size_t n = 16 + kArrivedBytes;
+  if (may_stream(tokens, requests, max_new, group)) n += (attention_decode_workspace(dim) + 255) / 256 * 256;
   if (may_tile(max_new, group)) n += attention_chunk_workspace(requests, dim);
   return n;
 }
@@ -699,13 +692,14 @@ hipError_t launch_paged_attention(const AttentionArgs& args, hipStream_t st) {
     a.group_mul = power ? 1u << 31 : (uint32_t)(((uint64_t)1 << (32 + s)) / a.group + 1);
     a.group_shift = power ? s - 1 : s;
   }
-  uint8_t* ws = (uint8_t*)a.workspace;
+  // the counters that have to be 0 between calls lie first whichever kernels run
+  uint8_t* ws = (uint8_t*)a.workspace + kArrivedBytes;
   a.stream_rows = 0;
   if (may_stream(a.tokens, a.requests, a.max_new, a.group)) {
     a.stream_rows = kDecodeRows;
     hipError_t e = launch_attention_decode(a, st);
     if (e != hipSuccess) return e;
-    ws += (attention_decode_workspace(a.requests, a.cache.dim) + 255) / 256 * 256;
+    ws += (attention_decode_workspace(a.cache.dim) + 255) / 256 * 256;
   }
   return may_tile(a.max_new, a.group) ? launch_attention_chunk(a, ws, st) : hipSuccess;
 }

@@ -27,9 +27,11 @@
 // Split: the key tiles of all requests and KV heads form one line that a fixed
 // grid shares evenly, so a long request among short ones, or one request alone,
 // fills the chip.  A workgroup that holds all of a (request, head) writes its
-// output; a part leaves (max, sum, O) in the workspace (at most two a
-// workgroup) and a second kernel joins the parts in the order of their keys.
-// The line's prefix is recomputed by every workgroup (8 bytes a request).
+// output; a part leaves (max, sum, O) in the workspace (at most two a workgroup),
+// and the workgroup whose part arrives last joins all of them in the order of
+// their keys, whatever the order in which they came (a second kernel for that
+// cost 4 us of the GPU's time and as much of the host's, a third of one decoded
+// token).  The line's prefix is recomputed by every workgroup (8 bytes a request).
 #include <float.h>
 
 #include "attention.h"
@@ -41,16 +43,15 @@ namespace {
 constexpr int kThreads = 64 * kDecodeWaves;
 
 struct DecodeWorkspace {
-  int64_t* prefix;   // [requests + 1] tiles before a request (of one head); then the tiles per workgroup
-  float2* ml;        // [2 * grid][kDecodeRows] (max in log2 units, sum)
-  float* o;          // [2 * grid][kDecodeRows][dim]
+  uint32_t* arrived;   // [grid] parts that have been left of the item that begins in a workgroup's share; 0 between calls
+  float2* ml;          // [2 * grid][kDecodeRows] (max in log2 units, sum)
+  float* o;            // [2 * grid][kDecodeRows][dim]
 };
-__host__ __device__ inline DecodeWorkspace decode_workspace(void* ws, int64_t requests) {
+__host__ __device__ inline DecodeWorkspace decode_workspace(void* ws) {
   DecodeWorkspace w;
-  w.prefix = (int64_t*)ws;
-  uint8_t* p = (uint8_t*)ws + ((requests + 2) * 8 + 255) / 256 * 256;
-  w.ml = (float2*)p;
-  w.o = (float*)(p + (size_t)2 * kDecodeGrid * kDecodeRows * sizeof(float2));
+  w.arrived = (uint32_t*)ws;
+  w.ml = (float2*)((uint8_t*)ws + kArrivedBytes);
+  w.o = (float*)(w.ml + 2 * kDecodeGrid * kDecodeRows);
   return w;
 }
 
@@ -113,11 +114,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   __shared__ int64_t wave_sum[kDecodeWaves];
   __shared__ __attribute__((aligned(16))) float o_part[kDecodeWaves][16][LD];
   __shared__ float2 ml_part[kDecodeWaves][16];
+  __shared__ int last_part;
 
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hkv = a.cache.heads, group = a.group;
-  const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
+  const DecodeWorkspace ws = decode_workspace(a.workspace);
 
   // prefix of the tiles over runs of requests
   const int requests = (int)a.requests, run = (requests + kThreads - 1) / kThreads;
@@ -139,18 +141,6 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   const int64_t total = uniform(before[kThreads] * hkv);
   // at least one tile a wave: a smaller share would only add parts to join
   const int64_t per = max((total + GRID - 1) / GRID, (int64_t)kDecodeWaves);
-  if (blockIdx.x == 0) {
-    int64_t t = inc - sum;
-    for (int r = r0; r < r1; ++r) {
-      ws.prefix[r] = t;
-      t += decode_item(a, r).tiles;
-    }
-    if (tid == 0) {
-      ws.prefix[a.requests] = before[kThreads];
-      ws.prefix[a.requests + 1] = per;
-    }
-  }
-
   const int64_t x_begin = blockIdx.x * per, x_end = min(x_begin + per, total);
   const int page_mask = (1 << a.cache.page_shift) - 1;
   const uint32_t page_units = (uint32_t)(a.cache.page_stride * EB / 16), row_bytes = (uint32_t)a.cache.token_stride * EB;
@@ -435,62 +425,46 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
           for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
         }
         if (whole) {
-          const int token = div_group(a, at), hq = head * group + at - token * group;
-          const int64_t trow = it.l.start + token;
-          const float inv = den == 0.f ? 0.f : vs / den;
-          if (a.out_bf16)
-            *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
-          else
-            *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
-          if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
+          write_row<D>(a, it.l.start, head, at, d, top, den, num, vs);
         } else {
           const int64_t slot = ((int64_t)blockIdx.x * 2 + part) * kDecodeRows + at;
-          *(f32x4*)(ws.o + slot * D + d) = num;
-          if (d == 0) ws.ml[slot] = make_float2(top, den);
+          store_shared(ws.o + slot * D + d, num[0], num[1]);
+          store_shared(ws.o + slot * D + d + 2, num[2], num[3]);
+          if (d == 0) store_shared((float*)&ws.ml[slot], top, den);
         }
       }
     }
+    if (whole) continue;
+
+    // the item's parts lie in workgroups g0 .. g1; every one counts itself at g0,
+    // in whose share no other item can begin and go on
+    const int64_t x0 = x - n - first;
+    const int g0 = uniform((int)div_f64(x0, per)), g1 = uniform((int)div_f64(x0 + it.tiles - 1, per));
+    // Parts are written and read as device-scope atomics, which pass the L2 that an XCD
+    // keeps for itself, so that a part is where every XCD sees it once its stores are
+    // acknowledged (the wait), and no cache has to be written back or invalidated: a
+    // release and an acquire of the device cost 30 us of the drafts' 140.
+    wait_stores();
+    __syncthreads();
+    if (tid == 0) last_part = __hip_atomic_fetch_add(&ws.arrived[g0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(g1 - g0);
+    __syncthreads();
+    if (!last_part) continue;
+    for (int e = tid; e < nrows * (D / 4); e += kThreads) {
+      const int at = e / (D / 4), d = (e % (D / 4)) * 4;
+      // workgroup g's part is its first unless the item starts inside g's share
+      auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (x0 > wg * per ? 1 : 0)) * kDecodeRows + at; };
+      float den;
+      f32x4 num;
+      const float top = join_parts<D, true>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
+      write_row<D>(a, it.l.start, head, at, d, top, den, num, vs);
+    }
+    if (tid == 0) ws.arrived[g0] = 0;   // for the next call
   }
 }
 
-// Joins the parts of a (request, head) that several workgroups of the
-// streaming kernel hold, in the order of their keys; four columns a thread.
-template <int D>
-__global__ __launch_bounds__(256) void attention_decode_join_kernel(AttentionArgs a) {
-  const DecodeWorkspace ws = decode_workspace(a.workspace, a.requests);
-  const int hkv = a.cache.heads, group = a.group;
-  const int r = blockIdx.x / hkv, head = blockIdx.x % hkv;
-  const int64_t p0 = ws.prefix[r], tiles = ws.prefix[r + 1] - p0, per = ws.prefix[a.requests + 1];
-  if (tiles == 0) return;
-  const int64_t x0 = p0 * hkv + head * tiles;
-  const int g0 = (int)div_f64(x0, per), g1 = (int)div_f64(x0 + tiles - 1, per);
-  if (g0 == g1) return;
-  const RequestLens l = request_lens(a, r);
-  const int nrows = (int)l.tokens * group;
-  const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
-  {
-    const int e = blockIdx.y * 256 + threadIdx.x;
-    if (e >= nrows * (D / 4)) return;
-    const int at = e / (D / 4), d = (e % (D / 4)) * 4;
-    // workgroup g's part is its first unless the item starts inside g's share
-    auto slot_of = [&](int wg) { return (int64_t)(wg * 2 + (x0 > wg * per ? 1 : 0)) * kDecodeRows + at; };
-    float den;
-    f32x4 num;
-    const float top = join_parts<D>(ws.ml, ws.o, slot_of, g0, g1, d, &den, &num);
-    const int token = div_group(a, at), hq = head * group + at - token * group;
-    const int64_t trow = l.start + token;
-    const float inv = den == 0.f ? 0.f : vs / den;
-    if (a.out_bf16)
-      *(u32x2*)((uint16_t*)a.out + trow * a.ld_out + hq * D + d) = u32x2{pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv)};
-    else
-      *(f32x4*)((float*)a.out + trow * a.ld_out + hq * D + d) = num * inv;
-    if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
-  }
-}
-
-size_t attention_decode_workspace(int64_t requests, int dim) {
-  const DecodeWorkspace w = decode_workspace(nullptr, requests);
-  return (size_t)(uintptr_t)w.o + (size_t)2 * kDecodeGrid * kDecodeRows * dim * sizeof(float);
+size_t attention_decode_workspace(int dim) {
+  const DecodeWorkspace w = decode_workspace(nullptr);
+  return (size_t)(uintptr_t)w.o - kArrivedBytes + (size_t)2 * kDecodeGrid * kDecodeRows * dim * sizeof(float);
 }
 
 namespace {
@@ -504,9 +478,6 @@ hipError_t launch(const AttentionArgs& a, hipStream_t st) {
     attention_decode_kernel<D, FP8, 1><<<grid, kThreads, 0, st>>>(a);
   else
     attention_decode_kernel<D, FP8, 2><<<grid, kThreads, 0, st>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  attention_decode_join_kernel<D><<<dim3((unsigned)(a.requests * a.cache.heads), (unsigned)((rows * (D / 4) + 255) / 256)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -605,11 +605,13 @@ def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new
 
 
 def verify_drafts_workspace(num_requests, max_drafts, vocab, device="cuda"):
-    """A workspace for verify_drafts calls of these sizes."""
+    """A workspace for verify_drafts calls of these sizes (zero where the first call needs it)."""
     n = load().verify_drafts_workspace_bytes(num_requests, max_drafts, vocab)
     if n == 0:
         raise NVFP4Error("verify_drafts does not take these sizes")
-    return torch.empty(n, dtype=_u8, device=device)
+    workspace = torch.empty(n, dtype=_u8, device=device)
+    workspace[:1 << 18].zero_()
+    return workspace
 
 
 def verify_drafts(logits, row_start, num_drafts, draft_tokens, uniform, noise, draft_probs=None, temperature=None,

@@ -34,6 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kBatch = 4;              // vectors of 8 logits that a thread has in flight
 constexpr int64_t kSlice = 8192;      // elements of a slice at least: one batch a thread
 constexpr int kMaxSlices = 64;        // one a lane of the joins
+constexpr int kMaxRequests = 65536;   // counters, at one place whatever a call's sizes
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct RowPart {
@@ -45,12 +46,14 @@ struct DrawPart {
   int32_t at, any, pad;   // any: a weight is positive
 };
 struct VerifyWorkspace {
+  uint32_t* arrived;   // [kMaxRequests] slices that have been left of a request; 0 between calls
   RowPart* rows;       // [requests][max_drafts + 1][slices]
   DrawPart* draws;     // [requests][slices]
 };
 __host__ __device__ inline VerifyWorkspace verify_workspace(void* ws, int64_t requests, int64_t max_drafts, int slices) {
   VerifyWorkspace w;
-  w.rows = (RowPart*)ws;
+  w.arrived = (uint32_t*)ws;
+  w.rows = (RowPart*)(w.arrived + kMaxRequests);
   w.draws = (DrawPart*)(w.rows + requests * (max_drafts + 1) * slices);
   return w;
 }
@@ -320,35 +323,18 @@ __device__ DrawPart race(const void* row, const RowPart& p, float k, const float
 
 }  // namespace
 
-// Grid (slices, requests): the race over a slice of the row after the kept drafts.
+// Grid (slices, requests): the race over a slice of the row after the kept drafts,
+// and by the last slice to arrive (or the first, where there is nothing to draw) the
+// tokens, their count and their log-probabilities.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, VerifyWorkspace ws) {
   __shared__ RowPart rows[kThreads];
-  const int slices = gridDim.x, slice = blockIdx.x;
-  const int64_t r = blockIdx.y;
+  __shared__ int last_slice;
+  const int slices = gridDim.x, slice = blockIdx.x, i = threadIdx.x;
+  const int64_t r = blockIdx.y, out = r * (a.max_drafts + 1) + i;
   const int n = drafts_of(a, r);
-  if (n < 0) return;
-  bool greedy;
-  const float k = kLog2e / temperature_of(a, r, &greedy);
-  if (greedy) return;   // the argument of the maximum is known
-  const int kept = accept<F32>(a, ws, r, n, slices, k, greedy, rows);
-  const bool rest = kept < n;   // a draft was refused: draw from what it leaves
-  const int64_t each = slice_length(a.vocab, slices), v0 = min(slice * each, a.vocab), v1 = min(v0 + each, a.vocab);
-  const DrawPart d = race<F32>(logits_row<F32>(a, r, kept), rows[kept], k,
-                               rest && a.draft_probs ? a.draft_probs + (r * a.max_drafts + kept) * a.ld_probs : nullptr,
-                               rest && !a.draft_probs ? a.draft_tokens[r * a.max_drafts + kept] : -1,
-                               a.noise + r * a.ld_noise, v0, v1);
-  if (threadIdx.x == 0) ws.draws[r * slices + slice] = d;
-}
-
-// Grid (requests): the tokens, their count and their log-probabilities.
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void verify_join_kernel(VerifyArgs a, VerifyWorkspace ws, int slices) {
-  __shared__ RowPart rows[kThreads];
-  const int64_t r = blockIdx.x;
-  const int i = threadIdx.x, n = drafts_of(a, r);
-  const int64_t out = r * (a.max_drafts + 1) + i;
   if (n < 0) {
+    if (slice > 0) return;
     if (i <= a.max_drafts) {
       a.out_tokens[out] = -1;
       a.logprobs[out] = 0.f;
@@ -358,15 +344,43 @@ __global__ __launch_bounds__(kThreads) void verify_join_kernel(VerifyArgs a, Ver
   }
   bool greedy;
   const float t = temperature_of(a, r, &greedy), k = kLog2e / t;
-  DrawPart d = {-INFINITY, INT32_MAX, 0, 0};   // every wave joins the slices, a slice a lane
-  if (!greedy && (i & 63) < slices) d = ws.draws[r * slices + (i & 63)];
+  if (greedy && slice > 0) return;   // the argument of the maximum is known
   const int kept = accept<F32>(a, ws, r, n, slices, k, greedy, rows);
+  DrawPart d = {-INFINITY, INT32_MAX, 0, 0};
   if (!greedy) {
-    const Best b = wave_best(Best{d.score, d.at});
-    d = DrawPart{b.score, b.at, __any(d.any), 0};
+    const bool rest = kept < n;      // a draft was refused: draw from what it leaves
+    const void* row = logits_row<F32>(a, r, kept);
+    const float* noise = a.noise + r * a.ld_noise;
+    const int64_t each = slice_length(a.vocab, slices), v0 = min(slice * each, a.vocab), v1 = min(v0 + each, a.vocab);
+    d = race<F32>(row, rows[kept], k, rest && a.draft_probs ? a.draft_probs + (r * a.max_drafts + kept) * a.ld_probs : nullptr,
+                  rest && !a.draft_probs ? a.draft_tokens[r * a.max_drafts + kept] : -1, noise, v0, v1);
+    if (slices > 1) {
+      // Slices are left and read as device-scope atomics, which pass the L2 that an XCD
+      // keeps for itself: a slice is where every XCD sees it once its stores are
+      // acknowledged (the wait).
+      if (i == 0) {
+        uint64_t* to = (uint64_t*)(ws.draws + r * slices + slice);
+        __hip_atomic_store(to, (uint64_t)(uint32_t)d.at << 32 | __float_as_uint(d.score), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(to + 1, (uint64_t)d.any, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last_slice = __hip_atomic_fetch_add(&ws.arrived[r], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(slices - 1);
+      }
+      __syncthreads();
+      if (!last_slice) return;
+      if (i == 0) ws.arrived[r] = 0;   // for the next call
+      d = DrawPart{-INFINITY, INT32_MAX, 0, 0};
+      if ((i & 63) < slices) {         // every wave joins the slices, a slice a lane
+        const uint64_t* from = (const uint64_t*)(ws.draws + r * slices + (i & 63));
+        const uint64_t v = __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        d.score = __uint_as_float((uint32_t)v);
+        d.at = (int32_t)(v >> 32);
+        d.any = (int32_t)__hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      const Best b = wave_best(Best{d.score, d.at});
+      d = DrawPart{b.score, b.at, __any(d.any), 0};
+    }
     // a refused draft that leaves nothing (p = q up to rounding): p in its place
-    if (!d.any && kept < n)
-      d = race<F32>(logits_row<F32>(a, r, kept), rows[kept], k, nullptr, -1, a.noise + r * a.ld_noise, 0, a.vocab);
+    if (!d.any && rest) d = race<F32>(row, rows[kept], k, nullptr, -1, noise, 0, a.vocab);
   }
   if (i == 0) a.num_accepted[r] = kept;
   if (i > a.max_drafts) return;
@@ -397,9 +411,6 @@ hipError_t launch(const VerifyArgs& a, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   verify_draw_kernel<F32><<<dim3(slices, (unsigned)a.requests), kThreads, 0, st>>>(a, ws);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  verify_join_kernel<F32><<<(unsigned)a.requests, kThreads, 0, st>>>(a, ws, slices);
   return hipGetLastError();
 }
 

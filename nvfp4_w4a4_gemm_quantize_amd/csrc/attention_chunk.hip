@@ -144,6 +144,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   constexpr int LOADS = KT / RPI / kChunkWaves;   // such instructions a wave issues for K (and for V)
   constexpr bool SPARE = LOADS == 0;          // heads of 64 in FP8: half of the waves bring a tile
   constexpr int NL = SPARE ? 1 : LOADS;
+  // Softmax beside the matrix unit.  Heads of 64 and 128: the two waves of a SIMD take
+  // turns, one multiplies while the other computes weights (a prompt of 8192 over 8192
+  // keys, 40 heads of 128: 1750 us; mixed 1930 - 2000).  Heads of 256, whose O leaves a
+  // wave no registers for operands of two products at once: every wave weighs between
+  // the matrix instructions (4096 over 4096, 24 heads: 640 us, E4M3 810; turns 1336 and
+  // 1585, with 65 registers spilled).
+  constexpr bool MIXED = D == 256;
   __shared__ __attribute__((aligned(1024))) uint8_t lds_k[kSlots][KT * ROW], lds_v[kSlots][KT * ROW];
 
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
@@ -408,57 +415,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const int v_r = 4 * h + ((lane & 15) >> 2);
   const int v_row = v_r * ROW + (lane & 1) * 8, v_x = ((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<D>(v_r)) * 16;
 
-  auto key_fragment = [&](const uint8_t* kt, int e) {     // e-th of the first product: key fragment fastest
-    return *(const bf16x8*)(kt + (e % NK) * 32 * ROW + k_row + (((e / NK) * 32) ^ k_x));
+  auto key_fragment = [&](const uint8_t* kt, int f, int st) {        // keys 32f on, columns 16st on
+    return *(const bf16x8*)(kt + f * 32 * ROW + k_row + ((st * 32) ^ k_x));
   };
-  auto value_fragment = [&](const uint8_t* vt, int e) {   // e-th of the second product: O's fragment fastest
-    const uint8_t* vp = vt + (e / DF) * 16 * ROW + v_row + (((e % DF) * 64) ^ v_x);
+  auto value_fragment = [&](const uint8_t* vt, int u, int i) {       // keys 16u on, columns 32i on
+    const uint8_t* vp = vt + u * 16 * ROW + v_row + ((i * 64) ^ v_x);
     const u32x2 v0 = read_transposed(vp), v1 = read_transposed(vp + 8 * ROW);
     return __builtin_bit_cast(bf16x8, u32x4{v0[0], v0[1], v1[0], v1[1]});
   };
-  auto clear_scores = [&] {
-#pragma unroll
-    for (int f = 0; f < NK; ++f)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[f][j] = 0.f;
-  };
-  auto multiply_keys = [&](const bf16x8& kf, int e) {
-    s[e % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[e / NK], s[e % NK], 0, 0, 0);
-  };
-  auto multiply_values = [&](const bf16x8& vf, int e) {
-    o[e % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[e / DF], o[e % DF], 0, 0, 0);
-  };
-  // Both products, two fragments of each a step, their operands read kAhead
-  // steps before (an LDS read takes longer than the four instructions of a step);
-  // those of the first steps are read before the barrier that begins the phase.
-  constexpr int kAhead = D == 256 ? 1 : 2;
-  constexpr int STEPS = NK * DF;
-  bf16x8 vf[kAhead + 1][2], kf[kAhead + 1][2];
-  auto read_operands = [&](const uint8_t* kt, const uint8_t* vt, int t) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      vf[t % (kAhead + 1)][i] = value_fragment(vt, 2 * t + i);
-      kf[t % (kAhead + 1)][i] = key_fragment(kt, 2 * t + i);
-    }
-  };
-  auto products = [&](const uint8_t* kt, const uint8_t* vt, auto between) {
-    clear_scores();
-#pragma unroll
-    for (int t = 0; t < STEPS; ++t) {
-      if (t + kAhead < STEPS) {
-        read_operands(kt, vt, t + kAhead);
-        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);   // six LDS reads, then four products
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        multiply_values(vf[t % (kAhead + 1)][i], 2 * t + i);
-        multiply_keys(kf[t % (kAhead + 1)][i], 2 * t + i);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-      between(t);
-    }
-  };
-  auto softmax_step = [&](int j) {
+  // Scores of tile j that the lane's row does not see.
+  auto hide = [&](int j) {
     if (j < seen_from || j >= seen_to) {
       // a bit for every key of the tile that this lane's row sees
       const int bottom = my_low - j * KT, end = my_pos + 1 - j * KT;
@@ -473,13 +439,15 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
           s[f][i] = bits >> (8 * (i >> 2) + (i & 3)) & 1 ? s[f][i] : -INFINITY;
       }
     }
+  };
+  // Brings the maximum up to date.  It may lag behind by a factor of 2^8, which
+  // costs no precision: O is scaled anew only when it does not suffice any more.
+  auto raise = [&] {
     float top = s[0][0];
 #pragma unroll
     for (int f = 0; f < NK; ++f)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[f][i]);
-    // The maximum may lag behind by a factor of 2^8, which costs no precision: O
-    // is scaled anew only when it does not suffice any more.
     if (__any(c * (top - m) > 8.f || (m == -INFINITY && top > m))) {
       top = fmaxf(top, __shfl_xor(top, 32));
       const float to = fmaxf(m, top);
@@ -490,85 +458,255 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       for (int i = 0; i < DF; ++i)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[i][k] *= by;
-    }
-    const float ref = m == -INFINITY ? 0.f : c * m;
+      if constexpr (MIXED) {                 // the weights still to be multiplied, rounded once more
 #pragma unroll
-    for (int u = 0; u < 2 * NK; ++u) {
-      float e[8];
+        for (int u = 0; u < 2 * NK; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = exp2_fast(fmaf(s[u >> 1][8 * (u & 1) + i], c, -ref));
-      sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      // P in bf16, the matrix instruction's type with V: 2^-8 relative a term at most, averaged over the keys
-      p[u] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
+          for (int i = 0; i < 8; ++i) p[u][i] = (__bf16)((float)p[u][i] * by);
+      }
     }
+    return m == -INFINITY ? 0.f : c * m;
+  };
+  // Weights of 16 keys.  In bf16, the matrix instruction's type with V: 2^-8 relative a
+  // term at most, averaged over the keys.
+  auto weigh = [&](int u, float ref) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = exp2_fast(fmaf(s[u >> 1][8 * (u & 1) + i], c, -ref));
+    sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    u32x4 w = {pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])};
+    if constexpr (MIXED) asm volatile("" : "+v"(w), "+v"(sum));   // here, among the products, and not where the next turn needs them
+    p[u] = __builtin_bit_cast(bf16x8, w);
   };
 
   if (n > 0) {
-    // Before the loop: keys 0 - 2, values 0 and 1.  The loop begins at tile -1, whose
-    // values and weights are 0, so that tile 0's scores need no code of their own.
-    constexpr int kLead = FP8 ? 5 : 4;       // the tile whose keys are asked for while tile 0's values are multiplied
-    locate(0);
-    Offsets key_at, value_at;
+    if constexpr (!MIXED) {
+      // Both products, two fragments of each a step, their operands read kAhead
+      // steps before (an LDS read takes longer than the four instructions of a step);
+      // those of the first steps are read before the barrier that begins the phase.
+      constexpr int kAhead = 2;
+      constexpr int STEPS = NK * DF;
+      bf16x8 vf[kAhead + 1][2], kf[kAhead + 1][2];
+      auto read_operands = [&](const uint8_t* kt, const uint8_t* vt, int t) {
 #pragma unroll
-    for (int i = 0; i < KT * ROW / 16 / kThreads; ++i) *(u32x4*)(lds_v[3] + (i * kThreads + tid) * 16) = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll 1
-    for (int j = 0; j < 3; ++j) {
-      key_at = offsets_of(j);
-      bring_all(k_base, key_at, lds_k[j], k_voff, kr);
-      settle(lds_k[j], kr, false, 0);
-      if (j == 2) break;
-      bring_all(v_base, key_at, lds_v[j], v_voff, vr);
-      settle(lds_v[j], vr, true, held_keys(j));
-    }
-    value_at = key_at;
-    if constexpr (FP8) {                     // in registers: keys 3, values 2
-      bring_all(v_base, value_at, nullptr, v_voff, vr);
-      value_at = offsets_of(3);
-      bring_all(k_base, value_at, nullptr, k_voff, kr);
-    }
-    key_at = offsets_of(kLead - 1);
+        for (int i = 0; i < 2; ++i) {
+          vf[t % (kAhead + 1)][i] = value_fragment(vt, (2 * t + i) / DF, (2 * t + i) % DF);
+          kf[t % (kAhead + 1)][i] = key_fragment(kt, (2 * t + i) % NK, (2 * t + i) / NK);
+        }
+      };
+      auto products = [&](const uint8_t* kt, const uint8_t* vt, auto between) {
 #pragma unroll
-    for (int u = 0; u < 2 * NK; ++u) p[u] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-    wait_arrived<0>();
-#pragma unroll 1
-    for (int j = 0; j < 2; ++j)
-      if (j < held_from || j >= held_to) clear_values(lds_v[j], held_keys(j));
-    phase_barrier<true>();
-    // The two waves of a SIMD take turns: while waves 0-3 multiply, waves 4-7,
-    // one barrier behind, run their softmax, and the other way round.
-    if (wave >= kChunkWaves / 2) phase_barrier<false>();
+        for (int f = 0; f < NK; ++f)
 #pragma unroll
-    for (int t = 0; t < kAhead; ++t) read_operands(lds_k[0], lds_v[3], t);
+          for (int j = 0; j < 16; ++j) s[f][j] = 0.f;
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+          if (t + kAhead < STEPS) {
+            read_operands(kt, vt, t + kAhead);
+            __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);   // six LDS reads, then four products
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int e = 2 * t + i, at = t % (kAhead + 1);
+            o[e % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[at][i], p[e / DF], o[e % DF], 0, 0, 0);
+            s[e % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[at][i], q[e / NK], s[e % NK], 0, 0, 0);
+          }
+          __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+          between(t);
+        }
+      };
+      // Before the loop: keys 0 - 2, values 0 and 1.  The loop begins at tile -1, whose
+      // values and weights are 0, so that tile 0's scores need no code of their own.
+      constexpr int kLead = FP8 ? 5 : 4;       // the tile whose keys are asked for while tile 0's values are multiplied
+      locate(0);
+      Offsets key_at, value_at;
+#pragma unroll
+      for (int i = 0; i < KT * ROW / 16 / kThreads; ++i) *(u32x4*)(lds_v[3] + (i * kThreads + tid) * 16) = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll 1
-    for (int j = -1; j < n; ++j) {
-      // Products: O += values j, S = keys j + 1.  Tile j + 4's keys take the place of
-      // tile j's, tile j + 3's values that of tile j - 1's, which all have read; they
-      // are waited for in the next products and read at the end of the softmax after.
-      uint8_t* const free_k = lds_k[j & 3];
-      uint8_t* const free_v = lds_v[(j + 3) & 3];
-      settle(free_k, kr, false, 0);
-      settle(free_v, vr, true, FP8 && (j + 3 < held_from || j + 3 >= held_to) ? held_keys(j + 3) : kAll);
-      __builtin_amdgcn_s_setprio(1);
-      products(lds_k[(j + 1) & 3], lds_v[j & 3], [&](int step) {
-        if (step < NL) bring(k_base, key_at, step, free_k, k_voff, kr);
-        else if (step < 2 * NL) bring(v_base, value_at, step - NL, free_v, v_voff, vr);
-      });
-      __builtin_amdgcn_s_setprio(0);
-      if constexpr (!FP8) {                  // all but what this phase asked for has arrived: tile j + 2's values
-        wait_arrived<2 * NL>();
-        if (j + 2 < held_from || j + 2 >= held_to) clear_values(lds_v[(j + 2) & 3], held_keys(j + 2));
+      for (int j = 0; j < 3; ++j) {
+        key_at = offsets_of(j);
+        bring_all(k_base, key_at, lds_k[j], k_voff, kr);
+        settle(lds_k[j], kr, false, 0);
+        if (j == 2) break;
+        bring_all(v_base, key_at, lds_v[j], v_voff, vr);
+        settle(lds_v[j], vr, true, held_keys(j));
       }
-      phase_barrier<true>();
-      if (j + 1 < n) softmax_step(j + 1);
-      if (((j + 1 + kLead) & 63) == 0) locate(j + 1 + kLead);
       value_at = key_at;
-      key_at = offsets_of(j + 1 + kLead);
+      if constexpr (FP8) {                     // in registers: keys 3, values 2
+        bring_all(v_base, value_at, nullptr, v_voff, vr);
+        value_at = offsets_of(3);
+        bring_all(k_base, value_at, nullptr, k_voff, kr);
+      }
+      key_at = offsets_of(kLead - 1);
 #pragma unroll
-      for (int t = 0; t < kAhead; ++t) read_operands(lds_k[(j + 2) & 3], lds_v[(j + 1) & 3], t);
-      phase_barrier<false>();
+      for (int u = 0; u < 2 * NK; ++u) p[u] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+      wait_arrived<0>();
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j)
+        if (j < held_from || j >= held_to) clear_values(lds_v[j], held_keys(j));
+      phase_barrier<true>();
+      // The two waves of a SIMD take turns: while waves 0-3 multiply, waves 4-7,
+      // one barrier behind, run their softmax, and the other way round.
+      if (wave >= kChunkWaves / 2) phase_barrier<false>();
+#pragma unroll
+      for (int t = 0; t < kAhead; ++t) read_operands(lds_k[0], lds_v[3], t);
+#pragma unroll 1
+      for (int j = -1; j < n; ++j) {
+        // Products: O += values j, S = keys j + 1.  Tile j + 4's keys take the place of
+        // tile j's, tile j + 3's values that of tile j - 1's, which all have read; they
+        // are waited for in the next products and read at the end of the softmax after.
+        uint8_t* const free_k = lds_k[j & 3];
+        uint8_t* const free_v = lds_v[(j + 3) & 3];
+        settle(free_k, kr, false, 0);
+        settle(free_v, vr, true, FP8 && (j + 3 < held_from || j + 3 >= held_to) ? held_keys(j + 3) : kAll);
+        __builtin_amdgcn_s_setprio(1);
+        products(lds_k[(j + 1) & 3], lds_v[j & 3], [&](int step) {
+          if (step < NL) bring(k_base, key_at, step, free_k, k_voff, kr);
+          else if (step < 2 * NL) bring(v_base, value_at, step - NL, free_v, v_voff, vr);
+        });
+        __builtin_amdgcn_s_setprio(0);
+        if constexpr (!FP8) {                  // all but what this phase asked for has arrived: tile j + 2's values
+          wait_arrived<2 * NL>();
+          if (j + 2 < held_from || j + 2 >= held_to) clear_values(lds_v[(j + 2) & 3], held_keys(j + 2));
+        }
+        phase_barrier<true>();
+        if (j + 1 < n) {
+          hide(j + 1);
+          const float ref = raise();
+#pragma unroll
+          for (int u = 0; u < 2 * NK; ++u) weigh(u, ref);
+        }
+        if (((j + 1 + kLead) & 63) == 0) locate(j + 1 + kLead);
+        value_at = key_at;
+        key_at = offsets_of(j + 1 + kLead);
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) read_operands(lds_k[(j + 2) & 3], lds_v[(j + 1) & 3], t);
+        phase_barrier<false>();
+      }
+      if (wave < kChunkWaves / 2) phase_barrier<false>();
+    } else {
+      // Fragment e of the second product (O's fragment fastest), then of the first: the
+      // matrix instructions of a tile in order, operands RING - 1 instructions ahead.
+      constexpr int PV = 2 * DF, QK = KS, RING = 4;
+      bf16x8 ring[RING];
+      auto read_fragment = [&](const uint8_t* kt, const uint8_t* vt, int e) {
+        ring[e % RING] = e < PV ? value_fragment(vt, e / DF, e % DF) : key_fragment(kt, 0, e - PV);
+      };
+      auto multiply = [&](int e) {
+        if (e < PV) {
+          o[e % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[e % RING], p[e / DF], o[e % DF], 0, 0, 0);
+        } else {
+          f32x16 zero;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) zero[j] = 0.f;
+          s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[e % RING], q[e - PV], e == PV ? zero : s[0], 0, 0, 0);
+        }
+      };
+      auto read_first = [&](const uint8_t* kt, const uint8_t* vt) {
+#pragma unroll
+        for (int e = 0; e < RING - 1; ++e) read_fragment(kt, vt, e);
+      };
+      // Before the loop: keys 0 - 3, values 0 and 1, and tile 0's scores.  Tile -1's
+      // values and weights are 0.
+      constexpr int kLead = FP8 ? 5 : 4;       // the tile whose keys are asked for in tile 0's turn
+      locate(0);
+      Offsets key_at, value_at, value_next;
+#pragma unroll
+      for (int i = 0; i < KT * ROW / 16 / kThreads; ++i) *(u32x4*)(lds_v[3] + (i * kThreads + tid) * 16) = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        key_at = offsets_of(j);
+        bring_all(k_base, key_at, lds_k[j], k_voff, kr);
+        settle(lds_k[j], kr, false, 0);
+        if (j >= 2) continue;
+        bring_all(v_base, key_at, lds_v[j], v_voff, vr);
+        settle(lds_v[j], vr, true, held_keys(j));
+      }
+      value_at = offsets_of(2);
+      value_next = offsets_of(3);
+      if constexpr (FP8) {                     // in registers: keys 4, values 2
+        bring_all(v_base, value_at, nullptr, v_voff, vr);
+        key_at = offsets_of(4);
+        bring_all(k_base, key_at, nullptr, k_voff, kr);
+        value_at = value_next;
+        value_next = key_at;
+      }
+      key_at = offsets_of(kLead);
+#pragma unroll
+      for (int u = 0; u < 2 * NK; ++u) p[u] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+      wait_arrived<0>();
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j)
+        if (j < held_from || j >= held_to) clear_values(lds_v[j], held_keys(j));
+      phase_barrier<true>();
+#pragma unroll
+      for (int e = PV; e < PV + QK; ++e) {
+        read_fragment(lds_k[0], lds_v[3], e);
+        multiply(e);
+      }
+      if constexpr (!FP8) read_first(lds_k[1], lds_v[3]);
+      phase_barrier<true>();                   // tile 0's keys have been read by all
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        // Tile j's turn: O += values j - 1, weights j from scores j, scores j + 1 from
+        // keys j + 1.  Tile j + 4's keys take the place of tile j's, tile j + 2's values
+        // that of tile j - 2's, which all have read; they are waited for in the next turn
+        // and read from the end of the one after.
+        uint8_t* const free_k = lds_k[j & 3];
+        uint8_t* const free_v = lds_v[(j + 2) & 3];
+        const uint8_t* const kt = lds_k[(j + 1) & 3];
+        const uint8_t* const vt = lds_v[(j + 3) & 3];
+        settle(free_k, kr, false, 0);
+        settle(free_v, vr, true, FP8 && (j + 2 < held_from || j + 2 >= held_to) ? held_keys(j + 2) : kAll);
+        if constexpr (FP8) read_first(kt, vt);   // not across the conversions, whose registers they would take
+        hide(j);
+        const float ref = raise();
+        auto turn = [&](int e) {               // fragment e's product, the read of the one RING - 1 on before it
+          const int ahead = e + RING - 1;
+          if (ahead < PV + QK) {
+            read_fragment(kt, vt, ahead);
+            if (ahead < PV) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
+          multiply(e);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        };
+#pragma unroll
+        for (int e = 0; e < PV; ++e) {
+          turn(e);
+          const int u = e / DF;
+          if (u > 0) {                         // the weights of the 16 keys whose old ones are done with
+            if (e % DF == 0) weigh(0, ref);
+            __builtin_amdgcn_sched_group_barrier(0x002, 28 / DF, 0);
+          }
+          if (e % (PV / 4) == 1) {
+            const int i = e / (PV / 4);
+            if (i < NL) bring(k_base, key_at, i, free_k, k_voff, kr);
+            else if (i < 2 * NL) bring(v_base, value_at, i - NL, free_v, v_voff, vr);
+          }
+        }
+        weigh(1, ref);
+#pragma unroll
+        for (int e = PV; e < PV + QK; ++e) turn(e);
+        if (((j + 1 + kLead) & 63) == 0) locate(j + 1 + kLead);
+        value_at = value_next;
+        value_next = key_at;
+        key_at = offsets_of(j + 1 + kLead);
+        if constexpr (!FP8) {                  // all but what this turn asked for has arrived: tile j + 1's values
+          wait_arrived<2 * NL>();
+          if (j + 1 < held_from || j + 1 >= held_to) clear_values(lds_v[(j + 1) & 3], held_keys(j + 1));
+        }
+        if constexpr (!FP8) read_first(lds_k[(j + 2) & 3], lds_v[j & 3]);
+        phase_barrier<true>();
+      }
+#pragma unroll
+      for (int e = 0; e < PV; ++e) {           // the last tile's values
+        if (FP8 || e >= RING - 1) read_fragment(lds_k[0], lds_v[(n - 1) & 3], e);
+        multiply(e);
+      }
     }
-    if (wave < kChunkWaves / 2) phase_barrier<false>();
     wait_arrived<0>();                       // nothing may still be on its way into LDS when the workgroup ends
+    if constexpr (MIXED) phase_barrier<true>();   // nor may the next row tile's first writes pass the last reads
   }
 
   sum += __shfl_xor(sum, 32);

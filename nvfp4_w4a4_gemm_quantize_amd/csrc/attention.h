@@ -78,6 +78,38 @@ __device__ __forceinline__ int div_group(const AttentionArgs& a, int n) {
 // floor(n / d) through the fp64 reciprocal, 0 <= n < 2^43, 0 < d.
 __device__ __forceinline__ int64_t div_f64(int64_t n, int64_t d) { return (int64_t)((double)n / (double)d); }
 
+// Infinities and NaN among the values.  0 * inf is not 0, so in a tile of which some
+// row does not see every key they are taken out of the product, and a row that sees
+// them gets them added at the end: its sum is infinite or NaN whatever the weight is.
+// A word of the cache without them:
+template <bool FP8>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  if (FP8) {
+    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    return w & ~((nan >> 7) * 0xffu);
+  }
+  const uint32_t bad = ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  return w & ~((bad >> 15) * 0xffffu);
+}
+// x + what four columns at p hold of infinities and NaN, times by.
+template <bool FP8>
+__device__ __forceinline__ f32x4 add_not_finite(f32x4 x, const uint8_t* p, float by) {
+  float v[4];
+  if constexpr (FP8) {
+    const uint32_t w = *(const uint32_t*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (w >> 8 * i & 0x7f) == 0x7f ? NAN : 0.f;
+  } else {
+    const u32x2 w = *(const u32x2*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i >> 1] >> 16 * (i & 1) << 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!(fabsf(v[i]) < INFINITY)) x[i] = fmaf(v[i], by, x[i]);
+  return x;
+}
+
 // Two neighbouring floats as one device-scope atomic: past the XCD's own L2.
 __device__ __forceinline__ void store_shared(float* p, float x, float y) {
   const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);

@@ -205,6 +205,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     x_end = uniform(min(x_begin + share, per_head * hkv));
   }
 
+  __shared__ int not_finite[kChunkWaves];   // the wave took infinities or NaN out of values of the row tile
+
   for (int64_t x = x_begin; x < x_end;) {
   // the head, request and row tile, and the part of its keys
   int head, r, b, part = 0;
@@ -258,6 +260,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
     share_from = (double)from / (double)length;           // the same on both sides of a cut
     share_to = to == length ? 1. : (double)to / (double)length;
   }
+  __syncthreads();   // what the row tile before left in LDS has been read
+  if (lane == 0) not_finite[wave] = 0;
   l.start = uniform(l.start), l.tokens = uniform(l.tokens), l.keys = uniform(l.keys), l.pos0 = uniform(l.pos0);
 
   const int nrows = l.tokens * group;
@@ -324,6 +328,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const int held_from = missing ? 0 : max(low_rel + KT - 1, 0) / KT, held_to = missing ? 0 : max(keys_rel, 0) / KT;
   const int seen_from = max(held_from, (max(wave_low, 0) + KT - 1) / KT);
   const int seen_to = min(held_to, (max(wave_pos, -1) + 1) / KT);
+  // ... and tiles [all_from, all_to) by every row of the workgroup.
+  const int all_from = max(held_from, (max(low_of(a, pos_last) - origin, 0) + KT - 1) / KT);
+  const int all_to = min(held_to, (max(pos_first, -1) + 1 > origin ? max(pos_first, -1) + 1 - origin : 0) / KT);
+  auto partly = [&](int j) { return j < all_from || j >= all_to; };
 
   // A load instruction i of this wave brings rows (i * 8 + wave) * RPI on; a
   // lane's 16 bytes go to consecutive LDS addresses, so the bank permutation is
@@ -372,19 +380,34 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
 #pragma unroll
     for (int i = 0; i < NL; ++i) bring(base, at, i, lds, voff, regs);
   };
-  // Values of keys that the request does not hold are cleared in LDS, by the
-  // lanes that brought them: they may be NaN, and 0 * NaN is not 0.
-  auto settle = [&](uint8_t* lds, const u32x4* regs, bool values, uint64_t held) {
+  // Values of keys that the request does not hold are cleared in LDS, by the lanes
+  // that brought them: they may be NaN, and 0 * NaN is not 0.  Nor may infinities and
+  // NaN of keys that not every row sees stay: they are added at the end.
+  auto settle = [&](uint8_t* lds, u32x4* regs, bool values, int j) {
     if constexpr (FP8) {
       if (brings) {
+        if (values && partly(j)) {
+          const uint64_t held = held_keys(j);
+          uint32_t odd = 0;
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            const uint32_t keep = held >> ((i * kChunkWaves + wave) * RPI + lane_row) & 1 ? 0xffffffffu : 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w = regs[i][k] & keep;
+              regs[i][k] = finite_only<true>(w);
+              odd |= w ^ regs[i][k];
+            }
+          }
+          if (odd) not_finite[wave] = 1;
+        }
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
           const int row = (i * kChunkWaves + wave) * RPI + lane_row;
           const int x = values ? value_swizzle<D>(row) : key_swizzle<D>(row);
-          const uint32_t keep = !values || (held >> row & 1) ? 0xffffffffu : 0u;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t w0 = regs[i][2 * k] & keep, w1 = regs[i][2 * k + 1] & keep;
+            const uint32_t w0 = regs[i][2 * k], w1 = regs[i][2 * k + 1];
             *(u32x4*)(lds + row * ROW + ((2 * lane_col + k) ^ x) * 16) =
                 u32x4{e4m3_bf16<false>(w0), e4m3_bf16<true>(w0), e4m3_bf16<false>(w1), e4m3_bf16<true>(w1)};
           }
@@ -392,13 +415,27 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       }
     }
   };
-  auto clear_values = [&](uint8_t* lds, uint64_t held) {
+  auto clear_values = [&](uint8_t* lds, int j) {
     if constexpr (!FP8) {
+      if (!partly(j)) return;
+      const uint64_t held = held_keys(j);
+      bool odd = false;
+      constexpr int kUnroll = MIXED ? 1 : 2 * NL;   // heads of 256 have no registers to spare here
+#pragma unroll kUnroll
+      for (int i = 0; i < 2 * NL; ++i) {
+        const int at = (i >> 1) * kChunkWaves + wave;
+        const uint32_t keep = held >> (at * RPI + lane_row) & 1 ? 0xffffffffu : 0u;
+        u32x2* p = (u32x2*)(lds + at * 1024 + lane * 16 + (i & 1) * 8);
+        u32x2 w = *p;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int at = i * kChunkWaves + wave;
-        if (!(held >> (at * RPI + lane_row) & 1)) *(u32x4*)(lds + at * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t x = w[k] & keep;
+          w[k] = finite_only<false>(x);
+          odd |= w[k] != x;
+        }
+        *p = w;
       }
+      if (odd) not_finite[wave] = 1;
     }
   };
 
@@ -526,10 +563,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       for (int j = 0; j < 3; ++j) {
         key_at = offsets_of(j);
         bring_all(k_base, key_at, lds_k[j], k_voff, kr);
-        settle(lds_k[j], kr, false, 0);
+        settle(lds_k[j], kr, false, j);
         if (j == 2) break;
         bring_all(v_base, key_at, lds_v[j], v_voff, vr);
-        settle(lds_v[j], vr, true, held_keys(j));
+        settle(lds_v[j], vr, true, j);
       }
       value_at = key_at;
       if constexpr (FP8) {                     // in registers: keys 3, values 2
@@ -543,7 +580,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       wait_arrived<0>();
 #pragma unroll 1
       for (int j = 0; j < 2; ++j)
-        if (j < held_from || j >= held_to) clear_values(lds_v[j], held_keys(j));
+        clear_values(lds_v[j], j);
       phase_barrier<true>();
       // The two waves of a SIMD take turns: while waves 0-3 multiply, waves 4-7,
       // one barrier behind, run their softmax, and the other way round.
@@ -557,8 +594,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         // are waited for in the next products and read at the end of the softmax after.
         uint8_t* const free_k = lds_k[j & 3];
         uint8_t* const free_v = lds_v[(j + 3) & 3];
-        settle(free_k, kr, false, 0);
-        settle(free_v, vr, true, FP8 && (j + 3 < held_from || j + 3 >= held_to) ? held_keys(j + 3) : kAll);
+        settle(free_k, kr, false, j);
+        settle(free_v, vr, true, j + 3);
         __builtin_amdgcn_s_setprio(1);
         products(lds_k[(j + 1) & 3], lds_v[j & 3], [&](int step) {
           if (step < NL) bring(k_base, key_at, step, free_k, k_voff, kr);
@@ -567,7 +604,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         __builtin_amdgcn_s_setprio(0);
         if constexpr (!FP8) {                  // all but what this phase asked for has arrived: tile j + 2's values
           wait_arrived<2 * NL>();
-          if (j + 2 < held_from || j + 2 >= held_to) clear_values(lds_v[(j + 2) & 3], held_keys(j + 2));
+          clear_values(lds_v[(j + 2) & 3], j + 2);
         }
         phase_barrier<true>();
         if (j + 1 < n) {
@@ -617,10 +654,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       for (int j = 0; j < 4; ++j) {
         key_at = offsets_of(j);
         bring_all(k_base, key_at, lds_k[j], k_voff, kr);
-        settle(lds_k[j], kr, false, 0);
+        settle(lds_k[j], kr, false, j);
         if (j >= 2) continue;
         bring_all(v_base, key_at, lds_v[j], v_voff, vr);
-        settle(lds_v[j], vr, true, held_keys(j));
+        settle(lds_v[j], vr, true, j);
       }
       value_at = offsets_of(2);
       value_next = offsets_of(3);
@@ -637,7 +674,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       wait_arrived<0>();
 #pragma unroll 1
       for (int j = 0; j < 2; ++j)
-        if (j < held_from || j >= held_to) clear_values(lds_v[j], held_keys(j));
+        clear_values(lds_v[j], j);
       phase_barrier<true>();
 #pragma unroll
       for (int e = PV; e < PV + QK; ++e) {
@@ -656,8 +693,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         uint8_t* const free_v = lds_v[(j + 2) & 3];
         const uint8_t* const kt = lds_k[(j + 1) & 3];
         const uint8_t* const vt = lds_v[(j + 3) & 3];
-        settle(free_k, kr, false, 0);
-        settle(free_v, vr, true, FP8 && (j + 2 < held_from || j + 2 >= held_to) ? held_keys(j + 2) : kAll);
+        settle(free_k, kr, false, j);
+        settle(free_v, vr, true, j + 2);
         if constexpr (FP8) read_first(kt, vt);   // not across the conversions, whose registers they would take
         hide(j);
         const float ref = raise();
@@ -694,7 +731,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         key_at = offsets_of(j + 1 + kLead);
         if constexpr (!FP8) {                  // all but what this turn asked for has arrived: tile j + 1's values
           wait_arrived<2 * NL>();
-          if (j + 1 < held_from || j + 1 >= held_to) clear_values(lds_v[(j + 1) & 3], held_keys(j + 1));
+          clear_values(lds_v[(j + 1) & 3], j + 1);
         }
         if constexpr (!FP8) read_first(lds_k[(j + 2) & 3], lds_v[j & 3]);
         phase_barrier<true>();
@@ -706,7 +743,6 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       }
     }
     wait_arrived<0>();                       // nothing may still be on its way into LDS when the workgroup ends
-    if constexpr (MIXED) phase_barrier<true>();   // nor may the next row tile's first writes pass the last reads
   }
 
   sum += __shfl_xor(sum, 32);
@@ -731,6 +767,35 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *(f32x4*)(to + 32 * i + 8 * j) = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]} * by;
+    }
+    bool odd = false;
+    if (n > 0)
+#pragma unroll 1
+      for (int w = 0; w < kChunkWaves; ++w) odd |= not_finite[w] != 0;
+    if (odd) {   // rare, and slow: what the row sees of them, added to what has just been written
+#pragma unroll 1
+      for (int key = max(my_low, 0); key < min(min(keys_rel, my_pos + 1), n * KT); ++key) {
+        if (!partly(key / KT)) {
+          key = all_to * KT - 1;
+          continue;
+        }
+        const uint32_t page = page_at(key);
+        if (page >= num_pages) continue;
+        const uint8_t* token = v_base + (int64_t)((uint64_t)page * page_units << 4) + (uint32_t)((origin + key) & page_mask) * row_bytes;
+#pragma unroll 1
+        for (int d = 4 * h; d < D; d += 8) {
+          if (whole && a.out_bf16) {
+            uint16_t* to = (uint16_t*)a.out + at - 4 * h + d;
+            const u32x2 w = *(u32x2*)to;
+            const f32x4 x = add_not_finite<FP8>(f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                                                      __uint_as_float(w[1] & 0xffff0000u)}, token + d * EB, by);
+            *(u32x2*)to = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+          } else {
+            f32x4* to = (f32x4*)(whole ? (float*)a.out + at - 4 * h + d : ws.o + slot * D + d);
+            *to = add_not_finite<FP8>(*to, token + d * EB, by);
+          }
+        }
+      }
     }
     if (h == 0) {
       if (!whole) ws.ml[slot] = make_float2(top, sum);

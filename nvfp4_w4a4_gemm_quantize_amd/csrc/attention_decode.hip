@@ -69,7 +69,7 @@ __device__ __forceinline__ DecodeItem decode_item(const AttentionArgs& a, int r)
   if (it.l.tokens == 0 || it.l.tokens > kDecodeRows || it.l.tokens * a.group > kDecodeRows) it.tiles = 0;
   return it;
 }
-static_assert(kDecodeTile == 32, "");
+static_assert(kDecodeTile == 32 && kDecodeWaves == 4, "");
 
 // One key tile's K and V in registers.
 template <int D, bool FP8>
@@ -114,6 +114,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   __shared__ int64_t wave_sum[kDecodeWaves];
   __shared__ __attribute__((aligned(16))) float o_part[kDecodeWaves][16][LD];
   __shared__ float2 ml_part[kDecodeWaves][16];
+  __shared__ int not_finite[kDecodeWaves];
   __shared__ int last_part;
 
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
@@ -213,6 +214,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       }
     }
 
+    bool odd = false;   // infinities or NaN were taken out of values that not every row sees
     float m[NF], l[NF];
     f32x4 o[NF][DV];
 #pragma unroll
@@ -289,7 +291,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
     // softmax step and second product
     auto values = [&](Tile& tile, f32x4 (&s)[NF][2], int k, bool gap0, bool gap1) {
       const int at = wave + k * kDecodeWaves;
-      if (gap0 || gap1 || at < seen_from || at >= seen_to) {
+      const bool partly = at < seen_from || at >= seen_to;
+      if (gap0 || gap1 || partly) {
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -303,7 +306,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
             }
             // what lies in unwritten or foreign places may be NaN, and 0 * NaN is not 0
 #pragma unroll
-            for (int w = 0; w < Tile::VW; ++w) tile.v[4 * f + j][w] = held ? tile.v[4 * f + j][w] : 0u;
+            for (int w = 0; w < Tile::VW; ++w) {
+              const uint32_t x = held ? tile.v[4 * f + j][w] : 0u, finite = finite_only<FP8>(x);
+              odd |= partly && finite != x;
+              tile.v[4 * f + j][w] = partly ? finite : x;
+            }
           }
       }
       bf16x8 p[NF];
@@ -393,6 +400,22 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       }
     }
 
+    // what a row of the part sees of them, four columns at d (rare, and slow)
+    auto add_odd = [&](int row, int d, f32x4 x) {
+      const int pos = max(pos0 + div_group(a, row), -1), row_end = min(min(keys, pos + 1 - origin), n * kDecodeTile);
+      for (int key = max(max(low_of(a, pos) - origin, low), 0); key < row_end; ++key) {
+        if (key >> 5 >= seen_from && key >> 5 < seen_to) {   // seen by every row: nothing was taken out
+          key = seen_to * kDecodeTile - 1;
+          continue;
+        }
+        const uint32_t page = (uint32_t)table[(uint32_t)(origin + key) >> a.cache.page_shift];
+        if (page >= num_pages) continue;
+        const int64_t token = (int64_t)((uint64_t)page * page_units << 4) + (uint32_t)((origin + key) & page_mask) * row_bytes;
+        x = add_not_finite<FP8>(x, v_base + token + d * EB, 1.f);
+      }
+      return x;
+    };
+
     // join the waves in their order, 16 rows at a time
     const float vs = a.cache.v_scale ? a.cache.v_scale[head] : 1.f;
 #pragma unroll
@@ -401,6 +424,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       ls += __shfl_xor(ls, 16);
       ls += __shfl_xor(ls, 32);
       __syncthreads();   // the buffers of the fragment or item before have been read
+      if (lane == 0) not_finite[wave] = 0;
+      if (odd) not_finite[wave] = 1;
       if (g == 0) ml_part[wave][c16] = make_float2(m[n] == -INFINITY ? -INFINITY : c * m[n], ls);
 #pragma unroll
       for (int rr = 0; rr < 4; ++rr)
@@ -424,6 +449,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
 #pragma unroll
           for (int i = 0; i < 4; ++i) num[i] = fmaf(by, ow[i], num[i]);
         }
+        if (not_finite[0] | not_finite[1] | not_finite[2] | not_finite[3]) num = add_odd(at, d, num);
         if (whole) {
           write_row<D>(a, it.l.start, head, at, d, top, den, num, vs);
         } else {

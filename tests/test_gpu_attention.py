@@ -237,6 +237,56 @@ def test_fused_projection_views_other_streams_and_graphs(gpu_lib):
         assert torch.equal(got[0], res) and torch.equal(got[1], lse)
 
 
+@pytest.mark.parametrize("dim,fp8", [(64, False), (128, False), (256, False), (64, True), (128, True), (256, True)])
+@pytest.mark.parametrize("new,window", [(1, 0), (2, 0), (5, 40), (40, 0), (150, 0), (150, 90)])
+def test_infinities_and_nan_reach_the_rows_that_see_them_and_no_others(gpu_lib, dim, fp8, new, window):
+    b = build([700, 130], [new, new], 4, 2, dim, 32, fp8, seed=new + dim)
+    kinds = [float("nan")] * 3 if fp8 else [float("nan"), float("inf"), float("-inf")]
+    raw = torch.uint8 if fp8 else torch.bfloat16
+
+    def put(cache, r, pos, d, x):
+        x = torch.tensor([x], device="cuda").to(cache.dtype).view(raw)
+        cache.view(raw)[int(b["table"][r, pos // 32]), 1, pos % 32, d] = x[0]
+    for r, length in enumerate(b["lens"]):
+        # new tokens, which only later ones see, and old ones, which a window hides from some
+        for i, pos in enumerate({length - 1, length - 1 - new // 2, length - 2, length - new, length - 1 - max(window - 1, 0), length - 20 - window}):
+            put(b["v"], r, pos, 5 + 7 * i, kinds[i % 3])
+        put(b["k"], r, length - 1 - new // 4, 9, float("nan"))
+    f = lambda x: x.float().cpu().numpy().astype(np.float64)  # noqa: E731
+    scales = [None if s is None else f(s) for s in (b["k_scale"], b["v_scale"])]
+    want, wlse, tol, ltol = OP.attention(f(b["q"]), f(b["k"]), f(b["v"]), b["table"], b["q_start"], b["lens"], b["page"], 4,
+                                         dim ** -0.5, window, *scales)
+    # a row that sees such a value has it in its own column alone
+    clean = f(b["v"])
+    _, _, tol, _ = OP.attention(f(b["q"]), f(b["k"]), np.where(np.isfinite(clean), clean, 0.0), b["table"], b["q_start"], b["lens"],
+                                b["page"], 4, dim ** -0.5, window, *scales)
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse = call(gpu_lib, b, window=window, out_dtype=dtype)
+        got, glse = f(out).reshape(want.shape), f(lse)
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isnan(glse), np.isnan(wlse))
+        assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+        fin, lfin = np.isfinite(want), np.isfinite(wlse)
+        bound = tol + (OP.U_BF16 * (np.abs(want) + tol) if dtype == torch.bfloat16 else 0)
+        assert (np.abs(got - want)[fin] <= bound[fin]).all() and (np.abs(glse - wlse)[lfin] <= ltol[lfin]).all()
+
+
+def test_one_workspace_serves_calls_of_other_sizes(gpu_lib):
+    """The counters that a call needs at zero are zero after every other one."""
+    batches = [build(*a, seed=i) for i, a in enumerate([
+        ([9000, 40, 3000], [1, 1, 1], 8, 2, 128, 64), ([300, 5000], [3, 200], 8, 2, 128, 64), ([4000], [900], 8, 2, 128, 64),
+        ([20000], [1], 16, 1, 256, 64), ([100] * 40, [4] * 40, 4, 4, 64, 16)])]
+    size = max(gpu_lib.paged_attention_workspace(b["q"].shape[0], len(b["ctx"]), b["hq"], b["k"].shape[1], b["k"].shape[3],
+                                                 max(b["new"]), max(b["lens"])).numel() for b in batches)
+    shared = torch.full((size,), 0x5a, dtype=torch.uint8, device="cuda")
+    shared[:2048] = 0
+    want = [call(gpu_lib, b) for b in batches]
+    for order in ([0, 1, 2, 3, 4], [4, 2, 0, 3, 1], [1, 1, 0, 0, 2]):
+        for i in order:
+            out, lse = call(gpu_lib, batches[i], workspace=shared)
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+            assert int(shared[:2048].count_nonzero()) == 0
+
+
 def test_refusals(gpu_lib):
     E = gpu_lib.NVFP4Error
     b = build([20], [2], 4, 2, 64, 16)

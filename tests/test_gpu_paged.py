@@ -190,6 +190,37 @@ def test_kv_write_far_pages(gpu_lib):
     assert int(store.ne(0).sum()) == int(x.ne(0).sum())
 
 
+def test_plan_and_write_in_a_graph(gpu_lib):
+    """A captured plan and write, replayed on new lengths with other work between, against the eager calls."""
+    R, page, T = 3, 16, 40
+    ctx, new, free = i32([5, 16, 0]), i32([1, 3, 20]), i32(np.arange(20)[::-1].copy())
+    held = 20 + torch.arange(R * 6, dtype=torch.int32, device="cuda").reshape(R, 6)   # contexts' pages: no slot twice
+    table = held.clone()
+    k, v = (torch.randn(T, 2 * 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    caches = [torch.zeros(20 + R * 6, 2, page, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    plan = gpu_lib.paged_plan(ctx, new, free, table, page, T)
+
+    def step():
+        gpu_lib.paged_plan(ctx, new, free, table, page, T, plan=plan)
+        gpu_lib.paged_kv_write(k, v, plan.slots, *caches)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for c, n in (([0, 0, 0], [1, 1, 1]), ([40, 3, 31], [0, 30, 2]), ([16, 15, 17], [5, 1, 34])):
+        ctx.copy_(i32(c)), new.copy_(i32(n))
+        seen = []
+        for call in (graph.replay, step):
+            table.copy_(held)
+            for x in (*plan, *caches):
+                x.zero_()
+            call()
+            torch.cuda.synchronize()
+            seen.append([x.clone() for x in (*plan, table, *caches)])
+        assert all(torch.equal(a, b) for a, b in zip(*seen))
+
+
 def test_refusals(gpu_lib):
     E = gpu_lib.NVFP4Error
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731

@@ -147,6 +147,57 @@ def test_emitted_tokens_follow_the_target(gpu_lib):
     assert chi2 < 40, chi2                         # 11 degrees of freedom: P(> 40) = 4e-5
 
 
+def on_device(b):
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    f32 = lambda x: None if x is None else torch.tensor(x, device="cuda")  # noqa: E731
+    return dict(logits=b["logits"].cuda(), row_start=i32(b["row_start"]), num_drafts=i32(b["num_drafts"]),
+                draft_tokens=i32(b["draft_tokens"]), uniform=f32(b["uniform"]), noise=f32(b["noise"]),
+                draft_probs=f32(b["draft_probs"]), temperature=f32(b["temperature"]))
+
+
+def test_one_workspace_serves_calls_of_other_sizes(gpu_lib):
+    """The counters that a call needs at zero are zero after every other one."""
+    batches = [build(1, 0, 70003, [0], False, False, None), build(5, 3, 20001, [3, 0, 2, 1, 3], True, True, None, seed=1),
+               build(40, 2, 900, [2, -1] * 20, False, True, [0.0, 0.8] * 20, seed=2), build(2, 8, 33000, [8, 5], False, False, [0.5, 0.0], seed=3)]
+    sizes = [(*b["draft_tokens"].shape, b["logits"].shape[1]) for b in batches]
+    shared = torch.full((max(gpu_lib.verify_drafts_workspace(*s).numel() for s in sizes),), 0x5a, dtype=torch.uint8, device="cuda")
+    shared[:1 << 18] = 0
+    want = [run(gpu_lib, b) for b in batches]
+    dev = [on_device(b) for b in batches]
+    for order in ([0, 1, 2, 3], [3, 1, 0, 2], [2, 2, 1, 1]):
+        for i in order:
+            for got, w in zip(gpu_lib.verify_drafts(workspace=shared, **dev[i]), want[i]):
+                np.testing.assert_array_equal(got.cpu().numpy(), w)
+            assert int(shared[:1 << 18].count_nonzero()) == 0
+
+
+def test_other_streams_and_graphs(gpu_lib):
+    """A call on a side stream, and a captured one replayed on new inputs with other work between."""
+    b = build(3, 4, 20001, [4, 2, 0], False, True, [1.0, 0.0, 0.6], seed=4)
+    want, d = run(gpu_lib, b), on_device(b)
+    ws = gpu_lib.verify_drafts_workspace(3, 4, 20001)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = gpu_lib.verify_drafts(workspace=ws, **d)
+    torch.cuda.current_stream().wait_stream(side)
+    for g, w in zip(got, want):
+        np.testing.assert_array_equal(g.cpu().numpy(), w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = gpu_lib.verify_drafts(workspace=ws, **d)
+    for drafts in ([0, 4, 1], [4, 4, -1], [1, 0, 3]):
+        d["num_drafts"].copy_(torch.tensor(drafts, dtype=torch.int32))
+        d["uniform"].mul_(0.7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in held]
+        for g, w in zip(got, gpu_lib.verify_drafts(**d)):
+            assert torch.equal(g, w)
+        torch.cuda.synchronize()
+
+
 def test_refusals(gpu_lib):
     E = gpu_lib.NVFP4Error
     z = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731

@@ -12,6 +12,7 @@
 // for heads of 256).  An E4M3 cache becomes bf16 on its way into LDS, once for
 // all eight waves.
 #include <float.h>
+#include <math.h>
 
 #include "attention.h"
 
@@ -839,13 +840,34 @@ size_t attention_chunk_workspace(int64_t requests, int dim) {
 
 namespace {
 
+// Whether row tiles are handed out whole, one a workgroup as they finish, with nothing
+// to join, or cut into equal shares.  Shares cost what a workgroup takes for about 1500
+// keys (parts of O written and read, the join's launch); whole tiles cost the longest
+// one at least, and a last round that is not full, of which the shortest tile at most
+// is lost where they come long ones first.  The host knows bounds alone: it takes the
+// lengths of several requests as three quarters of the longest, and their last tiles
+// as half full.  Three tiles a workgroup and more fill the chip whatever they are.
+// Heads of 128, whole against shares: prompts of 1024, 2048, 4096, 5000, 8192 tokens 38
+// against 46, 65 / 78, 155 / 183, 227 / 240, 507 / 559 us; 512 tokens after 8192 190 /
+// 100, 128 after 65536 1353 / 175; 8 windowed chunks (heads of 64) 103 / 92.
+bool tiles_alone(const AttentionArgs& a) {
+  const double rows = (double)a.tokens * a.group / kChunkRows, round = (double)kChunkGrid / a.cache.heads;
+  const bool one = a.requests == 1;
+  const double tiles = (one ? ceil(rows) : rows + 0.5 * a.requests) / round;
+  if (tiles >= 3.) return true;
+  const double rounds = ceil((one ? ceil(rows) : rows + a.requests) / round);
+  double longest = (double)max(a.max_seq, a.max_new);
+  if (a.window) longest = fmin(longest, (double)a.window + (double)kChunkRows / a.group);
+  const double average = kExtraKeys + (one ? fmax(longest - 0.5 * a.tokens, 0.5 * longest) : 0.75 * longest);
+  const double shortest = one ? kExtraKeys + fmax(longest - a.tokens, 0.) : average;
+  return fmax(longest + kExtraKeys, fmin(rounds * average, tiles * average + shortest)) < tiles * average + 1500.;
+}
+
 template <int D, bool FP8>
 hipError_t launch(const AttentionArgs& a, void* workspace, hipStream_t st) {
   const ChunkWorkspace ws = chunk_workspace(workspace, a.requests);
   const int64_t numbers = row_tiles(a.tokens, a.requests, a.group);
-  // Row tiles alone keep the chip busy: one a workgroup, handed out as they finish, and
-  // nothing to join.  Fewer are cut into equal shares.
-  if (a.tokens * a.group / kChunkRows * a.cache.heads >= 3 * kChunkGrid) {
+  if (tiles_alone(a)) {
     attention_chunk_kernel<D, FP8><<<(unsigned)(numbers * a.cache.heads), kThreads, 0, st>>>(a, ws, (int)numbers);
     return hipGetLastError();
   }
@@ -869,13 +891,17 @@ hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipSt
 // ------------------------------------------------------------- dispatch ----
 
 // A request with at most 32 rows a KV head goes to the streaming kernel, any
-// other to the tiled one; both are launched where the batch may hold both.  Where
-// the batch has 64 rows a request and more on average, the tiled kernel takes all
-// of them: it streams a lone token's keys at 4 TB/s, and two launches are spared
-// (10 us of a 2048-token prompt's 95).
+// other to the tiled one (64 decoded tokens over 8192 keys, heads of 128: streaming
+// 362 us, tiled 496); both are launched where the batch may hold both.  Where it has
+// no request of 33 rows the tiled kernel is not launched, and where requests bring 64
+// rows and more on average, or a quarter of the largest request's, the tiled kernel
+// takes all of them, which spares launches and the second pass over the chip (32
+// requests of up to 32 tokens over 4096 keys: 92 us, both kernels 112; of up to 10
+// 93 against 113).
 static bool may_tile(int64_t max_new, int group) { return max_new * group > kDecodeRows; }
 static bool may_stream(int64_t tokens, int64_t requests, int64_t max_new, int group) {
-  return max_new > 0 && group <= kDecodeRows && !(may_tile(max_new, group) && tokens * group >= 64 * requests);
+  return max_new > 0 && group <= kDecodeRows && 
+         !(may_tile(max_new, group) && (tokens * group >= 64 * requests || 4 * tokens >= max_new * requests));
 }
 
 size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_new,

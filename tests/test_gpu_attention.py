@@ -237,9 +237,7 @@ def test_fused_projection_views_other_streams_and_graphs(gpu_lib):
         assert torch.equal(got[0], res) and torch.equal(got[1], lse)
 
 
-@pytest.mark.parametrize("dim,fp8", [(64, False), (128, False), (256, False), (64, True), (128, True), (256, True)])
-@pytest.mark.parametrize("new,window", [(1, 0), (2, 0), (5, 40), (40, 0), (150, 0), (150, 90)])
-def test_infinities_and_nan_reach_the_rows_that_see_them_and_no_others(gpu_lib, dim, fp8, new, window):
+def check_not_finite(gpu_lib, dim, fp8, new, window, **kw):
     b = build([700, 130], [new, new], 4, 2, dim, 32, fp8, seed=new + dim)
     kinds = [float("nan")] * 3 if fp8 else [float("nan"), float("inf"), float("-inf")]
     raw = torch.uint8 if fp8 else torch.bfloat16
@@ -261,13 +259,43 @@ def test_infinities_and_nan_reach_the_rows_that_see_them_and_no_others(gpu_lib, 
     _, _, tol, _ = OP.attention(f(b["q"]), f(b["k"]), np.where(np.isfinite(clean), clean, 0.0), b["table"], b["q_start"], b["lens"],
                                 b["page"], 4, dim ** -0.5, window, *scales)
     for dtype in (torch.float32, torch.bfloat16):
-        out, lse = call(gpu_lib, b, window=window, out_dtype=dtype)
+        out, lse = call(gpu_lib, b, window=window, out_dtype=dtype, **kw)
         got, glse = f(out).reshape(want.shape), f(lse)
         assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isnan(glse), np.isnan(wlse))
         assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
         fin, lfin = np.isfinite(want), np.isfinite(wlse)
         bound = tol + (OP.U_BF16 * (np.abs(want) + tol) if dtype == torch.bfloat16 else 0)
         assert (np.abs(got - want)[fin] <= bound[fin]).all() and (np.abs(glse - wlse)[lfin] <= ltol[lfin]).all()
+
+
+@pytest.mark.parametrize("dim,fp8", [(64, False), (128, False), (256, False), (64, True), (128, True), (256, True)])
+@pytest.mark.parametrize("new,window", [(1, 0), (2, 0), (5, 40), (40, 0), (150, 0), (150, 90)])
+def test_infinities_and_nan_reach_the_rows_that_see_them_and_no_others(gpu_lib, dim, fp8, new, window):
+    check_not_finite(gpu_lib, dim, fp8, new, window)
+
+
+# A bound far above the lengths makes the tiled kernel cut row tiles into shares.
+LOOSE = 1 << 20
+
+
+@pytest.mark.parametrize("dim,fp8", [(64, False), (128, False), (256, False), (64, True), (128, True), (256, True)])
+@pytest.mark.parametrize("new,window", [(40, 0), (150, 90)])
+def test_infinities_and_nan_in_shares(gpu_lib, dim, fp8, new, window):
+    check_not_finite(gpu_lib, dim, fp8, new, window, max_seq=LOOSE)
+
+
+@pytest.mark.parametrize("dim,fp8", [(64, False), (128, False), (256, False), (64, True), (128, True), (256, True)])
+@pytest.mark.parametrize("ctx,new", [([0], [33]), ([3000, 0, 1], [100, 257, 1]), ([2000, 5000], [70, 40])])
+def test_chunks_in_shares(gpu_lib, dim, fp8, ctx, new):
+    check(gpu_lib, build(ctx, new, 4, 2, dim, 64, fp8, seed=len(ctx) + dim), max_seq=LOOSE)
+
+
+@pytest.mark.parametrize("new", [(1, 33), (5, 40), (9, 9), (2, 100, 1, 1, 1, 1, 1, 1)])
+def test_batches_that_one_kernel_takes_and_that_both_share(gpu_lib, new):
+    """Requests of few rows among larger ones: with a bound on the new tokens that fits, and with one far above."""
+    b = build([300 + 7 * i for i in range(len(new))], list(new), 4, 1, 128, 32, seed=len(new))
+    check(gpu_lib, b)
+    check(gpu_lib, b, max_new=512, max_seq=LOOSE)
 
 
 def test_one_workspace_serves_calls_of_other_sizes(gpu_lib):

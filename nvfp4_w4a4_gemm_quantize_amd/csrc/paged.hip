@@ -19,7 +19,9 @@ namespace nvfp4 {
 // is found from its request's prefix alone and no workgroup waits for another.
 //
 // One launch, bound by latency: every workgroup repeats the scan (8 bytes a
-// request, from L2), which costs less than a second launch to share it; then
+// request, from L2), which costs less than a second launch to share it (a launch takes
+// the host 3.6 us; 8 requests of one token 3.2 us on the GPU, 1024 requests with 5000
+// tokens 6.2); then
 // tokens, pages and requests are dealt out over the whole grid.  A thread owns
 // a run of ceil(R / 256) requests in the scan; a token finds its run by binary
 // search in LDS and its request by walking the run.
@@ -159,7 +161,8 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t st) {
 // even of clamp(x / scale[h], +-448) (the clamp: E4M3 has no infinity, and a
 // calibrated scale may be exceeded).  Bound by HBM: every thread moves 16 bytes
 // of K and of V, the two loads in flight together; a token's row is contiguous
-// on the way in, and per head on the way out.
+// on the way in, and per head on the way out.  Measured: 16384 tokens, 8 heads of 128,
+// into E4M3: 22 us, 4.5 TB/s (a large copy moves 5.0); 64 decoded tokens 2.7 us.
 namespace {
 
 __device__ __forceinline__ float bf16_f32(uint32_t bits) { return __uint_as_float(bits << 16); }

@@ -474,33 +474,36 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   };
   // Scores of tile j that the lane's row does not see.
   auto hide = [&](int j) {
-    if (j < seen_from || j >= seen_to) {
-      // a bit for every key of the tile that this lane's row sees
-      const int bottom = my_low - j * KT, end = my_pos + 1 - j * KT;
-      uint64_t see = held_keys(j);
-      see = end <= 0 ? 0 : end < 64 ? see & (((uint64_t)1 << end) - 1) : see;
-      see = bottom <= 0 ? see : bottom < 64 ? see & (~(uint64_t)0 << bottom) : 0;
+    // a bit for every key of the tile that this lane's row sees
+    const int bottom = my_low - j * KT, end = my_pos + 1 - j * KT;
+    uint64_t see = held_keys(j);
+    see = end <= 0 ? 0 : end < 64 ? see & (((uint64_t)1 << end) - 1) : see;
+    see = bottom <= 0 ? see : bottom < 64 ? see & (~(uint64_t)0 << bottom) : 0;
 #pragma unroll
-      for (int f = 0; f < NK; ++f) {
-        const uint32_t bits = (uint32_t)(see >> (32 * f)) >> (4 * h);
+    for (int f = 0; f < NK; ++f) {
+      const uint32_t bits = (uint32_t)(see >> (32 * f)) >> (4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[f][i] = bits >> (8 * (i >> 2) + (i & 3)) & 1 ? s[f][i] : -INFINITY;
-      }
+      for (int i = 0; i < 16; ++i)
+        s[f][i] = bits >> (8 * (i >> 2) + (i & 3)) & 1 ? s[f][i] : -INFINITY;
     }
   };
-  // Brings the maximum up to date.  It may lag behind by a factor of 2^8, which
-  // costs no precision: O is scaled anew only when it does not suffice any more.
-  auto raise = [&] {
+  auto largest = [&] {
     float top = s[0][0];
 #pragma unroll
     for (int f = 0; f < NK; ++f)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[f][i]);
-    if (__any(c * (top - m) > 8.f || (m == -INFINITY && top > m))) {
+    return top;
+  };
+  // The maximum, in log2 units, up to date; top is the tile's beyond what it is taken
+  // for (0 before there is one).  It may lag behind by a factor of 2^8, which costs no
+  // precision: O is scaled anew only when it does not suffice any more.
+  auto reference = [&] { return m == -INFINITY ? 0.f : m; };
+  auto raise = [&](float top) {
+    if (__any(top > 8.f || (m == -INFINITY && top > m))) {
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float to = fmaxf(m, top);
-      const float by = m == to ? 1.f : m == -INFINITY ? 0.f : exp2_fast(c * (m - to));
+      const float old = reference(), to = fmaxf(m, old + top);
+      const float by = m == to ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - to);
       m = to;
       sum *= by;
 #pragma unroll
@@ -512,16 +515,24 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         for (int u = 0; u < 2 * NK; ++u)
 #pragma unroll
           for (int i = 0; i < 8; ++i) p[u][i] = (__bf16)((float)p[u][i] * by);
+      } else {                               // the exponents, which are at hand already
+        const float shift = old - reference();
+#pragma unroll
+        for (int f = 0; f < NK; ++f)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[f][i] += shift;
       }
     }
-    return m == -INFINITY ? 0.f : c * m;
   };
   // Weights of 16 keys.  In bf16, the matrix instruction's type with V: 2^-8 relative a
   // term at most, averaged over the keys.
   auto weigh = [&](int u, float ref) {
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = exp2_fast(fmaf(s[u >> 1][8 * (u & 1) + i], c, -ref));
+    for (int i = 0; i < 8; ++i) {
+      const float x = s[u >> 1][8 * (u & 1) + i];
+      e[i] = exp2_fast(MIXED ? fmaf(x, c, -ref) : x);
+    }
     sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
     u32x4 w = {pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])};
     if constexpr (MIXED) asm volatile("" : "+v"(w), "+v"(sum));   // here, among the products, and not where the next turn needs them
@@ -530,20 +541,24 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
 
   if (n > 0) {
     if constexpr (!MIXED) {
-      // Both products, two fragments of each a step, their operands read kAhead
-      // steps before (an LDS read takes longer than the four instructions of a step);
-      // those of the first steps are read before the barrier that begins the phase.
+      // The first product of the next tile, then the second of this one, four fragments
+      // a step, their operands read kAhead steps before (an LDS read takes longer than
+      // the four instructions of a step); those of the first steps are read before the
+      // barrier that begins the phase.  The exponents' arguments and their maximum are
+      // found beside the second product, where the vector unit would idle.
       constexpr int kAhead = 2;
-      constexpr int STEPS = NK * DF;
-      bf16x8 vf[kAhead + 1][2], kf[kAhead + 1][2];
+      constexpr int QK = NK * KS / 4, STEPS = QK + NK * DF / 2;
+      bf16x8 frag[kAhead + 1][4];
       auto read_operands = [&](const uint8_t* kt, const uint8_t* vt, int t) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          vf[t % (kAhead + 1)][i] = value_fragment(vt, (2 * t + i) / DF, (2 * t + i) % DF);
-          kf[t % (kAhead + 1)][i] = key_fragment(kt, (2 * t + i) % NK, (2 * t + i) / NK);
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * t + i, v = e - 4 * QK;
+          frag[t % (kAhead + 1)][i] = t < QK ? key_fragment(kt, e % NK, e / NK) : value_fragment(vt, v / DF, v % DF);
         }
       };
+      float top0;
       auto products = [&](const uint8_t* kt, const uint8_t* vt, auto between) {
+        const float ref = reference();
 #pragma unroll
         for (int f = 0; f < NK; ++f)
 #pragma unroll
@@ -552,13 +567,24 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         for (int t = 0; t < STEPS; ++t) {
           if (t + kAhead < STEPS) {
             read_operands(kt, vt, t + kAhead);
-            __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);   // six LDS reads, then four products
+            if (t + kAhead < QK) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);   // a step's LDS reads, then four products
+            else __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int e = 2 * t + i, at = t % (kAhead + 1);
-            o[e % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[at][i], p[e / DF], o[e % DF], 0, 0, 0);
-            s[e % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[at][i], q[e / NK], s[e % NK], 0, 0, 0);
+          for (int i = 0; i < 4; ++i) {
+            const int e = 4 * t + i, v = e - 4 * QK, at = t % (kAhead + 1);
+            if (t < QK) s[e % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag[at][i], q[e / NK], s[e % NK], 0, 0, 0);
+            else o[v % DF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag[at][i], p[v / DF], o[v % DF], 0, 0, 0);
+          }
+          if (t > QK) {                      // a step after the last of the scores
+            constexpr int kEach = 16 / (STEPS - QK - 1) + 1;
+#pragma unroll
+            for (int i = (t - QK - 1) * kEach; i < (t - QK) * kEach && i < 16; ++i)
+#pragma unroll
+              for (int f = 0; f < NK; ++f) {
+                s[f][i] = fmaf(s[f][i], c, -ref);
+                top0 = i + f == 0 ? s[0][0] : fmaxf(top0, s[f][i]);
+              }
           }
           __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
           between(t);
@@ -620,10 +646,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         }
         phase_barrier<true>();
         if (j + 1 < n) {
-          hide(j + 1);
-          const float ref = raise();
+          if (j + 1 < seen_from || j + 1 >= seen_to) {
+            hide(j + 1);
+            top0 = largest();
+          }
+          raise(top0);
 #pragma unroll
-          for (int u = 0; u < 2 * NK; ++u) weigh(u, ref);
+          for (int u = 0; u < 2 * NK; ++u) weigh(u, 0.f);
         }
         if (((j + 1 + kLead) & 63) == 0) locate(j + 1 + kLead);
         value_at = key_at;
@@ -708,8 +737,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         settle(free_k, kr, false, j);
         settle(free_v, vr, true, j + 2);
         if constexpr (FP8) read_first(kt, vt);   // not across the conversions, whose registers they would take
-        hide(j);
-        const float ref = raise();
+        if (j < seen_from || j >= seen_to) hide(j);
+        raise(fmaf(largest(), c, -reference()));
+        const float ref = reference();
         auto turn = [&](int e) {               // fragment e's product, the read of the one RING - 1 on before it
           const int ahead = e + RING - 1;
           if (ahead < PV + QK) {
@@ -758,7 +788,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   }
 
   sum += __shfl_xor(sum, 32);
-  const float top = m == -INFINITY ? -INFINITY : c * m;
+  const float top = m;
   if (live) {
     const int trow = l.start + my_token;
     const int64_t slot = ((int64_t)place * 2 + part) * kChunkRows + wave * 32 + c32;

@@ -15,13 +15,14 @@
 // An E4M3 cache becomes bf16 on its way into LDS, once for all eight waves.
 //
 // Bound by the matrix unit and the power it may draw: a long prompt holds 1.8 -
-// 2.05 GHz, and the MFMAs take 59% of the cycles; the rest is the softmax, whose
+// 2.05 GHz, and the MFMAs take 60% of the cycles; the rest is the softmax, whose
 // exponentials share the issue slots.  8192 tokens after 8192, 40 heads of 128 over
-// 8: 1750 - 1890 us on different cards, 1.09 - 1.18 PFLOP/s (a large bf16 product
-// reaches 1.61), E4M3 1980; heads of 64 (64 over 16) 1920 us, 860 TFLOP/s: half the
-// product for each exponential; 4096 after 4096, 24 heads of 256 over 4: 625 us, 990
-// TFLOP/s, E4M3 804.  Short chunks are bound by what a row tile costs beside its keys
-// (about 11 us): 8 windowed chunks of up to 777, heads of 64, 85 us.
+// 8: 1750 - 1840 us on different cards, 1.12 - 1.18 PFLOP/s (a large bf16 product
+// reaches 1.61), E4M3 1960; heads of 64 (64 over 16) 1835 us, 900 TFLOP/s, E4M3 1850:
+// half the product for each exponential; 4096 after 4096, 24 heads of 256 over 4: 615
+// us, 1006 TFLOP/s, E4M3 845.  8 windowed chunks of up to 777, heads of 64, take 81 us:
+// 1.4 us a tile of keys, shares between 57 and 80 us long, and a part's 8 us beside
+// its keys (its queries, page numbers and first keys; its output).
 #include <float.h>
 #include <math.h>
 
@@ -81,11 +82,11 @@ __device__ __forceinline__ void phase_barrier() {
 
 // The work of all row tiles and KV heads forms one line that a fixed grid shares
 // evenly.  A row tile's length on it is the keys that its last row may see, in
-// units of 1 / group keys, and `extra`, what a tile costs beside (about 11 us:
-// its queries, page numbers and first keys have to arrive); it grows by 256 from
-// a request's tile to the next until the window ends it, so a request's length
-// has a closed form.  A cut between two shares that falls less than `extra` from
-// a tile's end or start is moved there.
+// units of 1 / group keys, and `extra`, what a tile costs beside and what a cut is
+// worth (512 keys; 256 to 1536 measured the same within 5%, 1 up to 60% slower);
+// it grows by 256 from a request's tile to the next until the window ends it, so a
+// request's length has a closed form.  A cut between two shares that falls less
+// than `extra` from a tile's end or start is moved there.
 struct ChunkLine {
   int tiles, rising;
   int64_t context, cap, extra;
@@ -158,9 +159,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   constexpr int NL = SPARE ? 1 : LOADS;
   // Softmax beside the matrix unit.  Heads of 64 and 128: the two waves of a SIMD take
   // turns, one multiplies while the other computes weights (a prompt of 8192 over 8192
-  // keys, 40 heads of 128: 1750 us; mixed 1930 - 2000).  Heads of 256, whose O leaves a
+  // keys, 40 heads of 128: 1840 us; mixed 1930 - 2080).  Heads of 256, whose O leaves a
   // wave no registers for operands of two products at once: every wave weighs between
-  // the matrix instructions (4096 over 4096, 24 heads: 640 us, E4M3 810; turns 1336 and
+  // the matrix instructions (4096 over 4096, 24 heads: 615 us, E4M3 845; turns 1336 and
   // 1585, with 65 registers spilled).
   constexpr bool MIXED = D == 256;
   __shared__ __attribute__((aligned(1024))) uint8_t lds_k[kSlots][KT * ROW], lds_v[kSlots][KT * ROW];

@@ -891,18 +891,23 @@ namespace {
 // as half full.  Three tiles a workgroup and more fill the chip whatever they are.
 // Heads of 128, whole against shares: prompts of 1024, 2048, 4096, 5000, 8192 tokens 38
 // against 46, 65 / 78, 155 / 183, 227 / 240, 507 / 559 us; 512 tokens after 8192 190 /
-// 100, 128 after 65536 1353 / 175; 8 windowed chunks (heads of 64) 103 / 92.
+// 100, 128 after 65536 1353 / 175; 8 windowed chunks (heads of 64) 103 / 92; both
+// kernels' times, 256 single tokens over 2000 keys beside 512 tokens after 8192 558 / 487.
 bool tiles_alone(const AttentionArgs& a) {
-  const double rows = (double)a.tokens * a.group / kChunkRows, round = (double)kChunkGrid / a.cache.heads;
+  const double round = (double)kChunkGrid / a.cache.heads, all = (double)row_tiles(a.tokens, a.requests, a.group) / round;
   const bool one = a.requests == 1;
-  const double tiles = (one ? ceil(rows) : rows + 0.5 * a.requests) / round;
-  if (tiles >= 3.) return true;
-  const double rounds = ceil((one ? ceil(rows) : rows + a.requests) / round);
+  // Where the other kernel takes the requests of few rows, those of many are taken for
+  // as few as their tokens allow, and a workgroup finds nothing for each other one: a
+  // round of these costs what 150 keys do.
+  const double many = a.stream_rows ? fmin((double)a.requests, ceil((double)a.tokens / a.max_new)) : (double)a.requests;
+  const double rows = (double)(a.stream_rows ? max(a.tokens - a.requests, (int64_t)1) : a.tokens) * a.group / kChunkRows;
+  const double tiles = (one ? ceil(rows) : rows + 0.5 * many) / round, rounds = ceil((one ? ceil(rows) : rows + many) / round);
   double longest = (double)max(a.max_seq, a.max_new);
   if (a.window) longest = fmin(longest, (double)a.window + (double)kChunkRows / a.group);
   const double average = kExtraKeys + (one ? fmax(longest - 0.5 * a.tokens, 0.5 * longest) : 0.75 * longest);
   const double shortest = one ? kExtraKeys + fmax(longest - a.tokens, 0.) : average;
-  return fmax(longest + kExtraKeys, fmin(rounds * average, tiles * average + shortest)) < tiles * average + 1500.;
+  const double whole = tiles >= 3. ? tiles * average : fmax(longest + kExtraKeys, fmin(rounds * average, tiles * average + shortest));
+  return whole + fmax(all - rounds, 0.) * 150. < tiles * average + 1500.;
 }
 
 template <int D, bool FP8>

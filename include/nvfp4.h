@@ -457,9 +457,9 @@ int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t l
  *                (multiple of 4), 16-byte aligned.
  *   lse          optional fp32 [tokens, num_heads] contiguous (natural log).
  *   workspace    16-byte aligned, at least paged_attention_workspace_bytes of
- *                the same sizes; its first 2048 bytes zero before its first use
- *                (each call leaves them so); not shared by calls in flight on
- *                different streams.
+ *                the same or larger sizes; its first 2048 bytes zero before its
+ *                first use (each call leaves them so); not shared by calls in
+ *                flight on different streams.
  * tokens == 0 or num_requests == 0 enqueues nothing.  Results are
  * deterministic.
  */
@@ -507,9 +507,10 @@ int paged_attention(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32
  *   logprobs     fp32 [num_requests, max_drafts + 1]: log p of each emitted
  *                token (temperature 0: of 1), 0 in the places of -1.
  *   num_requests 0..65535 (0 enqueues nothing), max_drafts 0..255, vocab >= 1.
- *   workspace    16-byte aligned, at least verify_drafts_workspace_bytes; its
- *                first 2^18 bytes zero before its first use (each call leaves
- *                them so); not shared by calls in flight on different streams.
+ *   workspace    16-byte aligned, at least verify_drafts_workspace_bytes of the
+ *                same or larger sizes; its first 2^18 bytes zero before its first
+ *                use (each call leaves them so); not shared by calls in flight on
+ *                different streams.
  */
 size_t verify_drafts_workspace_bytes(int64_t num_requests, int64_t max_drafts, int64_t vocab);
 int verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64_t rows, int64_t vocab,

@@ -955,7 +955,8 @@ size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int h
                                  int64_t max_seq) {
   const int group = hq / hkv;
   size_t n = 16 + kArrivedBytes;
-  if (may_stream(tokens, requests, max_new, group)) n += (attention_decode_workspace(dim) + 255) / 256 * 256;
+  // whatever the tokens: what serves a step serves smaller ones
+  if (max_new > 0 && group <= kDecodeRows) n += (attention_decode_workspace(dim) + 255) / 256 * 256;
   if (may_tile(max_new, group)) n += attention_chunk_workspace(requests, dim);
   return n;
 }

@@ -405,9 +405,12 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, Ver
   a.logprobs[out] = lp;
 }
 
+// Enough for any smaller call too: rows times slices is below 2560 + rows while there
+// are several slices, and the rows themselves after that.
 size_t verify_workspace_bytes(int64_t requests, int64_t max_drafts, int64_t vocab) {
-  const int slices = verify_slices(requests, max_drafts, vocab);
-  return (size_t)(uintptr_t)(verify_workspace(nullptr, requests, max_drafts, slices).draws + requests * slices) + 16;
+  const int64_t rows = requests * (max_drafts + 1), most = min((vocab + kSlice - 1) / kSlice, (int64_t)kMaxSlices);
+  const int64_t parts = max(rows, min(rows * most, (int64_t)2 * 2560));
+  return kMaxRequests * sizeof(uint32_t) + parts * (sizeof(RowPart) + sizeof(DrawPart)) + 16;
 }
 
 namespace {

@@ -315,6 +315,15 @@ def test_one_workspace_serves_calls_of_other_sizes(gpu_lib):
             assert int(shared[:2048].count_nonzero()) == 0
 
 
+def test_a_workspace_for_the_largest_step_serves_smaller_ones(gpu_lib):
+    ws = gpu_lib.paged_attention_workspace(400, 4, 8, 2, 128, 100, 5000)
+    for ctx, new in (([4900, 0, 3, 70], [100, 100, 100, 100]), ([3000, 9, 0, 70], [1, 1, 1, 1]), ([5], [40]), ([10, 4000], [1, 90])):
+        b = build(ctx, new, 8, 2, 128, 64, seed=sum(new))
+        out, lse = call(gpu_lib, b, max_new=100, max_seq=5000, workspace=ws)
+        want, wlse = call(gpu_lib, b, max_new=100, max_seq=5000)
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_refusals(gpu_lib):
     E = gpu_lib.NVFP4Error
     b = build([20], [2], 4, 2, 64, 16)

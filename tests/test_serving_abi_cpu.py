@@ -93,6 +93,18 @@ def test_attention_workspace_bytes(lib):
     assert f(8192, 1, 40, 8, 128, 8192, 8192) == f(8192, 1, 40, 8, 128, 8192, 10 ** 9) < 128 << 20
 
 
+def test_a_workspace_serves_smaller_steps(lib):
+    f, g = lib.paged_attention_workspace_bytes, lib.verify_drafts_workspace_bytes
+    for hq, hkv, dim in ((40, 8, 128), (24, 4, 256), (64, 1, 64)):
+        for new in (1, 16, 512):
+            sizes = [f(t, 64, hq, hkv, dim, new, 5000) for t in (1, 64, 300, 2000, 64 * new)]
+            assert max(sizes) == sizes[-1] and f(64, 7, hq, hkv, dim, new, 50) <= sizes[-1]
+    for vocab in (1, 8193, 131072, 1 << 20):
+        for drafts in (0, 1, 4, 7):
+            sizes = [g(r, drafts, vocab) for r in (1, 2, 3, 64, 100, 319, 320, 321, 511, 512, 2559, 2560, 2561, 9000)]
+            assert sizes == sorted(sizes) and g(64, drafts, vocab) <= g(64, drafts + 1, vocab) <= g(64, drafts + 1, vocab + 9000)
+
+
 def verify(lib, x=A16, dt=1, ldx=100, rows=6, V=100, rs=A16, nd=A16, R=2, K=2, d=A16, q=None, ldq=100, t=None, u=A16, e=A16,
            lde=100, tok=A16, acc=A16, lp=A16, ws=A16, nws=None):
     if nws is None:

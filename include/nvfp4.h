@@ -397,7 +397,7 @@ int nvfp4_weight_stream_read(const void* w_packed, int64_t n, int64_t k, uint32_
  *   ctx_lens, new_lens  int32 [num_requests], num_requests >= 0.
  *   free_pages   int32 [num_free], num_free >= 0.
  *   free_cursor  int32 [1]: how many of free_pages earlier steps took; may be
- *                null (0).  Must not lie in counts.
+ *                null (0).
  *   block_table  int32 [num_requests, max_pages], row stride ld_table: read for
  *                the contexts' columns, written for the new ones, else untouched.
  *   q_start [num_requests + 1], seq_lens [num_requests], positions
@@ -405,6 +405,10 @@ int nvfp4_weight_stream_read(const void* w_packed, int64_t n, int64_t k, uint32_
  *   counts       total new tokens; pages taken; pages missing; the cursor after
  *                this step.  A total above max_tokens means that the step does
  *                not fit (q_start stops at max_tokens).
+ * Lengths and cursor can be carried from step to step on the device: ctx_lens may
+ * be seq_lens itself, and free_cursor an element of counts (the last one: where
+ * the step before stopped); what a step reads of them is what the one before left.
+ * No other input may overlap an output.
  */
 int paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t num_requests, int page_size,
                const int32_t* free_pages, int64_t num_free, const int32_t* free_cursor, int32_t* block_table,

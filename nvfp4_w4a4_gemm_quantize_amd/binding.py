@@ -505,13 +505,26 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
             dim, ps if pages > 1 else 0, hs if heads > 1 else 0, ts), ks, vs, heads, dim
 
 
+def _plan_apart(ctx, new, free, cursor, outs):
+    """Refuse inputs inside a plan's outputs ((address, bytes) each), but for the two that are carried in place."""
+    low, high = min(o for o, _ in outs), max(o + n for o, n in outs)
+    for x in (ctx, new, free, cursor):
+        if x[0] >= high or x[0] + x[1] <= low or not x[1]:
+            continue
+        for out in outs:
+            carried = (x is ctx and out is outs[1] and x == out) or (x is cursor and out is outs[4])
+            if out[1] and x[0] < out[0] + out[1] and out[0] < x[0] + x[1] and not carried:
+                raise NVFP4Error("ctx_lens, new_lens, free_pages or free_cursor shares memory with an output of the plan")
+
+
 def paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens, free_cursor=None, plan=None):
     """Block tables and slot maps of a step from the requests' lengths, on the device.
 
     ctx_lens, new_lens int32 [R]; free_pages int32 [F]; block_table int32 [R, max_pages] (written in place for the
     new pages); free_cursor int32 [1] or None.  Returns PagedPlan(q_start int32 [R + 1], seq_lens int32 [R],
     positions int32 [max_tokens], slots int64 [max_tokens], counts int32 [4]: new tokens, pages taken, pages missing,
-    cursor after the step); ``plan`` reuses the tensors of an earlier one.
+    cursor after the step); ``plan`` reuses the tensors of an earlier one, whose seq_lens may be this step's ctx_lens and
+    whose counts[3:] its free_cursor (no other input may share memory with an output).
     """
     lib = _lib or load()
     if not isinstance(ctx_lens, _Tensor) or not isinstance(free_pages, _Tensor):
@@ -531,6 +544,8 @@ def paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size, max_token
         p0, p1 = _vec(plan.q_start, _i32, R + 1, "q_start"), _vec(plan.seq_lens, _i32, R, "seq_lens")
         p2, p3 = _vec(plan.positions, _i32, max_tokens, "positions"), _vec(plan.slots, _i64t, max_tokens, "slots")
         p4 = _vec(plan.counts, _i32, 4, "counts")
+        _plan_apart((ctx, 4 * R), (new, 4 * R), (free, 4 * F), (cursor or 0, 4 if cursor else 0),
+                    ((p0, 4 * R + 4), (p1, 4 * R), (p2, 4 * max_tokens), (p3, 8 * max_tokens), (p4, 16)))
     rc = lib.paged_plan(ctx, new, R, page_size, free, F, cursor, table, cols, ld, p0, p1, p2, p3, max_tokens, p4,
                         _raw_stream(ctx_lens.get_device()))
     if rc:

@@ -55,6 +55,7 @@ int paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t num_req
   a.ld_table = ld_table;
   a.max_tokens = max_tokens;
   a.page_shift = page_shift_of(page_size);
+  a.in_place = (num_requests > 0 && ctx_lens == seq_lens) || (free_cursor >= counts && free_cursor < counts + 4);
   return hip_status(launch_paged_plan(a, (hipStream_t)stream));
 }
 

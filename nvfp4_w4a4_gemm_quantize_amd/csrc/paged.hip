@@ -25,9 +25,23 @@ namespace nvfp4 {
 // tokens, pages and requests are dealt out over the whole grid.  A thread owns
 // a run of ceil(R / 256) requests in the scan; a token finds its run by binary
 // search in LDS and its request by walking the run.
+//
+// Every workgroup reads the lengths and the cursor at its own time, and twice, so
+// nothing of that launch may write them.  A step in place (seq_lens is ctx_lens, or
+// the cursor lies in counts) writes these two last where it has one workgroup (8
+// requests of one token, replayed in a graph: 2.8 us, with separate tensors 2.7);
+// otherwise a second launch of one workgroup does (1024 requests with 5000 tokens 7.8
+// us, 3.8).
 constexpr int kPlanThreads = 256;
 
 namespace {
+
+enum PlanPart {
+  kPlanAll,      // nothing in place
+  kPlanOne,      // in place, one workgroup
+  kPlanTables,   // all but seq_lens and counts
+  kPlanCarry,    // these two, one workgroup
+};
 
 struct PlanLens {
   int64_t ctx, tokens, before, need;
@@ -54,6 +68,7 @@ __device__ __forceinline__ int plan_run(const int64_t* prefix, int64_t x) {
 
 }  // namespace
 
+template <PlanPart PART>
 __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   __shared__ int64_t tok[kPlanThreads + 1], pg[kPlanThreads + 1];
   __shared__ int64_t wave_tok[kPlanThreads / 64], wave_pg[kPlanThreads / 64];
@@ -93,26 +108,8 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   const int64_t left = max(a.num_free - cursor, (int64_t)0);
   const int64_t stride = (int64_t)gridDim.x * kPlanThreads, first = (int64_t)blockIdx.x * kPlanThreads + tid;
 
-  // per request (a thread's run goes to one workgroup of the grid)
-  if (tid % gridDim.x == blockIdx.x) {
-    int64_t t = tok[tid];
-    for (int64_t r = r0; r < r1; ++r) {
-      const PlanLens l = plan_lens(a, r);
-      a.q_start[r] = (int32_t)min(t, a.max_tokens);
-      a.seq_lens[r] = (int32_t)min(l.ctx + l.tokens, (int64_t)INT32_MAX);
-      t += l.tokens;
-    }
-  }
-  if (first == 0) {
-    const int64_t taken = min(pages, left);
-    a.q_start[a.requests] = (int32_t)min(total, a.max_tokens);
-    a.counts[0] = (int32_t)min(total, (int64_t)INT32_MAX);
-    a.counts[1] = (int32_t)taken;
-    a.counts[2] = (int32_t)min(pages - taken, (int64_t)INT32_MAX);
-    a.counts[3] = (int32_t)(cursor + taken);
-  }
   // per page needed
-  for (int64_t p = first; p < pages; p += stride) {
+  for (int64_t p = first; PART != kPlanCarry && p < pages; p += stride) {
     const int w = plan_run(pg, p);
     int64_t r = w * run, base = pg[w];
     PlanLens l = plan_lens(a, r);
@@ -123,7 +120,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     a.block_table[r * a.ld_table + l.before + (p - base)] = p < left ? a.free_pages[cursor + p] : -1;
   }
   // per token; the tail of the buffers is padding
-  for (int64_t t = first; t < a.max_tokens; t += stride) {
+  for (int64_t t = first; PART != kPlanCarry && t < a.max_tokens; t += stride) {
     int64_t pos = -1, slot = -1;
     if (t < total) {
       const int w = plan_run(tok, t);
@@ -145,13 +142,45 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     a.positions[t] = (int32_t)pos;
     a.slots[t] = slot;
   }
+  if (PART == kPlanOne) __syncthreads();
+  // per request (a thread's run goes to one workgroup of the grid)
+  if (tid % gridDim.x == blockIdx.x) {
+    int64_t t = tok[tid];
+    for (int64_t r = r0; r < r1; ++r) {
+      const PlanLens l = plan_lens(a, r);
+      if (PART != kPlanCarry) a.q_start[r] = (int32_t)min(t, a.max_tokens);
+      if (PART != kPlanTables) a.seq_lens[r] = (int32_t)min(l.ctx + l.tokens, (int64_t)INT32_MAX);
+      t += l.tokens;
+    }
+  }
+  if (first == 0) {
+    const int64_t taken = min(pages, left);
+    if (PART != kPlanCarry) a.q_start[a.requests] = (int32_t)min(total, a.max_tokens);
+    if (PART != kPlanTables) {
+      a.counts[0] = (int32_t)min(total, (int64_t)INT32_MAX);
+      a.counts[1] = (int32_t)taken;
+      a.counts[2] = (int32_t)min(pages - taken, (int64_t)INT32_MAX);
+      a.counts[3] = (int32_t)(cursor + taken);
+    }
+  }
 }
 
 hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t st) {
   // one token a thread up to 1024 workgroups (four a CU), then several
   const int64_t want = (max(a.max_tokens, a.requests) + kPlanThreads - 1) / kPlanThreads;
   const unsigned grid = (unsigned)min(max(want, (int64_t)1), (int64_t)1024);
-  paged_plan_kernel<<<grid, kPlanThreads, 0, st>>>(a);
+  if (!a.in_place) {
+    paged_plan_kernel<kPlanAll><<<grid, kPlanThreads, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  if (grid == 1) {
+    paged_plan_kernel<kPlanOne><<<1, kPlanThreads, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  paged_plan_kernel<kPlanTables><<<grid, kPlanThreads, 0, st>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  paged_plan_kernel<kPlanCarry><<<1, kPlanThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 

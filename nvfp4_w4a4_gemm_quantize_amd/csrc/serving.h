@@ -22,6 +22,7 @@ struct PlanArgs {
   int32_t* counts;             // [4]
   int64_t requests, num_free, max_pages, ld_table, max_tokens;
   int page_shift;
+  bool in_place;               // seq_lens is ctx_lens, or counts hold free_cursor
 };
 hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t st);
 

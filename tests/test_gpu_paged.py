@@ -94,6 +94,57 @@ def test_plan_reuses_its_tensors_and_strided_tables(gpu_lib):
     assert table.tolist() == [[10, 11, -7, -7, -7, -7], [12, -7, -7, -7, -7, -7], [13, 14, 15, -7, -7, -7]]
 
 
+@pytest.mark.parametrize("requests,spare", [(1, 3), (7, 0), (300, 40), (1500, 1000)])
+def test_plan_carries_lengths_and_cursor_in_place(gpu_lib, requests, spare):
+    """Steps whose contexts are the plan's own seq_lens and whose cursor is its own last count, against the oracle's
+    steps: one workgroup and many, and steps that run out of pages."""
+    rng = np.random.default_rng(requests)
+    page, cols = 16, 12
+    ctx, cursor = rng.integers(0, 60, requests), 2
+    free = rng.permutation(4000).astype(np.int32)[:requests * 4]
+    table = context_table(ctx, cols, page, rng)
+    steps = [rng.integers(0, 3, requests), rng.integers(0, 33, requests), np.ones(requests, np.int64), rng.integers(0, 40, requests)]
+    most = max(int(n.sum()) for n in steps) + spare
+    dev, free_dev = i32(table), i32(free)
+    plan = gpu_lib.paged_plan(i32(ctx), i32(steps[0]), free_dev, dev, page, most, free_cursor=i32([cursor]))
+    for s, new in enumerate(steps):
+        if s:
+            gpu_lib.paged_plan(plan.seq_lens, i32(new), free_dev, dev, page, most, free_cursor=plan.counts[3:], plan=plan)
+        want = OP.plan(ctx, new, free, cursor, table, page, most)
+        for g, w, name in zip((dev, *plan), want, ("block_table", "q_start", "seq_lens", "positions", "slots", "counts")):
+            np.testing.assert_array_equal(g.cpu().numpy(), w, err_msg="step %d: %s" % (s, name))
+        table, ctx, cursor = want[0], want[2], int(want[5][3])
+
+
+def test_plan_in_place_in_a_graph(gpu_lib):
+    """A captured step that carries its own lengths: every replay is the next step."""
+    free, table, new = i32(np.arange(100, 400)), torch.full((3, 16), -1, dtype=torch.int32, device="cuda"), i32([1, 0, 5])
+    plan = gpu_lib.paged_plan(i32([14, 3, 0]), new, free, table, 16, 8)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        gpu_lib.paged_plan(plan.seq_lens, new, free, table, 16, 8, free_cursor=plan.counts[3:], plan=plan)
+    own, want = table.clone(), plan._make(x.clone() for x in plan)
+    for _ in range(9):
+        graph.replay()
+        want = gpu_lib.paged_plan(want.seq_lens.clone(), new, free, own, 16, 8, free_cursor=want.counts[3:].clone())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((table, *plan), (own, *want)))
+
+
+def test_plan_refuses_other_inputs_inside_its_outputs(gpu_lib):
+    new, free, table = i32([1, 2, 3]), i32(np.arange(9)), i32(np.full((3, 4), -1))
+    plan = gpu_lib.paged_plan(i32([0, 0, 0]), new, free, table, 16, 9)
+    for bad in (dict(ctx_lens=plan.q_start[:3]), dict(ctx_lens=plan.positions[2:5]), dict(new_lens=plan.seq_lens),
+                dict(free_pages=plan.positions), dict(free_cursor=plan.seq_lens[:1]), dict(free_cursor=plan.q_start[3:]),
+                dict(ctx_lens=plan.slots.view(torch.int32)[1:4])):
+        with pytest.raises(gpu_lib.NVFP4Error):
+            gpu_lib.paged_plan(**{**dict(ctx_lens=plan.seq_lens, new_lens=new, free_pages=free, block_table=table, page_size=16,
+                                         max_tokens=9, plan=plan), **bad})
+    gpu_lib.paged_plan(plan.seq_lens, new, free, table, 16, 9, plan=plan, free_cursor=plan.counts[3:])
+    assert plan.seq_lens.tolist() == [2, 4, 6] and plan.q_start.tolist() == [0, 1, 3, 6]
+
+
 # --------------------------------------------------------------- K/V write --
 
 FP8 = torch.float8_e4m3fn

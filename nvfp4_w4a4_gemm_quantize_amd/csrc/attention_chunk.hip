@@ -286,7 +286,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
 
   float c = a.scale * kLog2e;
   if (a.cache.k_scale) c *= a.cache.k_scale[head];
-  const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
+  const uint32_t flip = c < 0.f ? 0x80008000u : 0u, spoil = c == c ? 0u : 0x7fff7fffu;   // a NaN scale goes into q
   c = fmaxf(fabsf(c), FLT_MIN);   // never 0: a hidden score's -inf stays one
 
   // this lane's row of q, the B operand: column c32, k = 8 columns of q
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   for (int s = 0; s < KS; ++s) {
     u32x4 w = *(const u32x4*)(a.q + (int64_t)(l.start + my_token) * a.ld_q + my_head * D + s * 16 + h * 8);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = live ? w[i] ^ flip : 0u;
+    for (int i = 0; i < 4; ++i) w[i] = live ? (w[i] ^ flip) | spoil : 0u;
     q[s] = __builtin_bit_cast(bf16x8, w);
   }
   // positions relative to the first key of the part

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
     const int seen_to = uniform(max(min(keys, max(pos0, -1) + 1 - origin), 0) >> 5);
     float c = a.scale * kLog2e;
     if (a.cache.k_scale) c *= a.cache.k_scale[head];
-    const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
+    const uint32_t flip = c < 0.f ? 0x80008000u : 0u, spoil = c == c ? 0u : 0x7fff7fffu;   // a NaN scale goes into q
     c = fmaxf(fabsf(c), FLT_MIN);   // never 0: a hidden score's -inf stays one
 
     // Q, the B operand: column c16 = row of q, k = 8 columns of q
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
         const int chunk = FP8 ? (s >> 1) * 8 + g * 2 + (s & 1) : s * 4 + g;
         u32x4 w = *(const u32x4*)(qr + chunk * 8);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = live ? w[i] ^ flip : 0u;
+        for (int i = 0; i < 4; ++i) w[i] = live ? (w[i] ^ flip) | spoil : 0u;
         q[n][s] = __builtin_bit_cast(bf16x8, w);
       }
     }

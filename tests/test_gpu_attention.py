@@ -159,6 +159,23 @@ def test_negative_head_scale(gpu_lib):
     check(gpu_lib, b)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 5, 60])
+def test_a_nan_head_scale_reaches_its_heads_rows(gpu_lib, dim, new):
+    """Rows of the head that see a key are NaN, rows that see none stay 0, and the other head is as ever."""
+    b = build([77, 300, 6], [new] * 3, 4, 2, dim, 16, fp8=True, seed=1)
+    b["lens"][2] = max(b["lens"][2] - 8, 0)        # the first rows of request 2 stand at negative positions
+    want, wlse = call(gpu_lib, b)
+    b["k_scale"] = torch.tensor([float(b["k_scale"][0]), float("nan")], device="cuda")
+    out, lse = call(gpu_lib, b)
+    out, want = out.reshape(-1, 2, 2, dim), want.reshape(-1, 2, 2, dim)
+    lse, wlse = lse.reshape(-1, 2, 2), wlse.reshape(-1, 2, 2)
+    assert torch.equal(out[:, 0], want[:, 0]) and torch.equal(lse[:, 0], wlse[:, 0])
+    empty = torch.isneginf(wlse[:, 1])
+    assert torch.isnan(out[:, 1][~empty]).all() and torch.isnan(lse[:, 1][~empty]).all()
+    assert out[:, 1][empty].eq(0).all() and torch.isneginf(lse[:, 1][empty]).all()
+
+
 @pytest.mark.parametrize("new,fp8", [(1, False), (1, True), (60, False), (60, True)])
 def test_large_scores_and_rising_maximum(gpu_lib, new, fp8):
     """Keys that grow with their position: the running maximum rises in every tile, by hundreds."""

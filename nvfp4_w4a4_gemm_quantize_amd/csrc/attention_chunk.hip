@@ -503,15 +503,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   auto raise = [&](float top) {
     if (__any(top > 8.f || (m == -INFINITY && top > m))) {
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float old = reference(), to = fmaxf(m, old + top);
-      const float by = m == to ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - to);
+      // Heads of 256 have weights rounded to bf16 that are still to be multiplied: their
+      // maximum is taken in whole steps, by which a rounded weight is scaled exactly.
+      const float old = reference(), to = fmaxf(m, MIXED ? ceilf(old + top) : old + top);
+      const float by = m == to ? 1.f : m == -INFINITY ? 0.f : MIXED ? ldexpf(1.f, (int)fmaxf(m - to, -200.f)) : exp2_fast(m - to);
       m = to;
       sum *= by;
 #pragma unroll
       for (int i = 0; i < DF; ++i)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[i][k] *= by;
-      if constexpr (MIXED) {                 // the weights still to be multiplied, rounded once more
+      if constexpr (MIXED) {
 #pragma unroll
         for (int u = 0; u < 2 * NK; ++u)
 #pragma unroll

@@ -189,6 +189,35 @@ def test_large_scores_and_rising_maximum(gpu_lib, new, fp8):
     check(gpu_lib, b, scale=1.0, out_dtype=torch.float32)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_rising_maximum_rounds_no_weight_again(gpu_lib, dim, fp8):
+    """Keys 0 - 31 weigh 1 until the next tile's first key raises the maximum, by 2^0.96 for the rows looked at and by 2^20
+    for their neighbours (whose rise scales them all).  The values are 1 at the former and 0 elsewhere, and a weight of 1
+    needs no rounding: what is left is an exponent of 20 in fp32 (three roundings, 2.5e-6), the exponential's 2^-20 and a
+    sum of 33 terms (2e-6), under 2^-17 in all; a weight rounded anew would be off by 2^-8.1."""
+    tokens, rise, first = 64, 0.9609375, 32 if dim == 256 else 64
+    b = build([128], [tokens], 1, 1, dim, 16, seed=1, poison=False)
+    k, v = torch.zeros(192, dim, device="cuda"), torch.zeros(192, dim, device="cuda")
+    k[32:, 0] = -448
+    k[first, 0] = 1
+    v[:32] = 1
+    order = torch.tensor([int(p) for p in b["table"][0][:12]], device="cuda")
+    for name, x in (("k", k), ("v", v)):
+        b[name][order, 0] = x.view(12, 16, dim).to(torch.bfloat16)
+        if fp8:
+            b[name] = b[name].to(FP8)
+    q = torch.zeros(tokens, dim, device="cuda")
+    q[::2, 0], q[1::2, 0] = rise, 20
+    b["q"] = q.to(torch.bfloat16)
+    assert float(b["q"][0, 0]) == rise
+    out, lse = call(gpu_lib, b, scale=float(np.log(2)), out_dtype=torch.float32)
+    for x, got, glse in ((rise, out[::2], lse[::2]), (20, out[1::2], lse[1::2])):
+        want = 32 / (32 + 2.0 ** x)
+        assert (got.double() - want).abs().max() <= want * 2.0 ** -17, (got.double() / want - 1).abs().max()
+        assert (glse.double() - np.log(32 + 2.0 ** x)).abs().max() <= 2.0 ** -17
+
+
 @pytest.mark.parametrize("ctx,new,hq,heads,dim,fp8", [
     (20000, 1, 4, 2, 128, False), (9000, 5, 6, 1, 256, True), (9000, 40, 5, 1, 64, False), (6000, 300, 2, 1, 128, True),
 ])

@@ -69,13 +69,16 @@ class Model:
             self.workspaces[key] = make(*sizes)
         return self.workspaces[key]
 
-    def step(self, tokens, ctx, new, trace=None):
-        """Logits of the step's tokens (all requests' new ones end to end), and its plan."""
+    def step(self, tokens, ctx, new, trace=None, rows=None):
+        """Logits of the step's tokens (all requests' new ones end to end), and its plan.  `rows` above the number of
+        tokens makes a step of that size, as one that is captured has: the last rows are padding, zero from layer to
+        layer, so that they change no linear layer's global scale."""
         i32 = dict(dtype=torch.int32, device="cuda")
-        T, R = len(tokens), len(new)
+        T, R = len(tokens) if rows is None else rows, len(new)
         plan = B.paged_plan(torch.tensor(ctx, **i32), torch.tensor(new, **i32), torch.tensor(self.free, **i32), self.table,
                             self.page, T)
-        x = self.embed[torch.tensor(tokens, device="cuda")]
+        x = self.embed.new_zeros(T, self.embed.shape[1])
+        x[:len(tokens)] = self.embed[torch.tensor(tokens, device="cuda")]
         nq, nk = self.hq * self.dim, self.hkv * self.dim
         ws = self.workspace("attention", B.paged_attention_workspace, T, R, self.hq, self.hkv, self.dim, max(new), self.max_seq)
         for b in self.blocks:

@@ -378,6 +378,9 @@ int nvfp4_weight_stream_read(const void* w_packed, int64_t n, int64_t k, uint32_
 #define NVFP4_CACHE_BF16 0
 #define NVFP4_CACHE_E4M3 1
 
+/* Or'ed into paged_attention's out_dtype: padding rows of out and lse get 0 and -inf. */
+#define NVFP4_OUT_CLEAR_PADDING 16
+
 #define NVFP4_LOGITS_F32 0
 #define NVFP4_LOGITS_BF16 1
 
@@ -451,14 +454,17 @@ int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t l
  *   q            bf16 [tokens, num_heads * head_dim], row stride ld_q (multiple
  *                of 8), 16-byte aligned.
  *   q_start, seq_lens   as from paged_plan; rows of q from q_start[num_requests]
- *                on (padding) are left untouched in out and lse.
+ *                on (padding) are left untouched in out and lse, or get 0 and -inf
+ *                with NVFP4_OUT_CLEAR_PADDING: what takes all rows of out next
+ *                needs them cleared, such as a dynamic global scale, whose maximum
+ *                one stale row would set for all (nvfp4_quantize).
  *   max_new      >= every request's new tokens; max_seq >= every seq_lens[r]
  *                (it only sizes the split of the work).
  *   head_dim     64, 128 or 256 (others NVFP4_EUNSUPPORTED).
  *   block_table  int32 [num_requests, max_pages], row stride ld_table.
  *   k_scale, v_scale  device float [num_kv_heads], E4M3 only (null = 1).
- *   out          [tokens, num_heads * head_dim] of out_dtype, row stride ld_out
- *                (multiple of 4), 16-byte aligned.
+ *   out          [tokens, num_heads * head_dim] of out_dtype (NVFP4_OUT_*), row
+ *                stride ld_out (multiple of 4), 16-byte aligned.
  *   lse          optional fp32 [tokens, num_heads] contiguous (natural log).
  *   workspace    16-byte aligned, at least paged_attention_workspace_bytes of
  *                the same or larger sizes; its first 2048 bytes zero before its

@@ -15,6 +15,7 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libnvfp4.so")
 
 OUT_F32, OUT_BF16 = 0, 1
+OUT_CLEAR_PADDING = 16
 EPI_NONE, EPI_SILU_MUL = 0, 1
 SEG_NONE, SEG_SIGMOID, SEG_GDN_DECAY = 0, 1, 2
 MAX_SEGMENTS = 16
@@ -581,11 +582,13 @@ def paged_attention_workspace(tokens, num_requests, num_heads, num_kv_heads, hea
 
 def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new, max_seq, scale=None, window=0,
                     k_scale=None, v_scale=None, out_dtype=torch.bfloat16, out=None, lse=None, return_lse=False,
-                    workspace=None):
+                    workspace=None, clear_padding=None):
     """Attention of every request's new tokens over its cached keys (causal, optionally a sliding window).
 
     q: bf16 [T, num_heads * head_dim] view, rows of request r from q_start[r] to q_start[r + 1]; caches as in
     paged_kv_write; block_table int32 [R, max_pages]; max_new and max_seq bound the requests' new tokens and lengths.
+    Rows of q from q_start[R] on are padding: with clear_padding they get 0 (lse -inf), without they are left as they
+    are (None: cleared where out is allocated here).
     Returns out [T, num_heads * head_dim] (and lse fp32 [T, num_heads] with return_lse)."""
     lib = _lib or load()
     cache, ks, vs, heads, dim = _cache(k_cache, v_cache, k_scale, v_scale)
@@ -598,6 +601,8 @@ def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new
         raise NVFP4Error("seq_lens must be a GPU tensor")
     R = seq_lens.numel()
     table, ld_t, max_pages = _rows(block_table, _i32, R, None, "block_table")
+    if clear_padding is None:
+        clear_padding = out is None
     if out is None:
         out = q.new_empty((T, cols), dtype=_bf16 if out_dtype in (OUT_BF16, _bf16) else _f32)
         op, ld_o = out.data_ptr(), cols
@@ -611,7 +616,7 @@ def paged_attention(q, k_cache, v_cache, block_table, q_start, seq_lens, max_new
     rc = lib.paged_attention(qp, ld_q, T, _vec(q_start, _i32, R + 1, "q_start"), _vec(seq_lens, _i32, R, "seq_lens"), R,
                              max_new, max_seq, num_heads, *cache, table, max_pages, ld_t,
                              dim ** -0.5 if scale is None else scale, window, ks, vs, op,
-                             OUT_BF16 if out.dtype is _bf16 else OUT_F32, ld_o,
+                             (OUT_BF16 if out.dtype is _bf16 else OUT_F32) + (OUT_CLEAR_PADDING if clear_padding else 0), ld_o,
                              None if lse is None else _vec(lse, _f32, T * num_heads, "lse"),
                              _vec(workspace, _u8, bytes_, "workspace"), bytes_, _raw_stream(q.get_device()))
     if rc:

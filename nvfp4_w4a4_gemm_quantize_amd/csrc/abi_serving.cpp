@@ -126,7 +126,8 @@ int paged_attention(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32
   a.scale = scale;
   a.hq = num_heads;
   a.group = num_heads / num_kv_heads;
-  a.out_bf16 = out_dtype == NVFP4_OUT_BF16;
+  a.out_bf16 = (out_dtype & ~NVFP4_OUT_CLEAR_PADDING) == NVFP4_OUT_BF16;
+  a.clear_padding = (out_dtype & NVFP4_OUT_CLEAR_PADDING) != 0;
   return hip_status(launch_paged_attention(a, (hipStream_t)stream));
 }
 

@@ -183,6 +183,21 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int start, int
   if (a.lse && d == 0) a.lse[trow * a.hq + hq] = den == 0.f ? -INFINITY : kLn2 * (top + __log2f(den));
 }
 
+// Rows of no request, from `row` on: 0 and lse = -inf, a row a workgroup.
+__device__ __forceinline__ void clear_padding(const AttentionArgs& a, int row) {
+  const int pieces = a.hq * a.cache.dim / 4;
+  for (int64_t t = max(row, 0) + (int64_t)blockIdx.x; t < a.tokens; t += gridDim.x) {
+    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+      if (a.out_bf16)
+        *(u32x2*)((uint16_t*)a.out + t * a.ld_out + 4 * i) = u32x2{0u, 0u};
+      else
+        *(f32x4*)((float*)a.out + t * a.ld_out + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (a.lse)
+      for (int i = threadIdx.x; i < a.hq; i += blockDim.x) a.lse[t * a.hq + i] = -INFINITY;
+  }
+}
+
 // Launches of the two kernels and of their joins (attention_*.hip).
 hipError_t launch_attention_decode(const AttentionArgs& a, hipStream_t st);
 hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipStream_t st);

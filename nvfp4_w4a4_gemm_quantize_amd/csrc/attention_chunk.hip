@@ -170,6 +170,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hkv = a.cache.heads, group = a.group;
 
+  if (a.clear_padding) clear_padding(a, a.q_start[a.requests]);
+
   // prefix of the line over runs of requests
   __shared__ int64_t before[kThreads + 1];
   __shared__ int64_t wave_sum[kChunkWaves];
@@ -947,6 +949,9 @@ hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipSt
 // takes all of them, which spares launches and the second pass over the chip (32
 // requests of up to 32 tokens over 4096 keys: 92 us, both kernels 112; of up to 10
 // 93 against 113).
+// Clears the padding rows of a batch that has nothing else (it brings no new tokens).
+__global__ __launch_bounds__(256) void attention_padding_kernel(AttentionArgs a) { clear_padding(a, a.q_start[a.requests]); }
+
 static bool may_tile(int64_t max_new, int group) { return max_new * group > kDecodeRows; }
 static bool may_stream(int64_t tokens, int64_t requests, int64_t max_new, int group) {
   return max_new > 0 && group <= kDecodeRows && 
@@ -978,9 +983,13 @@ hipError_t launch_paged_attention(const AttentionArgs& args, hipStream_t st) {
     a.stream_rows = kDecodeRows;
     hipError_t e = launch_attention_decode(a, st);
     if (e != hipSuccess) return e;
+    a.clear_padding = false;   // done
     ws += (attention_decode_workspace(a.cache.dim) + 255) / 256 * 256;
   }
-  return may_tile(a.max_new, a.group) ? launch_attention_chunk(a, ws, st) : hipSuccess;
+  if (may_tile(a.max_new, a.group)) return launch_attention_chunk(a, ws, st);
+  if (!a.clear_padding) return hipSuccess;
+  attention_padding_kernel<<<(unsigned)min(a.tokens, (int64_t)1024), 256, 0, st>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4

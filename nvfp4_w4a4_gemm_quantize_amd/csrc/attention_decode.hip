@@ -130,6 +130,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hkv = a.cache.heads, group = a.group;
   const DecodeWorkspace ws = decode_workspace(a.workspace);
+  const int padding = a.clear_padding ? a.q_start[a.requests] : INT32_MAX;   // first row of no request
 
   // prefix of the tiles over runs of requests
   const int requests = (int)a.requests, run = (requests + kThreads - 1) / kThreads;
@@ -495,6 +496,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
     }
     if (tid == 0) ws.arrived[g0] = 0;   // for the next call
   }
+  clear_padding(a, padding);
 }
 
 size_t attention_decode_workspace(int dim) {

@@ -62,6 +62,7 @@ struct AttentionArgs {
   int window;                  // 0: none
   float scale;
   int hq, group, out_bf16;
+  bool clear_padding;          // rows of no request get 0 and lse = -inf
   // n / group = mulhi(n, group_mul) >> group_shift for n < 2^31, group > 1; set by the launcher
   uint32_t group_mul;
   int group_shift;

@@ -94,7 +94,8 @@ int validate_paged_attention(const void* q, int64_t ld_q, int64_t tokens, const 
                              int64_t ld_out, const void* lse, const void* workspace, size_t workspace_bytes,
                              size_t needed) {
   const int64_t cols = (int64_t)num_heads * head_dim;
-  if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_EINVAL;
+  const int out_kind = out_dtype & ~NVFP4_OUT_CLEAR_PADDING;
+  if (out_kind != NVFP4_OUT_F32 && out_kind != NVFP4_OUT_BF16) return NVFP4_EINVAL;
   if (!isfinite(scale) || window < 0) return NVFP4_EINVAL;
   if (ld_q < cols || ld_out < cols || max_pages <= 0 || ld_table < max_pages) return NVFP4_ESHAPE;
   if (max_pages > INT32_MAX) return NVFP4_EUNSUPPORTED;

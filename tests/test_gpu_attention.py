@@ -147,6 +147,47 @@ def test_requests_without_new_tokens_and_padding_rows(gpu_lib):
         assert out[-3:].eq(7).all() and lse[-3:].eq(7).all() and out[:-3].ne(7).all()
 
 
+@pytest.mark.parametrize("new,hq,heads", [([0, 1, 0, 3, 0], 4, 2), ([0, 50, 0, 1, 0], 4, 2), ([60, 2, 0, 64, 40], 4, 2),
+                                          ([0, 0, 0, 0, 0], 4, 2), ([0, 0, 0, 0, 0], 40, 1), ([1, 1, 0, 0, 1], 40, 1)])
+def test_padding_rows_are_cleared(gpu_lib, new, hq, heads):
+    """Outputs that the call allocates, and those it is asked to clear: 0 and -inf after the last request's rows, the
+    others as without padding; columns beside a strided output stay."""
+    b = build([9, 8, 7, 40, 0], new, hq, heads, 64, 16, seed=4)
+    live, pad = b["q"].shape[0], 700
+    b["q"] = torch.cat([b["q"], torch.full((pad, hq * 64), float("nan"), dtype=torch.bfloat16, device="cuda")])
+    # the rows count in the rules that choose a kernel: the same call, told to leave them
+    want, wlse = torch.zeros(live + pad, hq * 64, device="cuda"), torch.zeros(live + pad, hq, device="cuda")
+    call(gpu_lib, b, out=want, lse=wlse, out_dtype=torch.float32, clear_padding=False)
+    assert want[live:].eq(0).all() and wlse[live:].eq(0).all()
+    want, wlse = want[:live], wlse[:live]
+    stale = torch.full((live + pad, hq * 64), float("nan"), device="cuda")
+    del stale                                      # what the allocator hands out next
+    out, lse = call(gpu_lib, b, out_dtype=torch.float32)
+    wide, lse2 = torch.full((live + pad, hq * 64 + 8), 7.0, device="cuda"), torch.full((live + pad, hq), 7.0, device="cuda")
+    call(gpu_lib, b, out=wide[:, 4:-4], lse=lse2, out_dtype=torch.float32, clear_padding=True)
+    half = torch.full((live + pad, hq * 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    call(gpu_lib, b, out=half, clear_padding=True)
+    for o, l in ((out, lse), (wide[:, 4:-4], lse2)):
+        assert torch.equal(o[:live], want) and torch.equal(l[:live], wlse)
+        assert o[live:].eq(0).all() and torch.isneginf(l[live:]).all()
+    assert half[live:].eq(0).all() and torch.equal(half[:live], want.to(torch.bfloat16))
+    assert wide[:, :4].eq(7).all() and wide[:, -4:].eq(7).all()
+
+
+def test_a_padded_step_keeps_the_next_layers_scale(gpu_lib):
+    """The dynamic global scale of a linear layer after a padded step is that of the live rows."""
+    b = build([30, 70], [1, 4], 4, 2, 64, 16, seed=5)
+    b["q"] = torch.cat([b["q"], torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda")])
+    for _ in range(3):
+        stale = torch.full((8, 256), 3e38, dtype=torch.bfloat16, device="cuda")
+        del stale
+        out, _ = call(gpu_lib, b)
+        codes, scales, g = gpu_lib.nvfp4_quantize(out)
+        wcodes, wscales, wg = gpu_lib.nvfp4_quantize(out[:5].clone())
+        assert float(g) == float(wg) and torch.equal(codes[:5], wcodes) and torch.equal(scales[:5], wscales)
+        assert codes[5:].eq(0).all()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 @pytest.mark.parametrize("new", [1, 50])
 def test_scales(gpu_lib, scale, new):

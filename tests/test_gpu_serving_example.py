@@ -55,6 +55,30 @@ def test_steps_agree_with_the_oracle_on_their_own_inputs(serving):
         ctx = [c + n for c, n in zip(ctx, new)]
 
 
+def test_padded_steps_agree_with_steps_of_their_own_size(serving):
+    """Padding rows stay zero through every layer, and the live rows' logits are those of a step without padding: within the
+    differences of kernels for other row counts, which bf16 roundings of the layers between pass on."""
+    rng = np.random.default_rng(3)
+    models, ctx = [small(serving), small(serving)], [0, 0, 0]
+    for new in ([40, 1, 70], [1, 5, 1], [2, 0, 1]):
+        tokens, trace = rng.integers(0, 512, sum(new)).tolist(), []
+        want, plan = models[0].step(tokens, ctx, new)
+        for _ in range(3):
+            stale = torch.full((128, 4 * 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+            del stale
+        got, padded = models[1].step(tokens, ctx, new, trace, rows=128)
+        assert padded.counts.tolist() == plan.counts.tolist() and padded.slots[sum(new):].eq(-1).all()
+        assert torch.equal(padded.slots[:sum(new)], plan.slots)
+        for q, k, v, a in trace:
+            assert all(x[sum(new):].eq(0).all() for x in (q, k, v, a))
+        assert got[sum(new):].eq(0).all() and torch.isfinite(got.float()).all()
+        off = (got[:sum(new)].float() - want.float()).norm() / want.float().norm()
+        assert off < 0.05, off
+        for m in models:
+            m.take_pages(ctx, new, new)
+        ctx = [c + n for c, n in zip(ctx, new)]
+
+
 @pytest.mark.parametrize("temperature", [0.0, 0.7])
 def test_generation_keeps_its_books(serving, temperature):
     """Pages are neither lost nor given twice, every step says at least one token a request, and a rerun says the same."""

@@ -85,6 +85,13 @@ def test_attention_validation(lib):
     assert attn(lib, R=0, qs=None) == OK
 
 
+def test_attention_takes_the_padding_flag_with_either_type(lib):
+    for kind in (0, 1):
+        assert attn(lib, od=kind | 16, T=0, q=None, out=None) == OK and attn(lib, od=kind | 16, nws=100) == ESIZE
+    for od in (16 | 2, 16 | 32, 32, -1, -16):
+        assert attn(lib, od=od) == EINVAL, od
+
+
 def test_attention_workspace_bytes(lib):
     f = lib.paged_attention_workspace_bytes
     assert f(4, 2, 4, 3, 128, 1, 10) == 0 and f(4, 2, 4, 2, 96, 1, 10) == 0

@@ -467,9 +467,9 @@ int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t l
  *                stride ld_out (multiple of 4), 16-byte aligned.
  *   lse          optional fp32 [tokens, num_heads] contiguous (natural log).
  *   workspace    16-byte aligned, at least paged_attention_workspace_bytes of
- *                the same or larger sizes; its first 2048 bytes zero before its
- *                first use (each call leaves them so); not shared by calls in
- *                flight on different streams.
+ *                the same or larger sizes (num_kv_heads: the same or fewer); its
+ *                first 2048 bytes zero before its first use (each call leaves them
+ *                so); not shared by calls in flight on different streams.
  * tokens == 0 or num_requests == 0 enqueues nothing.  Results are
  * deterministic.
  */

@@ -960,11 +960,11 @@ static bool may_stream(int64_t tokens, int64_t requests, int64_t max_new, int gr
 
 size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int hkv, int dim, int64_t max_new,
                                  int64_t max_seq) {
-  const int group = hq / hkv;
   size_t n = 16 + kArrivedBytes;
-  // whatever the tokens: what serves a step serves smaller ones
-  if (max_new > 0 && group <= kDecodeRows) n += (attention_decode_workspace(dim) + 255) / 256 * 256;
-  if (may_tile(max_new, group)) n += attention_chunk_workspace(requests, dim);
+  // what serves a step serves smaller ones: whatever the tokens, and with the streaming
+  // kernel's parts for groups above its rows too, whose calls never use them
+  if (max_new > 0) n += (attention_decode_workspace(dim) + 255) / 256 * 256;
+  if (may_tile(max_new, hq / hkv)) n += attention_chunk_workspace(requests, dim);
   return n;
 }
 

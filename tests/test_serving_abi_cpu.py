@@ -112,6 +112,21 @@ def test_a_workspace_serves_smaller_steps(lib):
             assert sizes == sorted(sizes) and g(64, drafts, vocab) <= g(64, drafts + 1, vocab) <= g(64, drafts + 1, vocab + 9000)
 
 
+def test_a_workspace_serves_steps_of_smaller_layers(lib):
+    """The bytes rise with every size, with fewer KV heads for as many heads too."""
+    f = lib.paged_attention_workspace_bytes
+    for hkv in (1, 2, 4):
+        for dim in (64, 128, 256):
+            for new in (0, 1, 16, 33, 512):
+                for requests in (1, 64, 5000):
+                    sizes = [f(requests, requests, hkv * g, hkv, dim, new, 5000) for g in (1, 2, 8, 31, 32, 33, 40, 64, 100)]
+                    assert sizes == sorted(sizes), (hkv, dim, new, sizes)
+                    here = f(requests, requests, 32, hkv, dim, new, 5000)
+                    assert f(requests, requests, 32, 2 * hkv, dim, new, 5000) <= here <= f(requests, requests, 32, hkv, 256, new, 5000)
+                    assert here <= f(requests, requests, 32, hkv, dim, new + 1, 5000) and here <= f(requests, requests + 1, 32, hkv, dim, new, 5000)
+    assert attn(lib, hq=8, heads=1, R=64, mn=16, ldq=1024, ldo=1024, nws=f(4, 64, 40, 1, 128, 16, 100)) == EHIP   # no GPU here, but bytes enough
+
+
 def verify(lib, x=A16, dt=1, ldx=100, rows=6, V=100, rs=A16, nd=A16, R=2, K=2, d=A16, q=None, ldq=100, t=None, u=A16, e=A16,
            lde=100, tok=A16, acc=A16, lp=A16, ws=A16, nws=None):
     if nws is None:

@@ -26,6 +26,7 @@
 // (19 and 18 in the two kernels), 3.4 TB/s of what has to be read, 4.2 of what is (the
 // drawn row twice); 7 requests of seven drafts over 100003 fp32 words 17.6 us, one
 // request of three over 32768 15.8: two launches and the chain from rows to draw.
+#include <float.h>
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -128,6 +129,8 @@ __device__ __forceinline__ float temperature_of(const VerifyArgs& a, int64_t r, 
   *greedy = t == 0.f;
   return t == 0.f ? 1.f : t;
 }
+// log2 e / T, finite: below T = 4e-39 every logit but the largest is out of reach anyway
+__device__ __forceinline__ float scale_of(float t) { return fminf(kLog2e / t, FLT_MAX); }
 // Drafts of a request; -1: nothing to sample.  Its rows have to lie in the logits.
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int64_t r) {
   const int64_t n = min((int64_t)a.num_drafts[r], a.max_drafts), first = a.row_start[r];
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void verify_rows_kernel(VerifyArgs a, Ver
   const int n = drafts_of(a, r);
   if (i > n) return;
   bool greedy;
-  const float k = kLog2e / temperature_of(a, r, &greedy);
+  const float k = scale_of(temperature_of(a, r, &greedy));
   const void* row = logits_row<F32>(a, r, i);
   const int64_t each = slice_length(a.vocab, slices), v0 = min(slice * each, a.vocab), v1 = min(v0 + each, a.vocab);
   float top = -INFINITY, sum = 0.f;
@@ -352,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, Ver
     return;
   }
   bool greedy;
-  const float t = temperature_of(a, r, &greedy), k = kLog2e / t;
+  const float t = temperature_of(a, r, &greedy), k = scale_of(t);
   if (greedy && slice > 0) return;   // the argument of the maximum is known
   const int kept = accept<F32>(a, ws, r, n, slices, k, greedy, rows);
   DrawPart d = {-INFINITY, INT32_MAX, 0, 0};

@@ -95,6 +95,17 @@ def test_masked_vocabulary(gpu_lib):
     assert got[0][2, 0] == -1 and got[0][3, 0] == -1 and got[1][2] == 0
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("probs", [False, True])
+def test_extreme_temperatures(gpu_lib, f32, probs):
+    """Down to the smallest positive number the largest logit has all the probability; up to the largest, every word has the same."""
+    temps = [1e-30, 1.2e-38, 4.3e-39, 4e-39, 1e-39, 1e-44, 1e30, 3e38]
+    b = build(8, 2, 777, [2] * 8, f32, probs, temps, seed=21)
+    for r in range(8):
+        b["draft_tokens"][r, 0] = int(b["logits"][b["row_start"][r]].float().argmax())   # kept where all is on the largest
+    check(gpu_lib, b)
+
+
 def test_equal_maxima_and_equal_scores(gpu_lib):
     """Greedy ties and race ties go to the lowest index, also across lanes, waves and slices."""
     V = 40000

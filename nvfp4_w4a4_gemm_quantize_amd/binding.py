@@ -494,7 +494,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
         raise NVFP4Error("k_cache must be a bfloat16 or float8_e4m3fn tensor")
     if not isinstance(v_cache, _Tensor) or not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype is not kind:
         raise NVFP4Error("k_cache and v_cache must be GPU tensors of one type")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() \
+            or not k_cache.numel():
         raise NVFP4Error("k_cache and v_cache must be [pages, heads, page size, head dim] views of one shape and strides")
     pages, heads, page_size, dim = k_cache.shape
     ps, hs, ts, unit = k_cache.stride()

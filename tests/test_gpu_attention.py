@@ -425,3 +425,13 @@ def test_refusals(gpu_lib):
                 dict(out=torch.empty(2, 128, dtype=torch.bfloat16, device="cuda"))):
         with pytest.raises(E):
             call(gpu_lib, b, **bad)
+
+
+@pytest.mark.parametrize("shape", [(0, 1, 16, 64), (2, 0, 16, 64), (2, 1, 0, 64), (2, 1, 16, 0)])
+def test_empty_caches_are_refused(gpu_lib, shape):
+    b = build([20], [2], 1, 1, 64, 16)
+    b["k"], b["v"] = (torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    with pytest.raises(gpu_lib.NVFP4Error):
+        call(gpu_lib, b)
+    with pytest.raises(gpu_lib.NVFP4Error):
+        gpu_lib.paged_kv_write(b["q"], b["q"], torch.arange(2, device="cuda"), b["k"], b["v"])

@@ -494,13 +494,13 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
         raise NVFP4Error("k_cache must be a bfloat16 or float8_e4m3fn tensor")
     if not isinstance(v_cache, _Tensor) or not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype is not kind:
         raise NVFP4Error("k_cache and v_cache must be GPU tensors of one type")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() \
-            or not k_cache.numel():
-        raise NVFP4Error("k_cache and v_cache must be [pages, heads, page size, head dim] views of one shape and strides")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or not k_cache.numel():
+        raise NVFP4Error("k_cache and v_cache must be [pages, heads, page size, head dim] views of one shape")
     pages, heads, page_size, dim = k_cache.shape
     ps, hs, ts, unit = k_cache.stride()
-    if unit != 1:
-        raise NVFP4Error("the caches need a unit last stride")
+    vp, vh, vt, vu = v_cache.stride()
+    if unit != 1 or vu != 1 or ts != vt or (ps != vp and pages > 1) or (hs != vh and heads > 1):
+        raise NVFP4Error("k_cache and v_cache need the same strides, the last of them 1")
     ks = None if k_scale is None else _vec(k_scale, _f32, heads, "k_scale")
     vs = None if v_scale is None else _vec(v_scale, _f32, heads, "v_scale")
     return (k_cache.data_ptr(), v_cache.data_ptr(), CACHE_BF16 if kind is _bf16 else CACHE_E4M3, pages, page_size, heads,

@@ -435,3 +435,18 @@ def test_empty_caches_are_refused(gpu_lib, shape):
         call(gpu_lib, b)
     with pytest.raises(gpu_lib.NVFP4Error):
         gpu_lib.paged_kv_write(b["q"], b["q"], torch.arange(2, device="cuda"), b["k"], b["v"])
+
+
+def test_strides_of_single_pages_and_heads_do_not_matter(gpu_lib):
+    """K contiguous, V a view whose page and head strides say something else about the one page and the one head."""
+    b = build([9], [2], 1, 1, 64, 16, extra_pages=0)
+    want, _ = call(gpu_lib, b)
+    assert b["k"].shape[0] == 1
+    b["v"] = b["v"].as_strided(b["v"].shape, (8, 24, 64, 1))
+    got, _ = call(gpu_lib, b)
+    assert torch.equal(got, want)
+    with pytest.raises(gpu_lib.NVFP4Error):
+        call(gpu_lib, {**b, "v": torch.zeros(1, 1, 16, 128, dtype=torch.bfloat16, device="cuda")[..., :64]})   # another token stride
+    two = torch.zeros(2, 1, 32, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gpu_lib.NVFP4Error):
+        call(gpu_lib, {**b, "k": torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device="cuda"), "v": two[:, :, :16]})

@@ -499,6 +499,10 @@ int paged_attention(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32
  * w_v / sum(w).  temperature 0 is greedy: a draft is kept while it is the
  * lowest argument of the row's maximum, which is also the next token.
  *
+ * logits, draft_probs and noise begin 16-byte aligned (NVFP4_EALIGN otherwise); their
+ * rows may begin at any element, so that later rows of a matrix are named by
+ * row_start and not by a pointer into it.
+ *
  *   logits       [rows, vocab] of logits_dtype NVFP4_LOGITS_*, row stride
  *                ld_logits >= vocab; finite or -inf (NaN counts as -inf).
  *   row_start, num_drafts  int32 [num_requests]; num_drafts < 0 (or rows

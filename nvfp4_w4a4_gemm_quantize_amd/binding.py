@@ -642,6 +642,7 @@ def verify_drafts(logits, row_start, num_drafts, draft_tokens, uniform, noise, d
     logits bf16 or fp32 [N, V] view: row row_start[r] + i is the target's after i kept drafts of request r;
     row_start, num_drafts int32 [R]; draft_tokens int32 [R, K]; uniform fp32 [R, K]; noise fp32 [R, V] (standard
     exponential); draft_probs fp32 [R, K, V] or None; temperature fp32 [R] or None (0: greedy).
+    logits, noise and draft_probs begin 16-byte aligned: rows further on go by row_start, not by a slice of logits.
     Returns (tokens int32 [R, K + 1], accepted int32 [R], logprobs fp32 [R, K + 1])."""
     lib = _lib or load()
     kind = logits.dtype if isinstance(logits, _Tensor) else None

@@ -221,3 +221,16 @@ def test_refusals(gpu_lib):
                 dict(logits=z(4, 32).cpu())):
         with pytest.raises(E):
             gpu_lib.verify_drafts(**{**ok, **bad})
+
+
+def test_rows_further_on_go_by_row_start(gpu_lib):
+    """A slice that does not begin 16-byte aligned is refused, and says so; the same rows by their numbers are not."""
+    b = build(2, 2, 301, [2, 1], False, True, None, seed=8)
+    d = on_device(b)
+    want = gpu_lib.verify_drafts(**d)
+    more = torch.zeros(d["logits"].shape[0] + 1, 301, dtype=torch.bfloat16, device="cuda")
+    more[1:] = d["logits"]
+    with pytest.raises(gpu_lib.NVFP4Error, match="align"):
+        gpu_lib.verify_drafts(**{**d, "logits": more[1:]})
+    for g, w in zip(gpu_lib.verify_drafts(**{**d, "logits": more, "row_start": d["row_start"] + 1}), want):
+        assert torch.equal(g, w)

@@ -60,14 +60,9 @@ class Model:
         self.head = Linear(vocab, hidden, gen, self.embed * hidden ** -0.5)
         self.table = torch.full((requests, max_seq // page), -1, dtype=torch.int32, device="cuda")
         self.free = list(range(pages))
-        self.workspaces = {}
-
-    def workspace(self, kind, make, *sizes):
-        """One workspace for each set of sizes, kept from step to step."""
-        key = (kind,) + sizes
-        if key not in self.workspaces:
-            self.workspaces[key] = make(*sizes)
-        return self.workspaces[key]
+        # One workspace serves every step that is no larger.  An attention step's depends on its requests, and on whether
+        # one of them may bring more than 32 rows a KV head, as a prompt does.
+        self.attention_ws = B.paged_attention_workspace(requests * max_seq, requests, hq, hkv, dim, max_seq, max_seq)
 
     def step(self, tokens, ctx, new, trace=None, rows=None):
         """Logits of the step's tokens (all requests' new ones end to end), and its plan.  `rows` above the number of
@@ -80,13 +75,12 @@ class Model:
         x = self.embed.new_zeros(T, self.embed.shape[1])
         x[:len(tokens)] = self.embed[torch.tensor(tokens, device="cuda")]
         nq, nk = self.hq * self.dim, self.hkv * self.dim
-        ws = self.workspace("attention", B.paged_attention_workspace, T, R, self.hq, self.hkv, self.dim, max(new), self.max_seq)
         for b in self.blocks:
             y = b["qkv"](norm(x))
             q, k, v = y[:, :nq], y[:, nq:nq + nk], y[:, nq + nk:]    # views: no copies
             B.paged_kv_write(k, v, plan.slots, b["k"], b["v"], b["k_scale"], b["v_scale"])
             a = B.paged_attention(q, b["k"], b["v"], self.table, plan.q_start, plan.seq_lens, max(new), self.max_seq,
-                                  k_scale=b["k_scale"], v_scale=b["v_scale"], workspace=ws)
+                                  k_scale=b["k_scale"], v_scale=b["v_scale"], workspace=self.attention_ws)
             if trace is not None:
                 trace.append((q, k, v, a))
             x = x + b["o"](a)
@@ -116,6 +110,7 @@ def generate(model, prompts, steps, drafts, temperature=0.0, seed=0, log=None):
     R, V = len(prompts), model.vocab
     texts, ctx, guesses = [list(p) for p in prompts], [0] * R, [[] for _ in prompts]
     temps = torch.full((R,), temperature, device="cuda")
+    verify_ws = B.verify_drafts_workspace(R, drafts, V)
     for s in range(steps + 1):
         new = [len(t) - c + len(g) for t, c, g in zip(texts, ctx, guesses)]
         logits, plan = model.step([x for t, c, g in zip(texts, ctx, guesses) for x in t[c:] + g], ctx, new)
@@ -126,8 +121,7 @@ def generate(model, prompts, steps, drafts, temperature=0.0, seed=0, log=None):
         noise = torch.empty(R, V, device="cuda").exponential_(generator=gen)
         out, kept, _ = B.verify_drafts(logits, plan.q_start[:R] + first,
                                        torch.tensor([len(g) for g in guesses], dtype=torch.int32, device="cuda"), padded, u, noise,
-                                       temperature=temps,
-                                       workspace=model.workspace("verify", B.verify_drafts_workspace, R, drafts, V))
+                                       temperature=temps, workspace=verify_ws)
         assert int(plan.counts[2]) == 0, "out of pages"
         kept = kept.tolist()
         if log is not None:

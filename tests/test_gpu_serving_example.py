@@ -93,3 +93,15 @@ def test_generation_keeps_its_books(serving, temperature):
         assert sorted(held + m.free) == list(range(64))
         runs.append((texts, log))
     assert runs[0] == runs[1]
+
+
+def test_varied_steps_need_no_more_memory(serving):
+    """Workspaces are the model's, whatever the sizes of its steps."""
+    m, ctx, held = small(serving), [0, 0, 0], []
+    for new in ([5, 1, 9], [40, 1, 1], [1, 1, 1], [2, 9, 17], [3, 0, 33]):
+        m.step([1] * sum(new), ctx, new)
+        m.take_pages(ctx, new, new)
+        ctx = [c + n for c, n in zip(ctx, new)]
+        torch.cuda.synchronize()
+        held.append(torch.cuda.memory_allocated())
+    assert held == held[:1] * len(held), held

@@ -227,6 +227,24 @@ def test_kv_write_rounds_every_step_to_nearest_even(gpu_lib):
     assert torch.equal(cache[0], cache[1])
 
 
+def test_kv_write_infinities_and_nan(gpu_lib):
+    """In E4M3 a NaN stays one, an infinity saturates (there is none), also where a scale of 0 or infinity makes them."""
+    x = torch.tensor([float("nan"), float("-nan"), float("inf"), float("-inf"), 0.0, -0.0, 1.0, -3e38], dtype=torch.bfloat16)
+    bits = x.view(torch.int16).clone()
+    bits[1] = -1                                   # every bit set
+    x = bits.view(torch.bfloat16).repeat(1, 32)    # one row of four heads of 64
+    scales = torch.tensor([1.0, 0.0, float("inf"), -0.5], device="cuda")
+    cache = torch.zeros(2, 1, 4, 16, 64, dtype=torch.uint8, device="cuda")
+    gpu_lib.paged_kv_write(x.cuda(), x.cuda(), torch.zeros(1, dtype=torch.int64, device="cuda"), cache[0].view(FP8), cache[1].view(FP8),
+                           k_scale=scales, v_scale=scales)
+    want = (x.float().view(4, 64) / scales.cpu()[:, None]).numpy()
+    got = cache[0, 0, :, 0].cpu().view(FP8).float().numpy()
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    keep = ~np.isnan(want)
+    np.testing.assert_array_equal(cache[0, 0, :, 0].cpu().numpy()[keep], to_e4m3(np.clip(want[keep].astype(np.float64), -448, 448)))
+    assert torch.equal(cache[0], cache[1])
+
+
 def test_kv_write_far_pages(gpu_lib):
     """A cache of more than 2^32 bytes: the last page's offset passes 32 bits."""
     pages, heads, page, dim = 70000, 2, 128, 128

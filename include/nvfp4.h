@@ -449,7 +449,8 @@ int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t l
  * a row that sees none gets 0 and lse = -inf.  Nothing is read of what the
  * cache holds outside the keys of a request (it may be NaN), and an infinity or
  * NaN among its values reaches the rows that see it and no others.  Statistics
- * and sums are fp32; the weights are rounded to bf16 for the product with V.
+ * and sums are fp32; the weights are rounded to bf16, once, for the product with
+ * V, whatever the type of out.
  *
  *   q            bf16 [tokens, num_heads * head_dim], row stride ld_q (multiple
  *                of 8), 16-byte aligned.

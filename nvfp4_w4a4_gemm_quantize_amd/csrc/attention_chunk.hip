@@ -17,12 +17,15 @@
 // Bound by the matrix unit and the power it may draw: a long prompt holds 1.8 -
 // 2.05 GHz, and the MFMAs take 60% of the cycles; the rest is the softmax, whose
 // exponentials share the issue slots.  8192 tokens after 8192, 40 heads of 128 over
-// 8: 1750 - 1840 us on different cards, 1.12 - 1.18 PFLOP/s (a large bf16 product
-// reaches 1.61), E4M3 1960; heads of 64 (64 over 16) 1835 us, 900 TFLOP/s, E4M3 1850:
-// half the product for each exponential; 4096 after 4096, 24 heads of 256 over 4: 615
-// us, 1006 TFLOP/s, E4M3 845.  8 windowed chunks of up to 777, heads of 64, take 81 us:
-// 1.4 us a tile of keys, shares between 57 and 80 us long, and a part's 8 us beside
-// its keys (its queries, page numbers and first keys; its output).
+// 8: 1720 - 1830 us on different cards, 1.13 - 1.20 PFLOP/s (a large bf16 product
+// reaches 1.61); heads of 64 (64 over 16) 1770 - 1840 us, 900 - 930 TFLOP/s: half the
+// product for each exponential; 4096 after 4096, 24 heads of 256 over 4: 595 - 620 us,
+// 1.0 PFLOP/s.  Over E4M3, on a card where these took 1765, 1797 and 605: 1885, 1807
+// and 669; a third of the LDS' cycles go into the converted tiles' stores, whose bank
+// conflicts take a sixth of all, and the matrix unit is busy for 48% of the cycles in
+// place of 60% (heads of 256: 39%, 49%).  8 windowed chunks of up to 777, heads of 64,
+// take 82 us, over E4M3 85: 1.4 us a tile of keys, shares between 57 and 80 us long, and
+// a part's 8 us beside its keys (its queries, page numbers and first keys; its output).
 #include <float.h>
 #include <math.h>
 
@@ -161,7 +164,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   // turns, one multiplies while the other computes weights (a prompt of 8192 over 8192
   // keys, 40 heads of 128: 1840 us; mixed 1930 - 2080).  Heads of 256, whose O leaves a
   // wave no registers for operands of two products at once: every wave weighs between
-  // the matrix instructions (4096 over 4096, 24 heads: 615 us, E4M3 845; turns 1336 and
+  // the matrix instructions (4096 over 4096, 24 heads: 605 us, E4M3 669; turns 1336 and
   // 1585, with 65 registers spilled).
   constexpr bool MIXED = D == 256;
   __shared__ __attribute__((aligned(1024))) uint8_t lds_k[kSlots][KT * ROW], lds_v[kSlots][KT * ROW];

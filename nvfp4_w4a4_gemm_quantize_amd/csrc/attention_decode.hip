@@ -33,12 +33,15 @@
 // cost 4 us of the GPU's time and as much of the host's, a third of one decoded
 // token).  The line's prefix is recomputed by every workgroup (8 bytes a request).
 //
-// Measured: 64 requests of up to 16384 keys, 40 heads of 128 over 8: 386 us, 5.7 TB/s
+// Measured: 64 requests of up to 16384 keys, 40 heads of 128 over 8: 388 us, 5.7 TB/s
 // of the keys and values (a large copy moves 5.0).  E4M3: 32 requests of 8192 keys with
-// five tokens each, 24 heads of 256 over 4: 130 us, 4.2 TB/s; there the conversion and
-// the transpose share the issue slots with two fragments of rows, and O takes the
-// registers that more loads in flight would need (two tiles ahead spilled: 173 us).
-// One token over 1000 keys: 10 us, latency.
+// five tokens each, 24 heads of 256 over 4: 129 - 138 us among other calls, 133 - 151
+// alone, 3.9 - 4.2 TB/s; there the conversion and the transpose share the issue slots
+// with two fragments of rows, and O takes the registers that more loads in flight would
+// need (two tiles ahead spilled: 173 us).  With ragged lengths, and so fewer bytes, less:
+// 32 requests of up to 8192 keys, 32 rows of 256, 2.8 TB/s over E4M3 and 3.4 over bf16;
+// 64 requests, heads of 128, 20 rows, 3.6 over E4M3 and 5.1; one token, heads of 128,
+// 4.1 and 5.2, heads of 64 3.6 and 5.3.  One token over 1000 keys: 10 us, latency.
 #include <float.h>
 
 #include "attention.h"

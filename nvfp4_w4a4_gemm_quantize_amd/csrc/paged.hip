@@ -20,8 +20,8 @@ namespace nvfp4 {
 //
 // One launch, bound by latency: every workgroup repeats the scan (8 bytes a
 // request, from L2), which costs less than a second launch to share it (a launch takes
-// the host 3.6 us; 8 requests of one token 3.2 us on the GPU, 1024 requests with 5000
-// tokens 6.2); then
+// the host 3.6 us; 8 requests of one token 3.1 us on the GPU, 1024 requests with 5000
+// tokens 6.1); then
 // tokens, pages and requests are dealt out over the whole grid.  A thread owns
 // a run of ceil(R / 256) requests in the scan; a token finds its run by binary
 // search in LDS and its request by walking the run.

@@ -18,14 +18,17 @@
 // thread takes 32 logits at a time: their loads are in flight together, and the
 // running maximum and sum are touched once for all of them.  Exponentials are
 // 2^((x - top) k), k = log2 e / T (not x k - top k: logits may be the type's
-// lowest value, whose product overflows); scores use the hardware reciprocal of
-// the noise (1 ulp): a word is only misjudged against one whose score is the
-// same to 2^-22.
+// lowest value, whose product overflows).  A score's relative error is p's, about
+// 2^-22 + 2^-23 |x - top| k (the exponential, and three roundings of its argument), times
+// p / w where a draft's probability is taken off, and the 2^-23 of the noise's hardware
+// reciprocal: words are misjudged only against others whose scores lie that close.
 //
-// Measured: 64 requests of four drafts with their probabilities over 131072 words: 39 us
-// (19 and 18 in the two kernels), 3.4 TB/s of what has to be read, 4.2 of what is (the
-// drawn row twice); 7 requests of seven drafts over 100003 fp32 words 17.6 us, one
-// request of three over 32768 15.8: two launches and the chain from rows to draw.
+// Measured: 64 requests of four drafts with their probabilities over 131072 words: 39 us.
+// The rows take 19 of them, 3.4 TB/s: a workgroup has one batch of loads, then reduces
+// with none in flight (waves wait for 52% of their cycles); the draw takes 18, 4.6 TB/s
+// of what it reads (73 of its 84 MB from HBM: part of the drawn row is still in a cache);
+// 7 requests of seven drafts over 100003 fp32 words 17.6 us, one request of three over
+// 32768 15.1: two launches and the chain from rows to draw.
 #include <float.h>
 #include <hip/hip_runtime.h>
 

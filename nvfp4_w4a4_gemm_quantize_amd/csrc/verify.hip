@@ -133,7 +133,10 @@ __device__ __forceinline__ float temperature_of(const VerifyArgs& a, int64_t r, 
   return t == 0.f ? 1.f : t;
 }
 // log2 e / T, finite: below T = 4e-39 every logit but the largest is out of reach anyway
-__device__ __forceinline__ float scale_of(float t) { return fminf(kLog2e / t, FLT_MAX); }
+__device__ __forceinline__ float scale_of(float t) {
+  const float k = kLog2e / t;
+  return k > FLT_MAX ? FLT_MAX : k;   // a NaN stays one: nothing is sampled
+}
 // Drafts of a request; -1: nothing to sample.  Its rows have to lie in the logits.
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int64_t r) {
   const int64_t n = min((int64_t)a.num_drafts[r], a.max_drafts), first = a.row_start[r];

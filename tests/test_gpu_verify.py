@@ -106,6 +106,13 @@ def test_extreme_temperatures(gpu_lib, f32, probs):
     check(gpu_lib, b)
 
 
+def test_a_nan_temperature_samples_nothing(gpu_lib):
+    b = build(2, 1, 300, [1, 1], True, True, [float("nan"), 1.0], seed=22)
+    tokens, kept, logprobs = run(gpu_lib, b)
+    assert tokens[0].tolist() == [-1, -1] and kept[0] == 0 and logprobs[0].tolist() == [0, 0]
+    assert tokens[1, 0] >= 0
+
+
 def test_equal_maxima_and_equal_scores(gpu_lib):
     """Greedy ties and race ties go to the lowest index, also across lanes, waves and slices."""
     V = 40000

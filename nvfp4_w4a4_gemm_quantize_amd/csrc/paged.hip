@@ -31,7 +31,9 @@ namespace nvfp4 {
 // the cursor lies in counts) writes these two last where it has one workgroup (8
 // requests of one token, replayed in a graph: 2.8 us, with separate tensors 2.7);
 // otherwise a second launch of one workgroup does (1024 requests with 5000 tokens 7.8
-// us, 3.8).
+// us, 3.8).  Inputs that share memory with outputs in any other way give wrong plans, but
+// every walk ends with the requests and every column is checked, so nothing is read or
+// written out of range.
 constexpr int kPlanThreads = 256;
 
 namespace {
@@ -113,11 +115,11 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     const int w = plan_run(pg, p);
     int64_t r = w * run, base = pg[w];
     PlanLens l = plan_lens(a, r);
-    while (p >= base + l.need) {   // ends: p < pg[w + 1]
+    while (p >= base + l.need && r + 1 < a.requests) {   // p < pg[w + 1]
       base += l.need;
       l = plan_lens(a, ++r);
     }
-    a.block_table[r * a.ld_table + l.before + (p - base)] = p < left ? a.free_pages[cursor + p] : -1;
+    if (p - base < l.need) a.block_table[r * a.ld_table + l.before + (p - base)] = p < left ? a.free_pages[cursor + p] : -1;
   }
   // per token; the tail of the buffers is padding
   for (int64_t t = first; PART != kPlanCarry && t < a.max_tokens; t += stride) {
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
       const int w = plan_run(tok, t);
       int64_t r = w * run, base = tok[w], pbase = pg[w];
       PlanLens l = plan_lens(a, r);
-      while (t >= base + l.tokens) {   // ends: t < tok[w + 1]
+      while (t >= base + l.tokens && r + 1 < a.requests) {   // t < tok[w + 1]
         base += l.tokens;
         pbase += l.need;
         l = plan_lens(a, ++r);

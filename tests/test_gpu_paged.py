@@ -145,6 +145,31 @@ def test_plan_refuses_other_inputs_inside_its_outputs(gpu_lib):
     assert plan.seq_lens.tolist() == [2, 4, 6] and plan.q_start.tolist() == [0, 1, 3, 6]
 
 
+def test_plan_stays_in_range_whatever_shares_memory(gpu_lib):
+    """The C entry takes the caller's word that nothing else overlaps.  Where it does, the plan is wrong and its accesses
+    are not: the guards around every output stay."""
+    R, T, cols, rng = 700, 900, 6, np.random.default_rng(1)
+    lib, guard = gpu_lib.load(), 64
+    lens = torch.full((R + 9 + 2 * guard,), -77, dtype=torch.int32, device="cuda")
+    lens[guard:-guard] = i32(rng.integers(0, 90, R + 9))
+    wide = torch.full((R + 2, cols + 8), -77, dtype=torch.int32, device="cuda")
+    free, new = i32(np.arange(R * 4)), i32(rng.integers(0, 3, R))
+    out = torch.full((R + 1 + T + 4 + 4 * guard,), -77, dtype=torch.int32, device="cuda")
+    slots = torch.full((T + 2 * guard,), -77, dtype=torch.int64, device="cuda")
+    q0, p0, c0 = guard, 2 * guard + R + 1, 3 * guard + R + 1 + T
+    at = lambda x, i: x.data_ptr() + x.element_size() * i  # noqa: E731
+    rc = lib.paged_plan(at(lens, guard), new.data_ptr(), R, 16, free.data_ptr(), R * 4, None, at(wide, cols + 8), cols, cols + 8, at(out, q0),
+                        at(lens, guard + 9), at(out, p0), at(slots, guard), T, at(out, c0), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    for begin, n in ((q0, R + 1), (p0, T), (c0, 4)):
+        keep[begin:begin + n] = False
+    assert out[keep].eq(-77).all() and slots[:guard].eq(-77).all() and slots[-guard:].eq(-77).all()
+    assert lens[:guard].eq(-77).all() and lens[-guard:].eq(-77).all()
+    assert wide[0].eq(-77).all() and wide[-1].eq(-77).all() and wide[:, cols:].eq(-77).all()
+
+
 # --------------------------------------------------------------- K/V write --
 
 FP8 = torch.float8_e4m3fn

@@ -17,7 +17,7 @@
 // Bound by the matrix unit and the power it may draw: a long prompt holds 1.8 -
 // 2.05 GHz, and the MFMAs take 60% of the cycles; the rest is the softmax, whose
 // exponentials share the issue slots.  8192 tokens after 8192, 40 heads of 128 over
-// 8: 1720 - 1830 us on different cards, 1.13 - 1.20 PFLOP/s (a large bf16 product
+// 8: 1690 - 1830 us on different cards, 1.13 - 1.22 PFLOP/s (a large bf16 product
 // reaches 1.61); heads of 64 (64 over 16) 1770 - 1840 us, 900 - 930 TFLOP/s: half the
 // product for each exponential; 4096 after 4096, 24 heads of 256 over 4: 595 - 620 us,
 // 1.0 PFLOP/s.  Over E4M3, on a card where these took 1765, 1797 and 605: 1885, 1807

@@ -535,6 +535,117 @@ int verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64
                   int32_t* num_accepted, float* logprobs, void* workspace, size_t workspace_bytes,
                   nvfp4_stream_t stream);
 
+/*
+ * The attention layer in 8 bits, for the half of the hybrid model that the pages
+ * call the sensitive one: rotary positions (rotary_steps, rotary), the cache write
+ * with the rotation on the way (paged_kv_append), and attention over caches that
+ * hold a scale for each 16 tokens and head (paged_attention_blocks).
+ *
+ * Block-scaled caches.  The codes lie as in any cache of 8-bit elements; beside them
+ * k_blocks and v_blocks hold one E8M0 byte for each block of 16 tokens (a slot's
+ * block is slot / 16) of each head, [num_pages, num_kv_heads, page_size / 16]
+ * contiguous.  A code stands for code * 2^(byte - 127): an E4M3 value, or a whole
+ * number from -127 to 127.  Bytes run from 1 to 246 (E4M3) or 248 (INT8); others are
+ * read as the nearest of these.  Powers of two cost an E4M3 code none of its digits
+ * and INT8 at most one of its seven bits, and are exact wherever they are applied.
+ */
+#define NVFP4_CACHE_E4M3_BLOCKS 2
+#define NVFP4_CACHE_INT8_BLOCKS 3
+
+/* Pairs of a rotated head of which the first rotary_dim columns turn. */
+#define NVFP4_ROTARY_HALF 0        /* (i, i + rotary_dim / 2) */
+#define NVFP4_ROTARY_INTERLEAVED 1 /* (2 i, 2 i + 1) */
+
+/* How frequencies are scaled for contexts longer than the model's own. */
+#define NVFP4_ROPE_NONE 0
+#define NVFP4_ROPE_LINEAR 1     /* w / factor */
+#define NVFP4_ROPE_NTK 2        /* base * factor^(d / (d - 2)) in place of base */
+#define NVFP4_ROPE_YARN 3       /* w / factor r + w (1 - r), r rising over the pairs */
+#define NVFP4_ROPE_WAVELENGTH 4 /* w k + w / factor (1 - k), k rising with the turns */
+
+/*
+ * rotary_steps -- the table of a rotation, made on the HOST once a model: steps[i] is
+ * what pair i turns by at each position, in 2^-64ths of a turn, so that the kernels
+ * find position * steps[i] modulo a turn in whole numbers, exactly at any position.
+ * With d = rotary_dim, w_i = base^(-2 i / d) radians and L = original_length:
+ *     YARN: r_i = clamp((i - a) / max(b - a, 0.001), 0, 1) with a = max(floor(p(fast_turns)), 0),
+ *     b = min(ceil(p(slow_turns)), d - 1), p(t) = d ln(L / (2 pi t)) / (2 ln base);
+ *     its amplitude is 0.1 ln(factor) + 1, that of the others 1.
+ *     WAVELENGTH: k_i = clamp((L w_i / 2 pi - slow_turns) / (fast_turns - slow_turns), 0, 1).
+ *
+ *   rotary_dim    a multiple of 16 up to 1024 (others NVFP4_EUNSUPPORTED).
+ *   base          > 1; factor >= 1 (not read for NONE); original_length > 0,
+ *                 0 < slow_turns < fast_turns (YARN and WAVELENGTH alone read them).
+ *   pair_factors  host, optional [d / 2], positive: w_i is divided by them at last.
+ *   steps, amplitude   host, out: [d / 2] and [1].
+ */
+int rotary_steps(int rotary_dim, double base, int scaling, double factor, double original_length, double slow_turns,
+                 double fast_turns, const double* pair_factors, uint64_t* steps, float* amplitude);
+
+/*
+ * rotary -- rows of heads, rotated: with t = 2 pi steps[i] positions[row] / 2^64,
+ * pair (a, b) of every head becomes amplitude * (a cos t - b sin t, b cos t + a sin t),
+ * in fp32, rounded once.  Columns from rotary_dim on, and rows of a negative position
+ * (padding), are copied as they are.
+ *
+ *   x         bf16 [tokens, num_heads * head_dim], row stride ld_x (multiple of
+ *             8), 16-byte aligned; q and k side by side in a projection's output
+ *             are one such matrix.
+ *   head_dim  a multiple of 16 up to 1024.
+ *   positions int32 [tokens], as from paged_plan.
+ *   steps     device uint64 [rotary_dim / 2], from rotary_steps; layout NVFP4_ROTARY_*.
+ *   out       as x, row stride ld_out; may be x itself (ld_out == ld_x), must not
+ *             overlap it otherwise.
+ * tokens == 0 enqueues nothing.
+ */
+int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int head_dim, const int32_t* positions,
+           const uint64_t* steps, int rotary_dim, int layout, float amplitude, uint16_t* out, int64_t ld_out,
+           nvfp4_stream_t stream);
+
+/*
+ * paged_kv_append -- paged_kv_write with the rotation on the way: k is rotated in fp32
+ * and rounded to the cache's type alone, v goes in as it is, and q, if there is one, is
+ * rotated into q_out as rotary does it.
+ *
+ *   q, q_out     bf16 [tokens, num_heads * head_dim], as x and out of rotary; null
+ *                with num_heads 0.
+ *   k, v, slots, tokens, the caches   as in paged_kv_write.
+ *   positions, steps, rotary_dim, layout, amplitude   as in rotary; rotary_dim 0 (and
+ *                steps null) rotates nothing.
+ *   cache_dtype  any NVFP4_CACHE_*; k_scale, v_scale for E4M3 (null = 1), k_blocks,
+ *                v_blocks for the block-scaled ones, null otherwise.
+ *
+ * Block-scaled caches: rows of the call that follow each other in neighbouring slots of
+ * one block are a run, and a block must get at most one run from a call (as paged_plan
+ * lays tokens out).  A run's scale byte is the smallest one whose codes reach its largest
+ * finite value, or the block's old byte where that is larger.  A run that holds the block's
+ * first token begins the block: the old byte does not count, and the codes of places
+ * that the run does not fill become 0.  Any other run leaves them, rescaled (rounded to
+ * nearest even) where the byte rises.  E4M3: values beyond 448 steps (infinities) become
+ * 448 of them, NaN stays.  INT8: beyond 127 likewise, NaN becomes 0.
+ */
+int paged_kv_append(const uint16_t* q, int64_t ld_q, int num_heads, uint16_t* q_out, int64_t ld_q_out, const uint16_t* k,
+                    int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* positions, const int64_t* slots,
+                    int64_t tokens, const uint64_t* steps, int rotary_dim, int layout, float amplitude, void* k_cache,
+                    void* v_cache, int cache_dtype, int64_t num_pages, int page_size, int num_kv_heads, int head_dim,
+                    int64_t page_stride, int64_t head_stride, int64_t token_stride, const float* k_scale,
+                    const float* v_scale, uint8_t* k_blocks, uint8_t* v_blocks, nvfp4_stream_t stream);
+
+/*
+ * paged_attention_blocks -- paged_attention over a block-scaled cache: every argument is
+ * that call's (the workspace too, paged_attention_workspace_bytes), but for k_blocks and
+ * v_blocks in place of k_scale and v_scale, and cache_dtype NVFP4_CACHE_E4M3_BLOCKS or
+ * NVFP4_CACHE_INT8_BLOCKS.  Elements become bf16 with their scale, exactly, on their way
+ * into the matrix unit.
+ */
+int paged_attention_blocks(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32_t* q_start, const int32_t* seq_lens,
+                           int64_t num_requests, int64_t max_new, int64_t max_seq, int num_heads, const void* k_cache,
+                           const void* v_cache, int cache_dtype, int64_t num_pages, int page_size, int num_kv_heads,
+                           int head_dim, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                           const uint8_t* k_blocks, const uint8_t* v_blocks, const int32_t* block_table, int64_t max_pages,
+                           int64_t ld_table, float scale, int64_t window, void* out, int out_dtype, int64_t ld_out, float* lse,
+                           void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* nvfp4_status_string(int status);
 

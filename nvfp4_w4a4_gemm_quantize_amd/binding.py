@@ -59,6 +59,15 @@ _SIGNATURES = {
     "verify_drafts_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "verify_drafts": (_int, [_c_p, _int, _i64, _i64, _i64, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i64, _c_p, _c_p, _c_p,
                              _i64, _c_p, _c_p, _c_p, _c_p, ctypes.c_size_t, _c_p]),
+    "rotary_steps": (_int, [_int, ctypes.c_double, _int, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                            _c_p, _c_p, _c_p]),
+    "rotary": (_int, [_c_p, _i64, _i64, _int, _int, _c_p, _c_p, _int, _int, ctypes.c_float, _c_p, _i64, _c_p]),
+    "paged_kv_append": (_int, [_c_p, _i64, _int, _c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _c_p, _i64, _c_p, _int, _int,
+                               ctypes.c_float, _c_p, _c_p, _int, _i64, _int, _int, _int, _i64, _i64, _i64, _c_p, _c_p, _c_p,
+                               _c_p, _c_p]),
+    "paged_attention_blocks": (_int, [_c_p, _i64, _i64, _c_p, _c_p, _i64, _i64, _i64, _int, _c_p, _c_p, _int, _i64, _int, _int,
+                                      _int, _i64, _i64, _i64, _c_p, _c_p, _c_p, _i64, _i64, ctypes.c_float, _i64, _c_p, _int,
+                                      _i64, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "nvfp4_status_string": (ctypes.c_char_p, [_int]),
     "nvfp4_last_hip_error": (_int, []),
 }
@@ -676,3 +685,199 @@ def verify_drafts(logits, row_start, num_drafts, draft_tokens, uniform, noise, d
     if rc:
         _check(rc, "verify_drafts")
     return tokens, accepted, logprobs
+
+
+# ------------------------------------------- the attention layer in 8 bits ----
+
+CACHE_E4M3_BLOCKS, CACHE_INT8_BLOCKS = 2, 3
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+_LAYOUTS = {"half": ROTARY_HALF, "interleaved": ROTARY_INTERLEAVED}
+_ROPE = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+_e8m0, _int8 = torch.float8_e8m0fnu, torch.int8
+
+RotaryTable = collections.namedtuple("RotaryTable", "steps rotary_dim layout amplitude")
+
+
+def rotary_table(rotary_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_length=8192, slow_turns=1.0,
+                 fast_turns=None, pair_factors=None, amplitude=None, device="cuda"):
+    """A rotation of heads' first rotary_dim columns, for rotary and paged_kv_append; made once a model.
+
+    layout: "half" turns columns (i, i + rotary_dim / 2), "interleaved" (2 i, 2 i + 1).  scaling for long contexts:
+    "none", "linear", "ntk", "yarn" (pairs that make fewer than slow_turns turns over original_length are stretched by
+    factor, those that make more than fast_turns, 32, are not; amplitude 0.1 ln factor + 1), "wavelength" (likewise by
+    wavelength, fast_turns 4).  pair_factors (rotary_dim / 2 numbers) divide the frequencies one by one; amplitude
+    replaces the scaling's."""
+    if layout not in _LAYOUTS or scaling not in _ROPE:
+        raise NVFP4Error("layout is one of %s, scaling one of %s" % (", ".join(_LAYOUTS), ", ".join(_ROPE)))
+    n = max(int(rotary_dim), 0) // 2
+    steps, amp = (ctypes.c_uint64 * max(n, 1))(), ctypes.c_float()
+    factors = None
+    if pair_factors is not None:
+        factors = [float(x) for x in pair_factors]
+        if len(factors) != n:
+            raise NVFP4Error("pair_factors must hold %d numbers" % n)
+        factors = (ctypes.c_double * max(n, 1))(*factors)
+    if fast_turns is None:
+        fast_turns = 32.0 if scaling == "yarn" else 4.0
+    rc = load().rotary_steps(rotary_dim, base, _ROPE[scaling], factor, original_length, slow_turns, fast_turns, factors, steps,
+                             ctypes.byref(amp))
+    if rc:
+        _check(rc, "rotary_steps")
+    host = torch.tensor([x - (1 << 64) if x >> 63 else x for x in steps], dtype=_i64t)   # the 64 bits, as torch has them
+    return RotaryTable(host.to(device), rotary_dim, layout, amp.value if amplitude is None else float(amplitude))
+
+
+def _rotation(table, positions, tokens):
+    """The C arguments (positions, steps, rotary dim, layout, amplitude)."""
+    if table is None:
+        return None, None, 0, ROTARY_HALF, 1.0
+    if not isinstance(table, RotaryTable) or table.layout not in _LAYOUTS:
+        raise NVFP4Error("the rotation must come from rotary_table")
+    return (_vec(positions, _i32, tokens, "positions"), _vec(table.steps, _i64t, table.rotary_dim // 2, "steps"), table.rotary_dim,
+            _LAYOUTS[table.layout], table.amplitude)
+
+
+def _one_device(*tensors):
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise NVFP4Error("the tensors of a call must be on one GPU")
+
+
+def rotary(x, positions, table, head_dim, out=None):
+    """Rows of heads (bf16 view [T, heads * head_dim]) rotated to their positions (int32 [T]; negative: copied).
+
+    table: from rotary_table.  out may be x (in place).  Returns out."""
+    lib = _lib or load()
+    xp, ld_x, cols = _rows(x, _bf16, None, None, "x")
+    T = x.shape[0]
+    if head_dim <= 0 or cols == 0 or cols % head_dim:
+        raise NVFP4Error("x must be [T, heads * %d]" % head_dim)
+    if table is None:
+        raise NVFP4Error("the rotation must come from rotary_table")
+    pos, steps, dim, layout, amplitude = _rotation(table, positions, T)
+    if out is None:
+        out = x.new_empty((T, cols))
+    op, ld_o, _ = _rows(out, _bf16, T, cols, "out")
+    _one_device(x, positions, table.steps, out)
+    _apart(x, out, same=True)
+    rc = lib.rotary(xp, ld_x, T, cols // head_dim, head_dim, pos, steps, dim, layout, amplitude, op, ld_o,
+                    _raw_stream(x.get_device()))
+    if rc:
+        _check(rc, "rotary")
+    return out
+
+
+def _apart(x, out, same=False):
+    """Refuse an output that shares memory with an input (same: but for the input's own rows)."""
+    a, b = x.data_ptr(), out.data_ptr()
+    T, cols = x.shape
+    if not T or (same and a == b):
+        return
+    lx, lo = x.stride(0), out.stride(0)
+    if a < b + 2 * ((T - 1) * lo + out.shape[1]) and b < a + 2 * ((T - 1) * lx + cols):
+        # column slices of one matrix interleave without sharing an element
+        at = (a - b) // 2 % lo if lx == lo and lo > 0 else 0
+        if at < out.shape[1] or at + cols > lo:
+            raise NVFP4Error("an output overlaps an input")
+
+
+def _block_cache(k_cache, v_cache, k_scales, v_scales):
+    """_cache for block-scaled caches: the C arguments, the scales' addresses and (heads, head dim)."""
+    kind = k_cache.dtype if isinstance(k_cache, _Tensor) else None
+    if kind is not _e4m3 and kind is not _int8:
+        raise NVFP4Error("a block-scaled k_cache must be a float8_e4m3fn or int8 tensor")
+    if not isinstance(v_cache, _Tensor) or v_cache.dtype is not kind:
+        raise NVFP4Error("k_cache and v_cache must be GPU tensors of one type")
+    if kind is _int8:                           # the same bytes, as a type that _cache knows
+        args, _, _, heads, dim = _cache(k_cache.view(_e4m3), v_cache.view(_e4m3), None, None)
+    else:
+        args, _, _, heads, dim = _cache(k_cache, v_cache, None, None)
+    pages, page_size = args[3], args[4]
+    for name, t in (("k_scale", k_scales), ("v_scale", v_scales)):
+        if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _e8m0 or t.shape != (pages, heads, page_size // 16) \
+                or not t.is_contiguous():
+            _refuse(t, _e8m0, name, "[%d, %d, %d] contiguous" % (pages, heads, page_size // 16))
+    kind = CACHE_E4M3_BLOCKS if kind is _e4m3 else CACHE_INT8_BLOCKS
+    return args[:2] + (kind,) + args[3:], k_scales.data_ptr(), v_scales.data_ptr(), heads, dim
+
+
+def paged_kv_append(k, v, positions, slots, k_cache, v_cache, rotation=None, k_scale=None, v_scale=None, q=None, q_out=None):
+    """Rotate the rows of k (bf16 2-D views [T, heads * head_dim]) and write them and those of v into the caches at slots.
+
+    positions int32 [T], slots int64 [T] as from paged_plan (slots -1: skip); rotation: from rotary_table (None: none).
+    Caches as in paged_kv_write, with its float scales a head, or block-scaled: float8_e4m3fn or int8 caches with k_scale,
+    v_scale float8_e8m0fnu [pages, heads, page size / 16], which follow the values (a block's first token begins it anew;
+    a block's rows of one call are neighbours, as paged_plan lays them).  q (bf16 view [T, num_heads * head_dim]) is
+    rotated into q_out (allocated if None; may be q).  Returns q_out, or None without q."""
+    lib = _lib or load()
+    if isinstance(k_scale, _Tensor) and k_scale.dtype is _e8m0 or isinstance(k_cache, _Tensor) and k_cache.dtype is _int8:
+        cache, kb, vb, heads, dim = _block_cache(k_cache, v_cache, k_scale, v_scale)
+        ks = vs = None
+    else:
+        cache, ks, vs, heads, dim = _cache(k_cache, v_cache, k_scale, v_scale)
+        kb = vb = None
+    kp, ld_k, _ = _rows(k, _bf16, None, heads * dim, "k")
+    T = k.shape[0]
+    vp, ld_v, _ = _rows(v, _bf16, T, heads * dim, "v")
+    pos, steps, rdim, layout, amplitude = _rotation(rotation, positions, T)
+    qp = op = None
+    ld_q = ld_o = num_heads = 0
+    if q is not None:
+        qp, ld_q, cols = _rows(q, _bf16, T, None, "q")
+        if cols == 0 or cols % dim:
+            raise NVFP4Error("q must be [T, num_heads * %d]" % dim)
+        num_heads = cols // dim
+        if q_out is None:
+            q_out = q.new_empty((T, cols))
+        op, ld_o, _ = _rows(q_out, _bf16, T, cols, "q_out")
+        _apart(q, q_out, same=True)
+        _apart(k, q_out)
+        _apart(v, q_out)
+    elif q_out is not None:
+        raise NVFP4Error("q_out needs q")
+    _one_device(k, v, slots, k_cache, v_cache, k_scale, v_scale, q, q_out, *(() if rotation is None else (positions, rotation.steps)))
+    rc = lib.paged_kv_append(qp, ld_q, num_heads, op, ld_o, kp, ld_k, vp, ld_v, pos, _vec(slots, _i64t, T, "slots"), T, steps,
+                             rdim, layout, amplitude, *cache, ks, vs, kb, vb, _raw_stream(k.get_device()))
+    if rc:
+        _check(rc, "paged_kv_append")
+    return q_out
+
+
+def paged_attention_blocks(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, seq_lens, max_new, max_seq, scale=None,
+                           window=0, out_dtype=torch.bfloat16, out=None, lse=None, return_lse=False, workspace=None,
+                           clear_padding=None):
+    """paged_attention over a block-scaled cache: float8_e4m3fn or int8 caches with scales float8_e8m0fnu
+    [pages, heads, page size / 16], as paged_kv_append leaves them.  Everything else, the workspace too, as there."""
+    lib = _lib or load()
+    cache, kb, vb, heads, dim = _block_cache(k_cache, v_cache, k_scale, v_scale)
+    qp, ld_q, cols = _rows(q, _bf16, None, None, "q")
+    T = q.shape[0]
+    num_heads = cols // dim
+    if cols == 0 or cols % dim or num_heads % heads:
+        raise NVFP4Error("q must be [T, num_heads * %d] with num_heads a multiple of %d" % (dim, heads))
+    if not isinstance(seq_lens, _Tensor):
+        raise NVFP4Error("seq_lens must be a GPU tensor")
+    R = seq_lens.numel()
+    table, ld_t, max_pages = _rows(block_table, _i32, R, None, "block_table")
+    if clear_padding is None:
+        clear_padding = out is None
+    if out is None:
+        out = q.new_empty((T, cols), dtype=_bf16 if out_dtype in (OUT_BF16, _bf16) else _f32)
+        op, ld_o = out.data_ptr(), cols
+    else:
+        op, ld_o, _ = _rows(out, _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32, T, cols, "out")
+    if lse is None and return_lse:
+        lse = q.new_empty((T, num_heads), dtype=_f32)
+    if workspace is None:
+        workspace = paged_attention_workspace(T, R, num_heads, heads, dim, max_new, max_seq, q.device)
+    bytes_ = workspace.numel()
+    _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, seq_lens, out, lse, workspace)
+    rc = lib.paged_attention_blocks(qp, ld_q, T, _vec(q_start, _i32, R + 1, "q_start"), _vec(seq_lens, _i32, R, "seq_lens"), R,
+                                    max_new, max_seq, num_heads, *cache, kb, vb, table, max_pages, ld_t,
+                                    dim ** -0.5 if scale is None else scale, window, op,
+                                    (OUT_BF16 if out.dtype is _bf16 else OUT_F32) + (OUT_CLEAR_PADDING if clear_padding else 0),
+                                    ld_o, None if lse is None else _vec(lse, _f32, T * num_heads, "lse"),
+                                    _vec(workspace, _u8, bytes_, "workspace"), bytes_, _raw_stream(q.get_device()))
+    if rc:
+        _check(rc, "paged_attention_blocks")
+    return (out, lse) if return_lse else out

@@ -43,11 +43,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
-// Two E4M3 bytes (the low or high half of w) as bf16: exact, three significand
-// bits into eight.
-template <bool HI>
-__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
+// Element types of the cache as the kernels are built for them.
+enum CacheKind { kCacheBf16, kCacheE4m3, kCacheE4m3Blocks, kCacheInt8Blocks };
+constexpr bool has_blocks(int kind) { return kind >= kCacheE4m3Blocks; }
+inline CacheKind cache_kind(const CacheView& c) {
+  return c.blocks == kBlocksInt8 ? kCacheInt8Blocks : c.blocks == kBlocksE4m3 ? kCacheE4m3Blocks : c.fp8 ? kCacheE4m3 : kCacheBf16;
+}
+
+// Two 8-bit elements (the low or high half of w) times a power of two as bf16: exact,
+// E4M3's four significand bits and INT8's eight into eight.  The E4M3 conversion has
+// the scale as its operand, for nothing.
+template <int KIND, bool HI>
+__device__ __forceinline__ uint32_t to_bf16(uint32_t w, float scale) {
+  if constexpr (KIND == kCacheInt8Blocks) {
+    const int x = (int)w;
+    const float lo = (float)(HI ? x << 8 >> 24 : x << 24 >> 24), hi = (float)(HI ? x >> 24 : x << 16 >> 24);
+    return pack_bf16(lo * scale, hi * scale);
+  } else {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, KIND == kCacheE4m3 ? 1.0f : scale, HI));
+  }
+}
+
+// The scale byte of 16 tokens of a head, of K in bits 0-7 and of V in bits 8-15, as its
+// place (page, token in page) has it; within the bytes that stand for finite values.
+__device__ __forceinline__ int block_scales(const CacheView& c, int head, uint32_t page, int token) {
+  const int64_t at = ((int64_t)page * c.heads + head) << (c.page_shift - 4) | token >> 4;
+  const int most = c.blocks == kBlocksInt8 ? kMostInt8 : kMostE4m3;
+  return min(max((int)c.k_blocks[at], 1), most) | min(max((int)c.v_blocks[at], 1), most) << 8;
+}
+__device__ __forceinline__ float scale_of(int scales, bool values) {
+  return __uint_as_float((uint32_t)(values ? scales >> 8 : scales & 0xff) << 23);
 }
 
 // A request's new tokens and keys.  Lengths fit 32 bits; none is negative but
@@ -82,9 +107,10 @@ __device__ __forceinline__ int64_t div_f64(int64_t n, int64_t d) { return (int64
 // row does not see every key they are taken out of the product, and a row that sees
 // them gets them added at the end: its sum is infinite or NaN whatever the weight is.
 // A word of the cache without them:
-template <bool FP8>
+template <int KIND>
 __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-  if (FP8) {
+  if (KIND == kCacheInt8Blocks) return w;
+  if (KIND != kCacheBf16) {
     const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
     return w & ~((nan >> 7) * 0xffu);
   }
@@ -92,10 +118,11 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w & ~((bad >> 15) * 0xffffu);
 }
 // x + what four columns at p hold of infinities and NaN, times by.
-template <bool FP8>
+template <int KIND>
 __device__ __forceinline__ f32x4 add_not_finite(f32x4 x, const uint8_t* p, float by) {
+  if (KIND == kCacheInt8Blocks) return x;
   float v[4];
-  if constexpr (FP8) {
+  if constexpr (KIND != kCacheBf16) {
     const uint32_t w = *(const uint32_t*)p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (w >> 8 * i & 0x7f) == 0x7f ? NAN : 0.f;

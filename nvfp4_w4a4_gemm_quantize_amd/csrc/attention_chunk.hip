@@ -146,8 +146,10 @@ __device__ __forceinline__ RowTile row_tile(const AttentionArgs& a, int number) 
 
 }  // namespace
 
-template <int D, bool FP8>
+template <int D, int KIND>
 __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionArgs a, ChunkWorkspace ws, int numbers) {
+  constexpr bool FP8 = KIND != kCacheBf16;    // 8-bit elements
+  constexpr bool BLOCKS = has_blocks(KIND);
   constexpr int KT = D == 256 ? 32 : 64;      // keys of a tile
   constexpr int NK = KT / 32;                 // key fragments of a tile
   constexpr int NG = KT / 16;                 // 16-key groups: a page holds whole ones
@@ -366,6 +368,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
   auto row_of = [&](int i) { return (i * kChunkWaves + wave) * RPI; };
   // Byte offsets of this wave's load instructions for 64 tiles at a time, a tile a lane.
   int64_t lane_at[NL];
+  // BLOCKS: the scales of that instruction's rows, which lie in one block; they take the
+  // offsets' free element
+  int lane_scales = 0;
+  static_assert(!BLOCKS || (NL == 1 && RPI <= kBlockTokens), "");
   auto locate = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -373,6 +379,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       const uint32_t page = page_at(key);
       lane_at[i] = (int64_t)((uint64_t)(page < num_pages ? page : 0) * page_units << 4) +
                    (uint32_t)((origin + key) & page_mask) * row_bytes;
+      if constexpr (BLOCKS) lane_scales = block_scales(a.cache, head, page < num_pages ? page : 0, (origin + key) & page_mask);
     }
   };
   typedef int64_t Offsets __attribute__((ext_vector_type(2)));
@@ -383,11 +390,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
       const uint32_t lo = __builtin_amdgcn_readlane((int)lane_at[i], j & 63), hi = __builtin_amdgcn_readlane((int)(lane_at[i] >> 32), j & 63);
       at[i] = (int64_t)((uint64_t)hi << 32 | lo);
     }
+    if constexpr (BLOCKS) at[1] = __builtin_amdgcn_readlane(lane_scales, j & 63);
     return at;
   };
   // bf16: straight into LDS.  E4M3: into registers, a step later converted into LDS.
   u32x4 kr[FP8 ? NL : 1], vr[FP8 ? NL : 1];
+  int k_scales = 0, v_scales = 0;              // BLOCKS: of what these hold
   auto bring = [&](const uint8_t* base, const Offsets& at, int i, uint8_t* lds, uint32_t voff, u32x4* regs) {
+    if constexpr (BLOCKS) (regs == kr ? k_scales : v_scales) = (int)at[1];
     if constexpr (FP8) {
       if (brings) regs[i] = *(const u32x4*)(base + at[i] + voff);
     } else {
@@ -413,12 +423,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t w = regs[i][k] & keep;
-              regs[i][k] = finite_only<true>(w);
+              regs[i][k] = finite_only<KIND>(w);
               odd |= w ^ regs[i][k];
             }
           }
           if (odd) not_finite[wave] = 1;
         }
+        const float scale = scale_of(values ? v_scales : k_scales, values);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
           const int row = (i * kChunkWaves + wave) * RPI + lane_row;
@@ -427,7 +438,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
           for (int k = 0; k < 2; ++k) {
             const uint32_t w0 = regs[i][2 * k], w1 = regs[i][2 * k + 1];
             *(u32x4*)(lds + row * ROW + ((2 * lane_col + k) ^ x) * 16) =
-                u32x4{e4m3_bf16<false>(w0), e4m3_bf16<true>(w0), e4m3_bf16<false>(w1), e4m3_bf16<true>(w1)};
+                u32x4{to_bf16<KIND, false>(w0, scale), to_bf16<KIND, true>(w0, scale), to_bf16<KIND, false>(w1, scale), to_bf16<KIND, true>(w1, scale)};
           }
         }
       }
@@ -448,7 +459,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t x = w[k] & keep;
-          w[k] = finite_only<false>(x);
+          w[k] = finite_only<KIND>(x);
           odd |= w[k] != x;
         }
         *p = w;
@@ -840,12 +851,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
           if (whole && a.out_bf16) {
             uint16_t* to = (uint16_t*)a.out + at - 4 * h + d;
             const u32x2 w = *(u32x2*)to;
-            const f32x4 x = add_not_finite<FP8>(f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+            const f32x4 x = add_not_finite<KIND>(f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
                                                       __uint_as_float(w[1] & 0xffff0000u)}, token + d * EB, by);
             *(u32x2*)to = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
           } else {
             f32x4* to = (f32x4*)(whole ? (float*)a.out + at - 4 * h + d : ws.o + slot * D + d);
-            *to = add_not_finite<FP8>(*to, token + d * EB, by);
+            *to = add_not_finite<KIND>(*to, token + d * EB, by);
           }
         }
       }
@@ -920,28 +931,38 @@ bool tiles_alone(const AttentionArgs& a) {
   return whole + fmax(all - rounds, 0.) * 150. < tiles * average + 1500.;
 }
 
-template <int D, bool FP8>
+template <int D, int KIND>
 hipError_t launch(const AttentionArgs& a, void* workspace, hipStream_t st) {
   const ChunkWorkspace ws = chunk_workspace(workspace, a.requests);
   const int64_t numbers = row_tiles(a.tokens, a.requests, a.group);
   if (tiles_alone(a)) {
-    attention_chunk_kernel<D, FP8><<<(unsigned)(numbers * a.cache.heads), kThreads, 0, st>>>(a, ws, (int)numbers);
+    attention_chunk_kernel<D, KIND><<<(unsigned)(numbers * a.cache.heads), kThreads, 0, st>>>(a, ws, (int)numbers);
     return hipGetLastError();
   }
-  attention_chunk_kernel<D, FP8><<<kChunkGrid, kThreads, 0, st>>>(a, ws, 0);
+  attention_chunk_kernel<D, KIND><<<kChunkGrid, kThreads, 0, st>>>(a, ws, 0);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attention_chunk_join_kernel<D><<<dim3((unsigned)(numbers * a.cache.heads), 8), 256, 0, st>>>(a, ws);
   return hipGetLastError();
 }
 
+template <int D>
+hipError_t launch_kind(const AttentionArgs& a, void* workspace, hipStream_t st) {
+  switch (cache_kind(a.cache)) {
+    case kCacheBf16: return launch<D, kCacheBf16>(a, workspace, st);
+    case kCacheE4m3: return launch<D, kCacheE4m3>(a, workspace, st);
+    case kCacheE4m3Blocks: return launch<D, kCacheE4m3Blocks>(a, workspace, st);
+    default: return launch<D, kCacheInt8Blocks>(a, workspace, st);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipStream_t st) {
   switch (a.cache.dim) {
-    case 64: return a.cache.fp8 ? launch<64, true>(a, workspace, st) : launch<64, false>(a, workspace, st);
-    case 128: return a.cache.fp8 ? launch<128, true>(a, workspace, st) : launch<128, false>(a, workspace, st);
-    default: return a.cache.fp8 ? launch<256, true>(a, workspace, st) : launch<256, false>(a, workspace, st);
+    case 64: return launch_kind<64>(a, workspace, st);
+    case 128: return launch_kind<128>(a, workspace, st);
+    default: return launch_kind<256>(a, workspace, st);
   }
 }
 

@@ -82,7 +82,7 @@ __device__ __forceinline__ DecodeItem decode_item(const AttentionArgs& a, int r)
 static_assert(kDecodeTile == 32 && kDecodeWaves == 4, "");
 
 // One key tile's K and V in registers.
-template <int D, bool FP8>
+template <int D, bool FP8>   // FP8: 8-bit elements
 struct DecodeTile {
   static constexpr int KW = FP8 ? D / 64 : D / 32;             // 16-byte words a lane holds of a key
   static constexpr int VW = D / 16 * (FP8 ? 1 : 2) / 4;        // 4-byte words a lane holds of a value row
@@ -114,8 +114,10 @@ __device__ __forceinline__ void load_words(uint32_t* out, const uint8_t* p) {
 // keys of 256: 132 us with one, 159 with two, of which one waits for the other).
 constexpr int decode_grid(int dim) { return dim <= 128 ? kDecodeGrid : kDecodeGrid / 2; }
 
-template <int D, bool FP8, int NF>
+template <int D, int KIND, int NF>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_kernel(AttentionArgs a) {
+  constexpr bool FP8 = KIND != kCacheBf16;   // 8-bit elements
+  constexpr bool BLOCKS = has_blocks(KIND);
   using Tile = DecodeTile<D, FP8>;
   constexpr int KS = D / 32;      // k steps of the first product
   constexpr int DV = D / 16;      // value columns a lane holds = fragments of O
@@ -244,6 +246,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
     const int32_t* table = a.block_table + (int64_t)r * a.ld_table;
     const uint32_t num_pages = (uint32_t)a.cache.num_pages;
     int64_t lane_at[2];
+    int lane_scales[2] = {0, 0};    // BLOCKS: the groups' scales
     uint64_t without[2];            // a bit for each of these tiles whose group has no page
     auto locate = [&](int k0) {
 #pragma unroll
@@ -253,6 +256,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
         without[f] = __ballot(page >= num_pages);
         lane_at[f] = (int64_t)((uint64_t)(page < num_pages ? page : 0) * page_units << 4) +
                      (uint32_t)((origin + key) & page_mask) * row_bytes;
+        if constexpr (BLOCKS) lane_scales[f] = block_scales(a.cache, head, page < num_pages ? page : 0, (origin + key) & page_mask);
       }
     };
     auto group_at = [&](int k, int f) {
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
         for (int j = 0; j < 4; ++j) load_words<Tile::VW>(tile.v[4 * f + j], vp + v_lane[j]);
       }
     };
-    auto scores = [&](Tile& tile, f32x4 (&s)[NF][2]) {
+    auto scores = [&](Tile& tile, f32x4 (&s)[NF][2], const int (&scales)[2]) {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
 #pragma unroll
@@ -289,8 +293,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              w[2 * i] = e4m3_bf16<false>(tile.k[f][st >> 1][(st & 1) * 2 + i]);
-              w[2 * i + 1] = e4m3_bf16<true>(tile.k[f][st >> 1][(st & 1) * 2 + i]);
+              w[2 * i] = to_bf16<KIND, false>(tile.k[f][st >> 1][(st & 1) * 2 + i], scale_of(scales[f], false));
+              w[2 * i + 1] = to_bf16<KIND, true>(tile.k[f][st >> 1][(st & 1) * 2 + i], scale_of(scales[f], false));
             }
             kf = __builtin_bit_cast(bf16x8, w);
           } else {
@@ -302,7 +306,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       }
     };
     // softmax step and second product
-    auto values = [&](Tile& tile, f32x4 (&s)[NF][2], int k, bool gap0, bool gap1) {
+    auto values = [&](Tile& tile, f32x4 (&s)[NF][2], const int (&scales)[2], int k, bool gap0, bool gap1) {
       const int at = wave + k * kDecodeWaves;
       const bool partly = at < seen_from || at >= seen_to;
       if (gap0 || gap1 || partly) {
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
             // what lies in unwritten or foreign places may be NaN, and 0 * NaN is not 0
 #pragma unroll
             for (int w = 0; w < Tile::VW; ++w) {
-              const uint32_t x = held ? tile.v[4 * f + j][w] : 0u, finite = finite_only<FP8>(x);
+              const uint32_t x = held ? tile.v[4 * f + j][w] : 0u, finite = finite_only<KIND>(x);
               odd |= partly && finite != x;
               tile.v[4 * f + j][w] = partly ? finite : x;
             }
@@ -374,7 +378,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            vt[i] = u32x4{e4m3_bf16<false>(b[0][i]), e4m3_bf16<true>(b[0][i]), e4m3_bf16<false>(b[1][i]), e4m3_bf16<true>(b[1][i])};
+            vt[i] = u32x4{to_bf16<KIND, false>(b[0][i], scale_of(scales[0], true)), to_bf16<KIND, true>(b[0][i], scale_of(scales[0], true)),
+                          to_bf16<KIND, false>(b[1][i], scale_of(scales[1], true)), to_bf16<KIND, true>(b[1][i], scale_of(scales[1], true))};
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -401,14 +406,18 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
       load_values(tile, 0);
       for (int k = 0; k < mine; ++k) {
         const bool gap0 = without[0] >> (k & 63) & 1, gap1 = without[1] >> (k & 63) & 1;
+        int scales[2] = {0, 0};
+        if constexpr (BLOCKS)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) scales[f] = __builtin_amdgcn_readlane(lane_scales[f], k & 63);
         f32x4 s[NF][2];
-        scores(tile, s);
+        scores(tile, s, scales);
         const bool more = k + 1 < mine;
         if (more) {
           if (((k + 1) & 63) == 0) locate(k + 1);
           load_keys(tile, k + 1);
         }
-        values(tile, s, k, gap0, gap1);
+        values(tile, s, scales, k, gap0, gap1);
         if (more) load_values(tile, k + 1);
       }
     }
@@ -424,7 +433,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
         const uint32_t page = (uint32_t)table[(uint32_t)(origin + key) >> a.cache.page_shift];
         if (page >= num_pages) continue;
         const int64_t token = (int64_t)((uint64_t)page * page_units << 4) + (uint32_t)((origin + key) & page_mask) * row_bytes;
-        x = add_not_finite<FP8>(x, v_base + token + d * EB, 1.f);
+        x = add_not_finite<KIND>(x, v_base + token + d * EB, 1.f);
       }
       return x;
     };
@@ -509,25 +518,35 @@ size_t attention_decode_workspace(int dim) {
 
 namespace {
 
-template <int D, bool FP8>
+template <int D, int KIND>
 hipError_t launch(const AttentionArgs& a, hipStream_t st) {
   // rows a request may have here: one fragment of 16 or two
   const int64_t rows = min(a.max_new, (int64_t)(kDecodeRows / a.group)) * a.group;
   const unsigned grid = decode_grid(D);
   if (rows <= 16)
-    attention_decode_kernel<D, FP8, 1><<<grid, kThreads, 0, st>>>(a);
+    attention_decode_kernel<D, KIND, 1><<<grid, kThreads, 0, st>>>(a);
   else
-    attention_decode_kernel<D, FP8, 2><<<grid, kThreads, 0, st>>>(a);
+    attention_decode_kernel<D, KIND, 2><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_kind(const AttentionArgs& a, hipStream_t st) {
+  switch (cache_kind(a.cache)) {
+    case kCacheBf16: return launch<D, kCacheBf16>(a, st);
+    case kCacheE4m3: return launch<D, kCacheE4m3>(a, st);
+    case kCacheE4m3Blocks: return launch<D, kCacheE4m3Blocks>(a, st);
+    default: return launch<D, kCacheInt8Blocks>(a, st);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_attention_decode(const AttentionArgs& a, hipStream_t st) {
   switch (a.cache.dim) {
-    case 64: return a.cache.fp8 ? launch<64, true>(a, st) : launch<64, false>(a, st);
-    case 128: return a.cache.fp8 ? launch<128, true>(a, st) : launch<128, false>(a, st);
-    default: return a.cache.fp8 ? launch<256, true>(a, st) : launch<256, false>(a, st);
+    case 64: return launch_kind<64>(a, st);
+    case 128: return launch_kind<128>(a, st);
+    default: return launch_kind<256>(a, st);
   }
 }
 

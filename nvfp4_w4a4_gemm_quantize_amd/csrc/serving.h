@@ -38,7 +38,16 @@ struct CacheView {
   int fp8;                     // E4M3 elements, else bf16
   int page_shift;              // log2(page size)
   int heads, dim;
+  // Caches with a scale for each 16 tokens and head (kBlocks*): E8M0 bytes
+  // [pages, heads, page size / 16], contiguous; fp8 is 0 and k_scale, v_scale null.
+  int blocks;
+  uint8_t* k_blocks;
+  uint8_t* v_blocks;
 };
+enum { kBlocksNone, kBlocksE4m3, kBlocksInt8 };
+constexpr int kBlockTokens = 16;
+// The largest scale bytes: with them the largest code is still below 2^128.
+constexpr int kMostE4m3 = 246, kMostInt8 = 248;
 
 struct KvWriteArgs {
   const uint16_t* k;

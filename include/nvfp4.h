@@ -580,7 +580,7 @@ int verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64
  *   steps, amplitude   host, out: [d / 2] and [1].
  */
 int rotary_steps(int rotary_dim, double base, int scaling, double factor, double original_length, double slow_turns,
-                 double fast_turns, const double* pair_factors, uint64_t* steps, float* amplitude);
+                 double fast_turns, const double* pair_factors, uint64_t* steps, double* amplitude);
 
 /*
  * rotary -- rows of heads, rotated: with t = 2 pi steps[i] positions[row] / 2^64,
@@ -599,7 +599,7 @@ int rotary_steps(int rotary_dim, double base, int scaling, double factor, double
  * tokens == 0 enqueues nothing.
  */
 int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int head_dim, const int32_t* positions,
-           const uint64_t* steps, int rotary_dim, int layout, float amplitude, uint16_t* out, int64_t ld_out,
+           const uint64_t* steps, int rotary_dim, int layout, double amplitude, uint16_t* out, int64_t ld_out,
            nvfp4_stream_t stream);
 
 /*
@@ -626,7 +626,7 @@ int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int h
  */
 int paged_kv_append(const uint16_t* q, int64_t ld_q, int num_heads, uint16_t* q_out, int64_t ld_q_out, const uint16_t* k,
                     int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* positions, const int64_t* slots,
-                    int64_t tokens, const uint64_t* steps, int rotary_dim, int layout, float amplitude, void* k_cache,
+                    int64_t tokens, const uint64_t* steps, int rotary_dim, int layout, double amplitude, void* k_cache,
                     void* v_cache, int cache_dtype, int64_t num_pages, int page_size, int num_kv_heads, int head_dim,
                     int64_t page_stride, int64_t head_stride, int64_t token_stride, const float* k_scale,
                     const float* v_scale, uint8_t* k_blocks, uint8_t* v_blocks, nvfp4_stream_t stream);
@@ -645,6 +645,47 @@ int paged_attention_blocks(const uint16_t* q, int64_t ld_q, int64_t tokens, cons
                            const uint8_t* k_blocks, const uint8_t* v_blocks, const int32_t* block_table, int64_t max_pages,
                            int64_t ld_table, float scale, int64_t window, void* out, int out_dtype, int64_t ld_out, float* lse,
                            void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * Linear layers in 8-bit integers, for modules that 4 bits harm: int8_quantize (a bf16
+ * matrix as codes with a scale for each row: a token's, or an output channel's of a
+ * weight), gemm_w8a8 (the product) and int8_linear (both, for an activation).
+ *     s_m = amax|x_m| / 127,  a_mk = round-to-nearest-even(x_mk * (127 / amax|x_m|)),
+ *     y_mn = (s_m * sum_k a_mk w_nk) * t_n,
+ * in fp32 but for the sum, which is exact.  A row whose amax is below 2^-120 has scale 0
+ * and codes 0; one with an infinity or NaN has scale NaN and codes 0, so that its outputs
+ * are NaN and no others.
+ */
+
+/*
+ * int8_quantize
+ *   x        bf16 [rows, cols], row stride ld_x (multiple of 8), 16-byte aligned;
+ *            cols a multiple of 16 below 2^17 (others NVFP4_EUNSUPPORTED).
+ *   codes    out, int8 [rows, cols] contiguous, 16-byte aligned.
+ *   scales   out, float [rows].
+ * rows == 0 enqueues nothing.
+ */
+int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, int8_t* codes, float* scales,
+                  nvfp4_stream_t stream);
+
+/*
+ * gemm_w8a8 -- out[m][n] = (a_scale[m] * sum_k a[m][k] w[n][k]) * w_scale[n].
+ *   a, w     int8 [m, k] and [n, k], contiguous, 16-byte aligned; any code (-128 too);
+ *            k a multiple of 16 below 2^17.
+ *   a_scale, w_scale   float [m] and [n].
+ *   out      [m, n] of out_dtype (NVFP4_OUT_*), row stride ld_out >= n, any alignment of
+ *            its elements (rows of 16-byte aligned ones leave in wide stores).
+ * m == 0 enqueues nothing.  Results are deterministic, and a row's do not depend on the
+ * others or on m.
+ */
+int gemm_w8a8(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n, int64_t k,
+              void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream);
+
+/*
+ * int8_linear -- int8_quantize of x [m, k] into a and a_scale, and gemm_w8a8 on them.
+ */
+int int8_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ld_x, int8_t* a, float* a_scale, const int8_t* w,
+                const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream);
 
 /* Human-readable text of a status code (static storage). */
 const char* nvfp4_status_string(int status);

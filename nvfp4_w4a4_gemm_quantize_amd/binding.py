@@ -61,13 +61,16 @@ _SIGNATURES = {
                              _i64, _c_p, _c_p, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "rotary_steps": (_int, [_int, ctypes.c_double, _int, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                             _c_p, _c_p, _c_p]),
-    "rotary": (_int, [_c_p, _i64, _i64, _int, _int, _c_p, _c_p, _int, _int, ctypes.c_float, _c_p, _i64, _c_p]),
+    "rotary": (_int, [_c_p, _i64, _i64, _int, _int, _c_p, _c_p, _int, _int, ctypes.c_double, _c_p, _i64, _c_p]),
     "paged_kv_append": (_int, [_c_p, _i64, _int, _c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _c_p, _i64, _c_p, _int, _int,
-                               ctypes.c_float, _c_p, _c_p, _int, _i64, _int, _int, _int, _i64, _i64, _i64, _c_p, _c_p, _c_p,
+                               ctypes.c_double, _c_p, _c_p, _int, _i64, _int, _int, _int, _i64, _i64, _i64, _c_p, _c_p, _c_p,
                                _c_p, _c_p]),
     "paged_attention_blocks": (_int, [_c_p, _i64, _i64, _c_p, _c_p, _i64, _i64, _i64, _int, _c_p, _c_p, _int, _i64, _int, _int,
                                       _int, _i64, _i64, _i64, _c_p, _c_p, _c_p, _i64, _i64, ctypes.c_float, _i64, _c_p, _int,
                                       _i64, _c_p, _c_p, ctypes.c_size_t, _c_p]),
+    "int8_quantize": (_int, [_c_p, _i64, _i64, _i64, _c_p, _c_p, _c_p]),
+    "gemm_w8a8": (_int, [_c_p, _c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _int, _i64, _c_p]),
+    "int8_linear": (_int, [_c_p, _i64, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i64, _c_p, _int, _i64, _c_p]),
     "nvfp4_status_string": (ctypes.c_char_p, [_int]),
     "nvfp4_last_hip_error": (_int, []),
 }
@@ -710,7 +713,7 @@ def rotary_table(rotary_dim, base=10000.0, layout="half", scaling="none", factor
     if layout not in _LAYOUTS or scaling not in _ROPE:
         raise NVFP4Error("layout is one of %s, scaling one of %s" % (", ".join(_LAYOUTS), ", ".join(_ROPE)))
     n = max(int(rotary_dim), 0) // 2
-    steps, amp = (ctypes.c_uint64 * max(n, 1))(), ctypes.c_float()
+    steps, amp = (ctypes.c_uint64 * max(n, 1))(), ctypes.c_double()
     factors = None
     if pair_factors is not None:
         factors = [float(x) for x in pair_factors]
@@ -881,3 +884,74 @@ def paged_attention_blocks(q, k_cache, v_cache, k_scale, v_scale, block_table, q
     if rc:
         _check(rc, "paged_attention_blocks")
     return (out, lse) if return_lse else out
+
+
+def _codes8(t, rows, cols, name):
+    """(address, rows, columns) of a contiguous int8 matrix."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _int8 or t.dim() != 2 or not t.is_contiguous() \
+            or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        _refuse(t, _int8, name, "[%s, %s] contiguous" % (rows, cols))
+    return t.data_ptr(), t.shape[0], t.shape[1]
+
+
+def _int8_out(like, m, n, out_dtype, out):
+    dtype = _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32
+    if out is None:
+        out = like.new_empty((m, n), dtype=dtype)
+        return out, out.data_ptr(), n, OUT_BF16 if dtype is _bf16 else OUT_F32
+    op, ld, _ = _rows(out, dtype, m, n, "out")
+    return out, op, ld, OUT_BF16 if dtype is _bf16 else OUT_F32
+
+
+def int8_quantize(x, codes=None, scales=None):
+    """bf16 [rows, cols] (row stride allowed) -> (codes int8 [rows, cols], scales fp32 [rows]): a scale amax / 127 for each
+    row, a token's or an output channel's."""
+    lib = _lib or load()
+    xp, ld, cols = _rows(x, _bf16, None, None, "x")
+    rows = x.shape[0]
+    if codes is None:
+        codes = x.new_empty((rows, cols), dtype=_int8)
+    if scales is None:
+        scales = x.new_empty(rows, dtype=_f32)
+    cp, _, _ = _codes8(codes, rows, cols, "codes")
+    _one_device(x, codes, scales)
+    rc = lib.int8_quantize(xp, rows, cols, ld, cp, _vec(scales, _f32, rows, "scales"), _raw_stream(x.get_device()))
+    if rc:
+        _check(rc, "int8_quantize")
+    return codes, scales
+
+
+def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None):
+    """out [m, n] = a_scale[m] * (a [m, k] . w [n, k]^T) * w_scale[n]: int8 codes with a scale for each row, as
+    int8_quantize gives them."""
+    lib = _lib or load()
+    ap, m, k = _codes8(a, None, None, "a")
+    wp, n, _ = _codes8(w, None, k, "w")
+    out, op, ld, kind = _int8_out(a, m, n, out_dtype, out)
+    _one_device(a, a_scale, w, w_scale, out)
+    rc = lib.gemm_w8a8(ap, _vec(a_scale, _f32, m, "a_scale"), m, wp, _vec(w_scale, _f32, n, "w_scale"), n, k, op, kind, ld,
+                       _raw_stream(a.get_device()))
+    if rc:
+        _check(rc, "gemm_w8a8")
+    return out
+
+
+def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, scales=None):
+    """x bf16 [m, k] (row stride allowed), quantised to int8 with a scale for each token, times w (int8 [n, k], w_scale
+    fp32 [n]; from int8_quantize of the weight).  codes, scales: where x's are left (allocated if None)."""
+    lib = _lib or load()
+    xp, ld_x, k = _rows(x, _bf16, None, None, "x")
+    m = x.shape[0]
+    wp, n, _ = _codes8(w, None, k, "w")
+    if codes is None:
+        codes = x.new_empty((m, k), dtype=_int8)
+    if scales is None:
+        scales = x.new_empty(m, dtype=_f32)
+    cp, _, _ = _codes8(codes, m, k, "codes")
+    out, op, ld, kind = _int8_out(x, m, n, out_dtype, out)
+    _one_device(x, w, w_scale, codes, scales, out)
+    rc = lib.int8_linear(xp, m, k, ld_x, cp, _vec(scales, _f32, m, "scales"), wp, _vec(w_scale, _f32, n, "w_scale"), n, op, kind,
+                         ld, _raw_stream(x.get_device()))
+    if rc:
+        _check(rc, "int8_linear")
+    return out

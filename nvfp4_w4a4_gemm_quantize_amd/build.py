@@ -22,8 +22,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["quantize.hip", "gemm.hip", "decode.hip", "recurrence.hip", "paged.hip", "attention_decode.hip",
-           "attention_chunk.hip", "verify.hip", "rotary.hip", "abi.cpp", "abi_serving.cpp", "abi_layer8.cpp", "validate.cpp",
-           "validate_serving.cpp", "validate_layer8.cpp"]
+           "attention_chunk.hip", "verify.hip", "rotary.hip", "int8.hip", "abi.cpp", "abi_serving.cpp", "abi_layer8.cpp",
+           "validate.cpp", "validate_serving.cpp", "validate_layer8.cpp"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I" + os.path.join(ROOT, "include")]
 DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

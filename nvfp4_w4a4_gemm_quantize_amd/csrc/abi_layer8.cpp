@@ -33,7 +33,7 @@ static CacheView cache_view(void* k, void* v, int dtype, int64_t num_pages, int 
   return c;
 }
 
-static RotaryArgs rotation(const int32_t* positions, const uint64_t* steps, int rotary_dim, int layout, float amplitude) {
+static RotaryArgs rotation(const int32_t* positions, const uint64_t* steps, int rotary_dim, int layout, double amplitude) {
   RotaryArgs r{};
   r.steps = steps;
   r.positions = positions;
@@ -58,13 +58,13 @@ static RotaryRows rotary_rows(const uint16_t* x, int64_t ld_x, int64_t tokens, i
 extern "C" {
 
 int rotary_steps(int rotary_dim, double base, int scaling, double factor, double original_length, double slow_turns,
-                 double fast_turns, const double* pair_factors, uint64_t* steps, float* amplitude) {
+                 double fast_turns, const double* pair_factors, uint64_t* steps, double* amplitude) {
   return make_rotary_steps(rotary_dim, base, scaling, factor, original_length, slow_turns, fast_turns, pair_factors, steps,
                            amplitude);
 }
 
 int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int head_dim, const int32_t* positions,
-           const uint64_t* steps, int rotary_dim, int layout, float amplitude, uint16_t* out, int64_t ld_out,
+           const uint64_t* steps, int rotary_dim, int layout, double amplitude, uint16_t* out, int64_t ld_out,
            nvfp4_stream_t stream) {
   int rc = validate_rotary_rows(x, ld_x, tokens, num_heads, head_dim, out, ld_out);
   if (rc) return rc;
@@ -76,7 +76,7 @@ int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int h
 
 int paged_kv_append(const uint16_t* q, int64_t ld_q, int num_heads, uint16_t* q_out, int64_t ld_q_out, const uint16_t* k,
                     int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* positions, const int64_t* slots,
-                    int64_t tokens, const uint64_t* steps, int rotary_dim, int layout, float amplitude, void* k_cache,
+                    int64_t tokens, const uint64_t* steps, int rotary_dim, int layout, double amplitude, void* k_cache,
                     void* v_cache, int cache_dtype, int64_t num_pages, int page_size, int num_kv_heads, int head_dim,
                     int64_t page_stride, int64_t head_stride, int64_t token_stride, const float* k_scale,
                     const float* v_scale, uint8_t* k_blocks, uint8_t* v_blocks, nvfp4_stream_t stream) {
@@ -161,6 +161,47 @@ int paged_attention_blocks(const uint16_t* q, int64_t ld_q, int64_t tokens, cons
   a.out_bf16 = (out_dtype & ~NVFP4_OUT_CLEAR_PADDING) == NVFP4_OUT_BF16;
   a.clear_padding = (out_dtype & NVFP4_OUT_CLEAR_PADDING) != 0;
   return hip_status(launch_paged_attention(a, (hipStream_t)stream));
+}
+
+int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, int8_t* codes, float* scales,
+                  nvfp4_stream_t stream) {
+  const int rc = validate_int8_quantize(x, rows, cols, ld_x, codes, scales);
+  if (rc || rows == 0) return rc;
+  return hip_status(launch_int8_quantize(x, rows, cols, ld_x, codes, scales, (hipStream_t)stream));
+}
+
+static Int8Args int8_args(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n,
+                          int64_t k, void* out, int out_dtype, int64_t ld_out) {
+  Int8Args g{};
+  g.a = a;
+  g.a_scale = a_scale;
+  g.w = w;
+  g.w_scale = w_scale;
+  g.out = out;
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  g.ld_out = ld_out;
+  g.out_bf16 = out_dtype == NVFP4_OUT_BF16;
+  return g;
+}
+
+int gemm_w8a8(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n, int64_t k,
+              void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream) {
+  const int rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out);
+  if (rc || m == 0) return rc;
+  return hip_status(launch_gemm_w8a8(int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out), (hipStream_t)stream));
+}
+
+int int8_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ld_x, int8_t* a, float* a_scale, const int8_t* w,
+                const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream) {
+  int rc = validate_int8_quantize(x, m, k, ld_x, a, a_scale);
+  if (rc) return rc;
+  rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out);
+  if (rc || m == 0) return rc;
+  const hipError_t e = launch_int8_quantize(x, m, k, ld_x, a, a_scale, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_status(e);
+  return hip_status(launch_gemm_w8a8(int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out), (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -18,7 +18,7 @@ struct RotaryArgs {
   const int32_t* positions;    // [tokens]; negative: not turned
   int dim;                     // leading columns of a head that are rotated; 0: none
   int interleaved;             // pairs (2 i, 2 i + 1), else (i, i + dim / 2)
-  float amplitude;             // on cosine and sine
+  double amplitude;            // on cosine and sine
 };
 
 // Rows of `heads` heads of `dim` columns, rotated from x to out.
@@ -40,5 +40,19 @@ struct AppendArgs {
   CacheView cache;
 };
 hipError_t launch_paged_kv_append(const AppendArgs& a, hipStream_t st);
+
+hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, float* scales,
+                                hipStream_t st);
+
+struct Int8Args {
+  const int8_t* a;             // [m, k]
+  const float* a_scale;        // [m]
+  const int8_t* w;             // [n, k]
+  const float* w_scale;        // [n]
+  void* out;                   // [m, n], row stride ld_out
+  int64_t m, n, k, ld_out;
+  int out_bf16;
+};
+hipError_t launch_gemm_w8a8(const Int8Args& a, hipStream_t st);
 
 }  // namespace nvfp4

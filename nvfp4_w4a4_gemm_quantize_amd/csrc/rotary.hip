@@ -8,7 +8,7 @@
 //
 // A thread owns 16 columns of a head (a unit: 8 pairs) of one token, finds their
 // cosines and sines once and uses them for several heads, so that the angles' some
-// 300 instructions stay beside the loads.
+// 400 instructions stay beside the loads.
 #include <hip/hip_runtime.h>
 
 #include "attention.h"
@@ -20,16 +20,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// cos and sin of x / 2^32 turns.  The nearest quarter is taken off, which leaves at
-// most an eighth of a turn, where the Taylor series up to x^9 and x^10 are off by less
-// than 2 * 10^-9.
-__device__ __forceinline__ float2 cos_sin(uint32_t x) {
+// cos and sin of x / 2^32 turns times amplitude, rounded once.  The nearest quarter is
+// taken off, which leaves at most an eighth of a turn, where the Taylor series up to x^11
+// and x^10 are off by less than 10^-10.  In fp64, whose FMA takes no longer here: fp32's
+// last digit would move a hundred times as many 8-bit codes of rotated keys to the other
+// side of a tie.
+__device__ __forceinline__ float2 cos_sin(uint32_t x, double amplitude) {
   const uint32_t quarter = (x + 0x20000000u) >> 30;
-  const float t = (float)(int32_t)(x - (quarter << 30)) * 1.46291807926715968e-9f;   // 2 pi / 2^32
-  const float u = t * t;
-  const float s = fmaf(t * u, fmaf(u, fmaf(u, fmaf(u, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), t);
-  const float c = fmaf(u, fmaf(u, fmaf(u, fmaf(u, fmaf(u, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
-  const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
+  const double t = (double)(int32_t)(x - (quarter << 30)) * 1.46291807926715968e-9;   // 2 pi / 2^32
+  const double u = t * t;
+  const double s = fma(t * u, fma(u, fma(u, fma(u, fma(u, -1. / 39916800, 1. / 362880), -1. / 5040), 1. / 120), -1. / 6), t);
+  const double c = fma(u, fma(u, fma(u, fma(u, fma(u, -1. / 3628800, 1. / 40320), -1. / 720), 1. / 24), -0.5), 1.);
+  const float cc = (float)((quarter & 1 ? s : c) * amplitude), ss = (float)((quarter & 1 ? c : s) * amplitude);
   return make_float2((quarter + 1) & 2 ? -cc : cc, quarter & 2 ? -ss : ss);
 }
 
@@ -41,9 +43,9 @@ __device__ __forceinline__ void find_turn(Turn& t, const RotaryArgs& rot, int un
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t phase = rot.steps[unit * 8 + i] * (uint64_t)(uint32_t)position;
-    const float2 cs = cos_sin((uint32_t)(phase >> 32));
-    t.c[i] = position < 0 ? 1.f : cs.x * rot.amplitude;
-    t.s[i] = position < 0 ? 0.f : cs.y * rot.amplitude;
+    const float2 cs = cos_sin((uint32_t)(phase >> 32), rot.amplitude);
+    t.c[i] = position < 0 ? 1.f : cs.x;
+    t.s[i] = position < 0 ? 0.f : cs.y;
   }
 }
 

@@ -17,7 +17,7 @@ static int validate_rotary_dim(int rotary_dim) {
 
 int make_rotary_steps(int rotary_dim, double base, int scaling, double factor, double original_length,
                       double slow_turns, double fast_turns, const double* pair_factors, uint64_t* steps,
-                      float* amplitude) {
+                      double* amplitude) {
   const int rc = validate_rotary_dim(rotary_dim);
   if (rc) return rc;
   const bool ramp = scaling == NVFP4_ROPE_YARN || scaling == NVFP4_ROPE_WAVELENGTH;
@@ -59,11 +59,11 @@ int make_rotary_steps(int rotary_dim, double base, int scaling, double factor, d
     const long double units = rintl(ldexpl(w, 64));
     steps[i] = units >= ldexpl(1, 64) ? 0 : (uint64_t)units;
   }
-  *amplitude = scaling == NVFP4_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  *amplitude = scaling == NVFP4_ROPE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
   return NVFP4_OK;
 }
 
-int validate_rotation(const void* positions, const void* steps, int rotary_dim, int layout, float amplitude,
+int validate_rotation(const void* positions, const void* steps, int rotary_dim, int layout, double amplitude,
                       int head_dim, int64_t tokens) {
   const int rc = validate_rotary_dim(rotary_dim);
   if (rc) return rc;
@@ -96,6 +96,40 @@ int validate_block_cache(const void* k_cache, const void* v_cache, int cache_dty
                                 head_stride, token_stride, nullptr, nullptr);
   if (rc) return rc;
   return !k_blocks || !v_blocks ? NVFP4_EINVAL : NVFP4_OK;
+}
+
+// Columns of int8 rows: whole 16-byte pieces, and few enough that a sum of products of
+// two codes (2^14 at most) fits 32 bits.
+static int validate_int8_cols(int64_t cols) {
+  if (cols <= 0) return NVFP4_ESHAPE;
+  return cols % 16 || cols >= 1 << 17 ? NVFP4_EUNSUPPORTED : NVFP4_OK;
+}
+
+int validate_int8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, const void* codes, const void* scales) {
+  if (rows < 0) return NVFP4_ESHAPE;
+  const int rc = validate_int8_cols(cols);
+  if (rc) return rc;
+  if (ld_x < cols) return NVFP4_ESHAPE;
+  if (rows == 0) return NVFP4_OK;
+  if (rows > INT32_MAX) return NVFP4_EUNSUPPORTED;
+  if (!x || !codes || !scales) return NVFP4_EINVAL;
+  return !aligned(x, 16) || ld_x % 8 || !aligned(codes, 16) || !aligned(scales, 4) ? NVFP4_EALIGN : NVFP4_OK;
+}
+
+int validate_gemm_w8a8(const void* a, const void* a_scale, int64_t m, const void* w, const void* w_scale, int64_t n, int64_t k,
+                       const void* out, int out_dtype, int64_t ld_out) {
+  if (m < 0 || n <= 0) return NVFP4_ESHAPE;
+  const int rc = validate_int8_cols(k);
+  if (rc) return rc;
+  if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_EINVAL;
+  if (ld_out < n) return NVFP4_ESHAPE;
+  // tiles are counted in 32 bits
+  if (m > INT32_MAX || n > INT32_MAX || ((m + 127) / 128) * ((n + 127) / 128) > INT32_MAX) return NVFP4_EUNSUPPORTED;
+  if (m == 0) return NVFP4_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return NVFP4_EINVAL;
+  const unsigned element = out_dtype == NVFP4_OUT_BF16 ? 2 : 4;
+  return !aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(out, element)
+             ? NVFP4_EALIGN : NVFP4_OK;
 }
 
 }  // namespace nvfp4

@@ -134,3 +134,22 @@ def fill(x, kind):
     top = np.abs(b).max((-1, -2))
     e = np.vectorize(lambda t: scale_byte(t, kind))(top).astype(np.uint8)
     return round_codes(b * 2.0 ** (127.0 - e.astype(np.float64))[..., None, None], kind).reshape(x.shape), e
+
+
+# ---------------------------------------------------- int8 linear layers ----
+
+def int8_quantize(x):
+    """(codes, scales fp32) of the rows of x (values of bf16, as fp32): every step one fp32 operation."""
+    x = np.asarray(x, np.float32)
+    top = np.abs(x).max(1)
+    bad, small = ~np.isfinite(top), top < np.float32(2.0 ** -120)
+    safe = np.where(bad | small, np.float32(1), top)
+    by = np.where(bad | small, np.float32(0), np.float32(127) / safe)
+    scale = np.where(bad, np.float32(np.nan), np.where(small, np.float32(0), safe / np.float32(127)))
+    return np.rint(np.where((bad | small)[:, None], np.float32(0), x) * by[:, None]).astype(np.int8), scale.astype(np.float32)
+
+
+def gemm_w8a8(a, a_scale, w, w_scale):
+    """fp32 y: the exact sum rounded to fp32, then one fp32 product with each scale."""
+    s = a.astype(np.int64) @ w.astype(np.int64).T
+    return (s.astype(np.float32) * a_scale[:, None]) * w_scale[None]

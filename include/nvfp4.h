@@ -675,17 +675,23 @@ int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, i
  *   a_scale, w_scale   float [m] and [n].
  *   out      [m, n] of out_dtype (NVFP4_OUT_*), row stride ld_out >= n, any alignment of
  *            its elements (rows of 16-byte aligned ones leave in wide stores).
+ *   workspace  optional (null), 16-byte aligned, at least gemm_w8a8_workspace_bytes(m, n,
+ *            k) (which may be 0); its contents do not matter.  With it, products of few
+ *            rows are split along k over the chip.  Not shared by calls in flight on
+ *            different streams.
  * m == 0 enqueues nothing.  Results are deterministic, and a row's do not depend on the
- * others or on m.
+ * others, on m or on the workspace.
  */
+size_t gemm_w8a8_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int gemm_w8a8(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n, int64_t k,
-              void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream);
+              void* out, int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
 /*
  * int8_linear -- int8_quantize of x [m, k] into a and a_scale, and gemm_w8a8 on them.
  */
 int int8_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ld_x, int8_t* a, float* a_scale, const int8_t* w,
-                const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream);
+                const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, void* workspace,
+                size_t workspace_bytes, nvfp4_stream_t stream);
 
 /* Human-readable text of a status code (static storage). */
 const char* nvfp4_status_string(int status);

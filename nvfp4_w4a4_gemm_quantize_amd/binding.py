@@ -69,8 +69,9 @@ _SIGNATURES = {
                                       _int, _i64, _i64, _i64, _c_p, _c_p, _c_p, _i64, _i64, ctypes.c_float, _i64, _c_p, _int,
                                       _i64, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "int8_quantize": (_int, [_c_p, _i64, _i64, _i64, _c_p, _c_p, _c_p]),
-    "gemm_w8a8": (_int, [_c_p, _c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _int, _i64, _c_p]),
-    "int8_linear": (_int, [_c_p, _i64, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i64, _c_p, _int, _i64, _c_p]),
+    "gemm_w8a8_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "gemm_w8a8": (_int, [_c_p, _c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _int, _i64, _c_p, ctypes.c_size_t, _c_p]),
+    "int8_linear": (_int, [_c_p, _i64, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i64, _c_p, _int, _i64, _c_p, ctypes.c_size_t, _c_p]),
     "nvfp4_status_string": (ctypes.c_char_p, [_int]),
     "nvfp4_last_hip_error": (_int, []),
 }
@@ -921,24 +922,38 @@ def int8_quantize(x, codes=None, scales=None):
     return codes, scales
 
 
-def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None):
+def _int8_workspace(lib, like, m, n, k, workspace):
+    """(workspace or None, its address, its bytes): one that products of few rows are split with, allocated if None."""
+    if workspace is None:
+        need = lib.gemm_w8a8_workspace_bytes(m, n, k)
+        if not need:
+            return None, None, 0
+        workspace = like.new_empty(need, dtype=_u8)
+        return workspace, workspace.data_ptr(), need
+    bytes_ = workspace.numel() if isinstance(workspace, _Tensor) else 0
+    return workspace, _vec(workspace, _u8, bytes_, "workspace"), bytes_
+
+
+def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, workspace=None):
     """out [m, n] = a_scale[m] * (a [m, k] . w [n, k]^T) * w_scale[n]: int8 codes with a scale for each row, as
-    int8_quantize gives them."""
+    int8_quantize gives them.  workspace: uint8, gemm_w8a8_workspace_bytes of it (allocated if None)."""
     lib = _lib or load()
     ap, m, k = _codes8(a, None, None, "a")
     wp, n, _ = _codes8(w, None, k, "w")
     out, op, ld, kind = _int8_out(a, m, n, out_dtype, out)
-    _one_device(a, a_scale, w, w_scale, out)
-    rc = lib.gemm_w8a8(ap, _vec(a_scale, _f32, m, "a_scale"), m, wp, _vec(w_scale, _f32, n, "w_scale"), n, k, op, kind, ld,
-                       _raw_stream(a.get_device()))
+    workspace, wsp, bytes_ = _int8_workspace(lib, a, m, n, k, workspace)
+    _one_device(a, a_scale, w, w_scale, out, workspace)
+    rc = lib.gemm_w8a8(ap, _vec(a_scale, _f32, m, "a_scale"), m, wp, _vec(w_scale, _f32, n, "w_scale"), n, k, op, kind, ld, wsp,
+                       bytes_, _raw_stream(a.get_device()))
     if rc:
         _check(rc, "gemm_w8a8")
     return out
 
 
-def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, scales=None):
+def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, scales=None, workspace=None):
     """x bf16 [m, k] (row stride allowed), quantised to int8 with a scale for each token, times w (int8 [n, k], w_scale
-    fp32 [n]; from int8_quantize of the weight).  codes, scales: where x's are left (allocated if None)."""
+    fp32 [n]; from int8_quantize of the weight).  codes, scales: where x's are left (allocated if None); workspace as in
+    gemm_w8a8."""
     lib = _lib or load()
     xp, ld_x, k = _rows(x, _bf16, None, None, "x")
     m = x.shape[0]
@@ -949,9 +964,10 @@ def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, s
         scales = x.new_empty(m, dtype=_f32)
     cp, _, _ = _codes8(codes, m, k, "codes")
     out, op, ld, kind = _int8_out(x, m, n, out_dtype, out)
-    _one_device(x, w, w_scale, codes, scales, out)
+    workspace, wsp, bytes_ = _int8_workspace(lib, x, m, n, k, workspace)
+    _one_device(x, w, w_scale, codes, scales, out, workspace)
     rc = lib.int8_linear(xp, m, k, ld_x, cp, _vec(scales, _f32, m, "scales"), wp, _vec(w_scale, _f32, n, "w_scale"), n, op, kind,
-                         ld, _raw_stream(x.get_device()))
+                         ld, wsp, bytes_, _raw_stream(x.get_device()))
     if rc:
         _check(rc, "int8_linear")
     return out

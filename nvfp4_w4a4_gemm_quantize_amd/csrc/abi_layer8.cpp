@@ -171,13 +171,14 @@ int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, i
 }
 
 static Int8Args int8_args(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n,
-                          int64_t k, void* out, int out_dtype, int64_t ld_out) {
+                          int64_t k, void* out, int out_dtype, int64_t ld_out, void* workspace) {
   Int8Args g{};
   g.a = a;
   g.a_scale = a_scale;
   g.w = w;
   g.w_scale = w_scale;
   g.out = out;
+  g.workspace = workspace;
   g.m = m;
   g.n = n;
   g.k = k;
@@ -186,22 +187,30 @@ static Int8Args int8_args(const int8_t* a, const float* a_scale, int64_t m, cons
   return g;
 }
 
+size_t gemm_w8a8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return validate_w8a8_sizes(m, n, k) ? 0 : int8_workspace_bytes(m, n, k);
+}
+
 int gemm_w8a8(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n, int64_t k,
-              void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream) {
-  const int rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out);
+              void* out, int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+  const int rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace, workspace_bytes,
+                                    gemm_w8a8_workspace_bytes(m, n, k));
   if (rc || m == 0) return rc;
-  return hip_status(launch_gemm_w8a8(int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out), (hipStream_t)stream));
+  return hip_status(launch_gemm_w8a8(int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace),
+                                     (hipStream_t)stream));
 }
 
 int int8_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ld_x, int8_t* a, float* a_scale, const int8_t* w,
-                const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, nvfp4_stream_t stream) {
+                const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, void* workspace,
+                size_t workspace_bytes, nvfp4_stream_t stream) {
   int rc = validate_int8_quantize(x, m, k, ld_x, a, a_scale);
   if (rc) return rc;
-  rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out);
+  rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace, workspace_bytes,
+                          gemm_w8a8_workspace_bytes(m, n, k));
   if (rc || m == 0) return rc;
-  const hipError_t e = launch_int8_quantize(x, m, k, ld_x, a, a_scale, (hipStream_t)stream);
-  if (e != hipSuccess) return hip_status(e);
-  return hip_status(launch_gemm_w8a8(int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out), (hipStream_t)stream));
+  return hip_status(launch_int8_linear(x, ld_x, a, a_scale,
+                                       int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace),
+                                       (hipStream_t)stream));
 }
 
 }  // extern "C"

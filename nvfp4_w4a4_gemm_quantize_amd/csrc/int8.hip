@@ -6,6 +6,7 @@
 #include <hip/hip_bf16.h>
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kernels.h"
@@ -77,28 +78,30 @@ __device__ __forceinline__ u32x2 codes8(const u32x4& w, float by) {
 // ------------------------------------------------------------- quantise ----
 //
 // A wave or a workgroup a row: its largest magnitude, then its codes.  Bound by HBM: 3
-// bytes an element; the row's first kHeld x THREADS x 8 values stay in registers between
-// the two, the rest (rows beyond 16384) is read again from the caches.
-template <int THREADS>
-__global__ __launch_bounds__(256) void int8_quantize_kernel(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
-                                                            int8_t* codes, float* scales) {
-  constexpr int kHeld = 8, ROWS = 256 / THREADS;
-  __shared__ uint32_t tops[4];
+// bytes an element; the row's first HELD x THREADS x 8 values stay in registers between
+// the two, the rest is read again from the caches.
+template <int THREADS, int HELD>
+__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void int8_quantize_kernel(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
+                                                            int8_t* codes, float* scales, uint32_t* clear, int clears) {
+  // for the product behind
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < clears; i += gridDim.x * blockDim.x) clear[i] = 0;
+  constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, ROWS = BLOCK / THREADS;
+  __shared__ uint32_t tops[BLOCK / 64];
   const int tid = threadIdx.x % THREADS;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
   if (THREADS < 256 && row >= rows) return;
   const uint16_t* p = x + row * ld;
   const int64_t pieces = cols / 8;
-  u32x4 held[kHeld];
+  u32x4 held[HELD];
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int64_t at = tid + i * THREADS;
     held[i] = at < pieces ? *(const u32x4*)(p + at * 8) : u32x4{0u, 0u, 0u, 0u};
   }
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) top = max(top, magnitude(held[i]));
-  for (int64_t at = tid + kHeld * THREADS; at < pieces; at += THREADS) top = max(top, magnitude(*(const u32x4*)(p + at * 8)));
+  for (int i = 0; i < HELD; ++i) top = max(top, magnitude(held[i]));
+  for (int64_t at = tid + HELD * THREADS; at < pieces; at += THREADS) top = max(top, magnitude(*(const u32x4*)(p + at * 8)));
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
   if (THREADS > 64) {
@@ -110,51 +113,67 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const uint16_t* x, i
   const RowScale s = row_scale(top);
   int8_t* c = codes + row * cols;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int64_t at = tid + i * THREADS;
     if (at < pieces) *(u32x2*)(c + at * 8) = codes8(held[i], s.by);
   }
-  for (int64_t at = tid + kHeld * THREADS; at < pieces; at += THREADS)
+  for (int64_t at = tid + HELD * THREADS; at < pieces; at += THREADS)
     *(u32x2*)(c + at * 8) = codes8(*(const u32x4*)(p + at * 8), s.by);
   if (tid == 0) scales[row] = s.scale;
 }
 
+namespace {
+
+hipError_t quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, float* scales, uint32_t* clear,
+                    int clears, hipStream_t st) {
+  const unsigned four = (unsigned)((rows + 3) / 4);
+  if (rows >= 256 && cols <= 4096)
+    int8_quantize_kernel<64, 8><<<four, 256, 0, st>>>(x, rows, cols, ld, codes, scales, clear, clears);
+  else if (rows >= 1024 && cols <= 8192)
+    int8_quantize_kernel<64, 16><<<four, 256, 0, st>>>(x, rows, cols, ld, codes, scales, clear, clears);
+  else if (rows >= 256 || cols <= 2048)
+    int8_quantize_kernel<256, 8><<<(unsigned)rows, 256, 0, st>>>(x, rows, cols, ld, codes, scales, clear, clears);
+  else
+    int8_quantize_kernel<1024, 4><<<(unsigned)rows, 1024, 0, st>>>(x, rows, cols, ld, codes, scales, clear, clears);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, float* scales,
                                 hipStream_t st) {
-  if (cols <= 4096 && rows >= 1024)
-    int8_quantize_kernel<64><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(x, rows, cols, ld, codes, scales);
-  else
-    int8_quantize_kernel<256><<<(unsigned)rows, 256, 0, st>>>(x, rows, cols, ld, codes, scales);
-  return hipGetLastError();
+  return quantize(x, rows, cols, ld, codes, scales, nullptr, 0, st);
 }
 
 // ---------------------------------------------------------------- tiles ----
 //
-// Output tile BM tokens x BN channels; k in stages of 64 bytes of every row, which pass
-// through LDS four stages deep by direct loads (global_load_lds: no registers, no VALU).
-// The waves split the tile into MF x NF fragments of 32 x 32 each; a stage is two
-// products of 32 k.  v_mfma_i32_32x32x32_i8 takes W's rows as its rows and the tokens as
+// Output tile BM tokens x BN channels; k in stages of 128 bytes of every row, which pass
+// through LDS several stages deep by direct loads (global_load_lds: no registers, no
+// VALU).  Whole lines: with stages of 64 bytes such a load took twice as long, and they
+// bounded the kernel (4096 x 17408 x 5120: 367 us).  The waves split the tile into MF x NF
+// fragments of 32 x 32 each; a stage is four products of 32 k.  v_mfma_i32_32x32x32_i8 takes W's rows as its rows and the tokens as
 // its columns, so that a lane ends with one token and runs of four channels.
 //
-// LDS layout of a stage: [rows][64] bytes, the 16-byte pieces of row r permuted by
-// (r >> 2) & 3: sixteen lanes that read one piece of sixteen rows meet all banks once.
+// LDS layout of a stage: [rows][128] bytes, the 16-byte pieces of row r permuted by
+// (r >> 1) & 7: sixteen lanes that read one piece of sixteen rows meet all banks once.
 // The permutation is made by the loads' source addresses.
 //
 // Rows past m and n repeat the last one (their products are not stored).  A last stage
 // that is not full goes through registers, zero-filled, after the others.
 namespace {
 
-constexpr int kStageBytes = 64;   // of a row
-constexpr int kStages = 4;
+constexpr int kStageBytes = 128;   // of a row
 
-template <int MF, int NF, int WM, int WN>
+template <int MF, int NF, int WM, int WN, int STAGES>
 struct TileShape {
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int BM = 32 * MF * WM, BN = 32 * NF * WN;
   static constexpr int ROWS = BM + BN;                  // tokens, then channels
   static constexpr int STAGE = ROWS * kStageBytes;
-  static constexpr int LOADS = ROWS / 16 / WAVES;       // direct loads of a wave a stage, 16 rows each
-  static_assert(ROWS % (16 * WAVES) == 0, "");
+  static constexpr int LOADS = ROWS / 8 / WAVES;        // direct loads of a wave a stage, 8 rows each
+  static constexpr int TURN = WAVES * 32 * (32 * NF + 4) * 4;   // the epilogue's bytes
+  static constexpr int LDS = STAGES * STAGE > TURN ? STAGES * STAGE : TURN;
+  static_assert(ROWS % (8 * WAVES) == 0 && WAVES % 2 == 0 && STAGES >= 2, "");
 };
 
 // Global -> LDS copy of 16 bytes a lane: lane l's bytes land at dst + 16 l, read from
@@ -169,43 +188,75 @@ template <int N>
 __device__ __forceinline__ void wait_arrived() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
+// This wave's LDS reads have arrived.
+__device__ __forceinline__ void wait_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
-}  // namespace
+// Which tile workgroup b of `count` takes.  The hardware deals workgroups to the eight
+// XCDs in turn; each gets a contiguous run of the order, which goes through groups of
+// eight tile columns row by row, so that the tiles which an XCD holds at once read few
+// rows of a and of w through its L2.
+constexpr int kXcds = 8, kGroupCols = 8;
+__device__ __forceinline__ int xcd_order(int b, int count) {
+  const int x = b % kXcds, each = count / kXcds, rest = count % kXcds;
+  return x * each + min(x, rest) + b / kXcds;
+}
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
+  const int group = t / (kGroupCols * tiles_m), in = t - group * kGroupCols * tiles_m;
+  const int width = min(kGroupCols, tiles_n - group * kGroupCols);
+  return TileAt{in / width, group * kGroupCols + in % width};
+}
 
-template <int MF, int NF, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, int tiles_m, int tiles_n) {
-  using S = TileShape<MF, NF, WM, WN>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages][S::STAGE];
+// Parts of a sum that other workgroups add to: as device-scope atomics, which pass the
+// L2 that an XCD keeps for itself.
+__device__ __forceinline__ void store_shared(int* p, int x, int y) {
+  __hip_atomic_store((uint64_t*)p, (uint64_t)(uint32_t)y << 32 | (uint32_t)x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t load_shared(const int* p) {
+  return __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Channels [n0, n0 + BN) of tokens [m0, m0 + BM), stages [begin, end) of k.  With parts
+// of k in several workgroups (splits > 1) all of a tile's leave their sums at `part`
+// and the one that counts itself last at `arrived` adds them up: whole numbers, whose
+// order does not matter.
+template <int MF, int NF, int WM, int WN, int STAGES>
+__device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t n0, int begin, int end, int split, int splits,
+                                          int* part, uint32_t* arrived, uint8_t* lds) {
+  using S = TileShape<MF, NF, WM, WN, STAGES>;
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wave_m = wave / WN, wave_n = wave % WN;
-  const int tile = blockIdx.x;
-  const int bm = tile % tiles_m, bn = tile / tiles_m;
-  const int64_t m0 = (int64_t)bm * S::BM, n0 = (int64_t)bn * S::BN;
   const int64_t k = a.k;
-  const int full = (int)(k / kStageBytes);
+  const int full = min(end, (int)(k / kStageBytes)) - begin;
 
-  // this wave's loads: 16 rows of the stage each, lane = row * 4 + place of a piece
+  // this wave's loads: 8 rows of the stage each, lane = row * 8 + place of a piece (rows
+  // 8 i of waves of one parity have the same permutation)
   const int8_t* base[S::LOADS];
   uint32_t voff[S::LOADS];
-  const int lane_row = lane >> 2, piece = (lane & 3) ^ ((lane_row >> 2) & 3);
+  const int lane_row = lane >> 3, piece = (lane & 7) ^ ((wave * 4 + (lane_row >> 1)) & 7);
 #pragma unroll
   for (int i = 0; i < S::LOADS; ++i) {
-    const int row = (i * S::WAVES + wave) * 16;
+    const int row = (i * S::WAVES + wave) * 8;
     const bool tokens = row < S::BM;
     const int64_t first = tokens ? m0 + row : n0 + row - S::BM, last = (tokens ? a.m : a.n) - 1;
     const int64_t from = min(first, last);
-    base[i] = (tokens ? a.a : a.w) + from * k;
+    base[i] = (tokens ? a.a : a.w) + from * k + (int64_t)begin * kStageBytes;
     voff[i] = (uint32_t)(min((int64_t)lane_row, last - from) * k) + piece * 16;
   }
-  auto issue = [&](int stage) {
+  auto slot = [&](int s) { return lds + (uint32_t)s % STAGES * S::STAGE; };
+  auto issue_one = [&](int s, int i) {
+    dma16(base[i] + (int64_t)s * kStageBytes, voff[i], slot(s) + (i * S::WAVES + wave) * 1024);
+  };
+  auto issue = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < S::LOADS; ++i)
-      dma16(base[i] + (int64_t)stage * kStageBytes, voff[i], lds[stage % kStages] + (i * S::WAVES + wave) * 1024);
+    for (int i = 0; i < S::LOADS; ++i) issue_one(s, i);
   };
 
   i32x16 acc[MF][NF];
@@ -216,12 +267,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, 
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  const int lane_at = c32 * kStageBytes + ((h ^ ((c32 >> 2) & 3)) * 16);
+  const int lane_at = c32 * kStageBytes + ((h ^ ((c32 >> 1) & 7)) * 16);
   struct Fragments {
     i32x4 a[MF], w[NF];
   };
-  auto read = [&](Fragments& f, const uint8_t* stage, int half) {
-    const uint8_t* p = stage + (lane_at ^ (half * 32));
+  auto read = [&](Fragments& f, const uint8_t* stage, int quarter) {
+    const uint8_t* p = stage + (lane_at ^ (quarter * 32));
 #pragma unroll
     for (int i = 0; i < MF; ++i) f.a[i] = *(const i32x4*)(p + (wave_m * MF + i) * 32 * kStageBytes);
 #pragma unroll
@@ -234,59 +285,133 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, 
       for (int j = 0; j < NF; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[j], f.a[i], acc[i][j], 0, 0, 0);
   };
 
-  // Half 0 of a stage is read while half 1 of the stage before is multiplied, and half 1
-  // while half 0 is; the stage that three stages on will be needed is asked for behind the
-  // barrier, when all have read the one whose place it takes.
+  // A quarter of a stage is read while the one before is multiplied.  Before the last of
+  // them all have read the whole stage: behind that barrier its place is filled anew, and
+  // the next stage, waited for before it, is there for all.
   Fragments f0, f1;
   if (full > 0) {
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
+    for (int s = 0; s < STAGES - 1; ++s)
       if (s < full) issue(s);
-    if (full >= kStages - 1) wait_arrived<(kStages - 2) * S::LOADS>(); else wait_arrived<0>();
+    if (full >= STAGES) {
+#pragma unroll
+      for (int i = 0; i < S::LOADS / 2; ++i) issue_one(STAGES - 1, i);
+      wait_arrived<(STAGES - 2) * S::LOADS + S::LOADS / 2>();
+    } else {
+      wait_arrived<0>();
+    }
     stage_barrier();
-    read(f0, lds[0], 0);
-#pragma unroll 1
-    for (int s = 0; s < full; ++s) {
-      read(f1, lds[s % kStages], 1);
-      multiply(f0);
-      if (s + kStages - 1 < full) {
-        wait_arrived<(kStages - 3) * S::LOADS>();
-      } else {
-        wait_arrived<0>();
+    read(f0, slot(0), 0);
+    // products of a quarter with loads `first` .. `last` - 1 of stage `of` spread among them
+    auto multiply_and_issue = [&](const Fragments& f, int of, auto first, auto last) {
+      constexpr int FIRST = decltype(first)::value, COUNT = decltype(last)::value - FIRST, ALL = MF * NF;
+#pragma unroll
+      for (int e = 0; e < ALL; ++e) {
+        acc[e / NF][e % NF] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[e % NF], f.a[e / NF], acc[e / NF][e % NF], 0, 0, 0);
+#pragma unroll
+        for (int i = e * COUNT / ALL; i < (e + 1) * COUNT / ALL; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          issue_one(of, FIRST + i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+    };
+    constexpr std::integral_constant<int, 0> kNone{};
+    constexpr std::integral_constant<int, S::LOADS / 2> kHalf{};
+    constexpr std::integral_constant<int, S::LOADS> kAll{};
+    int s = 0;
+#pragma unroll 1
+    for (; s + STAGES < full; ++s) {
+      read(f1, slot(s), 1);
+      multiply_and_issue(f0, s + STAGES - 1, kHalf, kAll);
+      read(f0, slot(s), 2);
+      multiply(f1);
+      read(f1, slot(s), 3);
+      multiply(f0);
+      wait_arrived<(STAGES - 2) * S::LOADS>();
+      wait_read();
       stage_barrier();
-      if (s + kStages - 1 < full) issue(s + kStages - 1);
-      if (s + 1 < full) read(f0, lds[(s + 1) % kStages], 0);
+      read(f0, slot(s + 1), 0);
+      multiply_and_issue(f1, s + STAGES, kNone, kHalf);
+    }
+    if (full >= STAGES) {
+#pragma unroll
+      for (int i = S::LOADS / 2; i < S::LOADS; ++i) issue_one(s + STAGES - 1, i);
+    }
+#pragma unroll 1
+    for (; s < full; ++s) {
+      read(f1, slot(s), 1);
+      multiply(f0);
+      read(f0, slot(s), 2);
+      multiply(f1);
+      read(f1, slot(s), 3);
+      multiply(f0);
+      wait_arrived<0>();
+      stage_barrier();
+      if (s + 1 < full) read(f0, slot(s + 1), 0);
       multiply(f1);
     }
   }
-  if (k % kStageBytes) {   // the last pieces of the rows, the others 0
+  if (end > begin + full) {   // the last pieces of the rows, the others 0
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < S::LOADS; ++i) {
-      const bool in = (int64_t)full * kStageBytes + piece * 16 < k;
-      *(u32x4*)(lds[0] + (i * S::WAVES + wave) * 1024 + lane * 16) =
+      const bool in = (int64_t)(begin + full) * kStageBytes + piece * 16 < k;
+      *(u32x4*)(lds + (i * S::WAVES + wave) * 1024 + lane * 16) =
           in ? *(const u32x4*)(base[i] + (int64_t)full * kStageBytes + voff[i]) : u32x4{0u, 0u, 0u, 0u};
     }
     __syncthreads();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      read(f0, lds[0], half);
+    for (int quarter = 0; quarter < 4; ++quarter) {
+      read(f0, lds, quarter);
       multiply(f0);
+    }
+  }
+
+  if (splits > 1) {
+    constexpr int kEach = MF * NF * 16 * 64;   // numbers of a wave
+    int* mine = part + ((int64_t)split * S::WAVES + wave) * kEach + 2 * lane;
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) store_shared(mine + ((i * NF + j) * 16 + e) * 64, acc[i][j][e], acc[i][j][e + 1]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the parts have been acknowledged
+    __syncthreads();
+    uint32_t* last = (uint32_t*)lds;
+    if (tid == 0) *last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const bool join = *last == (uint32_t)(splits - 1);
+    __syncthreads();
+    if (!join) return;
+    for (int other = 0; other < splits; ++other) {
+      if (other == split) continue;
+      const int* theirs = part + ((int64_t)other * S::WAVES + wave) * kEach + 2 * lane;
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const uint64_t v = load_shared(theirs + ((i * NF + j) * 16 + e) * 64);
+            acc[i][j][e] += (int)(uint32_t)v;
+            acc[i][j][e + 1] += (int)(uint32_t)(v >> 32);
+          }
     }
   }
 
   // Epilogue: a wave turns 32 tokens x 32 NF channels at a time through its own part of
   // LDS (the stages are done with), so that rows leave in whole runs.
   constexpr int COLS = 32 * NF, LD = COLS + 4;
-  static_assert(S::WAVES * 32 * LD * 4 <= kStages * S::STAGE, "");
-  float* turn = (float*)&lds[0][0] + wave * 32 * LD;
+  float* turn = (float*)lds + wave * 32 * LD;
   __syncthreads();
   const int64_t col0 = n0 + wave_n * COLS;
   const bool wide = a.out_bf16 ? a.ld_out % 8 == 0 && ((uintptr_t)a.out & 15) == 0 : a.ld_out % 4 == 0 && ((uintptr_t)a.out & 15) == 0;
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
     const int64_t row0 = m0 + (wave_m * MF + i) * 32;
+    if (row0 >= a.m || col0 >= a.n) break;
     const float s = row0 + c32 < a.m ? a.a_scale[row0 + c32] : 0.f;
 #pragma unroll
     for (int j = 0; j < NF; ++j)
@@ -316,133 +441,326 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, 
         }
       }
     } else {
-      for (int e = lane; e < 32 * COLS; e += 64) {
-        const int r = e / COLS, c = e % COLS;
-        if (row0 + r >= a.m || col0 + c >= a.n) continue;
-        const float y = turn[r * LD + c] * a.w_scale[col0 + c];
-        const int64_t at = (row0 + r) * a.ld_out + col0 + c;
-        if (a.out_bf16)
-          ((uint16_t*)a.out)[at] = (uint16_t)pack_bf16(y, 0.f);
-        else
-          ((float*)a.out)[at] = y;
+      const int c = lane % COLS;               // a lane a channel
+      const int64_t col = min(col0 + c, a.n - 1);
+      const float t = a.w_scale[col];
+#pragma unroll 8
+      for (int r0 = 0; r0 < 32; r0 += 64 / COLS) {
+        const int r = r0 + lane / COLS;
+        const float y = turn[r * LD + c] * t;
+        if (row0 + r < a.m && col0 + c < a.n) {
+          const int64_t at = (row0 + r) * a.ld_out + col;
+          if (a.out_bf16)
+            ((uint16_t*)a.out)[at] = (uint16_t)pack_bf16(y, 0.f);
+          else
+            ((float*)a.out)[at] = y;
+        }
       }
     }
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-namespace {
+}  // namespace
 
-template <int MF, int NF, int WM, int WN>
-hipError_t launch_tiles(const Int8Args& a, hipStream_t st) {
-  using S = TileShape<MF, NF, WM, WN>;
-  const int64_t tm = (a.m + S::BM - 1) / S::BM, tn = (a.n + S::BN - 1) / S::BN;
-  int8_tile_kernel<MF, NF, WM, WN><<<(unsigned)(tm * tn), S::THREADS, 0, st>>>(a, (int)tm, (int)tn);
-  return hipGetLastError();
+template <int MF, int NF, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, int tiles_m, int tiles_n) {
+  using S = TileShape<MF, NF, WM, WN, STAGES>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  // the parts of a tile's k lie an XCD's run of tiles apart, so that parts of neighbouring
+  // tiles, which read the same rows, meet in one L2
+  const int tiles = tiles_m * tiles_n, order = xcd_order(blockIdx.x, tiles * a.splits);
+  const int split = order / tiles, tile = order - split * tiles;
+  const TileAt at = tile_at(tile, tiles_m, tiles_n);
+  const int stages = (int)((a.k + kStageBytes - 1) / kStageBytes);
+  const int begin = (int)((int64_t)stages * split / a.splits), end = (int)((int64_t)stages * (split + 1) / a.splits);
+  int8_tile<MF, NF, WM, WN, STAGES>(a, (int64_t)at.m * S::BM, (int64_t)at.n * S::BN, begin, end, split, a.splits,
+                                    a.parts + (int64_t)tile * a.splits * S::BM * S::BN, a.arrived + tile, lds);
 }
 
-}  // namespace
+// 256 x 256 tiles, one a CU, and the last ones, which would not fill the chip once more,
+// as four of 128 x 128 each.
+__global__ __launch_bounds__(512, 2) void int8_large_kernel(Int8Args a, int tiles_m, int tiles_n, int whole) {
+  using L = TileShape<4, 2, 2, 4, 2>;
+  using Q = TileShape<2, 1, 2, 4, 4>;
+  static_assert(L::BM == 2 * Q::BM && L::BN == 2 * Q::BN && L::LDS >= Q::LDS, "");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[L::LDS];
+  const int stages = (int)((a.k + kStageBytes - 1) / kStageBytes);
+  const int b = blockIdx.x;
+  if (b < whole) {
+    const int order = xcd_order(b, whole);
+    const TileAt at = tile_at(order, tiles_m, tiles_n);
+    int8_tile<4, 2, 2, 4, 2>(a, (int64_t)at.m * L::BM, (int64_t)at.n * L::BN, 0, stages, 0, 1, nullptr, nullptr, lds);
+  } else {
+    const int order = xcd_order(b - whole, (tiles_m * tiles_n - whole) * 4);
+    const TileAt at = tile_at(whole + order / 4, tiles_m, tiles_n);
+    const int64_t m0 = (int64_t)at.m * L::BM + (order & 1) * Q::BM, n0 = (int64_t)at.n * L::BN + (order >> 1 & 1) * Q::BN;
+    if (m0 >= a.m || n0 >= a.n) return;
+    int8_tile<2, 1, 2, 4, 4>(a, m0, n0, 0, stages, 0, 1, nullptr, nullptr, lds);
+  }
+}
 
 // --------------------------------------------------------------- stream ----
 //
-// Few tokens (up to 64): bound by the weights' bytes, so these go from HBM straight into
-// registers as operands of v_mfma_i32_16x16x64_i8, whose rows are 16 channels and whose
-// columns 16 tokens.  A workgroup owns 16 channels, its waves take k in parts (stages of 64
-// bytes of every row) and add their sums in LDS.
+// A few tokens: bound by the weights' bytes, so these go from HBM straight into registers
+// as operands of v_mfma_i32_16x16x64_i8, whose rows are 16 channels and whose columns 16
+// tokens; the tokens' codes lie in LDS.  A workgroup owns 16 channels, its waves take k in
+// parts (stages of 64 bytes of every row, eight of them in flight and eight more asked for)
+// and add their sums in LDS.
+//
+// QUANTISE: every workgroup finds the scales and codes itself while its first weights are
+// on their way, which spares a launch; the first one writes them out.
 namespace {
 
-constexpr int kStreamTokens = 64;
+constexpr int kStreamCodes = 40960;   // bytes of codes in LDS: four workgroups a CU
+constexpr int kStreamTokens = 16;
+constexpr int kQuantiseHeld = 8;      // pieces of eight values a thread holds: up to 16384 values in all
+
+// Bytes from a token's codes to the next one's: sixteen more than k, which moves the tokens
+// that a read takes together to different banks.
+__host__ __device__ inline int stream_row(int64_t k) { return (int)k + 16; }
 
 }  // namespace
 
-template <int MF, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void int8_stream_kernel(Int8Args a) {
-  constexpr int kAtOnce = MF == 1 ? 8 : 4;   // stages in flight
-  __shared__ int part[WAVES][MF][16][17];
+template <int WAVES, bool QUANTISE>
+__global__ __launch_bounds__(64 * WAVES) void int8_stream_kernel(Int8Args a, const uint16_t* x, int64_t ld_x, int8_t* codes_out,
+                                                                 float* scales_out) {
+  constexpr int N = 8, THREADS = 64 * WAVES;
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // [m][stream_row(k)]
+  __shared__ int part[WAVES][16][17];
+  __shared__ float scales[kStreamTokens];
+  __shared__ uint32_t tops[kStreamTokens];
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * 16, k = a.k;
-  const int stages = (int)((k + 63) / 64);
-  const int s0 = stages * wave / WAVES, s1 = stages * (wave + 1) / WAVES;
-  const int8_t* w = a.w + min(n0 + c16, a.n - 1) * k + g * 16;
-  const int8_t* x[MF];
+  const int m = (int)a.m, k = (int)a.k, row = stream_row(k);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int stages = (k + 63) / 64;
+  const int s0 = stages * wave / WAVES, count = stages * (wave + 1) / WAVES - s0, groups = (count + N - 1) / N;
+  const int8_t* w = a.w + min(n0 + c16, a.n - 1) * (int64_t)k;
+  // stage s0 + u of the rows, clamped to their last pieces: what is no stage of this wave,
+  // or lies behind the row's end, is multiplied by 0
+  auto at = [&](int u) { return min((s0 + u) * 64 + g * 16, k - 16); };
+  auto load = [&](i32x4 (&f)[N], int group) {
 #pragma unroll
-  for (int i = 0; i < MF; ++i) x[i] = a.a + min((int64_t)(i * 16 + c16), a.m - 1) * k + g * 16;
-  i32x4 acc[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) acc[i] = i32x4{0, 0, 0, 0};
-  const int whole = k % 64 ? min(s1, stages - 1) : s1;   // stages of all 64 bytes
-  int s = s0;
-  auto step = [&](auto count) {
-    constexpr int N = decltype(count)::value;
-    i32x4 wf[N], xf[MF][N];
-#pragma unroll
-    for (int u = 0; u < N; ++u) wf[u] = *(const i32x4*)(w + (int64_t)(s + u) * 64);
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-#pragma unroll
-      for (int i = 0; i < MF; ++i) xf[i][u] = *(const i32x4*)(x[i] + (int64_t)(s + u) * 64);
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-#pragma unroll
-      for (int i = 0; i < MF; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[u], xf[i][u], acc[i], 0, 0, 0);
-    s += N;
+    for (int u = 0; u < N; ++u) f[u] = *(const i32x4*)(w + at(group * N + u));
   };
-  while (s + kAtOnce <= whole) step(std::integral_constant<int, kAtOnce>{});
-  while (s < whole) step(std::integral_constant<int, 1>{});
-  if (s < s1) {   // the last stage of rows that end inside one
-    const bool in = (int64_t)s * 64 + g * 16 < k;
-    const i32x4 zero = {0, 0, 0, 0}, wf = in ? *(const i32x4*)(w + (int64_t)s * 64) : zero;
+  i32x4 even[N], odd[N];
+  if (groups > 0) load(even, 0);
+  if (groups > 1) load(odd, 1);
+
+  if (QUANTISE) {
+    const int pieces = m * k / 8, each = k / 8;
+    u32x4 held[kQuantiseHeld];
+    uint32_t top = 0;
+    if (tid < kStreamTokens) tops[tid] = 0;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf, in ? *(const i32x4*)(x[i] + (int64_t)s * 64) : zero, acc[i], 0, 0, 0);
+    for (int i = 0; i < kQuantiseHeld; ++i) {
+      const int p = tid + i * THREADS;
+      held[i] = u32x4{0u, 0u, 0u, 0u};
+      if (p < pieces) {
+        const int t = m == 1 ? 0 : p / each;
+        held[i] = *(const u32x4*)(x + t * ld_x + (p - t * each) * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantiseHeld; ++i) {
+      const int p = tid + i * THREADS;
+      if (m == 1)
+        top = max(top, magnitude(held[i]));
+      else if (p < pieces)
+        atomicMax(&tops[p / each], magnitude(held[i]));
+    }
+    if (m == 1) {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+      if (lane == 0) atomicMax(&tops[0], top);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQuantiseHeld; ++i) {
+      const int p = tid + i * THREADS;
+      if (p >= pieces) break;
+      const int t = m == 1 ? 0 : p / each, c = (p - t * each) * 8;
+      const u32x2 q = codes8(held[i], row_scale(tops[t]).by);
+      *(u32x2*)(codes + t * row + c) = q;
+      if (blockIdx.x == 0) *(u32x2*)(codes_out + (int64_t)t * k + c) = q;
+    }
+    if (tid < m) {
+      scales[tid] = row_scale(tops[tid]).scale;
+      if (blockIdx.x == 0) scales_out[tid] = scales[tid];
+    }
+  } else {
+    const int each = k / 16;
+    for (int p = tid; p < m * each; p += THREADS) {
+      const int t = p / each, c = (p - t * each) * 16;
+      *(u32x4*)(codes + t * row + c) = *(const u32x4*)(a.a + (int64_t)t * k + c);
+    }
+    if (tid < m) scales[tid] = a.a_scale[tid];
+  }
+  __syncthreads();
+
+  const uint8_t* mine = codes + min(c16, m - 1) * row;
+  i32x4 acc = {0, 0, 0, 0};
+  auto multiply = [&](i32x4 (&f)[N], int group) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int s = group * N + u;
+      i32x4 c = *(const i32x4*)(mine + at(s));
+      if (s >= count || (s0 + s) * 64 + g * 16 >= k) c = i32x4{0, 0, 0, 0};
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[u], c, acc, 0, 0, 0);
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < groups; i += 2) {
+    multiply(even, i);
+    if (i + 2 < groups) load(even, i + 2);
+    if (i + 1 < groups) multiply(odd, i + 1);
+    if (i + 3 < groups) load(odd, i + 3);
   }
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) part[wave][i][c16][4 * g + r] = acc[i][r];
+  for (int r = 0; r < 4; ++r) part[wave][c16][4 * g + r] = acc[r];
   __syncthreads();
-  for (int e = tid; e < MF * 256; e += 64 * WAVES) {
+  for (int e = tid; e < m * 16; e += THREADS) {
     const int token = e / 16, c = e % 16;
-    if (token >= a.m || n0 + c >= a.n) continue;
+    if (n0 + c >= a.n) continue;
     int sum = 0;
 #pragma unroll
-    for (int v = 0; v < WAVES; ++v) sum += part[v][token / 16][token % 16][c];
-    const float y = (float)sum * a.a_scale[token] * a.w_scale[n0 + c];
-    const int64_t at = token * a.ld_out + n0 + c;
+    for (int v = 0; v < WAVES; ++v) sum += part[v][token][c];
+    const float y = (float)sum * scales[token] * a.w_scale[n0 + c];
+    const int64_t to = token * a.ld_out + n0 + c;
     if (a.out_bf16)
-      ((uint16_t*)a.out)[at] = (uint16_t)pack_bf16(y, 0.f);
+      ((uint16_t*)a.out)[to] = (uint16_t)pack_bf16(y, 0.f);
     else
-      ((float*)a.out)[at] = y;
+      ((float*)a.out)[to] = y;
   }
 }
 
 namespace {
 
-template <int MF>
-hipError_t launch_stream(const Int8Args& a, hipStream_t st) {
+template <bool QUANTISE>
+hipError_t launch_stream(const Int8Args& a, const uint16_t* x, int64_t ld_x, int8_t* codes, float* scales, hipStream_t st) {
   const unsigned grid = (unsigned)((a.n + 15) / 16);
+  const size_t lds = (size_t)a.m * stream_row(a.k);
   if (grid >= 1024)
-    int8_stream_kernel<MF, 4><<<grid, 256, 0, st>>>(a);
+    int8_stream_kernel<4, QUANTISE><<<grid, 256, lds, st>>>(a, x, ld_x, codes, scales);
   else
-    int8_stream_kernel<MF, 8><<<grid, 512, 0, st>>>(a);
+    int8_stream_kernel<8, QUANTISE><<<grid, 512, lds, st>>>(a, x, ld_x, codes, scales);
+  return hipGetLastError();
+}
+
+// How a product is computed: by the streaming kernel, or in tiles of which kind and in how
+// many parts of k.
+enum Int8Kind { kStream, kTiles32, kTiles64, kTiles128, kTiles256, kTilesMany, kTiles64Square };
+struct Int8Plan {
+  Int8Kind kind;
+  int64_t bm, bn, tiles_m, tiles_n;
+  int splits;
+};
+void set_tiles(Int8Plan& p, int64_t m, int64_t n) {
+  p.bm = p.kind == kTiles32 ? 32 : p.kind == kTiles64 || p.kind == kTiles64Square ? 64 : p.kind == kTiles256 ? 256 : 128;
+  p.bn = p.kind == kTiles32 || p.kind == kTiles64Square ? 64 : p.kind == kTiles256 ? 256 : 128;
+  p.tiles_m = (m + p.bm - 1) / p.bm;
+  p.tiles_n = (n + p.bn - 1) / p.bn;
+}
+// Whether the streaming kernel takes it, and quantises too.
+bool streams(int64_t m, int64_t n, int64_t k) {
+  return m * k <= kStreamCodes && m <= (n * k <= 40000000 ? kStreamTokens : 4);
+}
+bool stream_quantises(int64_t m, int64_t k) { return m * k <= 8 * 256 * kQuantiseHeld; }
+
+Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
+  Int8Plan p{kStream, 0, 0, 0, 0, 1};
+  if (streams(m, n, k)) return p;
+  auto tiles_of = [&](Int8Kind kind) {
+    p.kind = kind;
+    set_tiles(p, m, n);
+    return p.tiles_m * p.tiles_n;
+  };
+  if (m <= 32)
+    tiles_of(kTiles32);
+  else if (tiles_of(kTiles256) < 110 && (m <= 64 || tiles_of(kTiles128) < 110) && tiles_of(kTiles64) < 110)
+    tiles_of(kTiles64Square);
+  else if (p.kind == kTiles128 && p.tiles_m * p.tiles_n > 256)
+    p.kind = kTilesMany;
+  const int64_t stages = (k + kStageBytes - 1) / kStageBytes;
+  if (p.kind != kTiles256) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(256 / (p.tiles_m * p.tiles_n), stages / 10));
+  return p;
+}
+
+size_t arrived_bytes(const Int8Plan& p) { return (size_t)(p.tiles_m * p.tiles_n * 4 + 255) / 256 * 256; }
+
+template <int MF, int NF, int WM, int WN, int STAGES>
+hipError_t launch_tiles(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
+  using S = TileShape<MF, NF, WM, WN, STAGES>;
+  const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * a.splits);
+  int8_tile_kernel<MF, NF, WM, WN, STAGES><<<grid, S::THREADS, 0, st>>>(a, (int)p.tiles_m, (int)p.tiles_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm_w8a8(const Int8Args& a, hipStream_t st) {
-  if (a.m <= kStreamTokens) {
-    switch ((a.m + 15) / 16) {
-      case 1: return launch_stream<1>(a, st);
-      case 2: return launch_stream<2>(a, st);
-      case 3: return launch_stream<3>(a, st);
-      default: return launch_stream<4>(a, st);
+size_t int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m == 0) return 0;
+  const Int8Plan p = plan_int8(m, n, k);
+  return p.splits == 1 ? 0 : arrived_bytes(p) + (size_t)(p.tiles_m * p.tiles_n * p.splits * p.bm * p.bn) * 4;
+}
+
+namespace {
+
+__global__ __launch_bounds__(256) void int8_clear_kernel(uint32_t* p, int count) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < count) p[i] = 0;
+}
+
+// The plan with its workspace; `clears` counters have to be 0 before it runs.
+Int8Args with_plan(const Int8Args& args, const Int8Plan& p, int* clears) {
+  Int8Args a = args;
+  a.splits = a.workspace ? p.splits : 1;
+  a.arrived = (uint32_t*)a.workspace;
+  a.parts = (int*)((uint8_t*)a.workspace + arrived_bytes(p));
+  *clears = a.splits > 1 ? (int)(p.tiles_m * p.tiles_n) : 0;
+  return a;
+}
+
+hipError_t product(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
+  switch (p.kind) {
+    case kStream: return launch_stream<false>(a, nullptr, 0, nullptr, nullptr, st);
+    case kTiles32: return launch_tiles<1, 1, 1, 2, 4>(a, p, st);
+    case kTiles64: return launch_tiles<1, 1, 2, 4, 4>(a, p, st);
+    case kTiles64Square: return launch_tiles<1, 1, 2, 2, 4>(a, p, st);
+    case kTiles128: return launch_tiles<1, 2, 4, 2, 4>(a, p, st);
+    case kTilesMany: return launch_tiles<2, 2, 2, 2, 2>(a, p, st);
+    default: {
+      // rounds of one tile a CU; the last one in quarters where that is shorter
+      const int tiles = (int)(p.tiles_m * p.tiles_n), rest = tiles % 256, whole = rest > 128 || tiles < 256 ? tiles : tiles - rest;
+      int8_large_kernel<<<(unsigned)(whole + 4 * (tiles - whole)), 512, 0, st>>>(a, (int)p.tiles_m, (int)p.tiles_n, whole);
+      return hipGetLastError();
     }
   }
-  // a tile of 256 x 256 reads half of what four of 128 x 128 read, where there are enough
-  const int64_t large = ((a.m + 255) / 256) * ((a.n + 255) / 256);
-  return large >= 256 ? launch_tiles<4, 2, 2, 4>(a, st) : launch_tiles<2, 2, 2, 2>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_w8a8(const Int8Args& args, hipStream_t st) {
+  const Int8Plan p = plan_int8(args.m, args.n, args.k);
+  int clears;
+  const Int8Args a = with_plan(args, p, &clears);
+  if (clears) {
+    int8_clear_kernel<<<(unsigned)((clears + 255) / 256), 256, 0, st>>>(a.arrived, clears);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return product(a, p, st);
+}
+
+hipError_t launch_int8_linear(const uint16_t* x, int64_t ld_x, int8_t* codes, float* scales, const Int8Args& args, hipStream_t st) {
+  const Int8Plan p = plan_int8(args.m, args.n, args.k);
+  if (p.kind == kStream && stream_quantises(args.m, args.k)) return launch_stream<true>(args, x, ld_x, codes, scales, st);
+  int clears;
+  const Int8Args a = with_plan(args, p, &clears);
+  const hipError_t e = quantize(x, a.m, a.k, ld_x, codes, scales, a.arrived, clears, st);
+  return e != hipSuccess ? e : product(a, p, st);
 }
 
 }  // namespace nvfp4

@@ -50,9 +50,17 @@ struct Int8Args {
   const int8_t* w;             // [n, k]
   const float* w_scale;        // [n]
   void* out;                   // [m, n], row stride ld_out
+  void* workspace;             // int8_workspace_bytes(m, n, k), or null: k is not split
   int64_t m, n, k, ld_out;
   int out_bf16;
+  // set by the launcher: parts of k, and where the workgroups of a tile count themselves and leave their sums
+  int splits;
+  uint32_t* arrived;
+  int* parts;
 };
+size_t int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_gemm_w8a8(const Int8Args& a, hipStream_t st);
+// x [g.m, g.k] quantised into codes and scales (g.a and g.a_scale), and the product.
+hipError_t launch_int8_linear(const uint16_t* x, int64_t ld_x, int8_t* codes, float* scales, const Int8Args& g, hipStream_t st);
 
 }  // namespace nvfp4

@@ -116,20 +116,28 @@ int validate_int8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld
   return !aligned(x, 16) || ld_x % 8 || !aligned(codes, 16) || !aligned(scales, 4) ? NVFP4_EALIGN : NVFP4_OK;
 }
 
-int validate_gemm_w8a8(const void* a, const void* a_scale, int64_t m, const void* w, const void* w_scale, int64_t n, int64_t k,
-                       const void* out, int out_dtype, int64_t ld_out) {
+int validate_w8a8_sizes(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n <= 0) return NVFP4_ESHAPE;
   const int rc = validate_int8_cols(k);
   if (rc) return rc;
+  // tiles are counted in 32 bits
+  return m > INT32_MAX || n > INT32_MAX || ((m + 63) / 64) * ((n + 63) / 64) > INT32_MAX / 64 ? NVFP4_EUNSUPPORTED : NVFP4_OK;
+}
+
+int validate_gemm_w8a8(const void* a, const void* a_scale, int64_t m, const void* w, const void* w_scale, int64_t n, int64_t k,
+                       const void* out, int out_dtype, int64_t ld_out, const void* workspace, size_t workspace_bytes,
+                       size_t needed) {
+  const int rc = validate_w8a8_sizes(m, n, k);
+  if (rc) return rc;
   if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_EINVAL;
   if (ld_out < n) return NVFP4_ESHAPE;
-  // tiles are counted in 32 bits
-  if (m > INT32_MAX || n > INT32_MAX || ((m + 127) / 128) * ((n + 127) / 128) > INT32_MAX) return NVFP4_EUNSUPPORTED;
   if (m == 0) return NVFP4_OK;
   if (!a || !a_scale || !w || !w_scale || !out) return NVFP4_EINVAL;
   const unsigned element = out_dtype == NVFP4_OUT_BF16 ? 2 : 4;
-  return !aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(out, element)
-             ? NVFP4_EALIGN : NVFP4_OK;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(out, element) ||
+      !aligned(workspace, 16))
+    return NVFP4_EALIGN;
+  return workspace && workspace_bytes < needed ? NVFP4_ESIZE : NVFP4_OK;
 }
 
 }  // namespace nvfp4

@@ -20,7 +20,9 @@ int validate_block_cache(const void* k_cache, const void* v_cache, int cache_dty
                          int num_kv_heads, int head_dim, int64_t page_stride, int64_t head_stride,
                          int64_t token_stride, const void* k_blocks, const void* v_blocks);
 int validate_int8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, const void* codes, const void* scales);
+int validate_w8a8_sizes(int64_t m, int64_t n, int64_t k);
 int validate_gemm_w8a8(const void* a, const void* a_scale, int64_t m, const void* w, const void* w_scale, int64_t n, int64_t k,
-                       const void* out, int out_dtype, int64_t ld_out);
+                       const void* out, int out_dtype, int64_t ld_out, const void* workspace, size_t workspace_bytes,
+                       size_t needed);
 
 }  // namespace nvfp4

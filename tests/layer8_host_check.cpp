@@ -47,9 +47,17 @@ hipError_t launch_int8_quantize(const uint16_t*, int64_t rows, int64_t cols, int
   g_quantize[2] = ld;
   return g_result;
 }
+size_t int8_workspace_bytes(int64_t, int64_t, int64_t) { return 700; }
 hipError_t launch_gemm_w8a8(const Int8Args& a, hipStream_t) {
   ++g_calls;
   g_int8 = a;
+  return g_result;
+}
+hipError_t launch_int8_linear(const uint16_t*, int64_t ld_x, int8_t* codes, float* scales, const Int8Args& a, hipStream_t) {
+  ++g_calls;
+  g_int8 = a;
+  g_quantize[2] = ld_x;
+  if (codes != a.a || scales != a.a_scale) exit(1);
   return g_result;
 }
 }  // namespace nvfp4
@@ -86,10 +94,10 @@ static int attention(int64_t tokens, int dtype, int heads, size_t bytes) {
                                 dtype, 6, 32, 2, 128, 8192, 4096, 128, dev<uint8_t>(0x30000), dev<uint8_t>(0x40000), dev<int32_t>(), 17, 20,
                                 0.5f, 33, dev<void>(), NVFP4_OUT_BF16 | NVFP4_OUT_CLEAR_PADDING, 1028, nullptr, dev<void>(), bytes, nullptr);
 }
-static int linear(int64_t m, int64_t k, int dtype) {
+static int linear(int64_t m, int64_t k, int dtype, size_t bytes = 700) {
   g_calls = 0;
   return int8_linear(dev<uint16_t>(), m, k, 2056, dev<int8_t>(), dev<float>(), dev<int8_t>(0x20000), dev<float>(0x30004), 99, dev<void>(), dtype,
-                     101, nullptr);
+                     101, dev<void>(0x70000), bytes, nullptr);
 }
 
 int main() {
@@ -135,7 +143,9 @@ int main() {
   CHECK(attention(10, NVFP4_CACHE_INT8_BLOCKS, 8, 999) == NVFP4_ESIZE && g_calls == 0);
   CHECK(attention(0, NVFP4_CACHE_INT8_BLOCKS, 8, 1000) == NVFP4_OK && g_calls == 0);
 
-  CHECK(linear(5, 2048, NVFP4_OUT_F32) == NVFP4_OK && g_calls >= 1);
+  CHECK(linear(5, 2048, NVFP4_OUT_F32) == NVFP4_OK && g_calls == 1 && g_quantize[2] == 2056 && g_int8.m == 5 && g_int8.k == 2048 &&
+        g_int8.n == 99 && g_int8.ld_out == 101 && g_int8.out_bf16 == 0 && g_int8.workspace == dev<void>(0x70000));
+  CHECK(linear(5, 2048, NVFP4_OUT_F32, 699) == NVFP4_ESIZE && g_calls == 0);
   CHECK(linear(0, 2048, NVFP4_OUT_F32) == NVFP4_OK && g_calls == 0);
   CHECK(linear(5, 2056, NVFP4_OUT_F32) == NVFP4_EUNSUPPORTED && g_calls == 0);
   CHECK(linear(5, 4096, NVFP4_OUT_F32) == NVFP4_ESHAPE && g_calls == 0);
@@ -145,8 +155,8 @@ int main() {
         g_quantize[1] == 64 && g_quantize[2] == 72);
   g_calls = 0;
   CHECK(gemm_w8a8(dev<int8_t>(), dev<float>(0x40000), 6, dev<int8_t>(0x20000), dev<float>(0x30000), 10, 96, dev<void>(), NVFP4_OUT_BF16, 12,
-                  nullptr) == NVFP4_OK && g_calls == 1 && g_int8.m == 6 && g_int8.n == 10 && g_int8.k == 96 && g_int8.ld_out == 12 &&
-        g_int8.out_bf16 == 1 && g_int8.w == dev<int8_t>(0x20000) && g_int8.a_scale == dev<float>(0x40000));
+                  nullptr, 0, nullptr) == NVFP4_OK && g_calls == 1 && g_int8.m == 6 && g_int8.n == 10 && g_int8.k == 96 && g_int8.ld_out == 12 &&
+        g_int8.out_bf16 == 1 && g_int8.workspace == nullptr && g_int8.w == dev<int8_t>(0x20000) && g_int8.a_scale == dev<float>(0x40000));
 
   g_result = hipErrorInvalidValue;   // a launch that fails is reported
   CHECK(rot(9, 256, 64, 2.f) == NVFP4_EHIP && append(7, NVFP4_CACHE_BF16, 8, 16) == NVFP4_EHIP &&

@@ -60,7 +60,8 @@ def product(lib, m, n, k, out_dtype=torch.bfloat16, ld=None, seed=0, offset=0):
     if ld is not None:
         wide = torch.full((m * ld + offset + 8,), 7.0, dtype=out_dtype, device="cuda")
         out = wide[offset:].as_strided((m, n), (ld, 1))
-    got = lib.gemm_w8a8(a, sa, w, sw, out_dtype=out_dtype, out=out)
+    ws = torch.randint(0, 256, (max(lib.load().gemm_w8a8_workspace_bytes(m, n, k), 1),), device="cuda", dtype=torch.int32).to(torch.uint8)
+    got = lib.gemm_w8a8(a, sa, w, sw, out_dtype=out_dtype, out=out, workspace=ws)
     # exact sums: fp64 holds them, and the GPU's fp64 product is checked against integers below
     s = (a.double() @ w.double().t()).float()
     want = ((s * sa[:, None]) * sw).to(out_dtype)
@@ -181,3 +182,31 @@ def test_refusals(gpu_lib):
                  lambda: gpu_lib.int8_linear(x.cpu(), w, s)):
         with pytest.raises(E):
             call()
+
+
+@pytest.mark.parametrize("m,n,k", [(37, 5120, 4096), (100, 700, 8192), (20, 64, 4112)])
+def test_split_sums(gpu_lib, m, n, k):
+    """With and without parts of k, from any workspace: the same bits; one workspace serves a graph and the calls between."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    a = torch.randint(-127, 128, (m, k), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+    w = torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+    sa, sw = torch.rand(m, device="cuda"), torch.rand(n, device="cuda")
+    need = gpu_lib.load().gemm_w8a8_workspace_bytes(m, n, k)
+    assert need > 0
+    none = torch.empty(m, n, device="cuda")
+    rc = gpu_lib.load().gemm_w8a8(a.data_ptr(), sa.data_ptr(), m, w.data_ptr(), sw.data_ptr(), n, k, none.data_ptr(), 0, n, None, 0,
+                                  torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    out = torch.empty(m, n, device="cuda")
+    f = lambda o: gpu_lib.gemm_w8a8(a, sa, w, sw, out_dtype=torch.float32, out=o, workspace=ws)  # noqa: E731
+    assert torch.equal(f(out), none) and torch.equal(f(torch.empty_like(out)), none)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f(out)
+    for i in range(4):
+        sa.mul_(-0.5)
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(got, f(torch.empty_like(out)))

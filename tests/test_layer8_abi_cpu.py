@@ -156,12 +156,12 @@ def quant(lib, x=A16, rows=4, cols=256, ld=256, c=A16, s=A16):
     return lib.int8_quantize(x, rows, cols, ld, c, s, None)
 
 
-def gemm(lib, a=A16, sa=A16, m=4, w=A16, sw=A16, n=24, k=256, out=A16, od=1, ldo=24):
-    return lib.gemm_w8a8(a, sa, m, w, sw, n, k, out, od, ldo, None)
+def gemm(lib, a=A16, sa=A16, m=4, w=A16, sw=A16, n=24, k=256, out=A16, od=1, ldo=24, ws=None, nws=0):
+    return lib.gemm_w8a8(a, sa, m, w, sw, n, k, out, od, ldo, ws, nws, None)
 
 
-def linear(lib, x=A16, m=4, k=256, ld=256, a=A16, sa=A16, w=A16, sw=A16, n=24, out=A16, od=1, ldo=24):
-    return lib.int8_linear(x, m, k, ld, a, sa, w, sw, n, out, od, ldo, None)
+def linear(lib, x=A16, m=4, k=256, ld=256, a=A16, sa=A16, w=A16, sw=A16, n=24, out=A16, od=1, ldo=24, ws=None, nws=0):
+    return lib.int8_linear(x, m, k, ld, a, sa, w, sw, n, out, od, ldo, ws, nws, None)
 
 
 def test_int8_validation(lib):
@@ -186,6 +186,13 @@ def test_int8_validation(lib):
         assert gemm(lib, **bad) == EALIGN, bad
         assert linear(lib, **bad) == EALIGN, bad
     assert linear(lib, x=None) == EINVAL and linear(lib, x=MIS) == EALIGN and linear(lib, ld=248) == ESHAPE
+    big = dict(m=40, n=512, k=4096)
+    need = lib.gemm_w8a8_workspace_bytes(40, 512, 4096)
+    assert need > 0 and lib.gemm_w8a8_workspace_bytes(-1, 512, 4096) == 0 and lib.gemm_w8a8_workspace_bytes(40, 512, 4095) == 0
+    for f in (gemm, linear):
+        more = dict(ldo=512, **(dict(ld=4096) if f is linear else {}), **big)
+        assert f(lib, ws=A16, nws=need, **more) == EHIP and f(lib, **more) == EHIP
+        assert f(lib, ws=A16, nws=need - 1, **more) == ESIZE and f(lib, ws=0x10008, nws=need, **more) == EALIGN
     assert quant(lib, rows=0, x=None, c=None, s=None) == OK
     assert gemm(lib, m=0, a=None, sa=None, out=None) == OK and linear(lib, m=0, x=None, a=None, sa=None, out=None) == OK
 

@@ -742,9 +742,10 @@ def _rotation(table, positions, tokens):
 
 
 def _one_device(*tensors):
-    devices = {t.get_device() for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise NVFP4Error("the tensors of a call must be on one GPU")
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise NVFP4Error("the tensors of a call must be on one GPU")
 
 
 def rotary(x, positions, table, head_dim, out=None):
@@ -761,9 +762,11 @@ def rotary(x, positions, table, head_dim, out=None):
     pos, steps, dim, layout, amplitude = _rotation(table, positions, T)
     if out is None:
         out = x.new_empty((T, cols))
-    op, ld_o, _ = _rows(out, _bf16, T, cols, "out")
+        op, ld_o = out.data_ptr(), cols
+    else:
+        op, ld_o, _ = _rows(out, _bf16, T, cols, "out")
+        _apart(x, out, same=True)
     _one_device(x, positions, table.steps, out)
-    _apart(x, out, same=True)
     rc = lib.rotary(xp, ld_x, T, cols // head_dim, head_dim, pos, steps, dim, layout, amplitude, op, ld_o,
                     _raw_stream(x.get_device()))
     if rc:
@@ -833,10 +836,12 @@ def paged_kv_append(k, v, positions, slots, k_cache, v_cache, rotation=None, k_s
         num_heads = cols // dim
         if q_out is None:
             q_out = q.new_empty((T, cols))
-        op, ld_o, _ = _rows(q_out, _bf16, T, cols, "q_out")
-        _apart(q, q_out, same=True)
-        _apart(k, q_out)
-        _apart(v, q_out)
+            op, ld_o = q_out.data_ptr(), cols
+        else:
+            op, ld_o, _ = _rows(q_out, _bf16, T, cols, "q_out")
+            _apart(q, q_out, same=True)
+            _apart(k, q_out)
+            _apart(v, q_out)
     elif q_out is not None:
         raise NVFP4Error("q_out needs q")
     _one_device(k, v, slots, k_cache, v_cache, k_scale, v_scale, q, q_out, *(() if rotation is None else (positions, rotation.steps)))
@@ -958,15 +963,26 @@ def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, s
     xp, ld_x, k = _rows(x, _bf16, None, None, "x")
     m = x.shape[0]
     wp, n, _ = _codes8(w, None, k, "w")
-    if codes is None:
-        codes = x.new_empty((m, k), dtype=_int8)
-    if scales is None:
-        scales = x.new_empty(m, dtype=_f32)
-    cp, _, _ = _codes8(codes, m, k, "codes")
+    need = lib.gemm_w8a8_workspace_bytes(m, n, k) if workspace is None else 0
+    if codes is None and scales is None and workspace is None:
+        # one allocation for all three, alive until the call has been enqueued
+        at, ws_at = m * k, (m * (k + 4) + 255) // 256 * 256
+        held = x.new_empty(ws_at + need, dtype=_u8)
+        cp = held.data_ptr()
+        sp, wsp, bytes_ = cp + at, cp + ws_at if need else None, need
+    else:
+        if codes is None:
+            codes = x.new_empty((m, k), dtype=_int8)
+        if scales is None:
+            scales = x.new_empty(m, dtype=_f32)
+        if workspace is None and need:
+            workspace = x.new_empty(need, dtype=_u8)
+        cp, sp = _codes8(codes, m, k, "codes")[0], _vec(scales, _f32, m, "scales")
+        bytes_ = workspace.numel() if isinstance(workspace, _Tensor) else 0
+        wsp = None if workspace is None else _vec(workspace, _u8, bytes_, "workspace")
     out, op, ld, kind = _int8_out(x, m, n, out_dtype, out)
-    workspace, wsp, bytes_ = _int8_workspace(lib, x, m, n, k, workspace)
     _one_device(x, w, w_scale, codes, scales, out, workspace)
-    rc = lib.int8_linear(xp, m, k, ld_x, cp, _vec(scales, _f32, m, "scales"), wp, _vec(w_scale, _f32, n, "w_scale"), n, op, kind,
+    rc = lib.int8_linear(xp, m, k, ld_x, cp, sp, wp, _vec(w_scale, _f32, n, "w_scale"), n, op, kind,
                          ld, wsp, bytes_, _raw_stream(x.get_device()))
     if rc:
         _check(rc, "int8_linear")

@@ -11,6 +11,8 @@
 // 400 instructions stay beside the loads.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "attention.h"
 #include "layer8.h"
 
@@ -35,32 +37,36 @@ __device__ __forceinline__ float2 cos_sin(uint32_t x, double amplitude) {
   return make_float2((quarter + 1) & 2 ? -cc : cc, quarter & 2 ? -ss : ss);
 }
 
-// The turns of unit u's eight pairs at a position.
-struct Turn {
-  float c[8], s[8];
-};
-__device__ __forceinline__ void find_turn(Turn& t, const RotaryArgs& rot, int unit, int position) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t phase = rot.steps[unit * 8 + i] * (uint64_t)(uint32_t)position;
-    const float2 cs = cos_sin((uint32_t)(phase >> 32), rot.amplitude);
-    t.c[i] = position < 0 ? 1.f : cs.x;
-    t.s[i] = position < 0 ? 0.f : cs.y;
-  }
-}
-
-// Columns of a unit: two runs of eight, at lo and hi.
+// Columns of a unit: two runs of eight, at lo and hi, half of the rotated part (or of the
+// rest) apart in either layout, so that neighbouring lanes read neighbouring 16 bytes.
+// Halves: pairs unit * 8 on.  Interleaved: four pairs in each run.
 struct UnitAt {
   int lo, hi;
   bool turns;
 };
-__device__ __forceinline__ UnitAt unit_at(const RotaryArgs& rot, int unit) {
+__device__ __forceinline__ UnitAt unit_at(int rotated, int dim, int unit) {
   UnitAt at;
-  at.turns = unit * 16 < rot.dim;
-  const bool split = at.turns && !rot.interleaved;
-  at.lo = split ? unit * 8 : unit * 16;
-  at.hi = split ? unit * 8 + rot.dim / 2 : unit * 16 + 8;
+  at.turns = unit * 16 < rotated;
+  const int from = at.turns ? 0 : rotated, half = (at.turns ? rotated : dim - rotated) / 2;
+  at.lo = from + (unit - from / 16) * 8;
+  at.hi = at.lo + half;
   return at;
+}
+
+// The turns of a unit's eight pairs at a position.
+struct Turn {
+  float c[8], s[8];
+};
+template <bool INTERLEAVED>
+__device__ __forceinline__ void find_turn(Turn& t, const RotaryArgs& rot, int unit, int position) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int pair = INTERLEAVED ? unit * 4 + (i < 4 ? i : rot.dim / 4 + i - 4) : unit * 8 + i;
+    const uint64_t phase = rot.steps[pair] * (uint64_t)(uint32_t)position;
+    const float2 cs = cos_sin((uint32_t)(phase >> 32), rot.amplitude);
+    t.c[i] = position < 0 ? 1.f : cs.x;
+    t.s[i] = position < 0 ? 0.f : cs.y;
+  }
 }
 
 __device__ __forceinline__ void unpack(const u32x4& w, float* f) {
@@ -75,19 +81,15 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
 }
 
 // x[0 .. 7] and x[8 .. 15]: the unit's two runs.
-__device__ __forceinline__ void turn_unit(float* x, const Turn& t, bool interleaved) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_unit(float* x, const Turn& t) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float a = interleaved ? x[2 * i] : x[i], b = interleaved ? x[2 * i + 1] : x[8 + i];
+    float& a = x[INTERLEAVED ? 2 * i : i];
+    float& b = x[INTERLEAVED ? 2 * i + 1 : 8 + i];
     const float ra = fmaf(a, t.c[i], -(b * t.s[i])), rb = fmaf(b, t.c[i], a * t.s[i]);
-    // (the other layout's registers: both are known at compile time but for the choice)
-    if (interleaved) {
-      x[2 * i] = ra;
-      x[2 * i + 1] = rb;
-    } else {
-      x[i] = ra;
-      x[8 + i] = rb;
-    }
+    a = ra;
+    b = rb;
   }
 }
 
@@ -95,30 +97,32 @@ __device__ __forceinline__ void turn_unit(float* x, const Turn& t, bool interlea
 
 // --------------------------------------------------------------- rotary ----
 //
-// Bound by HBM: 4 bytes an element.  Thread (token, unit) takes `per` heads from
-// `per * blockIdx.y` on, four heads' loads in flight.
+// Bound by HBM: 4 bytes an element.  Thread (token, unit) takes `per` heads of its
+// block's group, four heads' loads in flight.
+namespace {
+
 template <bool INTERLEAVED>
-__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryRows a, RotaryArgs rot, int per) {
-  const int units = a.dim / 16;
-  const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+__device__ __forceinline__ void rotary_rows(const RotaryRows& a, const RotaryArgs& rot, int units, int64_t block, int groups, int per) {
+  const int group = (int)(block % groups);
+  const int64_t item = block / groups * kThreads + threadIdx.x;
   const int64_t t = item / units;
   if (t >= a.tokens) return;
-  const int unit = (int)(item - t * units), h0 = blockIdx.y * per, h1 = min(h0 + per, a.heads);
-  const UnitAt at = unit_at(rot, unit);
+  const int unit = (int)(item - t * units), h0 = group * per, h1 = min(h0 + per, a.heads);
+  const UnitAt at = unit_at(rot.dim, a.dim, unit);
   if (!at.turns && a.x == a.out) return;   // in place
-  Turn turn;
-  if (at.turns) find_turn(turn, rot, unit, rot.positions[t]);
   const uint16_t* x = a.x + t * a.ld_x;
   uint16_t* out = a.out + t * a.ld_out;
   constexpr int kAtOnce = 4;
-  for (int h = h0; h < h1; h += kAtOnce) {
-    u32x4 lo[kAtOnce], hi[kAtOnce];
+  u32x4 lo[kAtOnce], hi[kAtOnce];
+  auto load = [&](int i, int h) {
+    lo[i] = *(const u32x4*)(x + (int64_t)h * a.dim + at.lo);
+    hi[i] = *(const u32x4*)(x + (int64_t)h * a.dim + at.hi);
+  };
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int64_t head = (int64_t)min(h + i, h1 - 1) * a.dim;
-      lo[i] = *(const u32x4*)(x + head + at.lo);
-      hi[i] = *(const u32x4*)(x + head + at.hi);
-    }
+  for (int i = 0; i < kAtOnce; ++i) load(i, min(h0 + i, h1 - 1));
+  Turn turn;
+  if (at.turns) find_turn<INTERLEAVED>(turn, rot, unit, rot.positions[t]);
+  for (int h = h0; h < h1; h += kAtOnce) {
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       if (h + i >= h1) break;
@@ -127,35 +131,52 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryRows a, RotaryAr
         float f[16];
         unpack(lo[i], f);
         unpack(hi[i], f + 8);
-        turn_unit(f, turn, INTERLEAVED);
+        turn_unit<INTERLEAVED>(f, turn);
         lo[i] = pack(f);
         hi[i] = pack(f + 8);
       }
       *(u32x4*)(out + head + at.lo) = lo[i];
       *(u32x4*)(out + head + at.hi) = hi[i];
+      if (h + kAtOnce + i < h1) load(i, h + kAtOnce + i);
     }
   }
 }
 
+}  // namespace
+
+template <bool INTERLEAVED>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryRows a, RotaryArgs rot, int groups, int per) {
+  rotary_rows<INTERLEAVED>(a, rot, a.dim / 16, blockIdx.x, groups, per);
+}
+
 namespace {
 
-// Heads a thread takes: as many as leave the chip 2^17 threads (eight waves a SIMD's
-// worth), four at least, which are in flight together.
-int heads_per_thread(int64_t items, int heads) {
-  const int64_t per = items * heads >> 17;
-  return (int)max((int64_t)1, min(per, (int64_t)heads));
+// Heads a thread takes, and the grid of blocks x groups of heads.  Four are in flight
+// together; more pay only where the chip is filled many times over (16384 tokens, 48
+// heads of 128: 6 heads a thread 77 us, 48 heads 92; 2000 tokens, 40 heads: 4 a thread 9.6
+// us, 1 12.4), and few tokens want all the threads there can be.
+struct RotaryGrid {
+  int groups, per;
+  int64_t blocks;
+};
+RotaryGrid rotary_grid(int64_t tokens, int heads, int dim) {
+  const int64_t items = tokens * (dim / 16);
+  RotaryGrid g;
+  const int64_t all = items * heads, per = std::max(std::min<int64_t>(all >> 16, 4), all >> 20);
+  g.per = (int)std::max<int64_t>(1, std::min<int64_t>(per, heads));
+  g.groups = (heads + g.per - 1) / g.per;
+  g.blocks = (items + kThreads - 1) / kThreads * g.groups;
+  return g;
 }
 
 }  // namespace
 
 hipError_t launch_rotary(const RotaryRows& a, const RotaryArgs& rot, hipStream_t st) {
-  const int64_t items = a.tokens * (a.dim / 16);
-  const int per = heads_per_thread(items, a.heads);
-  const dim3 grid((unsigned)((items + kThreads - 1) / kThreads), (unsigned)((a.heads + per - 1) / per));
+  const RotaryGrid g = rotary_grid(a.tokens, a.heads, a.dim);
   if (rot.interleaved)
-    rotary_kernel<true><<<grid, kThreads, 0, st>>>(a, rot, per);
+    rotary_kernel<true><<<(unsigned)g.blocks, kThreads, 0, st>>>(a, rot, g.groups, g.per);
   else
-    rotary_kernel<false><<<grid, kThreads, 0, st>>>(a, rot, per);
+    rotary_kernel<false><<<(unsigned)g.blocks, kThreads, 0, st>>>(a, rot, g.groups, g.per);
   return hipGetLastError();
 }
 
@@ -176,43 +197,51 @@ hipError_t launch_rotary(const RotaryRows& a, const RotaryArgs& rot, hipStream_t
 // with the scale in it.
 namespace {
 
-__device__ __forceinline__ uint32_t codes4(const float* f, bool int8) {
-  if (int8) {
-    uint32_t w = 0;
+// Four values in steps of their scale as codes, rounded to nearest even.  CLAMP: they may
+// lie beyond the largest code (infinities), or be NaN for INT8.
+template <bool INT8, bool CLAMP>
+__device__ __forceinline__ uint32_t codes4(const float* f) {
+  if constexpr (INT8) {
+    uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float r = fminf(fmaxf(rintf(f[i]), -127.f), 127.f);
-      w |= ((uint32_t)(int)(f[i] != f[i] ? 0.f : r) & 0xffu) << (8 * i);
+      float x = f[i];
+      if (CLAMP) x = x != x ? 0.f : fminf(fmaxf(x, -127.f), 127.f);
+      b[i] = __float_as_uint(x + 12582912.f);   // 1.5 * 2^23: the sum's last bits are the whole number
     }
-    return w;
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    return lo | hi;
+  } else {
+    float g[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = !CLAMP || f[i] != f[i] ? f[i] : fminf(fmaxf(f[i], -448.f), 448.f);   // a NaN stays one
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(g[0], g[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(g[2], g[3], w, true);
   }
-  float g[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) g[i] = f[i] != f[i] ? f[i] : fminf(fmaxf(f[i], -448.f), 448.f);   // a NaN stays one
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(g[0], g[1], 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(g[2], g[3], w, true);
 }
-__device__ __forceinline__ u32x2 codes8(const float* f, bool int8) { return u32x2{codes4(f, int8), codes4(f + 4, int8)}; }
+template <bool INT8, bool CLAMP>
+__device__ __forceinline__ u32x2 codes8(const float* f) {
+  return u32x2{codes4<INT8, CLAMP>(f), codes4<INT8, CLAMP>(f + 4)};
+}
 
-// Four codes times 2^by (by <= 0), rounded to nearest even again.
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, int by, bool int8) {
+// Four codes times a power of two up to 1, rounded to nearest even again.
+template <bool INT8>
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float by) {
   float f[4];
-  if (int8) {
+  if (INT8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = ldexpf((float)(int8_t)(w >> (8 * i)), by);
+    for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i)) * by;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = __builtin_amdgcn_cvt_f32_fp8((int)(w >> (8 * i)), 0);
-      f[i] = ldexpf(lo, by);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = __builtin_amdgcn_cvt_f32_fp8((int)(w >> (8 * i)), 0) * by;
   }
-  return codes4(f, int8);
+  return codes4<INT8, false>(f);
 }
 
-// E8M0 byte of the smallest power of two s with top <= M s, within 1 .. the largest.
-__device__ __forceinline__ int needed_scale(float top, bool int8) {
-  const uint32_t b = __float_as_uint(top), m = b & 0x7fffffu;
+// E8M0 byte of the smallest power of two s with top <= M s, within 1 .. the largest; top
+// by its bits.
+__device__ __forceinline__ int needed_scale(uint32_t top, bool int8) {
+  const uint32_t b = top, m = b & 0x7fffffu;
   const int e = (int)(b >> 23);
   // 127 = 1.984375 * 2^6, 448 = 1.75 * 2^8
   return int8 ? min(max(e - 6 + (m > 0x7e0000u), 1), kMostInt8) : min(max(e - 8 + (m > 0x600000u), 1), kMostE4m3);
@@ -226,39 +255,41 @@ __device__ __forceinline__ int64_t place_at(const CacheView& c, int64_t slot, in
 }  // namespace
 
 template <bool INTERLEAVED, bool FP8>
-__global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int per) {
+__global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int groups, int per) {
   const CacheView& c = a.cache;
-  const int units = c.dim / 16, heads = a.q.heads + 2 * c.heads;
-  const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int units = c.dim / 16, heads = a.q.heads + 2 * c.heads, group = blockIdx.x % groups;
+  const int64_t item = (int64_t)(blockIdx.x / groups) * kThreads + threadIdx.x;
   const int64_t t = item / units;
   if (t >= a.tokens) return;
-  const int unit = (int)(item - t * units), h0 = blockIdx.y * per, h1 = min(h0 + per, heads);
-  const UnitAt at = unit_at(a.rot, unit);
+  const int unit = (int)(item - t * units), h0 = group * per, h1 = min(h0 + per, heads);
+  const UnitAt at = unit_at(a.rot.dim, c.dim, unit);
+  constexpr int kAtOnce = 4;
+  u32x4 lo[kAtOnce], hi[kAtOnce];
+  auto load = [&](int i, int head) {
+    const int kv = head - a.q.heads;
+    const uint16_t* x = kv < 0           ? a.q.x + t * a.q.ld_x + (int64_t)head * c.dim
+                        : kv < c.heads ? a.k + t * a.ld_k + (int64_t)kv * c.dim
+                                       : a.v + t * a.ld_v + (int64_t)(kv - c.heads) * c.dim;
+    lo[i] = *(const u32x4*)(x + at.lo);
+    hi[i] = *(const u32x4*)(x + at.hi);
+  };
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) load(i, min(h0 + i, h1 - 1));
   Turn turn;
-  if (at.turns && h0 < a.q.heads + c.heads) find_turn(turn, a.rot, unit, a.rot.positions[t]);
+  if (at.turns && h0 < a.q.heads + c.heads) find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[t]);
   const int64_t slot = a.slots[t];
   const bool held = slot >= 0 && slot >> c.page_shift < c.num_pages;
-  constexpr int kAtOnce = 4;
   for (int h = h0; h < h1; h += kAtOnce) {
-    u32x4 lo[kAtOnce], hi[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int head = min(h + i, h1 - 1), kv = head - a.q.heads;
-      const uint16_t* x = kv < 0           ? a.q.x + t * a.q.ld_x + (int64_t)head * c.dim
-                          : kv < c.heads ? a.k + t * a.ld_k + (int64_t)kv * c.dim
-                                         : a.v + t * a.ld_v + (int64_t)(kv - c.heads) * c.dim;
-      lo[i] = *(const u32x4*)(x + at.lo);
-      hi[i] = *(const u32x4*)(x + at.hi);
-    }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const int head = h + i, kv = head - a.q.heads;
       if (head >= h1) break;
-      if (kv >= 0 && !held) continue;
       float f[16];
       unpack(lo[i], f);
       unpack(hi[i], f + 8);
-      if (at.turns && kv < c.heads) turn_unit(f, turn, INTERLEAVED);
+      if (head + kAtOnce < h1) load(i, head + kAtOnce);
+      if (kv >= 0 && !held) continue;
+      if (at.turns && kv < c.heads) turn_unit<INTERLEAVED>(f, turn);
       if (kv < 0) {
         uint16_t* out = a.q.out + t * a.q.ld_out + (int64_t)head * c.dim;
         *(u32x4*)(out + at.lo) = pack(f);
@@ -274,8 +305,8 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
 #pragma unroll
         for (int j = 0; j < 16; ++j) f[j] /= scale;
         uint8_t* p = (uint8_t*)(is_v ? c.v : c.k) + to;
-        *(u32x2*)(p + at.lo) = codes8(f, false);
-        *(u32x2*)(p + at.hi) = codes8(f + 8, false);
+        *(u32x2*)(p + at.lo) = codes8<false, true>(f);
+        *(u32x2*)(p + at.hi) = codes8<false, true>(f + 8);
       } else {
         uint16_t* p = (uint16_t*)(is_v ? c.v : c.k) + to;
         *(u32x4*)(p + at.lo) = pack(f);
@@ -285,29 +316,23 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
   }
 }
 
-// Rows 16 w .. 16 w + 15 of the call are window w; waves (window, share, head, K or V)
-// take every `shares`-th of the runs that begin in it.
+namespace {
+
+// Rows 16 w .. 16 w + 15 of the call are window w.  This wave takes heads [h0, h1) of K
+// or V, and of the runs that begin in its window every `shares`-th from `share` on.
 template <bool INTERLEAVED, bool INT8, int D>
-__global__ __launch_bounds__(kThreads) void append_blocks_kernel(AppendArgs a, int shares, int64_t waves) {
+__device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window, int share, int shares, int h0, int h1, bool is_v) {
   constexpr int U = D / 16;                 // units, so lanes, of a row
   constexpr int ROWS = 64 / U;              // places of the block that a pass covers
   constexpr int PASSES = kBlockTokens / ROWS;
   const CacheView& c = a.cache;
   const int lane = threadIdx.x & 63, unit = lane % U, lane_row = lane / U;
-  int64_t id = (int64_t)blockIdx.x * (kThreads / 64) + uniform((int)(threadIdx.x >> 6));
-  if (id >= waves) return;
-  const bool is_v = id & 1;
-  id >>= 1;
-  const int head = (int)(id % c.heads);
-  id /= c.heads;
-  const int share = (int)(id % shares);
-  const int64_t t0 = id / shares * kBlockTokens;
-  const uint16_t* x = is_v ? a.v + (int64_t)head * D : a.k + (int64_t)head * D;
+  const int64_t t0 = window * kBlockTokens;
+  const uint16_t* x = is_v ? a.v : a.k;
   const int64_t ld = is_v ? a.ld_v : a.ld_k;
   uint8_t* cache = (uint8_t*)(is_v ? c.v : c.k);
   uint8_t* scales = is_v ? c.v_blocks : c.k_blocks;
-  UnitAt at = unit_at(a.rot, unit);
-  if (is_v) at = UnitAt{unit * 16, unit * 16 + 8, false};
+  const UnitAt at = unit_at(is_v ? 0 : a.rot.dim, D, unit);
 
   // the window's rows that begin a run
   auto slot_of = [&](int64_t t) {
@@ -328,62 +353,105 @@ __global__ __launch_bounds__(kThreads) void append_blocks_kernel(AppendArgs a, i
     const bool next = lane < kBlockTokens - place0 && slot_of(t + lane) == s0 + lane;
     const int place1 = place0 + __builtin_ctzll(~__ballot(next));   // the run: places [place0, place1)
     const bool fresh = place0 == 0;
-    const int64_t block = ((s0 >> c.page_shift) * c.heads + head) << (c.page_shift - 4) | (s0 & (((int64_t)1 << c.page_shift) - 1)) >> 4;
-    const int64_t first = place_at(c, s0 - place0, head);
-    const int old = fresh ? 1 : min(max((int)scales[block], 1), INT8 ? kMostInt8 : kMostE4m3);
+    int64_t block = ((s0 >> c.page_shift) * c.heads + h0) << (c.page_shift - 4) | (s0 & (((int64_t)1 << c.page_shift) - 1)) >> 4;
+    uint8_t* to = cache + place_at(c, s0 - place0, h0);
 
-    u32x4 lo[PASSES], hi[PASSES];
+    // a lane's rows: of a place outside the run the run's first, which is not used
+    const uint16_t* row[PASSES];
+    bool in[PASSES];
+    Turn turn[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int place = p * ROWS + lane_row;
-      const bool in = place >= place0 && place < place1;
-      const uint16_t* row = x + (in ? t + place - place0 : t) * ld;
-      lo[p] = *(const u32x4*)(row + at.lo);
-      hi[p] = *(const u32x4*)(row + at.hi);
+      in[p] = place >= place0 && place < place1;
+      const int64_t from = in[p] ? t + place - place0 : t;
+      row[p] = x + from * ld;
+      if (in[p] && at.turns) find_turn<INTERLEAVED>(turn[p], a.rot, unit, a.rot.positions[from]);
     }
-    float f[PASSES][16];
-    float top = 0.f;
+    for (int h = h0; h < h1; ++h, block += (int64_t)1 << (c.page_shift - 4), to += c.head_stride) {
+      u32x4 lo[PASSES], hi[PASSES];
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int place = p * ROWS + lane_row;
-      const bool in = place >= place0 && place < place1;
-      unpack(lo[p], f[p]);
-      unpack(hi[p], f[p] + 8);
-      if (in && at.turns) {
-        Turn turn;
-        find_turn(turn, a.rot, unit, a.rot.positions[t + place - place0]);
-        turn_unit(f[p], turn, INTERLEAVED);
+      for (int p = 0; p < PASSES; ++p) {
+        lo[p] = *(const u32x4*)(row[p] + (int64_t)h * D + at.lo);
+        hi[p] = *(const u32x4*)(row[p] + (int64_t)h * D + at.hi);
+      }
+      constexpr int kMost = INT8 ? kMostInt8 : kMostE4m3;
+      const int old = fresh ? 1 : min(max((int)scales[block], 1), kMost);
+      float f[PASSES][16];
+      uint32_t top = 0;                     // largest magnitude's bits: infinities and NaN come last
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        unpack(lo[p], f[p]);
+        unpack(hi[p], f[p] + 8);
+        if (in[p] && at.turns) turn_unit<INTERLEAVED>(f[p], turn[p]);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[p][i]) & 0x7fffffffu);
+        top = in[p] ? max(top, m) : top;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float m = fabsf(f[p][i]);
-        top = in && m < INFINITY ? fmaxf(top, m) : top;
+      for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+      const bool odd = top >= 0x7f800000u;   // rare: the largest finite value, and clamped codes
+      if (odd) {
+        top = 0;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t m = __float_as_uint(f[p][i]) & 0x7fffffffu;
+            if (in[p] && m < 0x7f800000u) top = max(top, m);
+          }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
       }
-    }
+      const int e = max(needed_scale(top, INT8), old);
+      const bool clamp = odd || e == kMost;   // at the largest scale a value may lie beyond its codes
+      const bool rises = !fresh && e > old;
+      const float by = __uint_as_float((uint32_t)(254 - e) << 23), shrink = e - old > 126 ? 0.f : __uint_as_float((uint32_t)(127 + old - e) << 23);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const int e = max(needed_scale(top, INT8), old);
-    const bool rises = !fresh && e > old;
+      for (int p = 0; p < PASSES; ++p) {
+        uint8_t* place = to + (int64_t)(p * ROWS + lane_row) * c.token_stride;
+        if (in[p]) {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int place = p * ROWS + lane_row;
-      uint8_t* to = cache + first + place * c.token_stride;
-      if (place >= place0 && place < place1) {
+          for (int i = 0; i < 16; ++i) f[p][i] *= by;
+          if (clamp) {
+            *(u32x2*)(place + at.lo) = codes8<INT8, true>(f[p]);
+            *(u32x2*)(place + at.hi) = codes8<INT8, true>(f[p] + 8);
+          } else {
+            *(u32x2*)(place + at.lo) = codes8<INT8, false>(f[p]);
+            *(u32x2*)(place + at.hi) = codes8<INT8, false>(f[p] + 8);
+          }
+        } else if (fresh) {
+          *(u32x4*)(place + unit * 16) = u32x4{0u, 0u, 0u, 0u};
+        } else if (rises) {
+          u32x4 w = *(const u32x4*)(place + unit * 16);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[p][i] = ldexpf(f[p][i], 127 - e);
-        *(u32x2*)(to + at.lo) = codes8(f[p], INT8);
-        *(u32x2*)(to + at.hi) = codes8(f[p] + 8, INT8);
-      } else if (fresh) {
-        *(u32x4*)(to + unit * 16) = u32x4{0u, 0u, 0u, 0u};
-      } else if (rises) {
-        u32x4 w = *(const u32x4*)(to + unit * 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = rescale4(w[i], old - e, INT8);
-        *(u32x4*)(to + unit * 16) = w;
+          for (int i = 0; i < 4; ++i) w[i] = rescale4<INT8>(w[i], shrink);
+          *(u32x4*)(place + unit * 16) = w;
+        }
       }
+      if (lane == 0) scales[block] = (uint8_t)e;
     }
-    if (lane == 0) scales[block] = (uint8_t)e;
   }
+}
+
+}  // namespace
+
+// The first `kv` workgroups write K and V, the others rotate q.
+template <bool INTERLEAVED, bool INT8, int D>
+__global__ __launch_bounds__(kThreads) void append_blocks_kernel(AppendArgs a, int shares, int head_groups, int heads, int64_t waves, int kv,
+                                                                 int q_groups, int q_per) {
+  if ((int)blockIdx.x >= kv) {
+    rotary_rows<INTERLEAVED>(a.q, a.rot, D / 16, blockIdx.x - kv, q_groups, q_per);
+    return;
+  }
+  int64_t id = (int64_t)blockIdx.x * (kThreads / 64) + uniform((int)(threadIdx.x >> 6));
+  if (id >= waves) return;
+  const bool is_v = id & 1;
+  id >>= 1;
+  const int h0 = (int)(id % head_groups) * heads;
+  id /= head_groups;
+  append_runs<INTERLEAVED, INT8, D>(a, id / shares, (int)(id % shares), shares, h0, min(h0 + heads, a.cache.heads), is_v);
 }
 
 namespace {
@@ -392,16 +460,26 @@ template <bool INTERLEAVED, bool INT8>
 hipError_t launch_blocks(const AppendArgs& a, hipStream_t st) {
   const CacheView& c = a.cache;
   const int64_t windows = (a.tokens + kBlockTokens - 1) / kBlockTokens;
-  // every row may be a run of its own (single tokens): a wave for each of them while
-  // that leaves the chip room, else one a window, as prompts have
+  // Every row may be a run of its own (single tokens): a wave for each of them and for
+  // every head while that leaves the chip room; prompts, with one run a window, share
+  // a run's angles between heads.
   const int64_t each = windows * c.heads * 2;
   const int shares = each * 16 <= 8192 ? 16 : each * 4 <= 8192 ? 4 : 1;
-  const int64_t waves = each * shares;
-  const unsigned grid = (unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64));
+  const int heads = (int)std::max<int64_t>(1, std::min<int64_t>(each / 4096, c.heads)), groups = (c.heads + heads - 1) / heads;
+  const int64_t waves = windows * 2 * groups * shares;
+  const int64_t kv = (waves + kThreads / 64 - 1) / (kThreads / 64);
+  RotaryGrid q{1, 1, 0};
+  if (a.q.heads > 0) q = rotary_grid(a.tokens, a.q.heads, c.dim);
+  const unsigned grid = (unsigned)(kv + q.blocks);
   switch (c.dim) {
-    case 64: append_blocks_kernel<INTERLEAVED, INT8, 64><<<grid, kThreads, 0, st>>>(a, shares, waves); break;
-    case 128: append_blocks_kernel<INTERLEAVED, INT8, 128><<<grid, kThreads, 0, st>>>(a, shares, waves); break;
-    default: append_blocks_kernel<INTERLEAVED, INT8, 256><<<grid, kThreads, 0, st>>>(a, shares, waves);
+    case 64:
+      append_blocks_kernel<INTERLEAVED, INT8, 64><<<grid, kThreads, 0, st>>>(a, shares, groups, heads, waves, (int)kv, q.groups, q.per);
+      break;
+    case 128:
+      append_blocks_kernel<INTERLEAVED, INT8, 128><<<grid, kThreads, 0, st>>>(a, shares, groups, heads, waves, (int)kv, q.groups, q.per);
+      break;
+    default:
+      append_blocks_kernel<INTERLEAVED, INT8, 256><<<grid, kThreads, 0, st>>>(a, shares, groups, heads, waves, (int)kv, q.groups, q.per);
   }
   return hipGetLastError();
 }
@@ -411,24 +489,16 @@ hipError_t launch_blocks(const AppendArgs& a, hipStream_t st) {
 hipError_t launch_paged_kv_append(const AppendArgs& a, hipStream_t st) {
   const CacheView& c = a.cache;
   const bool inter = a.rot.interleaved;
-  if (c.blocks != kBlocksNone) {
-    if (a.q.heads > 0) {
-      const hipError_t e = launch_rotary(a.q, a.rot, st);
-      if (e != hipSuccess) return e;
-    }
-    if (c.blocks == kBlocksInt8) return inter ? launch_blocks<true, true>(a, st) : launch_blocks<false, true>(a, st);
-    return inter ? launch_blocks<true, false>(a, st) : launch_blocks<false, false>(a, st);
-  }
-  const int heads = a.q.heads + 2 * c.heads;
-  const int64_t items = a.tokens * (c.dim / 16);
-  const int per = heads_per_thread(items, heads);
-  const dim3 grid((unsigned)((items + kThreads - 1) / kThreads), (unsigned)((heads + per - 1) / per));
+  if (c.blocks == kBlocksInt8) return inter ? launch_blocks<true, true>(a, st) : launch_blocks<false, true>(a, st);
+  if (c.blocks == kBlocksE4m3) return inter ? launch_blocks<true, false>(a, st) : launch_blocks<false, false>(a, st);
+  const RotaryGrid g = rotary_grid(a.tokens, a.q.heads + 2 * c.heads, c.dim);
+  const unsigned grid = (unsigned)g.blocks;
   if (inter) {
-    if (c.fp8) append_rows_kernel<true, true><<<grid, kThreads, 0, st>>>(a, per);
-    else append_rows_kernel<true, false><<<grid, kThreads, 0, st>>>(a, per);
+    if (c.fp8) append_rows_kernel<true, true><<<grid, kThreads, 0, st>>>(a, g.groups, g.per);
+    else append_rows_kernel<true, false><<<grid, kThreads, 0, st>>>(a, g.groups, g.per);
   } else {
-    if (c.fp8) append_rows_kernel<false, true><<<grid, kThreads, 0, st>>>(a, per);
-    else append_rows_kernel<false, false><<<grid, kThreads, 0, st>>>(a, per);
+    if (c.fp8) append_rows_kernel<false, true><<<grid, kThreads, 0, st>>>(a, g.groups, g.per);
+    else append_rows_kernel<false, false><<<grid, kThreads, 0, st>>>(a, g.groups, g.per);
   }
   return hipGetLastError();
 }

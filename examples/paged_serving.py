@@ -11,7 +11,13 @@ The drafts are looked up in the request's own text (what followed the last two
 tokens before), so they cost nothing; verification keeps what the target would
 have said.  Weights are random: the text means nothing, the steps are real.
 
-    python examples/paged_serving.py [--steps N] [--drafts K] [--temperature T]
+With --layer8 the attention layers are those of a model whose attention half is kept
+in 8 bits: int8 linear layers, rotary positions on the way into a cache with a scale for
+each 16 tokens and head:
+
+    int8_linear (q, k, v) -> paged_kv_append -> paged_attention_blocks -> int8_linear (o)
+
+    python examples/paged_serving.py [--steps N] [--drafts K] [--temperature T] [--layer8 {e4m3,int8}]
 """
 import argparse
 import os
@@ -37,24 +43,46 @@ class Linear:
         return B.nvfp4_linear(x, self.packed, self.scale[:1], self.n, **kw)[0]
 
 
+class Int8Linear:
+    """A linear layer in 8-bit integers with random weights, a scale for each output channel."""
+
+    def __init__(self, n, k, gen):
+        self.w, self.scale = B.int8_quantize((torch.randn(n, k, generator=gen, device="cuda") * k ** -0.5).to(torch.bfloat16))
+
+    def __call__(self, x):
+        return B.int8_linear(x, self.w, self.scale)
+
+
 def norm(x):
     return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
 
 class Model:
-    """A decoder of softmax-attention layers with an E4M3 cache."""
+    """A decoder of softmax-attention layers: NVFP4 ones with an E4M3 cache, or with layer8 ("e4m3" or "int8", the codes of
+    its block-scaled cache) 8-bit ones with rotary positions."""
 
     def __init__(self, layers=2, hidden=1024, hq=8, hkv=2, dim=128, ffn=2048, vocab=4096, pages=256, page=64, requests=4,
-                 max_seq=2048, seed=0):
+                 max_seq=2048, seed=0, layer8=None, rotation=None):
         gen = torch.Generator(device="cuda").manual_seed(seed)
+        attention_linear = Int8Linear if layer8 else Linear
+        cache_type = torch.int8 if layer8 == "int8" else torch.float8_e4m3fn
+
+        def scales():
+            if layer8:      # they follow the values; a block's first token begins it anew
+                return torch.zeros(pages, hkv, page // 16, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+            # |k| and |v| stay below 448 of these steps; a real model has them calibrated
+            return torch.full((hkv,), 0.02, device="cuda")
+
+        # the first half of every head turns, frequencies stretched to four times 4096 tokens
+        self.rotation = rotation or (B.rotary_table(dim // 2, scaling="yarn", factor=4.0, original_length=4096) if layer8 else None)
+        self.layer8 = layer8
         self.hq, self.hkv, self.dim, self.page, self.vocab, self.max_seq = hq, hkv, dim, page, vocab, max_seq
         self.embed = torch.randn(vocab, hidden, generator=gen, device="cuda").to(torch.bfloat16)
-        self.blocks = [dict(qkv=Linear((hq + 2 * hkv) * dim, hidden, gen), o=Linear(hidden, hq * dim, gen),
+        self.blocks = [dict(qkv=attention_linear((hq + 2 * hkv) * dim, hidden, gen), o=attention_linear(hidden, hq * dim, gen),
                             gate_up=Linear(2 * ffn, hidden, gen), down=Linear(hidden, ffn, gen),
-                            k=torch.zeros(pages, hkv, page, dim, device="cuda").to(torch.float8_e4m3fn),
-                            v=torch.zeros(pages, hkv, page, dim, device="cuda").to(torch.float8_e4m3fn),
-                            # |k| and |v| stay below 448 of these steps; a real model has them calibrated
-                            k_scale=torch.full((hkv,), 0.02, device="cuda"), v_scale=torch.full((hkv,), 0.02, device="cuda"))
+                            k=torch.zeros(pages, hkv, page, dim, device="cuda").to(cache_type),
+                            v=torch.zeros(pages, hkv, page, dim, device="cuda").to(cache_type),
+                            k_scale=scales(), v_scale=scales())
                        for _ in range(layers)]
         # the embedding again, so that the model says what it has heard and drafts are worth their verification
         self.head = Linear(vocab, hidden, gen, self.embed * hidden ** -0.5)
@@ -78,11 +106,19 @@ class Model:
         for b in self.blocks:
             y = b["qkv"](norm(x))
             q, k, v = y[:, :nq], y[:, nq:nq + nk], y[:, nq + nk:]    # views: no copies
-            B.paged_kv_write(k, v, plan.slots, b["k"], b["v"], b["k_scale"], b["v_scale"])
-            a = B.paged_attention(q, b["k"], b["v"], self.table, plan.q_start, plan.seq_lens, max(new), self.max_seq,
-                                  k_scale=b["k_scale"], v_scale=b["v_scale"], workspace=self.attention_ws)
-            if trace is not None:
-                trace.append((q, k, v, a))
+            if self.layer8:
+                turned = B.paged_kv_append(k, v, plan.positions, plan.slots, b["k"], b["v"], rotation=self.rotation,
+                                           k_scale=b["k_scale"], v_scale=b["v_scale"], q=q)
+                a = B.paged_attention_blocks(turned, b["k"], b["v"], b["k_scale"], b["v_scale"], self.table, plan.q_start,
+                                             plan.seq_lens, max(new), self.max_seq, workspace=self.attention_ws)
+                if trace is not None:
+                    trace.append((q, k, v, a, turned))
+            else:
+                B.paged_kv_write(k, v, plan.slots, b["k"], b["v"], b["k_scale"], b["v_scale"])
+                a = B.paged_attention(q, b["k"], b["v"], self.table, plan.q_start, plan.seq_lens, max(new), self.max_seq,
+                                      k_scale=b["k_scale"], v_scale=b["v_scale"], workspace=self.attention_ws)
+                if trace is not None:
+                    trace.append((q, k, v, a))
             x = x + b["o"](a)
             x = x + b["down"](b["gate_up"](norm(x), epilogue="silu_mul"))
         return self.head(norm(x)), plan
@@ -140,8 +176,9 @@ def main():
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--drafts", type=int, default=4)
     ap.add_argument("--temperature", type=float, default=0.0)
+    ap.add_argument("--layer8", choices=("e4m3", "int8"), help="attention layers in 8 bits, with a block-scaled cache of these codes")
     args = ap.parse_args()
-    model = Model()
+    model = Model(layer8=args.layer8)
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, model.vocab, (n,), generator=gen).tolist() for n in (200, 17, 90, 1)]
     # prompts that repeat themselves give the look-up something to find

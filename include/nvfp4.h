@@ -545,7 +545,7 @@ int verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64
  * k_blocks and v_blocks hold one E8M0 byte for each block of 16 tokens (a slot's
  * block is slot / 16) of each head, [num_pages, num_kv_heads, page_size / 16]
  * contiguous.  A code stands for code * 2^(byte - 127): an E4M3 value, or a whole
- * number from -127 to 127.  Bytes run from 1 to 246 (E4M3) or 248 (INT8); others are
+ * number from -127 to 127.  Bytes run from 1 to 246 (E4M3) or 240 (INT8); others are
  * read as the nearest of these.  Powers of two cost an E4M3 code none of its digits
  * and INT8 at most one of its seven bits, and are exact wherever they are applied.
  */

@@ -118,6 +118,10 @@ template <int D, int KIND, int NF>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_kernel(AttentionArgs a) {
   constexpr bool FP8 = KIND != kCacheBf16;   // 8-bit elements
   constexpr bool BLOCKS = has_blocks(KIND);
+  // INT8: the conversion has no scale of its own.  Powers of two may as well multiply a
+  // group's scores and weights, of which there are fewer than elements (32 requests, five
+  // tokens over 8192 keys, heads of 256: 141 us, at the conversion 150).
+  constexpr bool FOLD = KIND == kCacheInt8Blocks;
   using Tile = DecodeTile<D, FP8>;
   constexpr int KS = D / 32;      // k steps of the first product
   constexpr int DV = D / 16;      // value columns a lane holds = fragments of O
@@ -293,8 +297,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              w[2 * i] = to_bf16<KIND, false>(tile.k[f][st >> 1][(st & 1) * 2 + i], scale_of(scales[f], false));
-              w[2 * i + 1] = to_bf16<KIND, true>(tile.k[f][st >> 1][(st & 1) * 2 + i], scale_of(scales[f], false));
+              w[2 * i] = to_bf16<KIND, false>(tile.k[f][st >> 1][(st & 1) * 2 + i], FOLD ? 1.f : scale_of(scales[f], false));
+              w[2 * i + 1] = to_bf16<KIND, true>(tile.k[f][st >> 1][(st & 1) * 2 + i], FOLD ? 1.f : scale_of(scales[f], false));
             }
             kf = __builtin_bit_cast(bf16x8, w);
           } else {
@@ -303,6 +307,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
 #pragma unroll
           for (int n = 0; n < NF; ++n) s[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][st], s[n][f], 0, 0, 0);
         }
+        if constexpr (FOLD)
+#pragma unroll
+          for (int n = 0; n < NF; ++n) s[n][f] *= scale_of(scales[f], false);
       }
     };
     // softmax step and second product
@@ -356,6 +363,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
           for (int j = 0; j < 4; ++j) e[j] = exp2_fast(fmaf(s[n][f][j], c, -ref));
           l[n] += (e[0] + e[1]) + (e[2] + e[3]);
           // P in bf16, the matrix instruction's type with V: 2^-8 relative a term at most, averaged over the keys
+          if constexpr (FOLD)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] *= scale_of(scales[f], true);
           w[2 * f] = pack_bf16(e[0], e[1]);
           w[2 * f + 1] = pack_bf16(e[2], e[3]);
         }
@@ -377,9 +387,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
             b[f][3] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            vt[i] = u32x4{to_bf16<KIND, false>(b[0][i], scale_of(scales[0], true)), to_bf16<KIND, true>(b[0][i], scale_of(scales[0], true)),
-                          to_bf16<KIND, false>(b[1][i], scale_of(scales[1], true)), to_bf16<KIND, true>(b[1][i], scale_of(scales[1], true))};
+          for (int i = 0; i < 4; ++i) {
+            const float v0 = FOLD ? 1.f : scale_of(scales[0], true), v1 = FOLD ? 1.f : scale_of(scales[1], true);
+            vt[i] = u32x4{to_bf16<KIND, false>(b[0][i], v0), to_bf16<KIND, true>(b[0][i], v0), to_bf16<KIND, false>(b[1][i], v1),
+                          to_bf16<KIND, true>(b[1][i], v1)};
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)

@@ -46,8 +46,9 @@ struct CacheView {
 };
 enum { kBlocksNone, kBlocksE4m3, kBlocksInt8 };
 constexpr int kBlockTokens = 16;
-// The largest scale bytes: with them the largest code is still below 2^128.
-constexpr int kMostE4m3 = 246, kMostInt8 = 248;
+// The largest scale bytes: with them the largest code is below 2^128, and INT8 scales
+// times weights up to 2^8 are.
+constexpr int kMostE4m3 = 246, kMostInt8 = 240;
 
 struct KvWriteArgs {
   const uint16_t* k;

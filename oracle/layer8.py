@@ -8,7 +8,7 @@ from oracle.formats import E4M3_POSITIVE, E4M3_TABLE
 
 BLOCK = 16
 MOST = {"e4m3": 448.0, "int8": 127.0}           # largest code
-MOST_BYTE = {"e4m3": 246, "int8": 248}
+MOST_BYTE = {"e4m3": 246, "int8": 240}
 
 
 # ------------------------------------------------------------- rotation ----

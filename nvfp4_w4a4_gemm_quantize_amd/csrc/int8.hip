@@ -663,28 +663,51 @@ void set_tiles(Int8Plan& p, int64_t m, int64_t n) {
   p.tiles_m = (m + p.bm - 1) / p.bm;
   p.tiles_n = (n + p.bn - 1) / p.bn;
 }
-// Whether the streaming kernel takes it, and quantises too.
-bool streams(int64_t m, int64_t n, int64_t k) {
-  return m * k <= kStreamCodes && m <= (n * k <= 40000000 ? kStreamTokens : 4);
-}
+// The streaming kernel finds the codes too where their values fit its registers (one
+// token, 17408 x 5120: 19.2 us, in two launches 21.7).
 bool stream_quantises(int64_t m, int64_t k) { return m * k <= 8 * 256 * kQuantiseHeld; }
+// It reads no weight twice and has nothing to fill, but every workgroup copies or finds
+// all codes (8 tokens, 1024 x 5120: 5.9 us, tiles 10.0; 8 tokens, 17408 x 5120: 24.6, tiles
+// 22.6; 2 tokens, 13605 x 12992: 48.9, tiles 41.7).
+bool streams(int64_t m, int64_t n, int64_t k) {
+  if (n * k > 40000000) return m <= 4 && stream_quantises(m, k);
+  return m * k <= kStreamCodes && m <= kStreamTokens;
+}
 
+// Tiles: what a round of them over the chip takes, in the time of 15 / 4 of a tile of 128 x
+// 128 where there are many, as measured with k = 5120: 64 x 128 (one a CU) 14, 128 x 128 21
+// (two a CU: 40 for both), 256 x 256 60, of which a last round in quarters takes a third.
+// 200 tokens, 5120 x 5120: 64 x 128 17.9 us, 128 x 128 21.3; 512 tokens: 32.6, 22.5; 1024 tokens:
+// 128 x 128 43.2, two a CU 38.5, 256 x 256 42.1; 2048 tokens: two a CU 71.6, 256 x 256 55.8; 713
+// tokens, 10312 x 4608: 48.6, 61.8.  Few tiles are split along k (37 tokens, 5120 x 17408, 80
+// tiles of 64 x 64: three parts 23.2 us, one 41).
 Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   Int8Plan p{kStream, 0, 0, 0, 0, 1};
   if (streams(m, n, k)) return p;
+  const int64_t cus = 256;
   auto tiles_of = [&](Int8Kind kind) {
     p.kind = kind;
     set_tiles(p, m, n);
     return p.tiles_m * p.tiles_n;
   };
-  if (m <= 32)
+  auto rounds = [](int64_t tiles, int64_t at_once) { return (double)((tiles + at_once - 1) / at_once); };
+  if (m <= 32) {
     tiles_of(kTiles32);
-  else if (tiles_of(kTiles256) < 110 && (m <= 64 || tiles_of(kTiles128) < 110) && tiles_of(kTiles64) < 110)
+  } else if (tiles_of(kTiles64) < 110) {
     tiles_of(kTiles64Square);
-  else if (p.kind == kTiles128 && p.tiles_m * p.tiles_n > 256)
-    p.kind = kTilesMany;
-  const int64_t stages = (k + kStageBytes - 1) / kStageBytes;
-  if (p.kind != kTiles256) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(256 / (p.tiles_m * p.tiles_n), stages / 10));
+  } else {
+    const int64_t t64 = tiles_of(kTiles64), t128 = tiles_of(kTiles128), t256 = tiles_of(kTiles256), rest = t256 % cus;
+    const double large = t256 > cus && rest <= 128 ? (double)(t256 / cus) + (rest ? 0.35 : 0.) : rounds(t256, cus);
+    const double cost[4] = {14. * rounds(t64, cus), 21. * rounds(t128, cus), 40. * rounds(t128, 2 * cus), 60. * large};
+    const Int8Kind kinds[4] = {kTiles64, kTiles128, kTilesMany, kTiles256};
+    tiles_of(kinds[std::min_element(cost, cost + 4) - cost]);
+  }
+  if (p.kind == kTiles256) return p;
+  const int64_t stages = (k + kStageBytes - 1) / kStageBytes, tiles = p.tiles_m * p.tiles_n;
+  int64_t splits = std::min(cus / tiles, stages / 10);
+  // two of these are in a CU (607 tokens, 1069 x 15744: 37.9 us, unsplit 45.4)
+  if (p.kind == kTiles64Square && tiles * splits < 200 && splits * 40 < stages) ++splits;
+  p.splits = (int)std::max<int64_t>(1, splits);
   return p;
 }
 

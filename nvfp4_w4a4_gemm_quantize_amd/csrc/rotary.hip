@@ -22,19 +22,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// cos and sin of x / 2^32 turns times amplitude, rounded once.  The nearest quarter is
+// cos and sin of x / 2^32 turns times amplitude, rounded by who uses them.  The nearest quarter is
 // taken off, which leaves at most an eighth of a turn, where the Taylor series up to x^11
 // and x^10 are off by less than 10^-10.  In fp64, whose FMA takes no longer here: fp32's
 // last digit would move a hundred times as many 8-bit codes of rotated keys to the other
 // side of a tie.
-__device__ __forceinline__ float2 cos_sin(uint32_t x, double amplitude) {
+__device__ __forceinline__ double2 cos_sin(uint32_t x, double amplitude) {
   const uint32_t quarter = (x + 0x20000000u) >> 30;
   const double t = (double)(int32_t)(x - (quarter << 30)) * 1.46291807926715968e-9;   // 2 pi / 2^32
   const double u = t * t;
   const double s = fma(t * u, fma(u, fma(u, fma(u, fma(u, -1. / 39916800, 1. / 362880), -1. / 5040), 1. / 120), -1. / 6), t);
   const double c = fma(u, fma(u, fma(u, fma(u, fma(u, -1. / 3628800, 1. / 40320), -1. / 720), 1. / 24), -0.5), 1.);
-  const float cc = (float)((quarter & 1 ? s : c) * amplitude), ss = (float)((quarter & 1 ? c : s) * amplitude);
-  return make_float2((quarter + 1) & 2 ? -cc : cc, quarter & 2 ? -ss : ss);
+  const double cc = (quarter & 1 ? s : c) * amplitude, ss = (quarter & 1 ? c : s) * amplitude;
+  return make_double2((quarter + 1) & 2 ? -cc : cc, quarter & 2 ? -ss : ss);
 }
 
 // Columns of a unit: two runs of eight, at lo and hi, half of the rotated part (or of the
@@ -54,18 +54,19 @@ __device__ __forceinline__ UnitAt unit_at(int rotated, int dim, int unit) {
 }
 
 // The turns of a unit's eight pairs at a position.
+template <typename T>
 struct Turn {
-  float c[8], s[8];
+  T c[8], s[8];
 };
-template <bool INTERLEAVED>
-__device__ __forceinline__ void find_turn(Turn& t, const RotaryArgs& rot, int unit, int position) {
+template <bool INTERLEAVED, typename T>
+__device__ __forceinline__ void find_turn(Turn<T>& t, const RotaryArgs& rot, int unit, int position) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int pair = INTERLEAVED ? unit * 4 + (i < 4 ? i : rot.dim / 4 + i - 4) : unit * 8 + i;
     const uint64_t phase = rot.steps[pair] * (uint64_t)(uint32_t)position;
-    const float2 cs = cos_sin((uint32_t)(phase >> 32), rot.amplitude);
-    t.c[i] = position < 0 ? 1.f : cs.x;
-    t.s[i] = position < 0 ? 0.f : cs.y;
+    const double2 cs = cos_sin((uint32_t)(phase >> 32), rot.amplitude);
+    t.c[i] = position < 0 ? T(1) : (T)cs.x;
+    t.s[i] = position < 0 ? T(0) : (T)cs.y;
   }
 }
 
@@ -81,15 +82,15 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
 }
 
 // x[0 .. 7] and x[8 .. 15]: the unit's two runs.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void turn_unit(float* x, const Turn& t) {
+template <bool INTERLEAVED, typename T>
+__device__ __forceinline__ void turn_unit(float* x, const Turn<T>& t) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float& a = x[INTERLEAVED ? 2 * i : i];
     float& b = x[INTERLEAVED ? 2 * i + 1 : 8 + i];
-    const float ra = fmaf(a, t.c[i], -(b * t.s[i])), rb = fmaf(b, t.c[i], a * t.s[i]);
-    a = ra;
-    b = rb;
+    const T ra = fma((T)a, t.c[i], -((T)b * t.s[i])), rb = fma((T)b, t.c[i], (T)a * t.s[i]);
+    a = (float)ra;
+    b = (float)rb;
   }
 }
 
@@ -101,10 +102,10 @@ __device__ __forceinline__ void turn_unit(float* x, const Turn& t) {
 // block's group, four heads' loads in flight.
 namespace {
 
-template <bool INTERLEAVED>
+template <bool INTERLEAVED, int THREADS>
 __device__ __forceinline__ void rotary_rows(const RotaryRows& a, const RotaryArgs& rot, int units, int64_t block, int groups, int per) {
   const int group = (int)(block % groups);
-  const int64_t item = block / groups * kThreads + threadIdx.x;
+  const int64_t item = block / groups * THREADS + threadIdx.x;
   const int64_t t = item / units;
   if (t >= a.tokens) return;
   const int unit = (int)(item - t * units), h0 = group * per, h1 = min(h0 + per, a.heads);
@@ -120,7 +121,7 @@ __device__ __forceinline__ void rotary_rows(const RotaryRows& a, const RotaryArg
   };
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i) load(i, min(h0 + i, h1 - 1));
-  Turn turn;
+  Turn<float> turn;
   if (at.turns) find_turn<INTERLEAVED>(turn, rot, unit, rot.positions[t]);
   for (int h = h0; h < h1; h += kAtOnce) {
 #pragma unroll
@@ -146,7 +147,7 @@ __device__ __forceinline__ void rotary_rows(const RotaryRows& a, const RotaryArg
 
 template <bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryRows a, RotaryArgs rot, int groups, int per) {
-  rotary_rows<INTERLEAVED>(a, rot, a.dim / 16, blockIdx.x, groups, per);
+  rotary_rows<INTERLEAVED, kThreads>(a, rot, a.dim / 16, blockIdx.x, groups, per);
 }
 
 namespace {
@@ -159,20 +160,20 @@ struct RotaryGrid {
   int groups, per;
   int64_t blocks;
 };
-RotaryGrid rotary_grid(int64_t tokens, int heads, int dim) {
+RotaryGrid rotary_grid(int64_t tokens, int heads, int dim, int threads) {
   const int64_t items = tokens * (dim / 16);
   RotaryGrid g;
   const int64_t all = items * heads, per = std::max(std::min<int64_t>(all >> 16, 4), all >> 20);
   g.per = (int)std::max<int64_t>(1, std::min<int64_t>(per, heads));
   g.groups = (heads + g.per - 1) / g.per;
-  g.blocks = (items + kThreads - 1) / kThreads * g.groups;
+  g.blocks = (items + threads - 1) / threads * g.groups;
   return g;
 }
 
 }  // namespace
 
 hipError_t launch_rotary(const RotaryRows& a, const RotaryArgs& rot, hipStream_t st) {
-  const RotaryGrid g = rotary_grid(a.tokens, a.heads, a.dim);
+  const RotaryGrid g = rotary_grid(a.tokens, a.heads, a.dim, kThreads);
   if (rot.interleaved)
     rotary_kernel<true><<<(unsigned)g.blocks, kThreads, 0, st>>>(a, rot, g.groups, g.per);
   else
@@ -186,9 +187,9 @@ hipError_t launch_rotary(const RotaryRows& a, const RotaryArgs& rot, hipStream_t
 // v goes there as it is.  Caches with one scale a head (or none) have nothing that
 // joins tokens: heads q, k, v are one list, of which a thread (token, unit) takes a part.
 //
-// Block-scaled caches: a wave takes one run (the neighbouring rows of the call that lie
-// in one block of 16 tokens) of one head of K or V, so that the block's largest value
-// is a reduction over the wave and its codes are written once.  Scale 2^(e - 127) with
+// Block-scaled caches: a workgroup takes one run (the neighbouring rows of the call that
+// lie in one block of 16 tokens) of one head of K or V, so that the block's largest value
+// is a reduction over its lanes and its codes are written once.  Scale 2^(e - 127) with
 //     e = max(e_old, smallest e with max |x| <= M 2^(e - 127)), M = 448 or 127;
 // a run that holds the block's first token begins the block (no e_old, the places that
 // are not the run's become 0), any other leaves the rest as it is, divided by
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
   };
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i) load(i, min(h0 + i, h1 - 1));
-  Turn turn;
+  Turn<float> turn;
   if (at.turns && h0 < a.q.heads + c.heads) find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[t]);
   const int64_t slot = a.slots[t];
   const bool held = slot >= 0 && slot >> c.page_shift < c.num_pages;
@@ -318,15 +319,36 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
 
 namespace {
 
-// Rows 16 w .. 16 w + 15 of the call are window w.  This wave takes heads [h0, h1) of K
+// Lanes of a run: all 16 places of its block, 16 columns a lane.  One, two or four waves
+// are a workgroup, so that a lane's values are few whatever the head (8192 tokens of q, k
+// and v, 24/4 heads of 256: one wave in four passes 74 us, here 43; 1000 tokens 58, 17).
+constexpr int run_threads(int dim) { return kBlockTokens * dim / 16; }
+
+// Largest of a workgroup's values.  Two turns of `joint`, one barrier: whoever writes a
+// turn again has passed the other's barrier, after which no one reads this one.
+template <int THREADS>
+__device__ __forceinline__ uint32_t max_of(uint32_t x, uint32_t (*joint)[4], int& turn) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = max(x, (uint32_t)__shfl_xor((int)x, d));
+  if constexpr (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) joint[turn][threadIdx.x >> 6] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) x = max(x, joint[turn][w]);
+    turn ^= 1;
+  }
+  return uniform((int)x);
+}
+
+// Rows 16 w .. 16 w + 15 of the call are window w.  This workgroup takes heads [h0, h1) of K
 // or V, and of the runs that begin in its window every `shares`-th from `share` on.
 template <bool INTERLEAVED, bool INT8, int D>
 __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window, int share, int shares, int h0, int h1, bool is_v) {
   constexpr int U = D / 16;                 // units, so lanes, of a row
-  constexpr int ROWS = 64 / U;              // places of the block that a pass covers
-  constexpr int PASSES = kBlockTokens / ROWS;
+  __shared__ uint32_t joint[2][4];
+  int joint_turn = 0;
   const CacheView& c = a.cache;
-  const int lane = threadIdx.x & 63, unit = lane % U, lane_row = lane / U;
+  const int lane = threadIdx.x & 63, unit = threadIdx.x % U, place = threadIdx.x / U;
   const int64_t t0 = window * kBlockTokens;
   const uint16_t* x = is_v ? a.v : a.k;
   const int64_t ld = is_v ? a.ld_v : a.ld_k;
@@ -334,7 +356,7 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
   uint8_t* scales = is_v ? c.v_blocks : c.k_blocks;
   const UnitAt at = unit_at(is_v ? 0 : a.rot.dim, D, unit);
 
-  // the window's rows that begin a run
+  // the window's rows that begin a run; every wave finds them for itself
   auto slot_of = [&](int64_t t) {
     if (t < 0 || t >= a.tokens) return (int64_t)-1;
     const int64_t s = a.slots[t];
@@ -352,85 +374,65 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
     const int place0 = (int)(s0 % kBlockTokens);
     const bool next = lane < kBlockTokens - place0 && slot_of(t + lane) == s0 + lane;
     const int place1 = place0 + __builtin_ctzll(~__ballot(next));   // the run: places [place0, place1)
-    const bool fresh = place0 == 0;
+    const bool fresh = place0 == 0, in = place >= place0 && place < place1;
     int64_t block = ((s0 >> c.page_shift) * c.heads + h0) << (c.page_shift - 4) | (s0 & (((int64_t)1 << c.page_shift) - 1)) >> 4;
-    uint8_t* to = cache + place_at(c, s0 - place0, h0);
+    uint8_t* to = cache + place_at(c, s0 - place0, h0) + place * c.token_stride;
 
-    // a lane's rows: of a place outside the run the run's first, which is not used
-    const uint16_t* row[PASSES];
-    bool in[PASSES];
-    Turn turn[PASSES];
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int place = p * ROWS + lane_row;
-      in[p] = place >= place0 && place < place1;
-      const int64_t from = in[p] ? t + place - place0 : t;
-      row[p] = x + from * ld;
-      if (in[p] && at.turns) find_turn<INTERLEAVED>(turn[p], a.rot, unit, a.rot.positions[from]);
-    }
+    // a lane's row: of a place outside the run the run's first, which is not used
+    const int64_t from = in ? t + place - place0 : t;
+    const uint16_t* row = x + from * ld;
+    u32x4 lo = *(const u32x4*)(row + (int64_t)h0 * D + at.lo), hi = *(const u32x4*)(row + (int64_t)h0 * D + at.hi);
+    // in fp64: of 16 million codes of rotated keys 0 to 3 are beside the formula's, with fp32's products 14 to 18
+    Turn<double> turn;
+    if (in && at.turns) find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[from]);
     for (int h = h0; h < h1; ++h, block += (int64_t)1 << (c.page_shift - 4), to += c.head_stride) {
-      u32x4 lo[PASSES], hi[PASSES];
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        lo[p] = *(const u32x4*)(row[p] + (int64_t)h * D + at.lo);
-        hi[p] = *(const u32x4*)(row[p] + (int64_t)h * D + at.hi);
-      }
       constexpr int kMost = INT8 ? kMostInt8 : kMostE4m3;
       const int old = fresh ? 1 : min(max((int)scales[block], 1), kMost);
-      float f[PASSES][16];
+      float f[16];
+      unpack(lo, f);
+      unpack(hi, f + 8);
+      if (h + 1 < h1) {
+        lo = *(const u32x4*)(row + (int64_t)(h + 1) * D + at.lo);
+        hi = *(const u32x4*)(row + (int64_t)(h + 1) * D + at.hi);
+      }
+      if (in && at.turns) turn_unit<INTERLEAVED>(f, turn);
       uint32_t top = 0;                     // largest magnitude's bits: infinities and NaN come last
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        unpack(lo[p], f[p]);
-        unpack(hi[p], f[p] + 8);
-        if (in[p] && at.turns) turn_unit<INTERLEAVED>(f[p], turn[p]);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[p][i]) & 0x7fffffffu);
-        top = in[p] ? max(top, m) : top;
-      }
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+      top = max_of<run_threads(D)>(in ? top : 0, joint, joint_turn);
       const bool odd = top >= 0x7f800000u;   // rare: the largest finite value, and clamped codes
       if (odd) {
         top = 0;
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t m = __float_as_uint(f[p][i]) & 0x7fffffffu;
-            if (in[p] && m < 0x7f800000u) top = max(top, m);
-          }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t m = __float_as_uint(f[i]) & 0x7fffffffu;
+          if (m < 0x7f800000u) top = max(top, m);
+        }
+        top = max_of<run_threads(D)>(in ? top : 0, joint, joint_turn);
       }
       const int e = max(needed_scale(top, INT8), old);
       const bool clamp = odd || e == kMost;   // at the largest scale a value may lie beyond its codes
       const bool rises = !fresh && e > old;
       const float by = __uint_as_float((uint32_t)(254 - e) << 23), shrink = e - old > 126 ? 0.f : __uint_as_float((uint32_t)(127 + old - e) << 23);
+      if (in) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        uint8_t* place = to + (int64_t)(p * ROWS + lane_row) * c.token_stride;
-        if (in[p]) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[p][i] *= by;
-          if (clamp) {
-            *(u32x2*)(place + at.lo) = codes8<INT8, true>(f[p]);
-            *(u32x2*)(place + at.hi) = codes8<INT8, true>(f[p] + 8);
-          } else {
-            *(u32x2*)(place + at.lo) = codes8<INT8, false>(f[p]);
-            *(u32x2*)(place + at.hi) = codes8<INT8, false>(f[p] + 8);
-          }
-        } else if (fresh) {
-          *(u32x4*)(place + unit * 16) = u32x4{0u, 0u, 0u, 0u};
-        } else if (rises) {
-          u32x4 w = *(const u32x4*)(place + unit * 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = rescale4<INT8>(w[i], shrink);
-          *(u32x4*)(place + unit * 16) = w;
+        for (int i = 0; i < 16; ++i) f[i] *= by;
+        if (clamp) {
+          *(u32x2*)(to + at.lo) = codes8<INT8, true>(f);
+          *(u32x2*)(to + at.hi) = codes8<INT8, true>(f + 8);
+        } else {
+          *(u32x2*)(to + at.lo) = codes8<INT8, false>(f);
+          *(u32x2*)(to + at.hi) = codes8<INT8, false>(f + 8);
         }
+      } else if (fresh) {
+        *(u32x4*)(to + unit * 16) = u32x4{0u, 0u, 0u, 0u};
+      } else if (rises) {
+        u32x4 w = *(const u32x4*)(to + unit * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = rescale4<INT8>(w[i], shrink);
+        *(u32x4*)(to + unit * 16) = w;
       }
-      if (lane == 0) scales[block] = (uint8_t)e;
+      if (threadIdx.x == 0) scales[block] = (uint8_t)e;
     }
   }
 }
@@ -439,49 +441,43 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
 
 // The first `kv` workgroups write K and V, the others rotate q.
 template <bool INTERLEAVED, bool INT8, int D>
-__global__ __launch_bounds__(kThreads) void append_blocks_kernel(AppendArgs a, int shares, int head_groups, int heads, int64_t waves, int kv,
-                                                                 int q_groups, int q_per) {
+__global__ __launch_bounds__(run_threads(D)) void append_blocks_kernel(AppendArgs a, int shares, int head_groups, int heads, int kv, int q_groups,
+                                                                       int q_per) {
   if ((int)blockIdx.x >= kv) {
-    rotary_rows<INTERLEAVED>(a.q, a.rot, D / 16, blockIdx.x - kv, q_groups, q_per);
+    rotary_rows<INTERLEAVED, run_threads(D)>(a.q, a.rot, D / 16, blockIdx.x - kv, q_groups, q_per);
     return;
   }
-  int64_t id = (int64_t)blockIdx.x * (kThreads / 64) + uniform((int)(threadIdx.x >> 6));
-  if (id >= waves) return;
+  int id = blockIdx.x;
   const bool is_v = id & 1;
   id >>= 1;
-  const int h0 = (int)(id % head_groups) * heads;
+  const int h0 = id % head_groups * heads;
   id /= head_groups;
-  append_runs<INTERLEAVED, INT8, D>(a, id / shares, (int)(id % shares), shares, h0, min(h0 + heads, a.cache.heads), is_v);
+  append_runs<INTERLEAVED, INT8, D>(a, id / shares, id % shares, shares, h0, min(h0 + heads, a.cache.heads), is_v);
 }
 
 namespace {
 
-template <bool INTERLEAVED, bool INT8>
+template <bool INTERLEAVED, bool INT8, int D>
 hipError_t launch_blocks(const AppendArgs& a, hipStream_t st) {
   const CacheView& c = a.cache;
   const int64_t windows = (a.tokens + kBlockTokens - 1) / kBlockTokens;
-  // Every row may be a run of its own (single tokens): a wave for each of them and for
-  // every head while that leaves the chip room; prompts, with one run a window, share
+  // Every row may be a run of its own (single tokens): a workgroup for each of them and
+  // for every head while that leaves the chip room; prompts, with one run a window, share
   // a run's angles between heads.
-  const int64_t each = windows * c.heads * 2;
-  const int shares = each * 16 <= 8192 ? 16 : each * 4 <= 8192 ? 4 : 1;
-  const int heads = (int)std::max<int64_t>(1, std::min<int64_t>(each / 4096, c.heads)), groups = (c.heads + heads - 1) / heads;
-  const int64_t waves = windows * 2 * groups * shares;
-  const int64_t kv = (waves + kThreads / 64 - 1) / (kThreads / 64);
+  const int64_t each = windows * c.heads * 2, waves = each * (run_threads(D) / 64);
+  const int shares = waves * 16 <= 16384 ? 16 : waves * 4 <= 16384 ? 4 : 1;
+  const int heads = (int)std::max<int64_t>(1, std::min<int64_t>(waves / 4096, c.heads)), groups = (c.heads + heads - 1) / heads;
+  const int64_t kv = windows * 2 * groups * shares;
   RotaryGrid q{1, 1, 0};
-  if (a.q.heads > 0) q = rotary_grid(a.tokens, a.q.heads, c.dim);
-  const unsigned grid = (unsigned)(kv + q.blocks);
-  switch (c.dim) {
-    case 64:
-      append_blocks_kernel<INTERLEAVED, INT8, 64><<<grid, kThreads, 0, st>>>(a, shares, groups, heads, waves, (int)kv, q.groups, q.per);
-      break;
-    case 128:
-      append_blocks_kernel<INTERLEAVED, INT8, 128><<<grid, kThreads, 0, st>>>(a, shares, groups, heads, waves, (int)kv, q.groups, q.per);
-      break;
-    default:
-      append_blocks_kernel<INTERLEAVED, INT8, 256><<<grid, kThreads, 0, st>>>(a, shares, groups, heads, waves, (int)kv, q.groups, q.per);
-  }
+  if (a.q.heads > 0) q = rotary_grid(a.tokens, a.q.heads, D, run_threads(D));
+  append_blocks_kernel<INTERLEAVED, INT8, D><<<(unsigned)(kv + q.blocks), run_threads(D), 0, st>>>(a, shares, groups, heads, (int)kv, q.groups, q.per);
   return hipGetLastError();
+}
+template <bool INTERLEAVED, bool INT8>
+hipError_t launch_blocks(const AppendArgs& a, hipStream_t st) {
+  return a.cache.dim == 64    ? launch_blocks<INTERLEAVED, INT8, 64>(a, st)
+         : a.cache.dim == 128 ? launch_blocks<INTERLEAVED, INT8, 128>(a, st)
+                              : launch_blocks<INTERLEAVED, INT8, 256>(a, st);
 }
 
 }  // namespace
@@ -491,7 +487,7 @@ hipError_t launch_paged_kv_append(const AppendArgs& a, hipStream_t st) {
   const bool inter = a.rot.interleaved;
   if (c.blocks == kBlocksInt8) return inter ? launch_blocks<true, true>(a, st) : launch_blocks<false, true>(a, st);
   if (c.blocks == kBlocksE4m3) return inter ? launch_blocks<true, false>(a, st) : launch_blocks<false, false>(a, st);
-  const RotaryGrid g = rotary_grid(a.tokens, a.q.heads + 2 * c.heads, c.dim);
+  const RotaryGrid g = rotary_grid(a.tokens, a.q.heads + 2 * c.heads, c.dim, kThreads);
   const unsigned grid = (unsigned)g.blocks;
   if (inter) {
     if (c.fp8) append_rows_kernel<true, true><<<grid, kThreads, 0, st>>>(a, g.groups, g.per);

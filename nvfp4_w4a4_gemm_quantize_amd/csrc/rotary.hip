@@ -356,23 +356,25 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
   uint8_t* scales = is_v ? c.v_blocks : c.k_blocks;
   const UnitAt at = unit_at(is_v ? 0 : a.rot.dim, D, unit);
 
-  // the window's rows that begin a run; every wave finds them for itself
+  // the window's rows that begin a run, and the window after it, where its last may end;
+  // every wave finds them for itself
   auto slot_of = [&](int64_t t) {
     if (t < 0 || t >= a.tokens) return (int64_t)-1;
     const int64_t s = a.slots[t];
     return s >= 0 && s >> c.page_shift < c.num_pages ? s : (int64_t)-1;
   };
-  const int64_t mine = lane < kBlockTokens ? slot_of(t0 + lane) : -1;
-  const int64_t prev = lane < kBlockTokens ? slot_of(t0 + lane - 1) : -1;
-  uint64_t begins = __ballot(mine >= 0 && (prev < 0 || prev != mine - 1 || mine % kBlockTokens == 0));
+  const int64_t mine = lane < 2 * kBlockTokens ? slot_of(t0 + lane) : -1;
+  const int64_t before = slot_of(t0 - 1), left = __shfl_up(mine, 1), prev = lane ? left : before;
+  uint64_t begins = __ballot(lane < kBlockTokens && mine >= 0 && (prev < 0 || prev != mine - 1 || mine % kBlockTokens == 0));
   for (int skip = share; begins; skip = shares - 1) {
     for (; skip > 0 && begins; --skip) begins &= begins - 1;
     if (!begins) break;
-    const int64_t t = t0 + __builtin_ctzll(begins);
+    const int first = __builtin_ctzll(begins);
+    const int64_t t = t0 + first;
     begins &= begins - 1;
-    const int64_t s0 = uniform(slot_of(t));
+    const int64_t s0 = uniform(__shfl(mine, first)), behind = __shfl(mine, first + lane);
     const int place0 = (int)(s0 % kBlockTokens);
-    const bool next = lane < kBlockTokens - place0 && slot_of(t + lane) == s0 + lane;
+    const bool next = lane < kBlockTokens - place0 && behind == s0 + lane;
     const int place1 = place0 + __builtin_ctzll(~__ballot(next));   // the run: places [place0, place1)
     const bool fresh = place0 == 0, in = place >= place0 && place < place1;
     int64_t block = ((s0 >> c.page_shift) * c.heads + h0) << (c.page_shift - 4) | (s0 & (((int64_t)1 << c.page_shift) - 1)) >> 4;
@@ -383,11 +385,12 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
     const uint16_t* row = x + from * ld;
     u32x4 lo = *(const u32x4*)(row + (int64_t)h0 * D + at.lo), hi = *(const u32x4*)(row + (int64_t)h0 * D + at.hi);
     // in fp64: of 16 million codes of rotated keys 0 to 3 are beside the formula's, with fp32's products 14 to 18
+    int old = scales[block];
     Turn<double> turn;
     if (in && at.turns) find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[from]);
     for (int h = h0; h < h1; ++h, block += (int64_t)1 << (c.page_shift - 4), to += c.head_stride) {
       constexpr int kMost = INT8 ? kMostInt8 : kMostE4m3;
-      const int old = fresh ? 1 : min(max((int)scales[block], 1), kMost);
+      old = fresh ? 1 : min(max(old, 1), kMost);
       float f[16];
       unpack(lo, f);
       unpack(hi, f + 8);
@@ -433,6 +436,7 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
         *(u32x4*)(to + unit * 16) = w;
       }
       if (threadIdx.x == 0) scales[block] = (uint8_t)e;
+      if (h + 1 < h1) old = scales[block + ((int64_t)1 << (c.page_shift - 4))];
     }
   }
 }

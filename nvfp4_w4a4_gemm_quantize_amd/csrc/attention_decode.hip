@@ -42,6 +42,12 @@
 // 32 requests of up to 8192 keys, 32 rows of 256, 2.8 TB/s over E4M3 and 3.4 over bf16;
 // 64 requests, heads of 128, 20 rows, 3.6 over E4M3 and 5.1; one token, heads of 128,
 // 4.1 and 5.2, heads of 64 3.6 and 5.3.  One token over 1000 keys: 10 us, latency.
+//
+// Block-scaled caches: a scale byte for 16 keys more.  An E4M3 block's scale is an operand
+// of the conversion and costs nothing: the first case takes 224 - 230 us, 4.9 TB/s (with one
+// scale a head 226), the second 133.  An INT8 element takes a conversion of its own and a
+// rounding for two; its block's scale is multiplied to scores and weights, of which there
+// are fewer than elements: 234 and 139 - 142 us, 3.8 TB/s.
 #include <float.h>
 
 #include "attention.h"

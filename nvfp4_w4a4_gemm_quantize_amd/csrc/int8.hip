@@ -79,7 +79,7 @@ __device__ __forceinline__ u32x2 codes8(const u32x4& w, float by) {
 //
 // A wave or a workgroup a row: its largest magnitude, then its codes.  Bound by HBM: 3
 // bytes an element; the row's first HELD x THREADS x 8 values stay in registers between
-// the two, the rest is read again from the caches.
+// the two, the rest is read again from the caches.  4096 rows of 5120: 18 us, 3.5 TB/s.
 template <int THREADS, int HELD>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void int8_quantize_kernel(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
                                                             int8_t* codes, float* scales, uint32_t* clear, int clears) {
@@ -149,10 +149,18 @@ hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, i
 //
 // Output tile BM tokens x BN channels; k in stages of 128 bytes of every row, which pass
 // through LDS several stages deep by direct loads (global_load_lds: no registers, no
-// VALU).  Whole lines: with stages of 64 bytes such a load took twice as long, and they
-// bounded the kernel (4096 x 17408 x 5120: 367 us).  The waves split the tile into MF x NF
-// fragments of 32 x 32 each; a stage is four products of 32 k.  v_mfma_i32_32x32x32_i8 takes W's rows as its rows and the tokens as
-// its columns, so that a lane ends with one token and runs of four channels.
+// VALU).  Whole lines: with stages of 64 bytes such a load took twice as long (27 bytes a
+// clock and CU against 44), and they bounded the kernel.  The waves split the tile into
+// MF x NF fragments of 32 x 32 each; a stage is four products of 32 k, and the next
+// stages' loads are spread among them.  v_mfma_i32_32x32x32_i8 takes W's rows as its rows
+// and the tokens as its columns, so that a lane ends with one token and runs of four
+// channels.
+//
+// Bound by the matrix unit and the power it may draw: 4096 tokens, 17408 x 5120, takes 308 -
+// 320 us, 2.3 PFLOP/s, the matrix unit busy for 61% of the cycles at 1.82 GHz (with codes
+// that are all zero it took 306 where random ones took 337; loads of the next tile before
+// the epilogue changed nothing).  777 tokens, 4104 x 2064: 16 - 17 us, 0.8 PFLOP/s, of which
+// 5 are the launch, the first stages and the epilogue: 231 tiles of 64 x 128 are one round.
 //
 // LDS layout of a stage: [rows][128] bytes, the 16-byte pieces of row r permuted by
 // (r >> 1) & 7: sixteen lanes that read one piece of sixteen rows meet all banks once.
@@ -506,7 +514,7 @@ __global__ __launch_bounds__(512, 2) void int8_large_kernel(Int8Args a, int tile
 // as operands of v_mfma_i32_16x16x64_i8, whose rows are 16 channels and whose columns 16
 // tokens; the tokens' codes lie in LDS.  A workgroup owns 16 channels, its waves take k in
 // parts (stages of 64 bytes of every row, eight of them in flight and eight more asked for)
-// and add their sums in LDS.
+// and add their sums in LDS.  One token, 17408 x 5120: 19.2 us, 4.7 TB/s.
 //
 // QUANTISE: every workgroup finds the scales and codes itself while its first weights are
 // on their way, which spares a launch; the first one writes them out.
@@ -674,9 +682,10 @@ bool streams(int64_t m, int64_t n, int64_t k) {
   return m * k <= kStreamCodes && m <= kStreamTokens;
 }
 
-// Tiles: what a round of them over the chip takes, in the time of 15 / 4 of a tile of 128 x
-// 128 where there are many, as measured with k = 5120: 64 x 128 (one a CU) 14, 128 x 128 21
-// (two a CU: 40 for both), 256 x 256 60, of which a last round in quarters takes a third.
+// Tiles: by what their rounds over the chip take, in one unit, as measured with k = 5120: a
+// round of 64 x 128 (one a CU) 14, of 128 x 128 21 (two a CU: 40 for both), of 256 x 256 60, of
+// which a last round in quarters takes a third.  Of 120 drawn sizes the choice was 1.3% off
+// the best on average, 10% at most.
 // 200 tokens, 5120 x 5120: 64 x 128 17.9 us, 128 x 128 21.3; 512 tokens: 32.6, 22.5; 1024 tokens:
 // 128 x 128 43.2, two a CU 38.5, 256 x 256 42.1; 2048 tokens: two a CU 71.6, 256 x 256 55.8; 713
 // tokens, 10312 x 4608: 48.6, 61.8.  Few tiles are split along k (37 tokens, 5120 x 17408, 80

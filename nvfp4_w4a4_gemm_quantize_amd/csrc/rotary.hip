@@ -98,8 +98,9 @@ __device__ __forceinline__ void turn_unit(float* x, const Turn<T>& t) {
 
 // --------------------------------------------------------------- rotary ----
 //
-// Bound by HBM: 4 bytes an element.  Thread (token, unit) takes `per` heads of its
-// block's group, four heads' loads in flight.
+// Bound by HBM: 4 bytes an element (16384 tokens, 48 heads of 128: 77 us, 5.2 TB/s; 8
+// tokens: 4.4 us, latency).  Thread (token, unit) takes `per` heads of its block's group,
+// four heads' loads in flight.
 namespace {
 
 template <bool INTERLEAVED, int THREADS>
@@ -196,6 +197,10 @@ hipError_t launch_rotary(const RotaryRows& a, const RotaryArgs& rot, hipStream_t
 // 2^(e - e_old) where the scale rises.  A power of two, because an E4M3 code then keeps
 // its digits whenever it is rescaled, and the attention's conversion to bf16 is exact
 // with the scale in it.
+//
+// Bound by HBM: 16384 tokens of 40 heads of q and 8 of k and v, 128 each, into E4M3 blocks
+// 84 us, 5.2 TB/s; 64 single tokens 6.2 us, latency: slots, then rows and scales, then
+// stores.  8 chunks of up to 777 tokens, 16 heads of 64, bf16: 11 us, 3.9 TB/s.
 namespace {
 
 // Four values in steps of their scale as codes, rounded to nearest even.  CLAMP: they may

@@ -39,6 +39,10 @@ Modules
 ``epilogue``  fp64 SiLU*mul, sigmoid and Gated-DeltaNet decay epilogues.
 ``recurrence`` the gated delta-rule recurrence of a Gated DeltaNet layer
               (fp64), the second workload.
+``paged``     the paged serving step (fp64): plan, cache write, attention and
+              draft verification.
+``layer8``    the attention layer in 8 bits (fp64): rotary positions,
+              block-scaled cache codes, int8 linear layers.
 ``mechanism`` the coarser-scaled reference formats (E4M3 scale per B
               elements; one per-tensor scale) and the error measures of the
               pages' mechanism study.

@@ -636,7 +636,8 @@ int paged_kv_append(const uint16_t* q, int64_t ld_q, int num_heads, uint16_t* q_
  * that call's (the workspace too, paged_attention_workspace_bytes), but for k_blocks and
  * v_blocks in place of k_scale and v_scale, and cache_dtype NVFP4_CACHE_E4M3_BLOCKS or
  * NVFP4_CACHE_INT8_BLOCKS.  Elements become bf16 with their scale, exactly, on their way
- * into the matrix unit.
+ * into the matrix unit; INT8's scales may be multiplied to sums over q and the codes
+ * instead, which are finite for |q| < 2^112.
  */
 int paged_attention_blocks(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32_t* q_start, const int32_t* seq_lens,
                            int64_t num_requests, int64_t max_new, int64_t max_seq, int num_heads, const void* k_cache,
@@ -674,7 +675,8 @@ int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, i
  *            k a multiple of 16 below 2^17.
  *   a_scale, w_scale   float [m] and [n].
  *   out      [m, n] of out_dtype (NVFP4_OUT_*), row stride ld_out >= n, any alignment of
- *            its elements (rows of 16-byte aligned ones leave in wide stores).
+ *            its elements (rows of 16-byte aligned ones leave in wide stores); it overlaps
+ *            no input.
  *   workspace  optional (null), 16-byte aligned, at least gemm_w8a8_workspace_bytes(m, n,
  *            k) (which may be 0); its contents do not matter.  With it, products of few
  *            rows are split along k over the chip.  Not shared by calls in flight on

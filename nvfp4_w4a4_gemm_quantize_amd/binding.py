@@ -741,11 +741,15 @@ def _rotation(table, positions, tokens):
             _LAYOUTS[table.layout], table.amplitude)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _one_device(*tensors):
-    device = tensors[0].get_device()
+    """Refuse tensors of more than one GPU, or of another than the current one, on which a default stream would run."""
+    device = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != device:
-            raise NVFP4Error("the tensors of a call must be on one GPU")
+            raise NVFP4Error("the tensors of a call must be on one GPU, the current one")
 
 
 def rotary(x, positions, table, head_dim, out=None):
@@ -900,12 +904,18 @@ def _codes8(t, rows, cols, name):
     return t.data_ptr(), t.shape[0], t.shape[1]
 
 
-def _int8_out(like, m, n, out_dtype, out):
+def _int8_out(x, m, n, out_dtype, out):
     dtype = _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32
     if out is None:
-        out = like.new_empty((m, n), dtype=dtype)
+        out = x.new_empty((m, n), dtype=dtype)
         return out, out.data_ptr(), n, OUT_BF16 if dtype is _bf16 else OUT_F32
     op, ld, _ = _rows(out, dtype, m, n, "out")
+    if x.dtype is dtype:
+        _apart(x, out)
+    elif m:
+        a, b, size = x.data_ptr(), op, x.element_size()
+        if a < b + out.element_size() * ((m - 1) * ld + n) and b < a + size * ((m - 1) * x.stride(0) + x.shape[1]):
+            raise NVFP4Error("an output overlaps an input")
     return out, op, ld, OUT_BF16 if dtype is _bf16 else OUT_F32
 
 

@@ -160,7 +160,8 @@ hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, i
 // 320 us, 2.3 PFLOP/s, the matrix unit busy for 61% of the cycles at 1.82 GHz (with codes
 // that are all zero it took 306 where random ones took 337; loads of the next tile before
 // the epilogue changed nothing).  777 tokens, 4104 x 2064: 16 - 17 us, 0.8 PFLOP/s, of which
-// 5 are the launch, the first stages and the epilogue: 231 tiles of 64 x 128 are one round.
+// 7 are the launch, the first stages and the epilogue: 231 tiles of 128 x 128 are one round
+// (at other sizes of it a stage is 0.35 us, its loads alone 0.25, its products alone 0.2).
 //
 // LDS layout of a stage: [rows][128] bytes, the 16-byte pieces of row r permuted by
 // (r >> 1) & 7: sixteen lanes that read one piece of sixteen rows meet all banks once.
@@ -235,32 +236,50 @@ __device__ __forceinline__ uint64_t load_shared(const int* p) {
 // of k in several workgroups (splits > 1) all of a tile's leave their sums at `part`
 // and the one that counts itself last at `arrived` adds them up: whole numbers, whose
 // order does not matter.
-template <int MF, int NF, int WM, int WN, int STAGES>
+//
+// LINES (k no multiple of 128, so that a stage's part of a row lies in two lines): the
+// loads take whole lines all the same.  Line l of a row holds its bytes from 128 l - o on, o
+// the row's offset in its first line, and stage s is read from lines s and s + 1, which has
+// to be there one stage earlier.  k is a multiple of 16, so rows 32 apart have the same o,
+// and a lane's fragments all lie alike.
+template <int MF, int NF, int WM, int WN, int STAGES, bool LINES>
 __device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t n0, int begin, int end, int split, int splits,
                                           int* part, uint32_t* arrived, uint8_t* lds) {
   using S = TileShape<MF, NF, WM, WN, STAGES>;
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wave_m = wave / WN, wave_n = wave % WN;
   const int64_t k = a.k;
-  const int full = min(end, (int)(k / kStageBytes)) - begin;
+  const int full = min(end, (int)(k / kStageBytes)) - begin, lines = full + LINES;
 
   // this wave's loads: 8 rows of the stage each, lane = row * 8 + place of a piece (rows
   // 8 i of waves of one parity have the same permutation)
   const int8_t* base[S::LOADS];
-  uint32_t voff[S::LOADS];
+  uint32_t voff[S::LOADS], most[S::LOADS];   // most: of the last line, what lies behind the matrix is its last piece
   const int lane_row = lane >> 3, piece = (lane & 7) ^ ((wave * 4 + (lane_row >> 1)) & 7);
-#pragma unroll
-  for (int i = 0; i < S::LOADS; ++i) {
+  // the part of a row that a lane of load i begins at
+  auto rows_of = [&](int i, int64_t& from, int64_t& last) {
     const int row = (i * S::WAVES + wave) * 8;
     const bool tokens = row < S::BM;
-    const int64_t first = tokens ? m0 + row : n0 + row - S::BM, last = (tokens ? a.m : a.n) - 1;
-    const int64_t from = min(first, last);
-    base[i] = (tokens ? a.a : a.w) + from * k + (int64_t)begin * kStageBytes;
+    last = (tokens ? a.m : a.n) - 1;
+    from = min(tokens ? m0 + row : n0 + row - S::BM, last);
+    return (tokens ? a.a : a.w) + from * k + (int64_t)begin * kStageBytes;
+  };
+#pragma unroll
+  for (int i = 0; i < S::LOADS; ++i) {
+    int64_t from, last;
+    base[i] = rows_of(i, from, last);
     voff[i] = (uint32_t)(min((int64_t)lane_row, last - from) * k) + piece * 16;
+    if constexpr (LINES) {
+      const uint32_t offset = (uint32_t)(uintptr_t)(base[i] + voff[i] - piece * 16) % kStageBytes;
+      base[i] -= kStageBytes;
+      voff[i] += kStageBytes - offset;
+      most[i] = (uint32_t)min((last + 1 - from) * k - 16 - (int64_t)(begin + full - 1) * kStageBytes, (int64_t)UINT32_MAX);
+    }
   }
   auto slot = [&](int s) { return lds + (uint32_t)s % STAGES * S::STAGE; };
   auto issue_one = [&](int s, int i) {
-    dma16(base[i] + (int64_t)s * kStageBytes, voff[i], slot(s) + (i * S::WAVES + wave) * 1024);
+    const uint32_t at = LINES ? min(voff[i], s == full ? most[i] : UINT32_MAX) : voff[i];
+    dma16(base[i] + (int64_t)s * kStageBytes, at, slot(s) + (i * S::WAVES + wave) * 1024);
   };
   auto issue = [&](int s) {
 #pragma unroll
@@ -276,15 +295,23 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
   const int lane_at = c32 * kStageBytes + ((h ^ ((c32 >> 1) & 7)) * 16);
+  const int a_skew = LINES ? (int)((uintptr_t)a.a / 16 + c32 * (uint32_t)(k / 16)) & 7 : 0;   // o / 16
+  const int w_skew = LINES ? (int)((uintptr_t)a.w / 16 + c32 * (uint32_t)(k / 16)) & 7 : 0;
   struct Fragments {
     i32x4 a[MF], w[NF];
   };
-  auto read = [&](Fragments& f, const uint8_t* stage, int quarter) {
-    const uint8_t* p = stage + (lane_at ^ (quarter * 32));
+  // quarter of the stage whose rows lie in place `stage`, and on from there in place `behind`
+  auto read = [&](Fragments& f, const uint8_t* stage, const uint8_t* behind, int quarter) {
+    auto lane_of = [&](int skew) {
+      if constexpr (!LINES) return stage + (lane_at ^ (quarter * 32));
+      const int at = quarter * 2 + h + skew;
+      return (at & 8 ? behind : stage) + c32 * kStageBytes + (((at & 7) ^ ((c32 >> 1) & 7)) * 16);
+    };
+    const uint8_t *pa = lane_of(a_skew), *pw = lane_of(w_skew);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) f.a[i] = *(const i32x4*)(p + (wave_m * MF + i) * 32 * kStageBytes);
+    for (int i = 0; i < MF; ++i) f.a[i] = *(const i32x4*)(pa + (wave_m * MF + i) * 32 * kStageBytes);
 #pragma unroll
-    for (int j = 0; j < NF; ++j) f.w[j] = *(const i32x4*)(p + (S::BM + (wave_n * NF + j) * 32) * kStageBytes);
+    for (int j = 0; j < NF; ++j) f.w[j] = *(const i32x4*)(pw + (S::BM + (wave_n * NF + j) * 32) * kStageBytes);
   };
   auto multiply = [&](const Fragments& f) {
 #pragma unroll
@@ -297,19 +324,20 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t
   // them all have read the whole stage: behind that barrier its place is filled anew, and
   // the next stage, waited for before it, is there for all.
   Fragments f0, f1;
+  constexpr int kAhead = STAGES - 2 - LINES;   // places of which nothing has to be there
   if (full > 0) {
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
-      if (s < full) issue(s);
-    if (full >= STAGES) {
+      if (s < lines) issue(s);
+    if (lines >= STAGES) {
 #pragma unroll
       for (int i = 0; i < S::LOADS / 2; ++i) issue_one(STAGES - 1, i);
-      wait_arrived<(STAGES - 2) * S::LOADS + S::LOADS / 2>();
+      wait_arrived<kAhead * S::LOADS + S::LOADS / 2>();
     } else {
       wait_arrived<0>();
     }
     stage_barrier();
-    read(f0, slot(0), 0);
+    read(f0, slot(0), slot(1), 0);
     // products of a quarter with loads `first` .. `last` - 1 of stage `of` spread among them
     auto multiply_and_issue = [&](const Fragments& f, int of, auto first, auto last) {
       constexpr int FIRST = decltype(first)::value, COUNT = decltype(last)::value - FIRST, ALL = MF * NF;
@@ -329,34 +357,34 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t
     constexpr std::integral_constant<int, S::LOADS> kAll{};
     int s = 0;
 #pragma unroll 1
-    for (; s + STAGES < full; ++s) {
-      read(f1, slot(s), 1);
+    for (; s + STAGES < lines; ++s) {
+      read(f1, slot(s), slot(s + 1), 1);
       multiply_and_issue(f0, s + STAGES - 1, kHalf, kAll);
-      read(f0, slot(s), 2);
+      read(f0, slot(s), slot(s + 1), 2);
       multiply(f1);
-      read(f1, slot(s), 3);
+      read(f1, slot(s), slot(s + 1), 3);
       multiply(f0);
-      wait_arrived<(STAGES - 2) * S::LOADS>();
+      wait_arrived<kAhead * S::LOADS>();
       wait_read();
       stage_barrier();
-      read(f0, slot(s + 1), 0);
+      read(f0, slot(s + 1), slot(s + 2), 0);
       multiply_and_issue(f1, s + STAGES, kNone, kHalf);
     }
-    if (full >= STAGES) {
+    if (lines >= STAGES) {
 #pragma unroll
       for (int i = S::LOADS / 2; i < S::LOADS; ++i) issue_one(s + STAGES - 1, i);
     }
 #pragma unroll 1
     for (; s < full; ++s) {
-      read(f1, slot(s), 1);
+      read(f1, slot(s), slot(s + 1), 1);
       multiply(f0);
-      read(f0, slot(s), 2);
+      read(f0, slot(s), slot(s + 1), 2);
       multiply(f1);
-      read(f1, slot(s), 3);
+      read(f1, slot(s), slot(s + 1), 3);
       multiply(f0);
       wait_arrived<0>();
       stage_barrier();
-      if (s + 1 < full) read(f0, slot(s + 1), 0);
+      if (s + 1 < full) read(f0, slot(s + 1), slot(s + 2), 0);
       multiply(f1);
     }
   }
@@ -365,13 +393,19 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t
 #pragma unroll
     for (int i = 0; i < S::LOADS; ++i) {
       const bool in = (int64_t)(begin + full) * kStageBytes + piece * 16 < k;
+      int64_t from, last;
+      const int8_t* row = rows_of(i, from, last) + min((int64_t)lane_row, last - from) * k;
       *(u32x4*)(lds + (i * S::WAVES + wave) * 1024 + lane * 16) =
-          in ? *(const u32x4*)(base[i] + (int64_t)full * kStageBytes + voff[i]) : u32x4{0u, 0u, 0u, 0u};
+          in ? *(const u32x4*)(row + (int64_t)full * kStageBytes + piece * 16) : u32x4{0u, 0u, 0u, 0u};
     }
     __syncthreads();
 #pragma unroll
     for (int quarter = 0; quarter < 4; ++quarter) {
-      read(f0, lds, quarter);
+      const uint8_t* p = lds + (lane_at ^ (quarter * 32));
+#pragma unroll
+      for (int i = 0; i < MF; ++i) f0.a[i] = *(const i32x4*)(p + (wave_m * MF + i) * 32 * kStageBytes);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) f0.w[j] = *(const i32x4*)(p + (S::BM + (wave_n * NF + j) * 32) * kStageBytes);
       multiply(f0);
     }
   }
@@ -471,7 +505,7 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, int64_t m0, int64_t
 
 }  // namespace
 
-template <int MF, int NF, int WM, int WN, int STAGES>
+template <int MF, int NF, int WM, int WN, int STAGES, bool LINES>
 __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, int tiles_m, int tiles_n) {
   using S = TileShape<MF, NF, WM, WN, STAGES>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
@@ -482,7 +516,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args a, 
   const TileAt at = tile_at(tile, tiles_m, tiles_n);
   const int stages = (int)((a.k + kStageBytes - 1) / kStageBytes);
   const int begin = (int)((int64_t)stages * split / a.splits), end = (int)((int64_t)stages * (split + 1) / a.splits);
-  int8_tile<MF, NF, WM, WN, STAGES>(a, (int64_t)at.m * S::BM, (int64_t)at.n * S::BN, begin, end, split, a.splits,
+  int8_tile<MF, NF, WM, WN, STAGES, LINES>(a, (int64_t)at.m * S::BM, (int64_t)at.n * S::BN, begin, end, split, a.splits,
                                     a.parts + (int64_t)tile * a.splits * S::BM * S::BN, a.arrived + tile, lds);
 }
 
@@ -498,13 +532,13 @@ __global__ __launch_bounds__(512, 2) void int8_large_kernel(Int8Args a, int tile
   if (b < whole) {
     const int order = xcd_order(b, whole);
     const TileAt at = tile_at(order, tiles_m, tiles_n);
-    int8_tile<4, 2, 2, 4, 2>(a, (int64_t)at.m * L::BM, (int64_t)at.n * L::BN, 0, stages, 0, 1, nullptr, nullptr, lds);
+    int8_tile<4, 2, 2, 4, 2, false>(a, (int64_t)at.m * L::BM, (int64_t)at.n * L::BN, 0, stages, 0, 1, nullptr, nullptr, lds);
   } else {
     const int order = xcd_order(b - whole, (tiles_m * tiles_n - whole) * 4);
     const TileAt at = tile_at(whole + order / 4, tiles_m, tiles_n);
     const int64_t m0 = (int64_t)at.m * L::BM + (order & 1) * Q::BM, n0 = (int64_t)at.n * L::BN + (order >> 1 & 1) * Q::BN;
     if (m0 >= a.m || n0 >= a.n) return;
-    int8_tile<2, 1, 2, 4, 4>(a, m0, n0, 0, stages, 0, 1, nullptr, nullptr, lds);
+    int8_tile<2, 1, 2, 4, 4, false>(a, m0, n0, 0, stages, 0, 1, nullptr, nullptr, lds);
   }
 }
 
@@ -722,11 +756,21 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
 
 size_t arrived_bytes(const Int8Plan& p) { return (size_t)(p.tiles_m * p.tiles_n * 4 + 255) / 256 * 256; }
 
-template <int MF, int NF, int WM, int WN, int STAGES>
+// Whether to load by lines where a tile kernel can; the first row's line must not begin
+// before the matrix.  Tiles of 128 channels gain (200 tokens, 5120 x 5136: 20.2 us, by stages
+// 24.2; 777 tokens, 4104 x 4112: 24.9, 27.0; k = 5120 and 4096 17.8 and 22.2), those of 64, whose
+// few loads a stage want all the places in flight, do not (20 tokens, 9000 x 4112: 15.6,
+// 13.8), and two places are too few for it.
+bool whole_lines(const Int8Args& a) { return a.k % kStageBytes && ((uintptr_t)a.a | (uintptr_t)a.w) % kStageBytes == 0; }
+
+template <int MF, int NF, int WM, int WN, int STAGES, bool LINES>
 hipError_t launch_tiles(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
   using S = TileShape<MF, NF, WM, WN, STAGES>;
   const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * a.splits);
-  int8_tile_kernel<MF, NF, WM, WN, STAGES><<<grid, S::THREADS, 0, st>>>(a, (int)p.tiles_m, (int)p.tiles_n);
+  if (LINES && whole_lines(a))
+    int8_tile_kernel<MF, NF, WM, WN, STAGES, LINES><<<grid, S::THREADS, 0, st>>>(a, (int)p.tiles_m, (int)p.tiles_n);
+  else
+    int8_tile_kernel<MF, NF, WM, WN, STAGES, false><<<grid, S::THREADS, 0, st>>>(a, (int)p.tiles_m, (int)p.tiles_n);
   return hipGetLastError();
 }
 
@@ -758,11 +802,11 @@ Int8Args with_plan(const Int8Args& args, const Int8Plan& p, int* clears) {
 hipError_t product(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
   switch (p.kind) {
     case kStream: return launch_stream<false>(a, nullptr, 0, nullptr, nullptr, st);
-    case kTiles32: return launch_tiles<1, 1, 1, 2, 4>(a, p, st);
-    case kTiles64: return launch_tiles<1, 1, 2, 4, 4>(a, p, st);
-    case kTiles64Square: return launch_tiles<1, 1, 2, 2, 4>(a, p, st);
-    case kTiles128: return launch_tiles<1, 2, 4, 2, 4>(a, p, st);
-    case kTilesMany: return launch_tiles<2, 2, 2, 2, 2>(a, p, st);
+    case kTiles32: return launch_tiles<1, 1, 1, 2, 4, false>(a, p, st);
+    case kTiles64: return launch_tiles<1, 1, 2, 4, 4, true>(a, p, st);
+    case kTiles64Square: return launch_tiles<1, 1, 2, 2, 4, false>(a, p, st);
+    case kTiles128: return launch_tiles<1, 2, 4, 2, 4, true>(a, p, st);
+    case kTilesMany: return launch_tiles<2, 2, 2, 2, 2, false>(a, p, st);
     default: {
       // rounds of one tile a CU; the last one in quarters where that is shorter
       const int tiles = (int)(p.tiles_m * p.tiles_n), rest = tiles % 256, whole = rest > 128 || tiles < 256 ? tiles : tiles - rest;

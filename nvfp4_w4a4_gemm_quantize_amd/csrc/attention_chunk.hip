@@ -28,9 +28,9 @@
 // a part's 8 us beside its keys (its queries, page numbers and first keys; its output).
 //
 // Block-scaled caches, 4096 after 4096, 40 heads of 128 over 8: E4M3 546 us, INT8 575 - 587 (bf16
-// and E4M3 with one scale a head 510).  A tile's scales are one more load to wait for, and two
-// INT8 elements take five instructions where E4M3 takes one: the matrix unit is busy for 38%
-// of the cycles.  Heads of 64: 512 and 523 (bf16 482); 256, 24 over 4: 794 and 680 (bf16 620,
+// and E4M3 with one scale a head 510).  The scales take scalar registers that are spilled already,
+// and two INT8 elements five instructions where E4M3 takes one: the matrix unit is busy for
+// 38% of the cycles.  Heads of 64: 512 and 523 (bf16 482); 256, 24 over 4: 794 and 680 (bf16 620,
 // E4M3 with one scale a head 808).
 #include <float.h>
 #include <math.h>

@@ -731,48 +731,70 @@ def rotary_table(rotary_dim, base=10000.0, layout="half", scaling="none", factor
     return RotaryTable(host.to(device), rotary_dim, layout, amp.value if amplitude is None else float(amplitude))
 
 
-def _rotation(table, positions, tokens):
-    """The C arguments (positions, steps, rotary dim, layout, amplitude)."""
-    if table is None:
-        return None, None, 0, ROTARY_HALF, 1.0
-    if not isinstance(table, RotaryTable) or table.layout not in _LAYOUTS:
-        raise NVFP4Error("the rotation must come from rotary_table")
-    return (_vec(positions, _i32, tokens, "positions"), _vec(table.steps, _i64t, table.rotary_dim // 2, "steps"), table.rotary_dim,
-            _LAYOUTS[table.layout], table.amplitude)
-
-
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _one_device(*tensors):
-    """Refuse tensors of more than one GPU, or of another than the current one, on which a default stream would run."""
-    device = _current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise NVFP4Error("the tensors of a call must be on one GPU, the current one")
+def _gpu_of(t):
+    """The GPU of a call's first tensor; refused if it is not the current one, on whose default stream the call would run.
+    The other tensors' devices are compared with it, which finds host tensors too (-1)."""
+    device = t.get_device() if isinstance(t, _Tensor) else -1
+    if device < 0:
+        return -2       # no tensor's
+    if device != _current_device():
+        raise NVFP4Error("the tensors of a call must be on one GPU, the current one")
+    return device
+
+
+def _misplaced(t, dtype, name, shape):
+    if isinstance(t, _Tensor) and t.is_cuda and t.get_device() != _current_device():
+        raise NVFP4Error("the tensors of a call must be on one GPU, the current one")
+    _refuse(t, dtype, name, shape)
+
+
+def _rows_on(device, t, dtype, rows, cols, name):
+    """_rows of a tensor on that GPU."""
+    if not isinstance(t, _Tensor) or t.get_device() != device or t.dtype is not dtype or t.dim() != 2:
+        _misplaced(t, dtype, name, "a 2-D view")
+    r, c = t.shape
+    ld, unit = t.stride()
+    if (unit != 1 and c > 1) or (rows is not None and r != rows) or (cols is not None and c != cols):
+        _refuse(t, dtype, name, "[%s, %s] with unit column stride" % (rows, cols))
+    return t.data_ptr(), (ld if r > 1 else c), c    # a size-1 dimension's stride is arbitrary
+
+
+def _vec_on(device, t, dtype, n, name):
+    """_vec of a tensor on that GPU."""
+    if not isinstance(t, _Tensor) or t.get_device() != device or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _misplaced(t, dtype, name, "contiguous with %d elements" % n)
+    return t.data_ptr()
+
+
+def _rotation(device, table, positions, tokens):
+    """The C arguments (positions, steps, rotary dim, layout, amplitude)."""
+    if not isinstance(table, RotaryTable) or table.layout not in _LAYOUTS:
+        raise NVFP4Error("the rotation must come from rotary_table")
+    steps, dim, layout, amplitude = table
+    return (_vec_on(device, positions, _i32, tokens, "positions"), _vec_on(device, steps, _i64t, dim // 2, "steps"), dim,
+            _LAYOUTS[layout], amplitude)
 
 
 def rotary(x, positions, table, head_dim, out=None):
     """Rows of heads (bf16 view [T, heads * head_dim]) rotated to their positions (int32 [T]; negative: copied).
 
     table: from rotary_table.  out may be x (in place).  Returns out."""
-    lib = _lib or load()
-    xp, ld_x, cols = _rows(x, _bf16, None, None, "x")
+    lib, device = _lib or load(), _gpu_of(x)
+    xp, ld_x, cols = _rows_on(device, x, _bf16, None, None, "x")
     T = x.shape[0]
     if head_dim <= 0 or cols == 0 or cols % head_dim:
         raise NVFP4Error("x must be [T, heads * %d]" % head_dim)
-    if table is None:
-        raise NVFP4Error("the rotation must come from rotary_table")
-    pos, steps, dim, layout, amplitude = _rotation(table, positions, T)
+    pos, steps, dim, layout, amplitude = _rotation(device, table, positions, T)
     if out is None:
         out = x.new_empty((T, cols))
         op, ld_o = out.data_ptr(), cols
     else:
-        op, ld_o, _ = _rows(out, _bf16, T, cols, "out")
+        op, ld_o, _ = _rows_on(device, out, _bf16, T, cols, "out")
         _apart(x, out, same=True)
-    _one_device(x, positions, table.steps, out)
-    rc = lib.rotary(xp, ld_x, T, cols // head_dim, head_dim, pos, steps, dim, layout, amplitude, op, ld_o,
-                    _raw_stream(x.get_device()))
+    rc = lib.rotary(xp, ld_x, T, cols // head_dim, head_dim, pos, steps, dim, layout, amplitude, op, ld_o, _raw_stream(device))
     if rc:
         _check(rc, "rotary")
     return out
@@ -792,24 +814,30 @@ def _apart(x, out, same=False):
             raise NVFP4Error("an output overlaps an input")
 
 
-def _block_cache(k_cache, v_cache, k_scales, v_scales):
+def _block_cache(device, k_cache, v_cache, k_scales, v_scales):
     """_cache for block-scaled caches: the C arguments, the scales' addresses and (heads, head dim)."""
-    kind = k_cache.dtype if isinstance(k_cache, _Tensor) else None
-    if kind is not _e4m3 and kind is not _int8:
+    if not isinstance(k_cache, _Tensor) or k_cache.dtype is not _e4m3 and k_cache.dtype is not _int8:
         raise NVFP4Error("a block-scaled k_cache must be a float8_e4m3fn or int8 tensor")
+    kind = k_cache.dtype
     if not isinstance(v_cache, _Tensor) or v_cache.dtype is not kind:
         raise NVFP4Error("k_cache and v_cache must be GPU tensors of one type")
-    if kind is _int8:                           # the same bytes, as a type that _cache knows
-        args, _, _, heads, dim = _cache(k_cache.view(_e4m3), v_cache.view(_e4m3), None, None)
-    else:
-        args, _, _, heads, dim = _cache(k_cache, v_cache, None, None)
-    pages, page_size = args[3], args[4]
+    shape = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.get_device() != device or t.dim() != 4 or t.shape != shape:
+            _misplaced(t, kind, name, "[pages, heads, page size, head dim], as the other cache")
+    pages, heads, page_size, dim = shape
+    ps, hs, ts, unit = k_cache.stride()
+    vp, vh, vt, vu = v_cache.stride()
+    if not pages * heads * page_size * dim or unit != 1 or vu != 1 or ts != vt or (ps != vp and pages > 1) \
+            or (hs != vh and heads > 1):
+        raise NVFP4Error("k_cache and v_cache need elements and the same strides, the last of them 1")
+    scales = (pages, heads, page_size // 16)
     for name, t in (("k_scale", k_scales), ("v_scale", v_scales)):
-        if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _e8m0 or t.shape != (pages, heads, page_size // 16) \
+        if not isinstance(t, _Tensor) or t.get_device() != device or t.dtype is not _e8m0 or t.shape != scales \
                 or not t.is_contiguous():
-            _refuse(t, _e8m0, name, "[%d, %d, %d] contiguous" % (pages, heads, page_size // 16))
-    kind = CACHE_E4M3_BLOCKS if kind is _e4m3 else CACHE_INT8_BLOCKS
-    return args[:2] + (kind,) + args[3:], k_scales.data_ptr(), v_scales.data_ptr(), heads, dim
+            _misplaced(t, _e8m0, name, "[%d, %d, %d] contiguous" % scales)
+    return ((k_cache.data_ptr(), v_cache.data_ptr(), CACHE_E4M3_BLOCKS if kind is _e4m3 else CACHE_INT8_BLOCKS, pages, page_size,
+             heads, dim, ps if pages > 1 else 0, hs if heads > 1 else 0, ts), k_scales.data_ptr(), v_scales.data_ptr(), heads, dim)
 
 
 def paged_kv_append(k, v, positions, slots, k_cache, v_cache, rotation=None, k_scale=None, v_scale=None, q=None, q_out=None):
@@ -820,21 +848,25 @@ def paged_kv_append(k, v, positions, slots, k_cache, v_cache, rotation=None, k_s
     v_scale float8_e8m0fnu [pages, heads, page size / 16], which follow the values (a block's first token begins it anew;
     a block's rows of one call are neighbours, as paged_plan lays them).  q (bf16 view [T, num_heads * head_dim]) is
     rotated into q_out (allocated if None; may be q).  Returns q_out, or None without q."""
-    lib = _lib or load()
+    lib, device = _lib or load(), _gpu_of(k)
     if isinstance(k_scale, _Tensor) and k_scale.dtype is _e8m0 or isinstance(k_cache, _Tensor) and k_cache.dtype is _int8:
-        cache, kb, vb, heads, dim = _block_cache(k_cache, v_cache, k_scale, v_scale)
+        cache, kb, vb, heads, dim = _block_cache(device, k_cache, v_cache, k_scale, v_scale)
         ks = vs = None
     else:
         cache, ks, vs, heads, dim = _cache(k_cache, v_cache, k_scale, v_scale)
         kb = vb = None
-    kp, ld_k, _ = _rows(k, _bf16, None, heads * dim, "k")
+        for t in (k_cache, v_cache, k_scale, v_scale):
+            if t is not None and t.get_device() != device:
+                _misplaced(t, t.dtype, "a cache", "on the current GPU")
+    kp, ld_k, _ = _rows_on(device, k, _bf16, None, heads * dim, "k")
     T = k.shape[0]
-    vp, ld_v, _ = _rows(v, _bf16, T, heads * dim, "v")
-    pos, steps, rdim, layout, amplitude = _rotation(rotation, positions, T)
+    vp, ld_v, _ = _rows_on(device, v, _bf16, T, heads * dim, "v")
+    pos, steps, rdim, layout, amplitude = (None, None, 0, ROTARY_HALF, 1.0) if rotation is None else \
+        _rotation(device, rotation, positions, T)
     qp = op = None
     ld_q = ld_o = num_heads = 0
     if q is not None:
-        qp, ld_q, cols = _rows(q, _bf16, T, None, "q")
+        qp, ld_q, cols = _rows_on(device, q, _bf16, T, None, "q")
         if cols == 0 or cols % dim:
             raise NVFP4Error("q must be [T, num_heads * %d]" % dim)
         num_heads = cols // dim
@@ -842,15 +874,14 @@ def paged_kv_append(k, v, positions, slots, k_cache, v_cache, rotation=None, k_s
             q_out = q.new_empty((T, cols))
             op, ld_o = q_out.data_ptr(), cols
         else:
-            op, ld_o, _ = _rows(q_out, _bf16, T, cols, "q_out")
+            op, ld_o, _ = _rows_on(device, q_out, _bf16, T, cols, "q_out")
             _apart(q, q_out, same=True)
             _apart(k, q_out)
             _apart(v, q_out)
     elif q_out is not None:
         raise NVFP4Error("q_out needs q")
-    _one_device(k, v, slots, k_cache, v_cache, k_scale, v_scale, q, q_out, *(() if rotation is None else (positions, rotation.steps)))
-    rc = lib.paged_kv_append(qp, ld_q, num_heads, op, ld_o, kp, ld_k, vp, ld_v, pos, _vec(slots, _i64t, T, "slots"), T, steps,
-                             rdim, layout, amplitude, *cache, ks, vs, kb, vb, _raw_stream(k.get_device()))
+    rc = lib.paged_kv_append(qp, ld_q, num_heads, op, ld_o, kp, ld_k, vp, ld_v, pos, _vec_on(device, slots, _i64t, T, "slots"), T,
+                             steps, rdim, layout, amplitude, *cache, ks, vs, kb, vb, _raw_stream(device))
     if rc:
         _check(rc, "paged_kv_append")
     return q_out
@@ -861,9 +892,9 @@ def paged_attention_blocks(q, k_cache, v_cache, k_scale, v_scale, block_table, q
                            clear_padding=None):
     """paged_attention over a block-scaled cache: float8_e4m3fn or int8 caches with scales float8_e8m0fnu
     [pages, heads, page size / 16], as paged_kv_append leaves them.  Everything else, the workspace too, as there."""
-    lib = _lib or load()
-    cache, kb, vb, heads, dim = _block_cache(k_cache, v_cache, k_scale, v_scale)
-    qp, ld_q, cols = _rows(q, _bf16, None, None, "q")
+    lib, device = _lib or load(), _gpu_of(q)
+    cache, kb, vb, heads, dim = _block_cache(device, k_cache, v_cache, k_scale, v_scale)
+    qp, ld_q, cols = _rows_on(device, q, _bf16, None, None, "q")
     T = q.shape[0]
     num_heads = cols // dim
     if cols == 0 or cols % dim or num_heads % heads:
@@ -871,45 +902,44 @@ def paged_attention_blocks(q, k_cache, v_cache, k_scale, v_scale, block_table, q
     if not isinstance(seq_lens, _Tensor):
         raise NVFP4Error("seq_lens must be a GPU tensor")
     R = seq_lens.numel()
-    table, ld_t, max_pages = _rows(block_table, _i32, R, None, "block_table")
+    table, ld_t, max_pages = _rows_on(device, block_table, _i32, R, None, "block_table")
     if clear_padding is None:
         clear_padding = out is None
     if out is None:
         out = q.new_empty((T, cols), dtype=_bf16 if out_dtype in (OUT_BF16, _bf16) else _f32)
         op, ld_o = out.data_ptr(), cols
     else:
-        op, ld_o, _ = _rows(out, _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32, T, cols, "out")
+        op, ld_o, _ = _rows_on(device, out, _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32, T, cols, "out")
     if lse is None and return_lse:
         lse = q.new_empty((T, num_heads), dtype=_f32)
     if workspace is None:
         workspace = paged_attention_workspace(T, R, num_heads, heads, dim, max_new, max_seq, q.device)
     bytes_ = workspace.numel()
-    _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, seq_lens, out, lse, workspace)
-    rc = lib.paged_attention_blocks(qp, ld_q, T, _vec(q_start, _i32, R + 1, "q_start"), _vec(seq_lens, _i32, R, "seq_lens"), R,
-                                    max_new, max_seq, num_heads, *cache, kb, vb, table, max_pages, ld_t,
+    rc = lib.paged_attention_blocks(qp, ld_q, T, _vec_on(device, q_start, _i32, R + 1, "q_start"),
+                                    _vec_on(device, seq_lens, _i32, R, "seq_lens"), R, max_new, max_seq, num_heads, *cache, kb, vb, table, max_pages, ld_t,
                                     dim ** -0.5 if scale is None else scale, window, op,
                                     (OUT_BF16 if out.dtype is _bf16 else OUT_F32) + (OUT_CLEAR_PADDING if clear_padding else 0),
-                                    ld_o, None if lse is None else _vec(lse, _f32, T * num_heads, "lse"),
-                                    _vec(workspace, _u8, bytes_, "workspace"), bytes_, _raw_stream(q.get_device()))
+                                    ld_o, None if lse is None else _vec_on(device, lse, _f32, T * num_heads, "lse"),
+                                    _vec_on(device, workspace, _u8, bytes_, "workspace"), bytes_, _raw_stream(device))
     if rc:
         _check(rc, "paged_attention_blocks")
     return (out, lse) if return_lse else out
 
 
-def _codes8(t, rows, cols, name):
+def _codes8(device, t, rows, cols, name):
     """(address, rows, columns) of a contiguous int8 matrix."""
-    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _int8 or t.dim() != 2 or not t.is_contiguous() \
+    if not isinstance(t, _Tensor) or t.get_device() != device or t.dtype is not _int8 or t.dim() != 2 or not t.is_contiguous() \
             or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        _refuse(t, _int8, name, "[%s, %s] contiguous" % (rows, cols))
+        _misplaced(t, _int8, name, "[%s, %s] contiguous" % (rows, cols))
     return t.data_ptr(), t.shape[0], t.shape[1]
 
 
-def _int8_out(x, m, n, out_dtype, out):
+def _int8_out(device, x, m, n, out_dtype, out):
     dtype = _bf16 if out_dtype in (OUT_BF16, _bf16) else _f32
     if out is None:
         out = x.new_empty((m, n), dtype=dtype)
         return out, out.data_ptr(), n, OUT_BF16 if dtype is _bf16 else OUT_F32
-    op, ld, _ = _rows(out, dtype, m, n, "out")
+    op, ld, _ = _rows_on(device, out, dtype, m, n, "out")
     if x.dtype is dtype:
         _apart(x, out)
     elif m:
@@ -922,22 +952,21 @@ def _int8_out(x, m, n, out_dtype, out):
 def int8_quantize(x, codes=None, scales=None):
     """bf16 [rows, cols] (row stride allowed) -> (codes int8 [rows, cols], scales fp32 [rows]): a scale amax / 127 for each
     row, a token's or an output channel's."""
-    lib = _lib or load()
-    xp, ld, cols = _rows(x, _bf16, None, None, "x")
+    lib, device = _lib or load(), _gpu_of(x)
+    xp, ld, cols = _rows_on(device, x, _bf16, None, None, "x")
     rows = x.shape[0]
     if codes is None:
         codes = x.new_empty((rows, cols), dtype=_int8)
     if scales is None:
         scales = x.new_empty(rows, dtype=_f32)
-    cp, _, _ = _codes8(codes, rows, cols, "codes")
-    _one_device(x, codes, scales)
-    rc = lib.int8_quantize(xp, rows, cols, ld, cp, _vec(scales, _f32, rows, "scales"), _raw_stream(x.get_device()))
+    cp, _, _ = _codes8(device, codes, rows, cols, "codes")
+    rc = lib.int8_quantize(xp, rows, cols, ld, cp, _vec_on(device, scales, _f32, rows, "scales"), _raw_stream(device))
     if rc:
         _check(rc, "int8_quantize")
     return codes, scales
 
 
-def _int8_workspace(lib, like, m, n, k, workspace):
+def _int8_workspace(device, lib, like, m, n, k, workspace):
     """(workspace or None, its address, its bytes): one that products of few rows are split with, allocated if None."""
     if workspace is None:
         need = lib.gemm_w8a8_workspace_bytes(m, n, k)
@@ -946,20 +975,19 @@ def _int8_workspace(lib, like, m, n, k, workspace):
         workspace = like.new_empty(need, dtype=_u8)
         return workspace, workspace.data_ptr(), need
     bytes_ = workspace.numel() if isinstance(workspace, _Tensor) else 0
-    return workspace, _vec(workspace, _u8, bytes_, "workspace"), bytes_
+    return workspace, _vec_on(device, workspace, _u8, bytes_, "workspace"), bytes_
 
 
 def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, workspace=None):
     """out [m, n] = a_scale[m] * (a [m, k] . w [n, k]^T) * w_scale[n]: int8 codes with a scale for each row, as
     int8_quantize gives them.  workspace: uint8, gemm_w8a8_workspace_bytes of it (allocated if None)."""
-    lib = _lib or load()
-    ap, m, k = _codes8(a, None, None, "a")
-    wp, n, _ = _codes8(w, None, k, "w")
-    out, op, ld, kind = _int8_out(a, m, n, out_dtype, out)
-    workspace, wsp, bytes_ = _int8_workspace(lib, a, m, n, k, workspace)
-    _one_device(a, a_scale, w, w_scale, out, workspace)
-    rc = lib.gemm_w8a8(ap, _vec(a_scale, _f32, m, "a_scale"), m, wp, _vec(w_scale, _f32, n, "w_scale"), n, k, op, kind, ld, wsp,
-                       bytes_, _raw_stream(a.get_device()))
+    lib, device = _lib or load(), _gpu_of(a)
+    ap, m, k = _codes8(device, a, None, None, "a")
+    wp, n, _ = _codes8(device, w, None, k, "w")
+    out, op, ld, kind = _int8_out(device, a, m, n, out_dtype, out)
+    workspace, wsp, bytes_ = _int8_workspace(device, lib, a, m, n, k, workspace)
+    rc = lib.gemm_w8a8(ap, _vec_on(device, a_scale, _f32, m, "a_scale"), m, wp, _vec_on(device, w_scale, _f32, n, "w_scale"), n, k,
+                       op, kind, ld, wsp, bytes_, _raw_stream(device))
     if rc:
         _check(rc, "gemm_w8a8")
     return out
@@ -969,10 +997,10 @@ def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, s
     """x bf16 [m, k] (row stride allowed), quantised to int8 with a scale for each token, times w (int8 [n, k], w_scale
     fp32 [n]; from int8_quantize of the weight).  codes, scales: where x's are left (allocated if None); workspace as in
     gemm_w8a8."""
-    lib = _lib or load()
-    xp, ld_x, k = _rows(x, _bf16, None, None, "x")
+    lib, device = _lib or load(), _gpu_of(x)
+    xp, ld_x, k = _rows_on(device, x, _bf16, None, None, "x")
     m = x.shape[0]
-    wp, n, _ = _codes8(w, None, k, "w")
+    wp, n, _ = _codes8(device, w, None, k, "w")
     need = lib.gemm_w8a8_workspace_bytes(m, n, k) if workspace is None else 0
     if codes is None and scales is None and workspace is None:
         # one allocation for all three, alive until the call has been enqueued
@@ -987,13 +1015,12 @@ def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, s
             scales = x.new_empty(m, dtype=_f32)
         if workspace is None and need:
             workspace = x.new_empty(need, dtype=_u8)
-        cp, sp = _codes8(codes, m, k, "codes")[0], _vec(scales, _f32, m, "scales")
+        cp, sp = _codes8(device, codes, m, k, "codes")[0], _vec_on(device, scales, _f32, m, "scales")
         bytes_ = workspace.numel() if isinstance(workspace, _Tensor) else 0
-        wsp = None if workspace is None else _vec(workspace, _u8, bytes_, "workspace")
-    out, op, ld, kind = _int8_out(x, m, n, out_dtype, out)
-    _one_device(x, w, w_scale, codes, scales, out, workspace)
-    rc = lib.int8_linear(xp, m, k, ld_x, cp, sp, wp, _vec(w_scale, _f32, n, "w_scale"), n, op, kind,
-                         ld, wsp, bytes_, _raw_stream(x.get_device()))
+        wsp = None if workspace is None else _vec_on(device, workspace, _u8, bytes_, "workspace")
+    out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, out)
+    rc = lib.int8_linear(xp, m, k, ld_x, cp, sp, wp, _vec_on(device, w_scale, _f32, n, "w_scale"), n, op, kind,
+                         ld, wsp, bytes_, _raw_stream(device))
     if rc:
         _check(rc, "int8_linear")
     return out

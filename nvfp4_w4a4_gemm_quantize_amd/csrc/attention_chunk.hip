@@ -27,10 +27,10 @@
 // take 82 us, over E4M3 85: 1.4 us a tile of keys, shares between 57 and 80 us long, and
 // a part's 8 us beside its keys (its queries, page numbers and first keys; its output).
 //
-// Block-scaled caches, 4096 after 4096, 40 heads of 128 over 8: E4M3 546 us, INT8 575 - 587 (bf16
-// and E4M3 with one scale a head 510).  The scales take scalar registers that are spilled already,
+// Block-scaled caches, 4096 after 4096, 40 heads of 128 over 8: E4M3 525 us, INT8 560 - 572 (bf16
+// and E4M3 with one scale a head 505 - 510).  The scales take scalar registers that are spilled already,
 // and two INT8 elements five instructions where E4M3 takes one: the matrix unit is busy for
-// 38% of the cycles.  Heads of 64: 512 and 523 (bf16 482); 256, 24 over 4: 794 and 680 (bf16 620,
+// 40% of the cycles.  Heads of 64: 512 and 523 (bf16 482); 256, 24 over 4: 794 and 680 (bf16 620,
 // E4M3 with one scale a head 808).
 #include <float.h>
 #include <math.h>
@@ -156,6 +156,11 @@ template <int D, int KIND>
 __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionArgs a, ChunkWorkspace ws, int numbers) {
   constexpr bool FP8 = KIND != kCacheBf16;    // 8-bit elements
   constexpr bool BLOCKS = has_blocks(KIND);
+  // Where a tile is converted: before the products, or, LATE, after the softmax, beside the
+  // other wave's products.  4096 after 4096, heads of 128: E4M3 544 us, late 525; INT8 598, 566
+  // (keys alone late 573, values alone 581).  With heads of 64 the softmax is the longer of
+  // the two as it is (E4M3 523, late 582; INT8 535, 609).
+  constexpr bool LATE = BLOCKS && D == 128;
   constexpr int KT = D == 256 ? 32 : 64;      // keys of a tile
   constexpr int NK = KT / 32;                 // key fragments of a tile
   constexpr int NG = KT / 16;                 // 16-key groups: a page holds whole ones
@@ -660,10 +665,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
         // are waited for in the next products and read at the end of the softmax after.
         uint8_t* const free_k = lds_k[j & 3];
         uint8_t* const free_v = lds_v[(j + 3) & 3];
-        settle(free_k, kr, false, j);
-        settle(free_v, vr, true, j + 3);
+        if constexpr (!LATE) {
+          settle(free_k, kr, false, j);
+          settle(free_v, vr, true, j + 3);
+        }
         __builtin_amdgcn_s_setprio(1);
         products(lds_k[(j + 1) & 3], lds_v[j & 3], [&](int step) {
+          if constexpr (LATE) return;
           if (step < NL) bring(k_base, key_at, step, free_k, k_voff, kr);
           else if (step < 2 * NL) bring(v_base, value_at, step - NL, free_v, v_voff, vr);
         });
@@ -681,6 +689,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
           raise(top0);
 #pragma unroll
           for (int u = 0; u < 2 * NK; ++u) weigh(u, 0.f);
+        }
+        if constexpr (LATE) {
+          settle(free_k, kr, false, j);
+          settle(free_v, vr, true, j + 3);
+          bring_all(k_base, key_at, nullptr, k_voff, kr);
+          bring_all(v_base, value_at, nullptr, v_voff, vr);
         }
         if (((j + 1 + kLead) & 63) == 0) locate(j + 1 + kLead);
         value_at = key_at;

@@ -916,7 +916,8 @@ def paged_attention_blocks(q, k_cache, v_cache, k_scale, v_scale, block_table, q
         workspace = paged_attention_workspace(T, R, num_heads, heads, dim, max_new, max_seq, q.device)
     bytes_ = workspace.numel()
     rc = lib.paged_attention_blocks(qp, ld_q, T, _vec_on(device, q_start, _i32, R + 1, "q_start"),
-                                    _vec_on(device, seq_lens, _i32, R, "seq_lens"), R, max_new, max_seq, num_heads, *cache, kb, vb, table, max_pages, ld_t,
+                                    _vec_on(device, seq_lens, _i32, R, "seq_lens"), R, max_new, max_seq, num_heads, *cache, kb, vb,
+                                    table, max_pages, ld_t,
                                     dim ** -0.5 if scale is None else scale, window, op,
                                     (OUT_BF16 if out.dtype is _bf16 else OUT_F32) + (OUT_CLEAR_PADDING if clear_padding else 0),
                                     ld_o, None if lse is None else _vec_on(device, lse, _f32, T * num_heads, "lse"),

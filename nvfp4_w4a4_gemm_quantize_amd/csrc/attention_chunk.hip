@@ -449,7 +449,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_chunk_kernel(AttentionA
           for (int k = 0; k < 2; ++k) {
             const uint32_t w0 = regs[i][2 * k], w1 = regs[i][2 * k + 1];
             *(u32x4*)(lds + row * ROW + ((2 * lane_col + k) ^ x) * 16) =
-                u32x4{to_bf16<KIND, false>(w0, scale), to_bf16<KIND, true>(w0, scale), to_bf16<KIND, false>(w1, scale), to_bf16<KIND, true>(w1, scale)};
+                u32x4{to_bf16<KIND, false>(w0, scale), to_bf16<KIND, true>(w0, scale), to_bf16<KIND, false>(w1, scale),
+                      to_bf16<KIND, true>(w1, scale)};
           }
         }
       }

@@ -479,7 +479,8 @@ hipError_t launch_blocks(const AppendArgs& a, hipStream_t st) {
   const int64_t kv = windows * 2 * groups * shares;
   RotaryGrid q{1, 1, 0};
   if (a.q.heads > 0) q = rotary_grid(a.tokens, a.q.heads, D, run_threads(D));
-  append_blocks_kernel<INTERLEAVED, INT8, D><<<(unsigned)(kv + q.blocks), run_threads(D), 0, st>>>(a, shares, groups, heads, (int)kv, q.groups, q.per);
+  append_blocks_kernel<INTERLEAVED, INT8, D>
+      <<<(unsigned)(kv + q.blocks), run_threads(D), 0, st>>>(a, shares, groups, heads, (int)kv, q.groups, q.per);
   return hipGetLastError();
 }
 template <bool INTERLEAVED, bool INT8>

@@ -53,21 +53,23 @@ __device__ __forceinline__ UnitAt unit_at(int rotated, int dim, int unit) {
   return at;
 }
 
-// The turns of a unit's eight pairs at a position.
+// The turns of a unit's eight pairs at a position; false for a negative one, whose row is not
+// turned.  It is left out and not turned by 0: 0 * inf is NaN, and -0 + 0 is 0.
 template <typename T>
 struct Turn {
   T c[8], s[8];
 };
 template <bool INTERLEAVED, typename T>
-__device__ __forceinline__ void find_turn(Turn<T>& t, const RotaryArgs& rot, int unit, int position) {
+__device__ __forceinline__ bool find_turn(Turn<T>& t, const RotaryArgs& rot, int unit, int position) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int pair = INTERLEAVED ? unit * 4 + (i < 4 ? i : rot.dim / 4 + i - 4) : unit * 8 + i;
     const uint64_t phase = rot.steps[pair] * (uint64_t)(uint32_t)position;
     const double2 cs = cos_sin((uint32_t)(phase >> 32), rot.amplitude);
-    t.c[i] = position < 0 ? T(1) : (T)cs.x;
-    t.s[i] = position < 0 ? T(0) : (T)cs.y;
+    t.c[i] = (T)cs.x;
+    t.s[i] = (T)cs.y;
   }
+  return position >= 0;
 }
 
 __device__ __forceinline__ void unpack(const u32x4& w, float* f) {
@@ -123,13 +125,13 @@ __device__ __forceinline__ void rotary_rows(const RotaryRows& a, const RotaryArg
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i) load(i, min(h0 + i, h1 - 1));
   Turn<float> turn;
-  if (at.turns) find_turn<INTERLEAVED>(turn, rot, unit, rot.positions[t]);
+  const bool turns = at.turns && find_turn<INTERLEAVED>(turn, rot, unit, rot.positions[t]);
   for (int h = h0; h < h1; h += kAtOnce) {
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       if (h + i >= h1) break;
       const int64_t head = (int64_t)(h + i) * a.dim;
-      if (at.turns) {
+      if (turns) {
         float f[16];
         unpack(lo[i], f);
         unpack(hi[i], f + 8);
@@ -282,7 +284,7 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i) load(i, min(h0 + i, h1 - 1));
   Turn<float> turn;
-  if (at.turns && h0 < a.q.heads + c.heads) find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[t]);
+  const bool turns = at.turns && h0 < a.q.heads + c.heads && find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[t]);
   const int64_t slot = a.slots[t];
   const bool held = slot >= 0 && slot >> c.page_shift < c.num_pages;
   for (int h = h0; h < h1; h += kAtOnce) {
@@ -290,16 +292,20 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
     for (int i = 0; i < kAtOnce; ++i) {
       const int head = h + i, kv = head - a.q.heads;
       if (head >= h1) break;
-      float f[16];
-      unpack(lo[i], f);
-      unpack(hi[i], f + 8);
+      u32x4 w[2] = {lo[i], hi[i]};
       if (head + kAtOnce < h1) load(i, head + kAtOnce);
       if (kv >= 0 && !held) continue;
-      if (at.turns && kv < c.heads) turn_unit<INTERLEAVED>(f, turn);
+      float f[16];
+      unpack(w[0], f);
+      unpack(w[1], f + 8);
+      if (turns && kv < c.heads) {
+        turn_unit<INTERLEAVED>(f, turn);
+        if (!FP8 || kv < 0) w[0] = pack(f), w[1] = pack(f + 8);   // else w stays as it is, a NaN's bits too
+      }
       if (kv < 0) {
         uint16_t* out = a.q.out + t * a.q.ld_out + (int64_t)head * c.dim;
-        *(u32x4*)(out + at.lo) = pack(f);
-        *(u32x4*)(out + at.hi) = pack(f + 8);
+        *(u32x4*)(out + at.lo) = w[0];
+        *(u32x4*)(out + at.hi) = w[1];
         continue;
       }
       const bool is_v = kv >= c.heads;
@@ -315,8 +321,8 @@ __global__ __launch_bounds__(kThreads) void append_rows_kernel(AppendArgs a, int
         *(u32x2*)(p + at.hi) = codes8<false, true>(f + 8);
       } else {
         uint16_t* p = (uint16_t*)(is_v ? c.v : c.k) + to;
-        *(u32x4*)(p + at.lo) = pack(f);
-        *(u32x4*)(p + at.hi) = pack(f + 8);
+        *(u32x4*)(p + at.lo) = w[0];
+        *(u32x4*)(p + at.hi) = w[1];
       }
     }
   }
@@ -392,7 +398,7 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
     // in fp64: of 16 million codes of rotated keys 0 to 3 are beside the formula's, with fp32's products 14 to 18
     int old = scales[block];
     Turn<double> turn;
-    if (in && at.turns) find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[from]);
+    const bool turns = in && at.turns && find_turn<INTERLEAVED>(turn, a.rot, unit, a.rot.positions[from]);
     for (int h = h0; h < h1; ++h, block += (int64_t)1 << (c.page_shift - 4), to += c.head_stride) {
       constexpr int kMost = INT8 ? kMostInt8 : kMostE4m3;
       old = fresh ? 1 : min(max(old, 1), kMost);
@@ -403,7 +409,7 @@ __device__ __forceinline__ void append_runs(const AppendArgs& a, int64_t window,
         lo = *(const u32x4*)(row + (int64_t)(h + 1) * D + at.lo);
         hi = *(const u32x4*)(row + (int64_t)(h + 1) * D + at.hi);
       }
-      if (in && at.turns) turn_unit<INTERLEAVED>(f, turn);
+      if (turns) turn_unit<INTERLEAVED>(f, turn);
       uint32_t top = 0;                     // largest magnitude's bits: infinities and NaN come last
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);

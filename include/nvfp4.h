@@ -539,7 +539,9 @@ int verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64
  * The attention layer in 8 bits, for the half of the hybrid model that the pages
  * call the sensitive one: rotary positions (rotary_steps, rotary), the cache write
  * with the rotation on the way (paged_kv_append), and attention over caches that
- * hold a scale for each 16 tokens and head (paged_attention_blocks).
+ * hold a scale for each 16 tokens and head (paged_attention_blocks).  Unless a call says
+ * otherwise, what it writes (outputs, codes, scales, workspaces) shares no memory with
+ * anything else that it is given; the int8 calls below too.
  *
  * Block-scaled caches.  The codes lie as in any cache of 8-bit elements; beside them
  * k_blocks and v_blocks hold one E8M0 byte for each block of 16 tokens (a slot's
@@ -675,8 +677,7 @@ int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, i
  *            k a multiple of 16 below 2^17.
  *   a_scale, w_scale   float [m] and [n].
  *   out      [m, n] of out_dtype (NVFP4_OUT_*), row stride ld_out >= n, any alignment of
- *            its elements (rows of 16-byte aligned ones leave in wide stores); it overlaps
- *            no input.
+ *            its elements (rows of 16-byte aligned ones leave in wide stores).
  *   workspace  optional (null), 16-byte aligned, at least gemm_w8a8_workspace_bytes(m, n,
  *            k) (which may be 0); its contents do not matter.  With it, products of few
  *            rows are split along k over the chip.  Not shared by calls in flight on
@@ -690,6 +691,8 @@ int gemm_w8a8(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w,
 
 /*
  * int8_linear -- int8_quantize of x [m, k] into a and a_scale, and gemm_w8a8 on them.
+ * x is read by workgroups that others' codes, scales and outputs may run ahead of, so
+ * none of these may lie over it.
  */
 int int8_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ld_x, int8_t* a, float* a_scale, const int8_t* w,
                 const float* w_scale, int64_t n, void* out, int out_dtype, int64_t ld_out, void* workspace,

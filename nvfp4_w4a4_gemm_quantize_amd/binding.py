@@ -806,12 +806,36 @@ def _apart(x, out, same=False):
     T, cols = x.shape
     if not T or (same and a == b):
         return
-    lx, lo = x.stride(0), out.stride(0)
-    if a < b + 2 * ((T - 1) * lo + out.shape[1]) and b < a + 2 * ((T - 1) * lx + cols):
+    ex, eo = x.element_size(), out.element_size()
+    lx, lo, wide, cols = x.stride(0) * ex, out.stride(0) * eo, out.shape[1] * eo, cols * ex
+    if a < b + (T - 1) * lo + wide and b < a + (T - 1) * lx + cols:
         # column slices of one matrix interleave without sharing an element
-        at = (a - b) // 2 % lo if lx == lo and lo > 0 else 0
-        if at < out.shape[1] or at + cols > lo:
+        at = (a - b) % lo if lx == lo and lo > 0 else 0
+        if at < wide or at + cols > lo:
             raise NVFP4Error("an output overlaps an input")
+
+
+def _apart_from(t, others):
+    """Refuse a 2-D view of which a row shares memory with one of others ((address, bytes) each)."""
+    rows, cols = t.shape
+    if not rows:
+        return
+    p, size = t.data_ptr(), t.element_size()
+    ld, cols = t.stride(0) * size, cols * size
+    end = p + (rows - 1) * ld + cols
+    for q, n in others:
+        if n and q < end and p < q + n:
+            at = (q - p) % ld if rows > 1 and q > p and ld >= cols else 0     # of the row that q lies in or behind
+            if at < cols or at + n > ld:
+                raise NVFP4Error("a tensor that the call writes overlaps another one")
+
+
+def _apart_all(written, read):
+    """Refuse written ranges ((address, bytes) each) that meet each other or one that is read."""
+    for i, (p, n) in enumerate(written):
+        for q, o in written[i + 1:] + read:
+            if n and o and p < q + o and q < p + n:
+                raise NVFP4Error("a tensor that the call writes overlaps another one")
 
 
 def _block_cache(device, k_cache, v_cache, k_scales, v_scales):
@@ -941,27 +965,26 @@ def _int8_out(device, x, m, n, out_dtype, out):
         out = x.new_empty((m, n), dtype=dtype)
         return out, out.data_ptr(), n, OUT_BF16 if dtype is _bf16 else OUT_F32
     op, ld, _ = _rows_on(device, out, dtype, m, n, "out")
-    if x.dtype is dtype:
-        _apart(x, out)
-    elif m:
-        a, b, size = x.data_ptr(), op, x.element_size()
-        if a < b + out.element_size() * ((m - 1) * ld + n) and b < a + size * ((m - 1) * x.stride(0) + x.shape[1]):
-            raise NVFP4Error("an output overlaps an input")
+    _apart(x, out)
     return out, op, ld, OUT_BF16 if dtype is _bf16 else OUT_F32
 
 
 def int8_quantize(x, codes=None, scales=None):
     """bf16 [rows, cols] (row stride allowed) -> (codes int8 [rows, cols], scales fp32 [rows]): a scale amax / 127 for each
-    row, a token's or an output channel's."""
+    row, a token's or an output channel's.  codes and scales share no memory with x or each other."""
     lib, device = _lib or load(), _gpu_of(x)
     xp, ld, cols = _rows_on(device, x, _bf16, None, None, "x")
-    rows = x.shape[0]
+    rows, given = x.shape[0], codes is not None or scales is not None
     if codes is None:
         codes = x.new_empty((rows, cols), dtype=_int8)
     if scales is None:
         scales = x.new_empty(rows, dtype=_f32)
-    cp, _, _ = _codes8(device, codes, rows, cols, "codes")
-    rc = lib.int8_quantize(xp, rows, cols, ld, cp, _vec_on(device, scales, _f32, rows, "scales"), _raw_stream(device))
+    cp, sp = _codes8(device, codes, rows, cols, "codes")[0], _vec_on(device, scales, _f32, rows, "scales")
+    if given:
+        written = [(cp, rows * cols), (sp, 4 * rows)]
+        _apart_all(written, [])
+        _apart_from(x, written)
+    rc = lib.int8_quantize(xp, rows, cols, ld, cp, sp, _raw_stream(device))
     if rc:
         _check(rc, "int8_quantize")
     return codes, scales
@@ -985,10 +1008,19 @@ def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, worksp
     lib, device = _lib or load(), _gpu_of(a)
     ap, m, k = _codes8(device, a, None, None, "a")
     wp, n, _ = _codes8(device, w, None, k, "w")
+    made = out is not None
     out, op, ld, kind = _int8_out(device, a, m, n, out_dtype, out)
+    sp, tp = _vec_on(device, a_scale, _f32, m, "a_scale"), _vec_on(device, w_scale, _f32, n, "w_scale")
+    given = workspace is not None
     workspace, wsp, bytes_ = _int8_workspace(device, lib, a, m, n, k, workspace)
-    rc = lib.gemm_w8a8(ap, _vec_on(device, a_scale, _f32, m, "a_scale"), m, wp, _vec_on(device, w_scale, _f32, n, "w_scale"), n, k,
-                       op, kind, ld, wsp, bytes_, _raw_stream(device))
+    if given or made:
+        read = [(ap, m * k), (sp, 4 * m), (wp, n * k), (tp, 4 * n)]
+        if given:
+            _apart_all([(wsp, bytes_)], read)
+            read.append((wsp, bytes_))
+        if made:
+            _apart_from(out, read)
+    rc = lib.gemm_w8a8(ap, sp, m, wp, tp, n, k, op, kind, ld, wsp, bytes_, _raw_stream(device))
     if rc:
         _check(rc, "gemm_w8a8")
     return out
@@ -997,12 +1029,14 @@ def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, worksp
 def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, scales=None, workspace=None):
     """x bf16 [m, k] (row stride allowed), quantised to int8 with a scale for each token, times w (int8 [n, k], w_scale
     fp32 [n]; from int8_quantize of the weight).  codes, scales: where x's are left (allocated if None); workspace as in
-    gemm_w8a8."""
+    gemm_w8a8.  What the call writes shares no memory with anything else of it (out may be other columns of x's matrix)."""
     lib, device = _lib or load(), _gpu_of(x)
     xp, ld_x, k = _rows_on(device, x, _bf16, None, None, "x")
     m = x.shape[0]
     wp, n, _ = _codes8(device, w, None, k, "w")
+    tp = _vec_on(device, w_scale, _f32, n, "w_scale")
     need = lib.gemm_w8a8_workspace_bytes(m, n, k) if workspace is None else 0
+    written = []
     if codes is None and scales is None and workspace is None:
         # one allocation for all three, alive until the call has been enqueued
         at, ws_at = m * k, (m * (k + 4) + 255) // 256 * 256
@@ -1019,9 +1053,15 @@ def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, s
         cp, sp = _codes8(device, codes, m, k, "codes")[0], _vec_on(device, scales, _f32, m, "scales")
         bytes_ = workspace.numel() if isinstance(workspace, _Tensor) else 0
         wsp = None if workspace is None else _vec_on(device, workspace, _u8, bytes_, "workspace")
-    out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, out)
-    rc = lib.int8_linear(xp, m, k, ld_x, cp, sp, wp, _vec_on(device, w_scale, _f32, n, "w_scale"), n, op, kind,
-                         ld, wsp, bytes_, _raw_stream(device))
+        written = [(cp, m * k), (sp, 4 * m), (wsp or 0, bytes_)]
+        _apart_all(written, [(wp, n * k), (tp, 4 * n)])
+        _apart_from(x, written)
+    if out is not None:
+        out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, out)
+        _apart_from(out, written + [(wp, n * k), (tp, 4 * n)])
+    else:
+        out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, None)
+    rc = lib.int8_linear(xp, m, k, ld_x, cp, sp, wp, tp, n, op, kind, ld, wsp, bytes_, _raw_stream(device))
     if rc:
         _check(rc, "int8_linear")
     return out

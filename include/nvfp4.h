@@ -678,10 +678,12 @@ int int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, i
  *   a_scale, w_scale   float [m] and [n].
  *   out      [m, n] of out_dtype (NVFP4_OUT_*), row stride ld_out >= n, any alignment of
  *            its elements (rows of 16-byte aligned ones leave in wide stores).
- *   workspace  optional (null), 16-byte aligned, at least gemm_w8a8_workspace_bytes(m, n,
- *            k) (which may be 0); its contents do not matter.  With it, products of few
- *            rows are split along k over the chip.  Not shared by calls in flight on
- *            different streams.
+ *   workspace  optional (null), 16-byte aligned, gemm_w8a8_workspace_bytes(m, n, k) (which
+ *            may be 0); its contents do not matter.  These bytes never fall as m rises: one
+ *            for the most tokens serves any fewer; for several layers take the largest.  With
+ *            it, products of few rows are split along k over the chip, without it none is (37
+ *            tokens, 5120 x 17408: 23 us, 41).  Not shared by calls in flight on different
+ *            streams.
  * m == 0 enqueues nothing.  Results are deterministic, and a row's do not depend on the
  * others, on m or on the workspace.
  */

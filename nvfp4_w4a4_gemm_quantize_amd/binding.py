@@ -990,6 +990,16 @@ def int8_quantize(x, codes=None, scales=None):
     return codes, scales
 
 
+def gemm_w8a8_workspace(tokens, n, k, device="cuda"):
+    """A workspace for gemm_w8a8 and int8_linear calls of up to these tokens, n channels and k columns; for several layers
+    the largest of theirs serves all.  Without an element where no such product is split."""
+    lib = load()
+    rc = lib.gemm_w8a8(None, None, tokens, None, None, n, k, None, OUT_BF16, n, None, 0, None)     # sizes come first
+    if rc not in (0, -1):
+        _check(rc, "gemm_w8a8")
+    return torch.empty(lib.gemm_w8a8_workspace_bytes(tokens, n, k), dtype=_u8, device=device)
+
+
 def _int8_workspace(device, lib, like, m, n, k, workspace):
     """(workspace or None, its address, its bytes): one that products of few rows are split with, allocated if None."""
     if workspace is None:
@@ -1004,7 +1014,8 @@ def _int8_workspace(device, lib, like, m, n, k, workspace):
 
 def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, workspace=None):
     """out [m, n] = a_scale[m] * (a [m, k] . w [n, k]^T) * w_scale[n]: int8 codes with a scale for each row, as
-    int8_quantize gives them.  workspace: uint8, gemm_w8a8_workspace_bytes of it (allocated if None)."""
+    int8_quantize gives them.  workspace: from gemm_w8a8_workspace, of as many tokens or more (allocated if None; without an
+    element: k is not split)."""
     lib, device = _lib or load(), _gpu_of(a)
     ap, m, k = _codes8(device, a, None, None, "a")
     wp, n, _ = _codes8(device, w, None, k, "w")

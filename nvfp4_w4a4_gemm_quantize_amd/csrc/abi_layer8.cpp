@@ -188,13 +188,26 @@ static Int8Args int8_args(const int8_t* a, const float* a_scale, int64_t m, cons
 }
 
 size_t gemm_w8a8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  return validate_w8a8_sizes(m, n, k) ? 0 : int8_workspace_bytes(m, n, k);
+  if (validate_w8a8_sizes(m, n, k)) return 0;
+  // the largest of any product of up to m tokens
+  size_t bytes = int8_workspace_bytes(m < kInt8FewTokens ? m : kInt8FewTokens, n, k);
+  const int64_t most = m < int8_split_tokens(n) ? m : int8_split_tokens(n);
+  for (int64_t t = kInt8FewTokens + 1; t <= most; t = t / kInt8TokenStep * kInt8TokenStep + kInt8TokenStep + 1) {
+    const size_t own = int8_workspace_bytes(t, n, k);
+    if (own > bytes) bytes = own;
+  }
+  return bytes;
+}
+
+// What a call with a workspace reads and writes of it: at most gemm_w8a8_workspace_bytes.
+static size_t needed_bytes(const void* workspace, int64_t m, int64_t n, int64_t k) {
+  return !workspace || validate_w8a8_sizes(m, n, k) ? 0 : int8_workspace_bytes(m, n, k);
 }
 
 int gemm_w8a8(const int8_t* a, const float* a_scale, int64_t m, const int8_t* w, const float* w_scale, int64_t n, int64_t k,
               void* out, int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
   const int rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace, workspace_bytes,
-                                    gemm_w8a8_workspace_bytes(m, n, k));
+                                    needed_bytes(workspace, m, n, k));
   if (rc || m == 0) return rc;
   return hip_status(launch_gemm_w8a8(int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace),
                                      (hipStream_t)stream));
@@ -206,7 +219,7 @@ int int8_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ld_x, int8_t* a
   int rc = validate_int8_quantize(x, m, k, ld_x, a, a_scale);
   if (rc) return rc;
   rc = validate_gemm_w8a8(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace, workspace_bytes,
-                          gemm_w8a8_workspace_bytes(m, n, k));
+                          needed_bytes(workspace, m, n, k));
   if (rc || m == 0) return rc;
   return hip_status(launch_int8_linear(x, ld_x, a, a_scale,
                                        int8_args(a, a_scale, m, w, w_scale, n, k, out, out_dtype, ld_out, workspace),

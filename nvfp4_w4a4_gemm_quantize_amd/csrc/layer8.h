@@ -58,7 +58,13 @@ struct Int8Args {
   uint32_t* arrived;
   int* parts;
 };
+// Of a product of exactly these sizes.  It is the same for tokens 1 - 32 (but for those of the
+// streaming kernel, which needs none) and for those of one multiple of 64.
 size_t int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+constexpr int64_t kInt8FewTokens = 32, kInt8TokenStep = 64;
+// Tokens beyond which no product of n channels is split along k: more than 128 tiles of
+// 128 x 128, or of smaller ones, fill the chip by themselves.
+inline int64_t int8_split_tokens(int64_t n) { return 128 / ((n + 127) / 128) * 128; }
 hipError_t launch_gemm_w8a8(const Int8Args& a, hipStream_t st);
 // x [g.m, g.k] quantised into codes and scales (g.a and g.a_scale), and the product.
 hipError_t launch_int8_linear(const uint16_t* x, int64_t ld_x, int8_t* codes, float* scales, const Int8Args& g, hipStream_t st);

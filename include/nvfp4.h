@@ -637,9 +637,12 @@ int paged_kv_append(const uint16_t* q, int64_t ld_q, int num_heads, uint16_t* q_
  * paged_attention_blocks -- paged_attention over a block-scaled cache: every argument is
  * that call's (the workspace too, paged_attention_workspace_bytes), but for k_blocks and
  * v_blocks in place of k_scale and v_scale, and cache_dtype NVFP4_CACHE_E4M3_BLOCKS or
- * NVFP4_CACHE_INT8_BLOCKS.  Elements become bf16 with their scale, exactly, on their way
- * into the matrix unit; INT8's scales may be multiplied to sums over q and the codes
- * instead, which are finite for |q| < 2^112.
+ * NVFP4_CACHE_INT8_BLOCKS.  Elements become bf16 with their scale on their way into the
+ * matrix unit, exactly, but that any below 2^-126 may count as 0.  INT8's scales may be
+ * multiplied to sums over q and the codes instead, which are finite for |q| < 2^112, and
+ * to the softmax's weights, which are bf16: a weight times scale below 2^-126 is rounded
+ * to bf16's subnormal numbers or counts as 0.  Either moves an output by less than n
+ * 2^-118 over n keys.  Sums are fp32 of weights up to 2^8: finite for |v| n < 2^119.
  */
 int paged_attention_blocks(const uint16_t* q, int64_t ld_q, int64_t tokens, const int32_t* q_start, const int32_t* seq_lens,
                            int64_t num_requests, int64_t max_new, int64_t max_seq, int num_heads, const void* k_cache,

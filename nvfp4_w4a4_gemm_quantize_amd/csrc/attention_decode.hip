@@ -127,6 +127,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attention_decode_k
   // INT8: the conversion has no scale of its own.  Powers of two may as well multiply a
   // group's scores and weights, of which there are fewer than elements (32 requests, five
   // tokens over 8192 keys, heads of 256: 141 us, at the conversion 150).
+  // Exact but at the ends of the scales' range: a weight times a scale below 2^-126 leaves
+  // bf16's normal numbers (blocks whose values are below 2^-95 or so).
   constexpr bool FOLD = KIND == kCacheInt8Blocks;
   using Tile = DecodeTile<D, FP8>;
   constexpr int KS = D / 32;      // k steps of the first product

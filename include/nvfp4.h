@@ -605,9 +605,10 @@ int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int h
            nvfp4_stream_t stream);
 
 /*
- * paged_kv_append -- paged_kv_write with the rotation on the way: k is rotated in fp32
- * and rounded to the cache's type alone, v goes in as it is, and q, if there is one, is
- * rotated into q_out as rotary does it.
+ * paged_kv_append -- paged_kv_write with the rotation on the way: k is rotated, in fp32,
+ * or into block-scaled caches in fp64 rounded to fp32, and rounded to the cache's type
+ * alone, v goes in as it is, and q, if there is one, is rotated into q_out as rotary does
+ * it.
  *
  *   q, q_out     bf16 [tokens, num_heads * head_dim], as x and out of rotary; null
  *                with num_heads 0.

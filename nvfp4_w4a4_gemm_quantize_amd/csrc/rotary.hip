@@ -24,9 +24,9 @@ constexpr int kThreads = 256;
 
 // cos and sin of x / 2^32 turns times amplitude, rounded by who uses them.  The nearest quarter is
 // taken off, which leaves at most an eighth of a turn, where the Taylor series up to x^11
-// and x^10 are off by less than 10^-10.  In fp64, whose FMA takes no longer here: fp32's
-// last digit would move a hundred times as many 8-bit codes of rotated keys to the other
-// side of a tie.
+// and x^10 are off by 7 10^-12 and 1.2 10^-10 at most (what x's last place weighs, 1.5 10^-9
+// radians, is more).  In fp64, whose FMA takes no longer here; block-scaled keys are turned
+// in it too.
 __device__ __forceinline__ double2 cos_sin(uint32_t x, double amplitude) {
   const uint32_t quarter = (x + 0x20000000u) >> 30;
   const double t = (double)(int32_t)(x - (quarter << 30)) * 1.46291807926715968e-9;   // 2 pi / 2^32
@@ -186,8 +186,9 @@ hipError_t launch_rotary(const RotaryRows& a, const RotaryArgs& rot, hipStream_t
 
 // --------------------------------------------------------------- append ----
 //
-// q and k are rotated in fp32, and q is rounded to bf16, k to the cache's type alone;
-// v goes there as it is.  Caches with one scale a head (or none) have nothing that
+// q and k are rotated in fp32, k of block-scaled caches in fp64 rounded to fp32 (its codes are
+// the formula's but for ties), and q is rounded to bf16, k to the cache's type alone; v
+// goes there as it is.  Caches with one scale a head (or none) have nothing that
 // joins tokens: heads q, k, v are one list, of which a thread (token, unit) takes a part.
 //
 // Block-scaled caches: a workgroup takes one run (the neighbouring rows of the call that

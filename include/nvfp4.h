@@ -593,7 +593,7 @@ int rotary_steps(int rotary_dim, double base, int scaling, double factor, double
  *   x         bf16 [tokens, num_heads * head_dim], row stride ld_x (multiple of
  *             8), 16-byte aligned; q and k side by side in a projection's output
  *             are one such matrix.
- *   head_dim  a multiple of 16 up to 1024.
+ *   head_dim  a multiple of 16 up to 1024; tokens * head_dim below 2^36.
  *   positions int32 [tokens], as from paged_plan.
  *   steps     device uint64 [rotary_dim / 2], from rotary_steps; layout NVFP4_ROTARY_*.
  *   out       as x, row stride ld_out; may be x itself (ld_out == ld_x), must not
@@ -612,7 +612,7 @@ int rotary(const uint16_t* x, int64_t ld_x, int64_t tokens, int num_heads, int h
  *
  *   q, q_out     bf16 [tokens, num_heads * head_dim], as x and out of rotary; null
  *                with num_heads 0.
- *   k, v, slots, tokens, the caches   as in paged_kv_write.
+ *   k, v, slots, tokens, the caches   as in paged_kv_write; tokens * head_dim below 2^34.
  *   positions, steps, rotary_dim, layout, amplitude   as in rotary; rotary_dim 0 (and
  *                steps null) rotates nothing.
  *   cache_dtype  any NVFP4_CACHE_*; k_scale, v_scale for E4M3 (null = 1), k_blocks,

@@ -89,6 +89,8 @@ int paged_kv_append(const uint16_t* q, int64_t ld_q, int num_heads, uint16_t* q_
   if (rc) return rc;
   rc = validate_paged_kv_write(k, ld_k, v, ld_v, slots, tokens, num_kv_heads, head_dim);
   if (rc) return rc;
+  // 2 head_dim threads for 16 tokens, and q's beside them: one launch
+  if (tokens * head_dim >= (int64_t)1 << 34) return NVFP4_EUNSUPPORTED;
   if (num_heads < 0) return NVFP4_ESHAPE;
   if (num_heads > 0) {
     rc = validate_rotary_rows(q, ld_q, tokens, num_heads, head_dim, q_out, ld_q_out);

@@ -5,6 +5,7 @@
 // k < 2^17), so no split of k and no order of its parts can change a result.
 #include <hip/hip_bf16.h>
 #include <hip/hip_runtime.h>
+#include <math.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -124,8 +125,14 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void int8_quantize_k
 
 namespace {
 
+constexpr int64_t kQuantiseRows = 1 << 23;   // of a launch: with 256 threads a row half of what it counts
+
 hipError_t quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, float* scales, uint32_t* clear,
                     int clears, hipStream_t st) {
+  for (; rows > kQuantiseRows; rows -= kQuantiseRows, x += kQuantiseRows * ld, codes += kQuantiseRows * cols, scales += kQuantiseRows, clears = 0) {
+    const hipError_t e = quantize(x, kQuantiseRows, cols, ld, codes, scales, clear, clears, st);
+    if (e != hipSuccess) return e;
+  }
   const unsigned four = (unsigned)((rows + 3) / 4);
   if (rows >= 256 && cols <= 4096)
     int8_quantize_kernel<64, 8><<<four, 256, 0, st>>>(x, rows, cols, ld, codes, scales, clear, clears);
@@ -724,6 +731,7 @@ bool stream_quantises(int64_t m, int64_t k) { return m * k <= 8 * 256 * kQuantis
 // all codes (8 tokens, 1024 x 5120: 5.9 us, tiles 10.0; 8 tokens, 17408 x 5120: 24.6, tiles
 // 22.6; 2 tokens, 13605 x 12992: 48.9, tiles 41.7).
 bool streams(int64_t m, int64_t n, int64_t k) {
+  if (n > 1 << 27) return false;   // 16 threads a channel: a launch has no more
   if (n * k > 40000000) return m <= 4 && stream_quantises(m, k);
   return m * k <= kStreamCodes && m <= kStreamTokens;
 }
@@ -753,8 +761,10 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   } else {
     const int64_t t64 = tiles_of(kTiles64), t128 = tiles_of(kTiles128), t256 = tiles_of(kTiles256), rest = t256 % cus;
     const double large = t256 > cus && rest <= 128 ? (double)(t256 / cus) + (rest ? 0.35 : 0.) : rounds(t256, cus);
-    const double cost[4] = {14. * rounds(t64, cus), 21. * rounds(t128, cus), 40. * rounds(t128, 2 * cus), 60. * large};
+    double cost[4] = {14. * rounds(t64, cus), 21. * rounds(t128, cus), 40. * rounds(t128, 2 * cus), 60. * large};
     const Int8Kind kinds[4] = {kTiles64, kTiles128, kTilesMany, kTiles256};
+    if (!one_launch(t64, 512)) cost[0] = HUGE_VAL;
+    if (!one_launch(t128, 512)) cost[1] = HUGE_VAL;
     tiles_of(kinds[std::min_element(cost, cost + 4) - cost]);
   }
   if (p.kind == kTiles256) return p;
@@ -779,6 +789,7 @@ template <int MF, int NF, int WM, int WN, int STAGES, bool LINES>
 hipError_t launch_tiles(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
   using S = TileShape<MF, NF, WM, WN, STAGES>;
   const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * a.splits);
+  if (!one_launch(p.tiles_m * p.tiles_n * a.splits, S::THREADS)) return hipErrorInvalidConfiguration;
   if (LINES && whole_lines(a))
     int8_tile_kernel<MF, NF, WM, WN, STAGES, LINES><<<grid, S::THREADS, 0, st>>>(a, (int)p.tiles_m, (int)p.tiles_n);
   else

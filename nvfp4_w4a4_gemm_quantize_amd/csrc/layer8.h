@@ -12,6 +12,9 @@
 
 namespace nvfp4 {
 
+// A launch counts its threads in 32 bits: of more, some are not started, without an error.
+inline bool one_launch(int64_t blocks, int threads) { return blocks * threads <= (int64_t)UINT32_MAX; }
+
 // A rotation: pair i of a head turns by steps[i] * position 2^-64ths of a turn.
 struct RotaryArgs {
   const uint64_t* steps;       // [dim / 2]

@@ -78,6 +78,7 @@ int validate_rotary_rows(const void* x, int64_t ld_x, int64_t tokens, int num_he
                          int64_t ld_out) {
   if (tokens < 0 || num_heads <= 0 || head_dim <= 0) return NVFP4_ESHAPE;
   if (head_dim % 16 || head_dim > 1024 || num_heads > 65536 || tokens > INT32_MAX) return NVFP4_EUNSUPPORTED;
+  if (tokens * head_dim >= (int64_t)1 << 36) return NVFP4_EUNSUPPORTED;   // a thread 16 columns of a token: one launch
   const int64_t cols = (int64_t)num_heads * head_dim;
   if (ld_x < cols || ld_out < cols) return NVFP4_ESHAPE;
   if (tokens == 0) return NVFP4_OK;

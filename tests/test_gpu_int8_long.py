@@ -15,7 +15,7 @@ def test_quantize_more_rows_than_a_launch_takes(gpu_lib):
     gpu_lib.int8_quantize(x, codes=codes, scales=scales)
     want, ws = gpu_lib.int8_quantize(x[at].contiguous())
     assert torch.equal(codes[at], want) and torch.equal(scales[at], ws)
-    codes[at], scales[at] = 127, scales[2]
+    codes[at], scales[at] = 127, scales[2].item()
     assert (codes == 127).all() and (scales == scales[2]).all()
 
 

@@ -471,8 +471,9 @@ int paged_kv_write(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t l
  *                the same or larger sizes (num_kv_heads: the same or fewer); its
  *                first 2048 bytes zero before its first use (each call leaves them
  *                so); not shared by calls in flight on different streams.
- * tokens == 0 or num_requests == 0 enqueues nothing.  Results are
- * deterministic.
+ * tokens == 0 enqueues nothing, and num_requests == 0 (q, q_start, seq_lens, block_table
+ * and workspace may be null then) no more than the clearing of padding, which all rows
+ * are.  Results are deterministic.
  */
 size_t paged_attention_workspace_bytes(int64_t tokens, int64_t num_requests, int num_heads, int num_kv_heads,
                                        int head_dim, int64_t max_new, int64_t max_seq);

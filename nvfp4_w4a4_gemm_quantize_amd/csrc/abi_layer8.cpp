@@ -131,11 +131,15 @@ int paged_attention_blocks(const uint16_t* q, int64_t ld_q, int64_t tokens, cons
   rc = validate_block_cache(k_cache, v_cache, cache_dtype, num_pages, page_size, num_kv_heads, head_dim, page_stride, head_stride,
                             token_stride, k_blocks, v_blocks);
   if (rc) return rc;
-  if (num_requests == 0) return NVFP4_OK;
-  rc = validate_paged_attention(q, ld_q, tokens, q_start, seq_lens, num_heads, head_dim, block_table, max_pages, ld_table, scale,
-                                window, out, out_dtype, ld_out, lse, workspace, workspace_bytes,
-                                attention_workspace_bytes(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new,
-                                                          max_seq));
+  if (num_requests == 0) {
+    if (!(out_dtype & NVFP4_OUT_CLEAR_PADDING)) return NVFP4_OK;
+    rc = validate_attention_padding(tokens, num_heads, head_dim, out, out_dtype, ld_out, lse);
+  } else {
+    rc = validate_paged_attention(q, ld_q, tokens, q_start, seq_lens, num_heads, head_dim, block_table, max_pages, ld_table, scale,
+                                  window, out, out_dtype, ld_out, lse, workspace, workspace_bytes,
+                                  attention_workspace_bytes(tokens, num_requests, num_heads, num_kv_heads, head_dim, max_new,
+                                                            max_seq));
+  }
   if (rc || tokens == 0) return rc;
   AttentionArgs a{};
   a.q = q;

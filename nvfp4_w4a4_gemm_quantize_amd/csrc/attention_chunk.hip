@@ -998,7 +998,9 @@ hipError_t launch_attention_chunk(const AttentionArgs& a, void* workspace, hipSt
 // requests of up to 32 tokens over 4096 keys: 92 us, both kernels 112; of up to 10
 // 93 against 113).
 // Clears the padding rows of a batch that has nothing else (it brings no new tokens).
-__global__ __launch_bounds__(256) void attention_padding_kernel(AttentionArgs a) { clear_padding(a, a.q_start[a.requests]); }
+__global__ __launch_bounds__(256) void attention_padding_kernel(AttentionArgs a) {
+  clear_padding(a, a.requests ? a.q_start[a.requests] : 0);
+}
 
 static bool may_tile(int64_t max_new, int group) { return max_new * group > kDecodeRows; }
 static bool may_stream(int64_t tokens, int64_t requests, int64_t max_new, int group) {
@@ -1018,6 +1020,7 @@ size_t attention_workspace_bytes(int64_t tokens, int64_t requests, int hq, int h
 
 hipError_t launch_paged_attention(const AttentionArgs& args, hipStream_t st) {
   AttentionArgs a = args;
+  if (a.requests == 0) a.max_new = 0;   // no row but padding
   if (a.group > 1) {
     int s = 31 - __builtin_clz(a.group);
     const bool power = (a.group & (a.group - 1)) == 0;

@@ -107,6 +107,16 @@ int validate_paged_attention(const void* q, int64_t ld_q, int64_t tokens, const 
   return workspace_bytes < needed ? NVFP4_ESIZE : NVFP4_OK;
 }
 
+int validate_attention_padding(int64_t tokens, int num_heads, int head_dim, const void* out, int out_dtype,
+                               int64_t ld_out, const void* lse) {
+  const int out_kind = out_dtype & ~NVFP4_OUT_CLEAR_PADDING;
+  if (out_kind != NVFP4_OUT_F32 && out_kind != NVFP4_OUT_BF16) return NVFP4_EINVAL;
+  if (ld_out < (int64_t)num_heads * head_dim) return NVFP4_ESHAPE;
+  if (tokens == 0) return NVFP4_OK;
+  if (!out) return NVFP4_EINVAL;
+  return !aligned(out, 16) || ld_out % 4 || !aligned(lse, 4) ? NVFP4_EALIGN : NVFP4_OK;
+}
+
 int validate_verify_sizes(int64_t num_requests, int64_t max_drafts, int64_t vocab) {
   if (num_requests < 0 || max_drafts < 0 || vocab <= 0) return NVFP4_ESHAPE;
   return num_requests > 65535 || max_drafts > 255 || vocab > INT32_MAX - 4096 ? NVFP4_EUNSUPPORTED : NVFP4_OK;

@@ -25,6 +25,9 @@ int validate_paged_attention(const void* q, int64_t ld_q, int64_t tokens, const 
                              int64_t ld_table, float scale, int64_t window, const void* out, int out_dtype,
                              int64_t ld_out, const void* lse, const void* workspace, size_t workspace_bytes,
                              size_t needed);
+// A batch without requests, whose rows are to be cleared.
+int validate_attention_padding(int64_t tokens, int num_heads, int head_dim, const void* out, int out_dtype,
+                               int64_t ld_out, const void* lse);
 int validate_verify_sizes(int64_t num_requests, int64_t max_drafts, int64_t vocab);
 int validate_verify_drafts(const void* logits, int logits_dtype, int64_t ld_logits, int64_t rows, int64_t vocab,
                            const void* row_start, const void* num_drafts, int64_t max_drafts,

@@ -80,7 +80,9 @@ __device__ __forceinline__ u32x2 codes8(const u32x4& w, float by) {
 //
 // A wave or a workgroup a row: its largest magnitude, then its codes.  Bound by HBM: 3
 // bytes an element; the row's first HELD x THREADS x 8 values stay in registers between
-// the two, the rest is read again from the caches.  4096 rows of 5120: 18 us, 3.5 TB/s.
+// the two, the rest is read again from the caches.  4096 rows of 5120: 17.4 - 20 us, 3.1 -
+// 3.6 TB/s (14.4 where the rows lie in the last-level cache): 4096 waves are one round of four
+// a SIMD, which all read and then all write; they wait 74% of their cycles.
 template <int THREADS, int HELD>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void int8_quantize_kernel(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
                                                             int8_t* codes, float* scales, uint32_t* clear, int clears) {
@@ -163,10 +165,12 @@ hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, i
 // and the tokens as its columns, so that a lane ends with one token and runs of four
 // channels.
 //
-// Bound by the matrix unit and the power it may draw: 4096 tokens, 17408 x 5120, takes 308 -
-// 320 us, 2.3 PFLOP/s, the matrix unit busy for 61% of the cycles at 1.82 GHz (with codes
-// that are all zero it took 306 where random ones took 337; loads of the next tile before
-// the epilogue changed nothing).  777 tokens, 4104 x 2064: 16 - 17 us, 0.8 PFLOP/s, of which
+// 4096 tokens, 17408 x 5120, take 297 - 320 us, 2.3 - 2.45 POP/s, the matrix unit busy for 61 -
+// 63% of the cycles at 1.82 GHz.  Bound by how the products are fed: the waves wait 39% of
+// their cycles, with two places in LDS and one workgroup a CU, whose start and epilogue
+// nothing covers; and less by the power that sets the clock (with codes that are all zero it
+// took 306 us where random ones took 337; loads of the next tile before the epilogue changed
+// nothing).  777 tokens, 4104 x 2064: 16 - 17 us, 0.8 PFLOP/s, of which
 // 7 are the launch, the first stages and the epilogue: 231 tiles of 128 x 128 are one round
 // (at other sizes of it a stage is 0.35 us, its loads alone 0.25, its products alone 0.2).
 //
@@ -573,7 +577,7 @@ __global__ __launch_bounds__(512, 2) void int8_large_kernel(Int8Args a, int tile
 // on their way, which spares a launch; the first one writes them out.
 namespace {
 
-constexpr int kStreamCodes = 40960;   // bytes of codes in LDS: four workgroups a CU
+constexpr int kStreamCodes = 40960;   // bytes of codes in LDS: with the sums beside them three workgroups a CU
 constexpr int kStreamTokens = 16;
 constexpr int kQuantiseHeld = 8;      // pieces of eight values a thread holds: up to 16384 values in all
 
@@ -744,6 +748,17 @@ bool streams(int64_t m, int64_t n, int64_t k) {
 // 128 x 128 43.2, two a CU 38.5, 256 x 256 42.1; 2048 tokens: two a CU 71.6, 256 x 256 55.8; 713
 // tokens, 10312 x 4608: 48.6, 61.8.  Few tiles are split along k (37 tokens, 5120 x 17408, 80
 // tiles of 64 x 64: three parts 23.2 us, one 41).
+//
+// A last round of up to 128 tiles of 256 x 256 goes as quarters: 2048 tokens, k = 5120, beyond a
+// full round 16 tiles 103 us (whole 128), 64 106 (126), 128 133 (138), but 144 148 (146) and
+// 160 151 (139).
+// Fewer than 110 tiles of 64 x 128 go as 64 x 64 ones: 64 of them (256 tokens, 2048 x 5120, two
+// parts) 12.9 us, as 64 x 128 in four parts 15.8; 80 (128 tokens, 5120 x 5120) 13.9, in three
+// parts 14.5; beyond a CU's tile each 160 (256 tokens, 5120 x 5120) 20.6, 18.2.  Between 110
+// and 128 the smaller ones would still be ahead (512 tokens, 2048 x 5120: 14.1, 16.6), and
+// over a long k the larger ones, with more parts, are already below 110 (k = 17408: 256 tokens,
+// 2048 channels 27.9, 25.6; 128 tokens, 5120 channels 47, 34; but 192 tokens, 4096 channels
+// 35.5, 40.3).
 Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   Int8Plan p{kStream, 0, 0, 0, 0, 1};
   if (streams(m, n, k)) return p;
@@ -770,7 +785,10 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   if (p.kind == kTiles256) return p;
   const int64_t stages = (k + kStageBytes - 1) / kStageBytes, tiles = p.tiles_m * p.tiles_n;
   int64_t splits = std::min(cus / tiles, stages / 10);
-  // two of these are in a CU (607 tokens, 1069 x 15744: 37.9 us, unsplit 45.4)
+  // Two of these are in a CU, so that a part more pays where the tiles are well below two
+  // a CU and k is long: one part and two, 607 tokens, 1069 x 15744 (170 tiles) 33.7 us, 30.6;
+  // 300 tokens, 2048 x 16384 (160) 35.8, 29.1; but x 8192 (607 tokens, 1069 channels) 19.9 both,
+  // and with 256 tiles (512 tokens, 2048 x 16384) 37.2, 39.5.
   if (p.kind == kTiles64Square && tiles * splits < 200 && splits * 40 < stages) ++splits;
   p.splits = (int)std::max<int64_t>(1, splits);
   return p;

@@ -27,7 +27,7 @@
 // take 82 us, over E4M3 85: 1.4 us a tile of keys, shares between 57 and 80 us long, and
 // a part's 8 us beside its keys (its queries, page numbers and first keys; its output).
 //
-// Block-scaled caches, 4096 after 4096, 40 heads of 128 over 8: E4M3 525 us, INT8 553 - 572 (bf16
+// Block-scaled caches, 4096 after 4096, 40 heads of 128 over 8: E4M3 525 us, INT8 553 - 580 (bf16
 // and E4M3 with one scale a head 505 - 510).  The scales take scalar registers that are spilled already,
 // and two INT8 elements five instructions where E4M3 takes one: the matrix unit is busy for
 // 40% of the cycles.  Heads of 64: 512 and 523 (bf16 482); 256, 24 over 4: 794 and 680 (bf16 620,

@@ -830,6 +830,16 @@ def _apart_from(t, others):
                 raise NVFP4Error("a tensor that the call writes overlaps another one")
 
 
+def _meet(*ranges):
+    """Whether any of (address, end) ranges meet: what most calls have to look at."""
+    end = 0
+    for p, e in sorted(ranges):
+        if p < end:
+            return True
+        end = e
+    return False
+
+
 def _apart_all(written, read):
     """Refuse written ranges ((address, bytes) each) that meet each other or one that is read."""
     for i, (p, n) in enumerate(written):
@@ -980,7 +990,7 @@ def int8_quantize(x, codes=None, scales=None):
     if scales is None:
         scales = x.new_empty(rows, dtype=_f32)
     cp, sp = _codes8(device, codes, rows, cols, "codes")[0], _vec_on(device, scales, _f32, rows, "scales")
-    if given:
+    if given and _meet((xp, xp + 2 * ((rows - 1) * ld + cols)), (cp, cp + rows * cols), (sp, sp + 4 * rows)):
         written = [(cp, rows * cols), (sp, 4 * rows)]
         _apart_all(written, [])
         _apart_from(x, written)
@@ -1024,7 +1034,8 @@ def gemm_w8a8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, worksp
     sp, tp = _vec_on(device, a_scale, _f32, m, "a_scale"), _vec_on(device, w_scale, _f32, n, "w_scale")
     given = workspace is not None
     workspace, wsp, bytes_ = _int8_workspace(device, lib, a, m, n, k, workspace)
-    if given or made:
+    if (given or made) and _meet((ap, ap + m * k), (sp, sp + 4 * m), (wp, wp + n * k), (tp, tp + 4 * n), (wsp or 0, (wsp or 0) + bytes_),
+                                 (op, op + ((m - 1) * ld + n) * out.element_size())):
         read = [(ap, m * k), (sp, 4 * m), (wp, n * k), (tp, 4 * n)]
         if given:
             _apart_all([(wsp, bytes_)], read)
@@ -1065,13 +1076,13 @@ def int8_linear(x, w, w_scale, out_dtype=torch.bfloat16, out=None, codes=None, s
         bytes_ = workspace.numel() if isinstance(workspace, _Tensor) else 0
         wsp = None if workspace is None else _vec_on(device, workspace, _u8, bytes_, "workspace")
         written = [(cp, m * k), (sp, 4 * m), (wsp or 0, bytes_)]
+    made = out is not None
+    out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, out)
+    if (made or written) and _meet((xp, xp + 2 * ((m - 1) * ld_x + k)), (wp, wp + n * k), (tp, tp + 4 * n),
+                                   (op, op + ((m - 1) * ld + n) * out.element_size()), *((p, p + size) for p, size in written)):
         _apart_all(written, [(wp, n * k), (tp, 4 * n)])
         _apart_from(x, written)
-    if out is not None:
-        out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, out)
         _apart_from(out, written + [(wp, n * k), (tp, 4 * n)])
-    else:
-        out, op, ld, kind = _int8_out(device, x, m, n, out_dtype, None)
     rc = lib.int8_linear(xp, m, k, ld_x, cp, sp, wp, tp, n, op, kind, ld, wsp, bytes_, _raw_stream(device))
     if rc:
         _check(rc, "int8_linear")
